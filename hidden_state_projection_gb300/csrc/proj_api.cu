@@ -29,6 +29,7 @@
 #include <cstring>
 #include <mutex>
 
+#include "api_internal.h"
 #include "launch.h"
 #include "proj.h"
 #include "stream_args.h"
@@ -444,11 +445,7 @@ std::mutex g_map_mu;
 MapEntry g_maps[kMapCache];
 int g_map_next = 0;
 
-// Tiled tensor map (128-byte swizzle, zero fill past the tensor), cached per
-// (pointer, shape, box).  dims[0] is the innermost extent in elements; strides[i]
-// is the byte stride of dimension i + 1.
-proj_status encode_map(const void *ptr, int rank, const uint64_t *dims, const uint64_t *strides, const uint32_t *box,
-                       proj_dtype dt, CUtensorMap *out) {
+proj_status load_encode() {
     std::call_once(g_encode_once, [] {
         void *fn = nullptr;
         cudaDriverEntryPointQueryResult q;
@@ -460,6 +457,15 @@ proj_status encode_map(const void *ptr, int rank, const uint64_t *dims, const ui
             (void)cudaGetLastError();
     });
     if (!g_encode) return fail(PROJ_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
+    return PROJ_OK;
+}
+
+// Tiled tensor map (128-byte swizzle, zero fill past the tensor), cached per
+// (pointer, shape, box).  dims[0] is the innermost extent in elements; strides[i]
+// is the byte stride of dimension i + 1.
+proj_status encode_map(const void *ptr, int rank, const uint64_t *dims, const uint64_t *strides, const uint32_t *box,
+                       proj_dtype dt, CUtensorMap *out) {
+    if (proj_status st = load_encode(); st != PROJ_OK) return st;
     MapEntry key{};
     key.ptr = reinterpret_cast<uint64_t>(ptr);
     key.rank = rank;
@@ -1112,6 +1118,67 @@ proj_status norm_layout(int32_t M, int32_t K, const int32_t *n_splits, int32_t n
 
 }  // namespace
 
+// ---- shared with the other entry-point files (api_internal.h) -------------------------
+
+namespace hsp {
+
+proj_status api_fail(proj_status st, const char *fmt, ...) {
+    va_list ap;
+    va_start(ap, fmt);
+    vsnprintf(g_last_error, sizeof g_last_error, fmt, ap);
+    va_end(ap);
+    return st;
+}
+proj_status api_cuda_fail(cudaError_t e, const char *what) { return cuda_fail(e, what); }
+proj_status api_ok() { return ok(); }
+
+proj_status api_device(ApiDevice *out) {
+    DeviceInfo d;
+    proj_status st = device_info(&d);
+    if (st != PROJ_OK) return st;
+    out->sms = d.sms;
+    out->err_word = d.err_word;
+    return PROJ_OK;
+}
+int api_plan_sms() {
+    int ctas[17], pairs[17], trios[17];
+    plan_ctas(ctas, pairs, trios);
+    return ctas[1];
+}
+
+ApiOptions api_options() {
+    ApiOptions o;
+    o.pdl = g_opt_pdl.load();
+    o.skip_stage = g_opt_skip_stage_plus1.load() - 1;
+    const int wus = g_opt_wait_us.load();
+    o.wait_limit_ns = wus > 0 ? static_cast<uint64_t>(wus) * 1000ull : kDefaultWaitNs;
+    return o;
+}
+void api_count_launches(int n) { g_launches.fetch_add(static_cast<uint64_t>(n), std::memory_order_relaxed); }
+
+proj_status api_encode_5d(const void *ptr, const uint64_t (&dims)[5], const uint64_t (&strides)[4],
+                          const uint32_t (&box)[5], CUtensorMap *out) {
+    proj_status st = load_encode();
+    if (st != PROJ_OK) return st;
+    cuuint64_t d[5], sd[4];
+    cuuint32_t b[5], estr[5] = {1, 1, 1, 1, 1};
+    for (int i = 0; i < 5; ++i) {
+        d[i] = dims[i];
+        b[i] = box[i];
+        if (i < 4) sd[i] = strides[i];
+    }
+    const CUresult r = g_encode(out, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, const_cast<void *>(ptr), d, sd, b, estr,
+                                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS)
+        return fail(PROJ_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d): dims [%llu %llu %llu %llu %llu], box [%u %u %u]",
+                    static_cast<int>(r), (unsigned long long)d[0], (unsigned long long)d[1], (unsigned long long)d[2],
+                    (unsigned long long)d[3], (unsigned long long)d[4], b[0], b[1], b[2]);
+    return PROJ_OK;
+}
+
+}  // namespace hsp
+
 // A recorded host step (proj_host_plan_create): the graph and its executable.
 struct proj_host_plan {
     cudaGraph_t graph = nullptr;
@@ -1507,6 +1574,8 @@ proj_status proj_check_device_error(proj_stream_t stream) {
         e = cudaMemcpy(dev.err_word, &zero, sizeof zero, cudaMemcpyHostToDevice);
         if (e != cudaSuccess) return cuda_fail(e, "clearing the device error word");
         if (v == PROJ_ERR_TIMEOUT) return fail(PROJ_ERR_TIMEOUT, "a kernel gave up a bounded wait (timeout)");
+        if (v == PROJ_ERR_BAD_INDEX)
+            return fail(PROJ_ERR_BAD_INDEX, "a kernel met a page, row, position or length outside its cache");
         return fail(PROJ_ERR_CUDA, "device error word %d", v);
     }
     return ok();

@@ -59,12 +59,16 @@ typedef enum {
     PROJ_ERR_UNSUPPORTED_DTYPE = 4,
     PROJ_ERR_DEVICE = 5,            /* current device is not compute capability 10.3 */
     PROJ_ERR_CUDA = 6,              /* a CUDA runtime/driver call failed */
-    PROJ_ERR_TIMEOUT = 7            /* a kernel's bounded wait ran out (see proj_check_device_error) */
+    PROJ_ERR_TIMEOUT = 7,           /* a kernel's bounded wait ran out (see proj_check_device_error) */
+    PROJ_ERR_BAD_INDEX = 8          /* a kernel met a page id, table row, position or length outside
+                                     * its cache (see proj_check_device_error) */
 } proj_status;
 
 #define PROJ_MAX_SPLITS 8
 #define PROJ_MAX_M 64
 #define PROJ_MAX_PREFETCH 4
+#define PROJ_MAX_POOLS 4
+#define PROJ_MAX_COPY_PAIRS 2048
 
 /* A global range to bring into L2 (proj_fused_gemm_prefetch). */
 typedef struct {
@@ -356,6 +360,184 @@ int proj_pack_check(const void *w, const void *w_cat, int64_t row_off, int32_t n
                     int32_t n_total, int32_t K, proj_dtype dtype);
 
 /*
+ * The paged cache: where the projected keys and values of a decode step go, and the
+ * attention that reads them.
+ *
+ * A cache is a pool of pages of page_size tokens each.  A sequence is a row of the block
+ * table: seq_lens[row] tokens, token t on page block_table[row][t / page_size] at line
+ * t mod page_size.  Several rows may hold the same page (a shared prefix);
+ * ref_counts[page] says how many do, 0 = free.  All of it lives in device memory, is
+ * owned by the caller and is read when the kernels run, so a call needs no copy to the
+ * host and can be captured in a CUDA graph.  Table entries past a row's last page are
+ * neither read nor written (proj_cache_resize leaves -1 where it gives a page back).
+ *
+ * What the device finds wrong -- a table row, page id, position or length outside the
+ * cache -- touches no memory outside the caller's arrays and is reported by
+ * proj_check_device_error as PROJ_ERR_BAD_INDEX; the outputs of the sequence it
+ * concerns are then unspecified.
+ */
+typedef struct {
+    int32_t *block_table;  /* [num_rows, max_pages] page ids, rows at table_stride */
+    int64_t table_stride;  /* elements, >= max_pages */
+    int32_t *seq_lens;     /* [num_rows] */
+    int32_t *ref_counts;   /* [num_pages]; NULL where only tokens are read or written */
+    int32_t num_rows;
+    int32_t max_pages;     /* table entries per row; max_pages * page_size < 2^31 - 1024 */
+    int32_t num_pages;
+    int32_t page_size;     /* tokens per page: a power of two, 16 to 1024 */
+} proj_page_index;
+
+/* The keys and values of one layer, bf16.  Token `t` of page `p`, kv head `h`: k_dim
+ * consecutive elements at k + p * k_page_stride + t * k_token_stride + h * k_head_stride
+ * (elements; multiples of 8, so either order of tokens and heads in a page will do).
+ *   latent cache: v = NULL, k_dim 576 or 512, v_dim 512: the values are the first 512
+ *                 columns of the keys (compressed KV ++ k_pe, or the wkv projection);
+ *   grouped cache: v of its own, k_dim = v_dim = 64 or 128. */
+typedef struct {
+    void *k;
+    void *v;
+    int32_t kv_heads, k_dim, v_dim;
+    int32_t reserved;
+    int64_t k_page_stride, k_token_stride, k_head_stride;
+    int64_t v_page_stride, v_token_stride, v_head_stride;
+} proj_kv_pages;
+
+/* Page data for the calls that move whole pages: `layers` arrays of num_pages pages.
+ * Page p of layer l is page_bytes consecutive bytes at base + l * layer_stride +
+ * p * page_stride (bytes, all multiples of 16; base 16-byte aligned). */
+typedef struct {
+    void *base;
+    int64_t layer_stride, page_stride, page_bytes;
+    int32_t layers;
+    int32_t reserved;
+} proj_page_pool;
+
+/*
+ * proj_paged_attention -- attention of one new token per sequence over its cache:
+ *     out[b, h] = sum_t p_t v[t],  p = softmax over t < len of scale * q[b, h] . k[t],
+ *     lse[b, h] = log sum_t exp(scale * q[b, h] . k[t])
+ * for sequence rows[b] (or b), query heads h sharing kv head h / (heads / kv_heads).
+ * fp32 scores, maxima and sums; the softmax weights are rounded to bf16 for the product
+ * with the values and the result once.  A sequence of length 0 gives zeros and lse =
+ * -infinity; what lies in a page behind a sequence's last token is never used, NaN
+ * included.  Sequences are cut over the GPU by their lengths and joined in a fixed order:
+ * the same lengths give the same bits, run to run and under CUDA-graph replay; another
+ * batch around a sequence may round it differently.
+ *   q          device [batch, heads, k_dim] bf16, 16-byte aligned, rows at q_row_stride
+ *              and heads at q_head_stride (elements, multiples of 8)
+ *   index      block_table, seq_lens and sizes (ref_counts is not read)
+ *   rows       device [batch] table rows (may repeat), or NULL for 0 .. batch - 1
+ *   out        device [batch, heads, v_dim] bf16, dense, 16-byte aligned
+ *   lse        device [batch, heads] fp32, or NULL
+ *   workspace  device, 16-byte aligned, at least proj_paged_attention_workspace_bytes
+ *              bytes; needs no initialisation and keeps nothing.  Calls that share one
+ *              must not overlap on the GPU.
+ * Two kernel launches.  batch = 0 succeeds and touches nothing.
+ */
+proj_status proj_paged_attention(const void *q, int64_t q_row_stride, int64_t q_head_stride,
+                                 const proj_kv_pages *kv, const proj_page_index *index,
+                                 const int32_t *rows, int32_t batch, int32_t heads, float scale,
+                                 void *out, float *lse, void *workspace, size_t workspace_bytes,
+                                 proj_stream_t stream);
+
+/* Workspace bytes of proj_paged_attention (host only; 0 when the heads and columns are not
+ * supported, with proj_last_error_string saying why). */
+size_t proj_paged_attention_workspace_bytes(int32_t heads, int32_t kv_heads, int32_t k_dim,
+                                            int32_t v_dim, int32_t latent);
+
+/* Rotary turn of proj_cache_append: the last `dim` columns of a key or query row, in pairs
+ * (2j, 2j + 1) if interleaved, else (j, j + dim / 2):
+ *     (a, b) -> (a cos - b sin, b cos + a sin)
+ * with the cosines in cos_sin[pos][0 .. dim / 2) and the sines behind them. */
+typedef struct {
+    const float *cos_sin;  /* device [max_pos, dim] fp32, 16-byte aligned */
+    int32_t max_pos;
+    int32_t dim;           /* a multiple of 16, at most k_dim */
+    int32_t interleaved;
+    int32_t reserved;
+} proj_rotary;
+
+/*
+ * proj_cache_append -- writes the keys and values of `tokens` new tokens into their pages,
+ * and turns the queries that go with them.
+ *   k_new      device [tokens, kv_heads, k_dim] bf16, tokens at k_row_stride (elements),
+ *              heads dense: a fused projection's output as it is
+ *   v_new      device [tokens, kv_heads, v_dim] (NULL for a latent cache)
+ *   rows       device [tokens] table rows, or NULL for token i = row i
+ *   positions  device [tokens], or NULL for the last place of the row, seq_lens[row] - 1
+ *   rotary     NULL: rows are copied as they are
+ *   q, q_out   device [tokens, heads, k_dim], turned at the same positions; q_out may be q.
+ *              NULL q: no queries.  Strides in elements, multiples of 8.
+ * Pages must already hold the positions (proj_cache_resize) and be the row's own.  Two
+ * tokens of one call must not name the same row and position (which one stays is not
+ * defined).  One kernel launch; tokens = 0 succeeds and touches nothing.
+ */
+proj_status proj_cache_append(const void *k_new, int64_t k_row_stride, const void *v_new,
+                              int64_t v_row_stride, const proj_kv_pages *kv,
+                              const proj_page_index *index, const int32_t *rows,
+                              const int32_t *positions, int32_t tokens, const proj_rotary *rotary,
+                              const void *q, int64_t q_row_stride, int64_t q_head_stride,
+                              void *q_out, int64_t q_out_row_stride, int64_t q_out_head_stride,
+                              int32_t heads, proj_stream_t stream);
+
+/*
+ * proj_cache_resize -- sets the lengths of n rows: rows[i] gets new_lens[i] tokens.
+ * Growing takes the lowest free pages, in the order of the call (the pages free when the
+ * call starts); a row that grows and whose last page is partly filled and held by other
+ * rows too gets a copy of that page (over all pools) first, so what is appended next
+ * belongs to it alone.  Shrinking gives the pages past the new length back (their counts
+ * drop, the table entries become -1); length 0 frees the row.
+ *   status     device [n]: 0 done; 1 not enough free pages (the row is left as it was);
+ *              2 refused: a row outside the table, named before in the call, or a length
+ *              outside 0 .. max_pages * page_size
+ *   pools      host [num_pools], 1..PROJ_MAX_POOLS
+ *   workspace  device, 16-byte aligned, proj_cache_workspace_bytes(index, n) bytes, as for
+ *              proj_paged_attention
+ * Two kernel launches; n = 0 succeeds and touches nothing.
+ */
+proj_status proj_cache_resize(const proj_page_index *index, const int32_t *rows,
+                              const int32_t *new_lens, int32_t n, const proj_page_pool *pools,
+                              int32_t num_pools, int32_t *status, void *workspace,
+                              size_t workspace_bytes, proj_stream_t stream);
+
+/*
+ * proj_cache_fork -- children[i] becomes a second holder of everything parents[i] holds:
+ * same length, same pages, counts raised.  A parent may have several children.  Nothing
+ * is copied until one of them grows (proj_cache_resize).
+ *   status     device [n]: 0 done; 2 refused: a row outside the table, a child that is not
+ *              empty, is named before in the call or is itself a parent in it
+ * One kernel launch.
+ */
+proj_status proj_cache_fork(const proj_page_index *index, const int32_t *parents,
+                            const int32_t *children, int32_t n, int32_t *status,
+                            proj_stream_t stream);
+
+/*
+ * proj_cache_compact -- moves the live pages into the first places of the pool: with L
+ * live pages, the k-th live page at or past L goes to the k-th free page before L; the
+ * block tables of all rows and the counts follow.  live (device [1]) receives L.
+ * Workspace as for proj_cache_resize (proj_cache_workspace_bytes(index, 0) bytes).  Two
+ * kernel launches.
+ */
+proj_status proj_cache_compact(const proj_page_index *index, const proj_page_pool *pools,
+                               int32_t num_pools, int32_t *live, void *workspace,
+                               size_t workspace_bytes, proj_stream_t stream);
+
+/* Workspace bytes of proj_cache_resize over n rows and of proj_cache_compact (host only;
+ * 0 for a bad index). */
+size_t proj_cache_workspace_bytes(const proj_page_index *index, int32_t n);
+
+/*
+ * proj_cache_copy_pages -- copies page src[i] to page dst[i] in every layer of every pool.
+ *   src, dst   HOST [n], 0 <= id < num_pages, n <= PROJ_MAX_COPY_PAIRS; the destinations
+ *              differ from each other and are no source of the call (PROJ_ERR_INVALID_ARG)
+ * One kernel launch; n = 0 succeeds and touches nothing.
+ */
+proj_status proj_cache_copy_pages(const proj_page_pool *pools, int32_t num_pools,
+                                  int32_t num_pages, const int32_t *src, const int32_t *dst,
+                                  int32_t n, proj_stream_t stream);
+
+/*
  * proj_supported -- host-side query: 1 if (M, K, n_total, dtype) is served,
  * 0 otherwise (the shape gate; TensorRT-LLM PR #20502, dense-MLP and fused-A
  * commit messages: a host query answers whether the kernels serve a shape).
@@ -372,8 +554,9 @@ proj_status proj_get_options(proj_options *opt);
 /*
  * proj_check_device_error -- synchronizes `stream`, then reads and clears the
  * device error word of the current device.  Returns PROJ_ERR_TIMEOUT if any
- * kernel since the last check gave up a bounded wait, PROJ_ERR_CUDA if the
- * stream reported an error, else PROJ_OK.
+ * kernel since the last check gave up a bounded wait, PROJ_ERR_BAD_INDEX if a cache
+ * kernel met an index outside its cache (the first of the two is kept),
+ * PROJ_ERR_CUDA if the stream reported an error, else PROJ_OK.
  */
 proj_status proj_check_device_error(proj_stream_t stream);
 
