@@ -417,78 +417,98 @@ def pack_check(w: torch.Tensor, w_cat: torch.Tensor, row_off: int) -> bool:
 
 
 # ---- the paged cache ------------------------------------------------------------
+#
+# A decode step makes a handful of these calls per layer, so the checks are written to cost
+# little: plain comparisons, packed structs, the raw stream.
 
-def _same_device(*tensors) -> int:
+_BF16, _I32, _F32 = torch.bfloat16, torch.int32, torch.float32
+
+
+def _device(*tensors) -> int:
     """Index of the CUDA device that every given tensor (None is left out) lies on: the current one."""
-    dev = torch.cuda.current_device() if torch.cuda.is_available() else -1
+    dev = tensors[0].get_device()
     for t in tensors:
-        if t is not None and (t.get_device() != dev or dev < 0):
+        if t is not None and t.get_device() != dev:
             raise ProjError(1, f"every tensor must be on the current CUDA device (one is on {t.device})")
+    if dev < 0 or dev != torch._C._cuda_getDevice():
+        raise ProjError(1, f"every tensor must be on the current CUDA device (they are on {tensors[0].device})")
     return dev
 
 
-def _ints(name: str, t: Optional[torch.Tensor], n: Optional[int] = None):
-    """Device pointer of a dense 1-D int32 tensor (of n elements); None stays None."""
+def _raw_stream(stream, dev: int) -> int:
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream_ptr(stream)
+
+
+def _ints(name: str, t: Optional[torch.Tensor], n: int):
+    """Device pointer of a dense 1-D int32 tensor of n elements; None stays None."""
     if t is None:
         return None
-    if t.dtype != torch.int32 or t.dim() != 1 or not t.is_contiguous() or (n is not None and t.shape[0] != n):
-        raise ProjError(1, f"{name} must be a dense 1-D int32 tensor" + ("" if n is None else f" of {n} elements"))
+    if t.dtype != _I32 or t.shape != (n,) or not t.is_contiguous():
+        raise ProjError(1, f"{name} must be a dense 1-D int32 tensor of {n} elements")
     return t.data_ptr()
 
 
+_pack_index = struct.Struct("PqPPiiii").pack      # proj_page_index
+_pack_kv = struct.Struct("PPiiiiqqqqqq").pack     # proj_kv_pages
+_pack_pool = struct.Struct("Pqqqii").pack         # proj_page_pool
+_pack_rotary = struct.Struct("Piiii").pack        # proj_rotary
+
+
 def _page_index(block_table, seq_lens, ref_counts, num_pages: int, page_size: int) -> bytes:
-    if block_table.dtype != torch.int32 or block_table.dim() != 2 or (block_table.shape[1] > 1 and block_table.stride(1) != 1):
+    if block_table.dtype != _I32 or block_table.dim() != 2:
         raise ProjError(1, "block_table must be a 2-D int32 tensor with dense rows")
     rows, width = block_table.shape
-    lens = _ints("seq_lens", seq_lens, rows)
-    refs = _ints("ref_counts", ref_counts, num_pages)
-    return struct.pack("PqPPiiii", block_table.data_ptr(), max(block_table.stride(0), width) if rows < 2 else block_table.stride(0),
-                       lens, refs or 0, rows, width, num_pages, page_size)
+    st, one = block_table.stride()
+    if one != 1 and width > 1:
+        raise ProjError(1, "block_table must be a 2-D int32 tensor with dense rows")
+    return _pack_index(block_table.data_ptr(), st if rows > 1 else max(st, width), _ints("seq_lens", seq_lens, rows),
+                       0 if ref_counts is None else _ints("ref_counts", ref_counts, num_pages), rows, width, num_pages,
+                       page_size)
 
 
-def _kv_pages(k_pages: torch.Tensor, v_pages: Optional[torch.Tensor], v_dim: Optional[int]) -> bytes:
-    if k_pages.dim() != 4 or k_pages.stride(3) != 1:
+def _kv_pages(k_pages: torch.Tensor, v_pages: Optional[torch.Tensor], v_dim: Optional[int]):
+    """(packed proj_kv_pages, shape of the keys, columns of the values)"""
+    if k_pages.dim() != 4:
         raise ProjError(1, "k_pages must be a [num_pages, page_size, kv_heads, k_dim] tensor with dense columns")
-    if k_pages.dtype != torch.bfloat16 or (v_pages is not None and v_pages.dtype != torch.bfloat16):
+    shape = k_pages.shape
+    sp, st, sh, one = k_pages.stride()
+    if one != 1:
+        raise ProjError(1, "k_pages must be a [num_pages, page_size, kv_heads, k_dim] tensor with dense columns")
+    if k_pages.dtype != _BF16 or (v_pages is not None and v_pages.dtype != _BF16):
         raise ProjError(4, "the cache holds bf16")
-    ks = k_pages.stride()
     if v_pages is None:
-        return struct.pack("PPiiiiqqqqqq", k_pages.data_ptr(), 0, k_pages.shape[2], k_pages.shape[3],
-                           512 if v_dim is None else int(v_dim), 0, ks[0], ks[1], ks[2], 0, 0, 0)
-    if v_pages.dim() != 4 or v_pages.stride(3) != 1 or v_pages.shape[:3] != k_pages.shape[:3]:
+        dv = 512 if v_dim is None else int(v_dim)
+        return _pack_kv(k_pages.data_ptr(), 0, shape[2], shape[3], dv, 0, sp, st, sh, 0, 0, 0), shape, dv
+    if v_pages.dim() != 4 or v_pages.stride(3) != 1 or v_pages.shape[:3] != shape[:3]:
         raise ProjError(1, "v_pages must be a [num_pages, page_size, kv_heads, v_dim] tensor like k_pages")
-    if v_dim is not None and int(v_dim) != v_pages.shape[3]:
-        raise ProjError(1, f"v_dim={v_dim}, but v_pages has {v_pages.shape[3]} columns")
-    vs = v_pages.stride()
-    return struct.pack("PPiiiiqqqqqq", k_pages.data_ptr(), v_pages.data_ptr(), k_pages.shape[2], k_pages.shape[3],
-                       v_pages.shape[3], 0, ks[0], ks[1], ks[2], vs[0], vs[1], vs[2])
+    dv = v_pages.shape[3]
+    if v_dim is not None and int(v_dim) != dv:
+        raise ProjError(1, f"v_dim={v_dim}, but v_pages has {dv} columns")
+    vp, vt, vh, _ = v_pages.stride()
+    return _pack_kv(k_pages.data_ptr(), v_pages.data_ptr(), shape[2], shape[3], dv, 0, sp, st, sh, vp, vt, vh), shape, dv
 
 
 def _pools(pools: Sequence[torch.Tensor], num_pages: Optional[int]):
     packed = []
     for t in pools:
-        if t.dim() < 3 or (num_pages is not None and t.shape[1] != num_pages):
+        shape = t.shape
+        if len(shape) < 3 or (num_pages is not None and shape[1] != num_pages):
             raise ProjError(1, "a pool is a [layers, num_pages, ...] tensor")
-        want, page = 1, t.element_size()
-        for n, st in zip(reversed(t.shape[2:]), reversed(t.stride()[2:])):
-            if n != 1 and st != want:
+        num_pages, strides, e = shape[1], t.stride(), t.element_size()
+        want = 1
+        for d in range(len(shape) - 1, 1, -1):
+            if shape[d] != 1 and strides[d] != want:
                 raise ProjError(1, "the pages of a pool must be dense")
-            want *= n
-        e = t.element_size()
+            want *= shape[d]
         page = want * e
-        packed.append(struct.pack("Pqqqii", t.data_ptr(), t.stride(0) * e if t.shape[0] > 1 else page,
-                                  t.stride(1) * e if t.shape[1] > 1 else page, page, t.shape[0], 0))
-        num_pages = t.shape[1]
+        packed.append(_pack_pool(t.data_ptr(), strides[0] * e if shape[0] > 1 else page, strides[1] * e if num_pages > 1 else page,
+                                 page, shape[0], 0))
     return b"".join(packed), num_pages
 
 
-def _scratch(nbytes: int, dev: int, stream) -> torch.Tensor:
-    """Workspace of one call, kept from reuse until the call's stream has passed it."""
-    return _made(torch.empty(nbytes, dtype=torch.uint8, device=dev), stream)
-
-
 def _made(t: torch.Tensor, stream) -> torch.Tensor:
-    """A tensor allocated on the current stream for use on `stream`."""
+    """A tensor allocated on the current stream for use on `stream`: its memory is not used before the current
+    stream has left it, nor given away before `stream` has."""
     if stream is not None:
         s = torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream
         if s.cuda_stream != torch.cuda.current_stream().cuda_stream:
@@ -498,11 +518,15 @@ def _made(t: torch.Tensor, stream) -> torch.Tensor:
 
 
 def _work(t: Optional[torch.Tensor], need: int, dev: int, stream) -> torch.Tensor:
+    """The caller's workspace, or one from torch for this call."""
     if t is None:
-        return _scratch(need, dev, stream)
+        return _made(torch.empty(need, dtype=torch.uint8, device=dev), stream)
     if not t.is_contiguous():
         raise ProjError(1, "workspace must be dense")
     return t
+
+
+_attn_workspace = {}  # bytes by shape and device: the library's answer depends on nothing else
 
 
 def paged_attention_workspace_bytes(heads: int, kv_heads: int, k_dim: int, v_dim: int, latent: bool) -> int:
@@ -522,29 +546,49 @@ def paged_attention(q: torch.Tensor, k_pages: torch.Tensor, v_pages: Optional[to
     cache, the values are the first v_dim = 512 columns of the keys); block_table [rows, max_pages] and seq_lens
     [rows] int32; `rows` maps batch entries to table rows.  Returns out [batch, heads, v_dim], or (out, lse) with
     return_lse.  `workspace` (paged_attention_workspace_bytes) is taken from torch per call if not given."""
-    dev = _same_device(q, k_pages, v_pages, block_table, seq_lens, rows, out, lse, workspace)
-    if q.dim() != 3 or (q.stride(2) != 1 and q.shape[2] != 1) or q.shape[2] != k_pages.shape[-1]:
+    dev = _device(q, k_pages, v_pages, block_table, seq_lens, rows, out, lse, workspace)
+    kv, kshape, dv = _kv_pages(k_pages, v_pages, v_dim)
+    if q.dim() != 3 or q.shape[2] != kshape[3] or q.stride(2) != 1:
         raise ProjError(1, "q must be a [batch, heads, k_dim] tensor with dense columns")
-    if q.dtype != torch.bfloat16:
+    if q.dtype != _BF16:
         raise ProjError(4, f"unsupported tensor dtype {q.dtype}")
     batch, heads, k_dim = q.shape
-    kv = _kv_pages(k_pages, v_pages, v_dim)
-    dv = v_pages.shape[3] if v_pages is not None else (512 if v_dim is None else int(v_dim))
-    index = _page_index(block_table, seq_lens, None, k_pages.shape[0], k_pages.shape[1])
-    need = paged_attention_workspace_bytes(heads, k_pages.shape[2], k_dim, dv, v_pages is None)
+    index = _page_index(block_table, seq_lens, None, kshape[0], kshape[1])
     if out is None:
-        out = _made(torch.empty((batch, heads, dv), dtype=q.dtype, device=dev), stream)
-    elif out.shape != (batch, heads, dv) or out.dtype != q.dtype or not out.is_contiguous():
+        out = _made(torch.empty((batch, heads, dv), dtype=_BF16, device=dev), stream)
+    elif out.shape != (batch, heads, dv) or out.dtype != _BF16 or not out.is_contiguous():
         raise ProjError(1, f"out must be a dense [{batch}, {heads}, {dv}] {q.dtype} tensor")
-    if lse is None and return_lse:
-        lse = _made(torch.empty((batch, heads), dtype=torch.float32, device=dev), stream)
-    elif lse is not None and (lse.shape != (batch, heads) or lse.dtype != torch.float32 or not lse.is_contiguous()):
+    if lse is None:
+        if return_lse:
+            lse = _made(torch.empty((batch, heads), dtype=_F32, device=dev), stream)
+    elif lse.shape != (batch, heads) or lse.dtype != _F32 or not lse.is_contiguous():
         raise ProjError(1, f"lse must be a dense [{batch}, {heads}] float32 tensor")
-    ws = _work(workspace, need, dev, stream)
-    _check(lib().proj_paged_attention(q.data_ptr(), q.stride(0), q.stride(1), kv, index, _ints("rows", rows, batch), batch,
-                                      heads, scale, out.data_ptr(), None if lse is None else lse.data_ptr(), ws.data_ptr(),
-                                      ws.numel() * ws.element_size(), _stream_ptr(stream)))
+    if workspace is None:
+        key = (heads, kshape[2], k_dim, dv, v_pages is None, dev)
+        need = _attn_workspace.get(key)
+        if need is None:
+            need = _attn_workspace[key] = paged_attention_workspace_bytes(heads, kshape[2], k_dim, dv, v_pages is None)
+        workspace = _work(None, need, dev, stream)
+    elif not workspace.is_contiguous():
+        raise ProjError(1, "workspace must be dense")
+    qb, qh, _ = q.stride()
+    rc = lib().proj_paged_attention(q.data_ptr(), qb, qh, kv, index, None if rows is None else _ints("rows", rows, batch), batch,
+                                    heads, scale, out.data_ptr(), None if lse is None else lse.data_ptr(), workspace.data_ptr(),
+                                    workspace.nbytes, _raw_stream(stream, dev))
+    if rc != 0:
+        _check(rc)
     return (out, lse) if return_lse else out
+
+
+def _new_rows(name: str, t: torch.Tensor, tokens: int, heads: int, dim: int):
+    """(pointer, token stride) of the new rows of a cache: [tokens, heads, dim] or [tokens, heads * dim]."""
+    if t.dtype != _BF16:
+        raise ProjError(4, f"unsupported tensor dtype {t.dtype}")
+    shape, st = t.shape, t.stride()
+    if not (len(shape) == 2 and shape == (tokens, heads * dim) and st[1] == 1) and \
+            not (len(shape) == 3 and shape == (tokens, heads, dim) and st[2] == 1 and (heads == 1 or st[1] == dim)):
+        raise ProjError(1, f"{name} must be [tokens, {heads}, {dim}] with dense tokens")
+    return t.data_ptr(), st[0] if tokens > 1 else heads * dim
 
 
 def cache_append(k_new: torch.Tensor, v_new: Optional[torch.Tensor], k_pages: torch.Tensor, v_pages: Optional[torch.Tensor],
@@ -554,62 +598,61 @@ def cache_append(k_new: torch.Tensor, v_new: Optional[torch.Tensor], k_pages: to
     """The new tokens' keys [tokens, (kv_heads,) k_dim] and values into their pages, at positions[i] of row rows[i]
     (default: the last place of row i).  cos_sin [max_pos, rot] fp32 turns the last `rot` columns of the keys and
     of the queries q [tokens, heads, k_dim] on the way; returns the turned queries (q_out; may be q), or None."""
-    dev = _same_device(k_new, v_new, k_pages, v_pages, block_table, seq_lens, rows, positions, cos_sin, q, q_out)
-    kv = _kv_pages(k_pages, v_pages, None)
-    tokens = k_new.shape[0]
-
-    def new(name, t, pages):
-        if t is None:
-            return 0, 0
-        heads, dim = pages.shape[2], pages.shape[3]
-        if t.dtype != torch.bfloat16:
-            raise ProjError(4, f"unsupported tensor dtype {t.dtype}")
-        if t.dim() not in (2, 3) or t.shape[0] != tokens or t.numel() != tokens * heads * dim or t.stride(-1) != 1 or \
-                (t.dim() == 3 and (t.shape[2] != dim or (t.shape[1] > 1 and t.stride(1) != dim))):
-            raise ProjError(1, f"{name} must be [tokens, {heads}, {dim}] with dense tokens")
-        return t.data_ptr(), t.stride(0) if tokens > 1 else heads * dim
-
+    dev = _device(k_new, v_new, k_pages, v_pages, block_table, seq_lens, rows, positions, cos_sin, q, q_out)
+    kv, kshape, dv = _kv_pages(k_pages, v_pages, None)
+    tokens, k_dim = k_new.shape[0], kshape[3]
     if (v_new is None) != (v_pages is None):
         raise ProjError(1, "v_new goes with a cache that has values of its own")
-    kp, ks = new("k_new", k_new, k_pages)
-    vp, vs = new("v_new", v_new, v_pages)
-    index = _page_index(block_table, seq_lens, None, k_pages.shape[0], k_pages.shape[1])
+    kp, ks = _new_rows("k_new", k_new, tokens, kshape[2], k_dim)
+    vp, vs = (None, 0) if v_new is None else _new_rows("v_new", v_new, tokens, kshape[2], dv)
+    index = _page_index(block_table, seq_lens, None, kshape[0], kshape[1])
     rot = None
     if cos_sin is not None:
-        if cos_sin.dtype != torch.float32 or cos_sin.dim() != 2 or not cos_sin.is_contiguous():
+        if cos_sin.dtype != _F32 or cos_sin.dim() != 2 or not cos_sin.is_contiguous():
             raise ProjError(1, "cos_sin must be a dense [max_pos, rot] float32 tensor")
-        rot = struct.pack("Piiii", cos_sin.data_ptr(), cos_sin.shape[0], cos_sin.shape[1], int(bool(interleaved)), 0)
-    heads = 0
-    qa = (None, 0, 0, None, 0, 0)
+        most, dim = cos_sin.shape
+        rot = _pack_rotary(cos_sin.data_ptr(), most, dim, 1 if interleaved else 0, 0)
+    heads, qp, qs, qh, op, os_, oh = 0, None, 0, 0, None, 0, 0
     if q is not None:
         if q_out is None:
             q_out = _made(torch.empty(q.shape, dtype=q.dtype, device=dev), stream)
-        for t in (q, q_out):
-            if t.dim() != 3 or t.shape[0] != tokens or t.shape[2] != k_pages.shape[3] or t.stride(2) != 1 or t.shape != q.shape:
-                raise ProjError(1, f"q and q_out must be [tokens, heads, {k_pages.shape[3]}] with dense columns")
-            if t.dtype != torch.bfloat16:
-                raise ProjError(4, f"unsupported tensor dtype {t.dtype}")
+        if q.dim() != 3 or q.shape[0] != tokens or q.shape[2] != k_dim or q_out.shape != q.shape:
+            raise ProjError(1, f"q and q_out must be [tokens, heads, {k_dim}] with dense columns")
+        if q.dtype != _BF16 or q_out.dtype != _BF16:
+            raise ProjError(4, f"unsupported tensor dtype {q.dtype}, {q_out.dtype}")
         heads = q.shape[1]
-        qa = (q.data_ptr(), q.stride(0), q.stride(1), q_out.data_ptr(), q_out.stride(0), q_out.stride(1))
-    _check(lib().proj_cache_append(kp, ks, vp or None, vs, kv, index, _ints("rows", rows, tokens),
-                                   _ints("positions", positions, tokens), tokens, rot, *qa, heads, _stream_ptr(stream)))
+        qs, qh, one = q.stride()
+        os_, oh, two = q_out.stride()
+        if one != 1 or two != 1:
+            raise ProjError(1, f"q and q_out must be [tokens, heads, {k_dim}] with dense columns")
+        qp, op = q.data_ptr(), q_out.data_ptr()
+    rc = lib().proj_cache_append(kp, ks, vp, vs, kv, index, None if rows is None else _ints("rows", rows, tokens),
+                                 None if positions is None else _ints("positions", positions, tokens), tokens, rot, qp, qs, qh,
+                                 op, os_, oh, heads, _raw_stream(stream, dev))
+    if rc != 0:
+        _check(rc)
     return q_out if q is not None else None
 
 
 def cache_workspace_bytes(block_table: torch.Tensor, num_pages: int, n: int) -> int:
     """Workspace bytes of cache_resize over n rows (cache_compact: n = 0)."""
-    index = struct.pack("PqPPiiii", 16, block_table.shape[1], 16, 16, block_table.shape[0], block_table.shape[1], num_pages, 16)
-    need = int(lib().proj_cache_workspace_bytes(index, n))
+    rows, width = block_table.shape
+    return _cache_need(_pack_index(16, width, 16, 16, rows, width, num_pages, 16), n)
+
+
+def _cache_need(index: bytes, n: int) -> int:
+    need = lib().proj_cache_workspace_bytes(index, n)
     if need == 0:
         raise ProjError(2, lib().proj_last_error_string().decode())
     return need
 
 
-def _status(status: Optional[torch.Tensor], n: int, dev: int, stream) -> torch.Tensor:
-    if status is None:
-        return _made(torch.empty(n, dtype=torch.int32, device=dev), stream)
-    _ints("status", status, n)
-    return status
+def _result(name: str, t: Optional[torch.Tensor], n: int, dev: int, stream) -> torch.Tensor:
+    """The caller's int32 output of n elements, or a new one."""
+    if t is None:
+        return _made(torch.empty(n, dtype=_I32, device=dev), stream)
+    _ints(name, t, n)
+    return t
 
 
 def cache_resize(block_table: torch.Tensor, seq_lens: torch.Tensor, ref_counts: torch.Tensor, rows: torch.Tensor,
@@ -618,32 +661,30 @@ def cache_resize(block_table: torch.Tensor, seq_lens: torch.Tensor, ref_counts: 
     """Rows get new lengths: growing takes the lowest free pages (and a private copy of a shared, partly filled last
     page, over all pools [layers, num_pages, ...]), shrinking gives pages back, 0 frees the row.  Returns the status
     per row: 0 done, 1 not enough free pages, 2 refused."""
-    dev = _same_device(block_table, seq_lens, ref_counts, rows, new_lens, status, workspace, *pools)
+    dev = _device(block_table, seq_lens, ref_counts, rows, new_lens, status, workspace, *pools)
     packed, num_pages = _pools(pools, ref_counts.shape[0])
     index = _page_index(block_table, seq_lens, ref_counts, num_pages, page_size)
     n = rows.shape[0]
-    status = _status(status, n, dev, stream)
-    ws = workspace
-    if ws is None:
-        need = int(lib().proj_cache_workspace_bytes(index, n))
-        if need == 0:
-            raise ProjError(2, lib().proj_last_error_string().decode())
-        ws = _scratch(need, dev, stream)
-    ws = _work(ws, 0, dev, stream)
-    _check(lib().proj_cache_resize(index, _ints("rows", rows), _ints("new_lens", new_lens, n), n, packed, len(pools),
-                                   status.data_ptr(), ws.data_ptr(), ws.numel() * ws.element_size(), _stream_ptr(stream)))
+    status = _result("status", status, n, dev, stream)
+    workspace = _work(workspace, _cache_need(index, n) if workspace is None else 0, dev, stream)
+    rc = lib().proj_cache_resize(index, _ints("rows", rows, n), _ints("new_lens", new_lens, n), n, packed, len(pools),
+                                 status.data_ptr(), workspace.data_ptr(), workspace.nbytes, _raw_stream(stream, dev))
+    if rc != 0:
+        _check(rc)
     return status
 
 
 def cache_fork(block_table: torch.Tensor, seq_lens: torch.Tensor, ref_counts: torch.Tensor, parents: torch.Tensor,
                children: torch.Tensor, page_size: int, status: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """children[i], an empty row, shares every page of parents[i].  Returns the status per child: 0 done, 2 refused."""
-    dev = _same_device(block_table, seq_lens, ref_counts, parents, children, status)
+    dev = _device(block_table, seq_lens, ref_counts, parents, children, status)
     index = _page_index(block_table, seq_lens, ref_counts, ref_counts.shape[0], page_size)
     n = parents.shape[0]
-    status = _status(status, n, dev, stream)
-    _check(lib().proj_cache_fork(index, _ints("parents", parents), _ints("children", children, n), n, status.data_ptr(),
-                                 _stream_ptr(stream)))
+    status = _result("status", status, n, dev, stream)
+    rc = lib().proj_cache_fork(index, _ints("parents", parents, n), _ints("children", children, n), n, status.data_ptr(),
+                               _raw_stream(stream, dev))
+    if rc != 0:
+        _check(rc)
     return status
 
 
@@ -652,33 +693,31 @@ def cache_compact(block_table: torch.Tensor, seq_lens: torch.Tensor, ref_counts:
                   workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """Moves the live pages into the first places of the pools; tables and counts follow.  Returns `live` [1], the
     number of live pages."""
-    dev = _same_device(block_table, seq_lens, ref_counts, live, workspace, *pools)
+    dev = _device(block_table, seq_lens, ref_counts, live, workspace, *pools)
     packed, num_pages = _pools(pools, ref_counts.shape[0])
     index = _page_index(block_table, seq_lens, ref_counts, num_pages, page_size)
-    live = _status(live, 1, dev, stream)
-    ws = workspace
-    if ws is None:
-        need = int(lib().proj_cache_workspace_bytes(index, 0))
-        if need == 0:
-            raise ProjError(2, lib().proj_last_error_string().decode())
-        ws = _scratch(need, dev, stream)
-    ws = _work(ws, 0, dev, stream)
-    _check(lib().proj_cache_compact(index, packed, len(pools), live.data_ptr(), ws.data_ptr(),
-                                    ws.numel() * ws.element_size(), _stream_ptr(stream)))
+    live = _result("live", live, 1, dev, stream)
+    workspace = _work(workspace, _cache_need(index, 0) if workspace is None else 0, dev, stream)
+    rc = lib().proj_cache_compact(index, packed, len(pools), live.data_ptr(), workspace.data_ptr(), workspace.nbytes,
+                                  _raw_stream(stream, dev))
+    if rc != 0:
+        _check(rc)
     return live
 
 
 def cache_copy_pages(pools: Sequence[torch.Tensor], src, dst, stream=None) -> None:
     """Copies page src[i] to page dst[i] in every layer of every pool [layers, num_pages, ...].  src and dst live on
     the host (CPU int32 tensors or sequences of ints); destinations differ and are no sources of the call."""
-    _same_device(*pools)
+    dev = _device(*pools)
     packed, num_pages = _pools(pools, None)
-    src, dst = (t if isinstance(t, torch.Tensor) else torch.tensor(t, dtype=torch.int32) for t in (src, dst))
-    for name, t in (("src", src), ("dst", dst)):
-        if t.is_cuda or t.shape != src.shape:
-            raise ProjError(1, f"{name} must be a CPU int32 tensor, src and dst of one length")
-    _check(lib().proj_cache_copy_pages(packed, len(pools), num_pages or 0, _ints("src", src), _ints("dst", dst), src.shape[0],
-                                       _stream_ptr(stream)))
+    src, dst = (t if isinstance(t, torch.Tensor) else torch.tensor(t, dtype=_I32) for t in (src, dst))
+    if src.is_cuda or dst.is_cuda:
+        raise ProjError(1, "src and dst must be on the host")
+    n = src.shape[0]
+    rc = lib().proj_cache_copy_pages(packed, len(pools), num_pages, _ints("src", src, n), _ints("dst", dst, n), n,
+                                     _raw_stream(stream, dev))
+    if rc != 0:
+        _check(rc)
 
 
 def supported(M: int, K: int, n_total: int, dtype: int) -> bool:

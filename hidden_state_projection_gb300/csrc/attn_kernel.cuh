@@ -123,6 +123,15 @@ __device__ __forceinline__ void tma_load_5d(uint32_t dst, const CUtensorMap *map
         : "memory");
 }
 
+// True in one thread of a converged warp.  The compiler knows that one thread runs what it
+// guards, and keeps the operands of tcgen05.mma in uniform registers (issued under a plain
+// lane test, a product of 64 x 64 x 16 took 74 cycles to issue, here 33, its time on the pipe).
+__device__ __forceinline__ bool elect_one() {
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+    return r != 0;
+}
+
 // Barrier 1 of the 128 softmax threads, and the same with an OR over their predicates.
 __device__ __forceinline__ void softmax_sync() { asm volatile("barrier.cta.sync.aligned 1, 128;" ::: "memory"); }
 __device__ __forceinline__ bool softmax_any(bool p) {
@@ -159,6 +168,14 @@ __device__ __forceinline__ bool attn_wait(uint32_t bar, uint32_t parity, uint64_
             }
         }
     }
+}
+
+// The softmax threads' wait: one of them polls, the others wait at their barrier (threads that
+// poll take issue slots from the thread that issues the products).
+__device__ __forceinline__ void softmax_wait(uint32_t bar, uint32_t parity, uint64_t limit_ns, volatile int *abort_flag,
+                                             int *err_word) {
+    if (threadIdx.x == 0) attn_wait(bar, parity, limit_ns, abort_flag, err_word);
+    softmax_sync();
 }
 
 // ---- the line of tiles ---------------------------------------------------------------
@@ -223,6 +240,16 @@ __device__ __forceinline__ bool attn_next_segment(const AttnArgs &a, const AttnL
     return true;
 }
 
+// Instruction descriptor: bf16 operands, fp32 accumulator, N columns.
+template <int N>
+constexpr uint32_t kIdescBase = (1u << 4) | (1u << 7) | (1u << 10) | (static_cast<uint32_t>(N >> 3) << 17);
+
+// A tile is loaded in groups of two 64-column boxes (one where a head has only one), each with
+// its own place in a ring: the scores start on the first group that is there, and a group's
+// place is free as soon as the product that reads it last is done.
+//   latent:  the value groups 0 .. 3 (read by the scores and by one O^T tile each), and for 576
+//            columns the rotary box in a small ring of its own (read by the scores only)
+//   grouped: the key group (scores only), then the value group
 template <int KB, int VB, bool SHARED, int N>
 struct AttnCfg {
     static constexpr int kDV = VB * 64;
@@ -231,16 +258,34 @@ struct AttnCfg {
     static constexpr int kCols = kOT * N + 2 * N;           // O^T, then two S^T
     static constexpr uint32_t kTmemCols = kCols <= 32 ? 32 : kCols <= 64 ? 64 : kCols <= 128 ? 128 : kCols <= 256 ? 256 : 512;
     static_assert(kCols <= 512, "tensor memory");
-    static constexpr int kStageBytes = (KB + (SHARED ? 0 : VB)) * kAttnTile * 128;
-    static constexpr int kVOff = SHARED ? 0 : KB * kAttnTile * 128;  // value boxes in a stage
+    static constexpr int kGB = kMV / 64;                    // boxes per group
+    static constexpr int kVG = VB / kGB;                    // value groups of a tile
+    static constexpr int kKG = SHARED ? 0 : KB / kGB;       // key groups of its own
+    static_assert(SHARED || (kKG == 1 && kVG == 1), "one key and one value group");
+    static constexpr int kGroups = kVG + kKG;
+    static constexpr int kExtra = SHARED ? KB - VB : 0;     // rotary boxes
+    static_assert(kExtra <= 1, "one rotary box");
+    static constexpr int kGroupBytes = kGB * kAttnTile * 128;
+    static constexpr int kBoxBytes = kAttnTile * 128;
     static constexpr int kQBytes = KB * N * 128;
     static constexpr int kPBytes = kAttnTile * 128;
+};
+// A place in a ring, walked by producer and consumers alike.
+struct RingPos {
+    int slot = 0;
+    uint32_t phase = 0;
+    __device__ __forceinline__ void next(int n) {
+        if (++slot == n) {
+            slot = 0;
+            phase ^= 1u;
+        }
+    }
 };
 
 template <int KB, int VB, bool SHARED, int N>
 __global__ void __launch_bounds__(kAttnThreads, 1)
-    hsp_attn_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v,
-                    const __grid_constant__ AttnArgs a) {
+    hsp_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ CUtensorMap tmap_k,
+                    const __grid_constant__ CUtensorMap tmap_v, const __grid_constant__ AttnArgs a) {
     using C = AttnCfg<KB, VB, SHARED, N>;
     constexpr int kS = N / 8;          // 8-column steps of S^T
     constexpr int kDV = C::kDV;
@@ -248,43 +293,56 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     const uint32_t raw = smem_u32(smem_raw);
     uint8_t *smem = smem_raw + ((1024u - (raw & 1023u)) & 1023u);
     const uint32_t ring = smem_u32(smem);
-    uint8_t *const q_smem = smem + a.stages * C::kStageBytes;
+    const uint32_t extra = ring + a.slots * C::kGroupBytes;             // the rotary boxes' two places
+    uint8_t *const q_smem = smem + a.slots * C::kGroupBytes + C::kExtra * 2 * C::kBoxBytes;
     uint8_t *const p_smem = q_smem + C::kQBytes;
     float *const red = reinterpret_cast<float *>(p_smem + C::kPBytes);  // [4 warps][N]
     float *const fac = red + 4 * N;                                     // [N]
-    uint64_t *const full = reinterpret_cast<uint64_t *>(fac + N);       // [stages]
-    uint64_t *const empty = full + a.stages;
-    uint64_t *const s_full = empty + a.stages;                          // [2]
-    uint64_t *const q_full = s_full + 2;
-    uint64_t *const p_full = q_full + 1;
+    uint64_t *const full = reinterpret_cast<uint64_t *>(fac + N);       // [slots]
+    uint64_t *const empty = full + a.slots;
+    uint64_t *const x_full = empty + a.slots;                           // [2] the rotary boxes
+    uint64_t *const x_empty = x_full + 2;                               // [2]
+    uint64_t *const s_full = x_empty + 2;                               // [2]
+    uint64_t *const s_free = s_full + 2;                                // [2]
+    uint64_t *const q_full = s_free + 2;
+    uint64_t *const q_free = q_full + 1;
+    uint64_t *const p_full = q_free + 1;
     uint64_t *const pv_done = p_full + 1;
     uint64_t *const drained = pv_done + 1;
     AttnLine *const line = reinterpret_cast<AttnLine *>(drained + 1);
     int *const ints = reinterpret_cast<int *>(line + 1);
     uint32_t *const tmem_slot = reinterpret_cast<uint32_t *>(ints);
     volatile int *const abort_flag = ints + 1;
-    int *const issued = ints + 2;                                       // tiles whose copies were issued
-    int *const warp_sum = ints + 4;                                     // [6]
+    int *const issued = ints + 2;                                       // groups, rotary boxes, queries whose copies were issued
+    int *const warp_sum = ints + 5;                                     // [7]
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int ht = blockIdx.x, cta = blockIdx.y;
 
     if (tid == 0) {
-        for (int s = 0; s < a.stages; ++s) {
+        for (int s = 0; s < a.slots; ++s) {
             mbar_init(smem_u32(&full[s]), 1);
             mbar_init(smem_u32(&empty[s]), 1);
         }
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(smem_u32(&x_full[s]), 1);
+            mbar_init(smem_u32(&x_empty[s]), 1);
+        }
         mbar_init(smem_u32(&s_full[0]), 1);
         mbar_init(smem_u32(&s_full[1]), 1);
-        mbar_init(smem_u32(q_full), 128);
+        mbar_init(smem_u32(&s_free[0]), 128);
+        mbar_init(smem_u32(&s_free[1]), 128);
+        mbar_init(smem_u32(q_full), 1);
+        mbar_init(smem_u32(q_free), 1);
         mbar_init(smem_u32(p_full), 128);
         mbar_init(smem_u32(pv_done), 1);
-        mbar_init(smem_u32(drained), 1);
+        mbar_init(smem_u32(drained), 2);
         *abort_flag = 0;
-        *issued = 0;
+        issued[0] = issued[1] = issued[2] = 0;
         mbar_fence_init();
+        tma_prefetch_map(&tmap_q);
         tma_prefetch_map(&tmap_k);
-        if (!SHARED) tma_prefetch_map(&tmap_v);
+        if (!SHARED || C::kExtra) tma_prefetch_map(&tmap_v);
     }
     if (warp == 5) {
         tmem_alloc(smem_u32(tmem_slot), C::kTmemCols);
@@ -339,130 +397,184 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     const AttnLine ln = *line;
 
     if (warp == 4) {
-        // ---------------- copy producer: the whole warp reads the table, lanes issue ----------------
-        int64_t x = ln.x0, base = ln.base;
-        int b = ln.b0, i = 0;
-        AttnSegment sg;
-        const int pbox = min(kAttnTile, 1 << a.page_shift);         // tokens per box
-        const int boxes = kAttnTile / pbox;                         // pages that meet a tile
-        bool alive = true;
-        while (alive && attn_next_segment(a, ln, x, b, base, sg)) {
-            const int row = a.rows ? a.rows[sg.b] : sg.b;
-            const int32_t *tbl = a.table + row * a.table_stride;
-            const int pages = static_cast<int>((static_cast<int64_t>(sg.len) + (1 << a.page_shift) - 1) >> a.page_shift);
-            int win0 = -64, win = 0;
-            for (int k = 0; k < sg.n && alive; ++k, ++i) {
-                const int64_t tok = static_cast<int64_t>(sg.t0 + k) * kAttnTile;
-                const int p0 = static_cast<int>(tok >> a.page_shift);
-                if (p0 + boxes > win0 + 32) {  // the next 32 ids in one load
-                    win0 = p0;
-                    win = 0;
-                    if (p0 + lane < pages) {
-                        win = tbl[p0 + lane];
-                        if (win < 0 || win >= a.num_pages) {
+        // ---------------- copy producer: one thread reads the table a tile ahead and issues ----------------
+        if (elect_one()) {
+            int64_t x = ln.x0, base = ln.base;
+            int b = ln.b0, i = 0;
+            AttnSegment sg;
+            RingPos rp, xp;
+            int ng = 0;
+            uint32_t seg = 0;
+            const int pbox = min(kAttnTile, 1 << a.page_shift);     // tokens per box
+            const int boxes = kAttnTile / pbox;                     // pages that meet a tile (1, 2 or 4)
+            const uint32_t line_bytes = static_cast<uint32_t>(pbox) * 128;
+            bool alive = true;
+            while (alive && attn_next_segment(a, ln, x, b, base, sg)) {
+                const int row = a.rows ? a.rows[sg.b] : sg.b;
+                const int32_t *tbl = a.table + row * a.table_stride;
+                const int pages = static_cast<int>((static_cast<int64_t>(sg.len) + (1 << a.page_shift) - 1) >> a.page_shift);
+                auto ids_of = [&](int tile, int (&id)[4]) {
+                    const int p0 = static_cast<int>((static_cast<int64_t>(tile) * kAttnTile) >> a.page_shift);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) id[e] = (e < boxes && p0 + e < pages) ? tbl[p0 + e] : 0;
+                };
+                // the sequence's queries for this head tile, once the scores of the last sequence are done
+                // with theirs (heads past the group are another group's, or zero past the last: columns
+                // that nothing reads); behind the first tile, which does not have to wait for that
+                auto queries = [&]() {
+                    alive = attn_wait(smem_u32(q_free), (seg & 1u) ^ 1u, a.wait_limit_ns, abort_flag, a.err_word);
+                    if (!alive) return;
+                    mbar_arrive_expect_tx(smem_u32(q_full), C::kQBytes);
+                    tma_load_5d(smem_u32(q_smem), &tmap_q, 0, sg.kv * a.group + ht * N, 0, sg.b, 0, smem_u32(q_full));
+                    issued[2] = static_cast<int>(++seg);
+                };
+                if (seg == 0) queries();
+                const uint32_t seg0 = seg;
+                int next[4];
+                ids_of(sg.t0, next);
+                for (int k = 0; k < sg.n && alive; ++k, ++i) {
+                    int id[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        id[e] = next[e];
+                        if (id[e] < 0 || id[e] >= a.num_pages) {
                             atomicCAS(a.err_word, 0, kDeviceErrIndex);
-                            win = 0;  // stays inside the pool; the call is reported
+                            id[e] = 0;  // stays inside the pool; the call is reported
                         }
                     }
-                }
-                const int slot = i % a.stages;
-                const uint32_t fb = smem_u32(&full[slot]);
-                if (i >= a.stages) {
-                    int ok = 1;
-                    if (lane == 0)
-                        ok = attn_wait(smem_u32(&empty[slot]), static_cast<uint32_t>(i / a.stages - 1) & 1u, a.wait_limit_ns,
-                                       abort_flag, a.err_word);
-                    if (!__shfl_sync(0xffffffffu, ok, 0)) {
-                        alive = false;
-                        break;
-                    }
-                }
-                if (i == a.skip_tile) continue;
-                const int np = min(boxes, pages - p0);
-                const uint32_t bytes = static_cast<uint32_t>(np * pbox * 128 * (KB + (SHARED ? 0 : VB)));
-                const uint32_t dst = ring + slot * C::kStageBytes;
-                const int id0 = __shfl_sync(0xffffffffu, win, p0 - win0);
-                if (lane == 0) {
-                    mbar_arrive_expect_tx(fb, bytes);
-                    *issued = i + 1;
-                    if (boxes == 1) {
-                        const int off = static_cast<int>(tok & ((1 << a.page_shift) - 1));
-                        tma_load_5d(dst, &tmap_k, 0, off, 0, sg.kv, id0, fb);
-                        if (!SHARED) tma_load_5d(dst + C::kVOff, &tmap_v, 0, off, 0, sg.kv, id0, fb);
-                    }
-                }
-                if (boxes > 1) {  // small pages: one copy per page and 64 columns, shared out over the lanes
-                    __syncwarp();
-                    for (int e0 = 0; e0 < np * KB; e0 += 32) {
-                        const int e = e0 + lane, pg = e / KB, kb = e - pg * KB;
-                        const int id = __shfl_sync(0xffffffffu, win, (p0 - win0 + pg) & 31);
-                        if (e < np * KB)
-                            tma_load_5d(dst + kb * (kAttnTile * 128) + pg * pbox * 128, &tmap_k, 0, 0, kb, sg.kv, id, fb);
-                    }
-                    if (!SHARED)
-                        for (int e0 = 0; e0 < np * VB; e0 += 32) {
-                            const int e = e0 + lane, pg = e / VB, vb = e - pg * VB;
-                            const int id = __shfl_sync(0xffffffffu, win, (p0 - win0 + pg) & 31);
-                            if (e < np * VB)
-                                tma_load_5d(dst + C::kVOff + vb * (kAttnTile * 128) + pg * pbox * 128, &tmap_v, 0, 0, vb,
-                                            sg.kv, id, fb);
+                    if (k + 1 < sg.n) ids_of(sg.t0 + k + 1, next);
+                    const int64_t tok = static_cast<int64_t>(sg.t0 + k) * kAttnTile;
+                    const int np = min(boxes, pages - static_cast<int>(tok >> a.page_shift));
+                    const int off = static_cast<int>(tok & ((1 << a.page_shift) - 1));
+                    // one group: `n` boxes from box `box` of a map; small pages: one copy per page and box
+                    auto load = [&](const CUtensorMap *map, int box, int n, uint32_t dst, uint32_t fb) {
+                        mbar_arrive_expect_tx(fb, static_cast<uint32_t>(np * n) * line_bytes);
+                        if (boxes == 1) {
+                            tma_load_5d(dst, map, 0, off, box, sg.kv, id[0], fb);
+                        } else {
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                if (e < np)
+                                    for (int kb = 0; kb < n; ++kb)
+                                        tma_load_5d(dst + kb * C::kBoxBytes + e * line_bytes, map, 0, 0, box + kb, sg.kv, id[e], fb);
                         }
+                    };
+                    const bool skip = i == a.skip_tile;
+#pragma unroll 1
+                    for (int g = 0; g < C::kGroups; ++g) {
+                        // (a fresh barrier's phase before the first counts as complete)
+                        alive = attn_wait(smem_u32(&empty[rp.slot]), rp.phase ^ 1u, a.wait_limit_ns, abort_flag, a.err_word);
+                        if (!alive) break;
+                        ++ng;
+                        if (!skip) {
+                            load(SHARED || g < C::kKG ? &tmap_k : &tmap_v, SHARED ? g * C::kGB : 0, C::kGB,
+                                 ring + rp.slot * C::kGroupBytes, smem_u32(&full[rp.slot]));
+                            issued[0] = ng;
+                        }
+                        rp.next(a.slots);
+                    }
+                    if (C::kExtra && alive) {
+                        alive = attn_wait(smem_u32(&x_empty[xp.slot]), xp.phase ^ 1u, a.wait_limit_ns, abort_flag, a.err_word);
+                        if (!alive) break;
+                        if (!skip) {
+                            load(&tmap_v, VB, 1, extra + xp.slot * C::kBoxBytes, smem_u32(&x_full[xp.slot]));
+                            issued[1] = i + 1;
+                        }
+                        xp.next(2);
+                    }
+                    if (k == 0 && alive && i > 0 && seg == seg0) queries();
                 }
             }
         }
+        __syncwarp();
     } else if (warp == 5) {
-        // ---------------- MMA issuer ----------------
-        if (lane == 0) {
-            constexpr uint32_t kBase = (1u << 4) | (1u << 7) | (1u << 10) | (static_cast<uint32_t>(N >> 3) << 17);
-            constexpr uint32_t kDescS = kBase | (static_cast<uint32_t>(kAttnTile >> 4) << 24);
-            constexpr uint32_t kDescO = kBase | (1u << 15) | (1u << 16) | (static_cast<uint32_t>(C::kMV >> 4) << 24);
+        // ---------------- issuer of the scores ----------------
+        if (elect_one()) {
+            constexpr uint32_t kDesc = kIdescBase<N> | (static_cast<uint32_t>(kAttnTile >> 4) << 24);
             int64_t x = ln.x0, base = ln.base;
-            int b = ln.b0, i = 0;
+            int b = ln.b0;
             uint32_t seg = 0;
             AttnSegment sg;
             bool alive = true;
-            const uint32_t qa = smem_u32(q_smem), pa = smem_u32(p_smem);
-            auto scores = [&](int j) {
-                const int slot = j % a.stages;
-                if (!attn_wait(smem_u32(&full[slot]), static_cast<uint32_t>(j / a.stages) & 1u, a.wait_limit_ns, abort_flag,
-                               a.err_word))
-                    return false;
-                tc_fence_after_sync();
-                const uint32_t ka = ring + slot * C::kStageBytes;
-                const uint32_t d = tmem_s + (j & 1) * N;
-#pragma unroll 1
-                for (int kb = 0; kb < KB; ++kb)
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        umma_f16(d, umma_desc_sw128(ka + kb * (kAttnTile * 128) + k * 32),
-                                 umma_desc_sw128(qa + kb * (N * 128) + k * 32), kDescS, (kb | k) != 0 ? 1u : 0u);
-                umma_commit(smem_u32(&s_full[j & 1]));
-                return true;
+            const uint64_t qd = umma_desc_sw128(smem_u32(q_smem));
+            RingPos rp, xp, sp;
+            auto ready = [&](uint64_t *bar, uint32_t phase) {
+                return attn_wait(smem_u32(bar), phase, a.wait_limit_ns, abort_flag, a.err_word);
             };
             while (alive && attn_next_segment(a, ln, x, b, base, sg)) {
-                if (!attn_wait(smem_u32(q_full), seg & 1u, a.wait_limit_ns, abort_flag, a.err_word)) break;
+                if (!ready(q_full, seg & 1u)) break;
                 ++seg;
-                alive = scores(i);
-                for (int k = 0; k < sg.n && alive; ++k, ++i) {
-                    if (k + 1 < sg.n && !(alive = scores(i + 1))) break;
-                    if (!(alive = attn_wait(smem_u32(p_full), static_cast<uint32_t>(i) & 1u, a.wait_limit_ns, abort_flag,
-                                            a.err_word)))
-                        break;
-                    tc_fence_after_sync();
-                    const int slot = i % a.stages;
-                    const uint32_t va = ring + slot * C::kStageBytes + C::kVOff;
-#pragma unroll 1
-                    for (int jt = 0; jt < C::kOT; ++jt)
+                for (int k = 0; k < sg.n; ++k) {
+                    // the scores of the tile before last have been read out of this accumulator
+                    if (!(alive = ready(&s_free[sp.slot], sp.phase ^ 1u))) break;
+                    const uint32_t d = tmem_s + sp.slot * N;
+                    constexpr int kGroupsK = SHARED ? C::kVG : C::kKG;
 #pragma unroll
-                        for (int kk = 0; kk < kAttnTile / 16; ++kk)
-                            umma_f16(tmem + jt * N,
-                                     umma_desc_mn_sw128(va + jt * (C::kMV / 64) * (kAttnTile * 128) + kk * 2048, kAttnTile * 128),
-                                     umma_desc_mn_sw128(pa + kk * 2048, kAttnTile * 128), kDescO, (k | kk) != 0 ? 1u : 0u);
-                    umma_commit(smem_u32(&empty[slot]));
+                    for (int g = 0; g < kGroupsK; ++g) {
+                        if (alive) alive = ready(&full[rp.slot], rp.phase);
+                        if (!alive) break;
+                        tc_fence_after_sync();
+                        const uint64_t kd = umma_desc_sw128(ring + rp.slot * C::kGroupBytes);
+#pragma unroll
+                        for (int e = 0; e < C::kGB * 4; ++e)  // (descriptors count 16 bytes)
+                            umma_f16(d, kd + (e >> 2) * (C::kBoxBytes / 16) + (e & 3) * 2,
+                                     qd + (g * C::kGB + (e >> 2)) * (N * 8) + (e & 3) * 2, kDesc, (g | e) != 0 ? 1u : 0u);
+                        if (!SHARED) umma_commit(smem_u32(&empty[rp.slot]));
+                        rp.next(a.slots);
+                    }
+                    if (!alive) break;
+                    if (!SHARED) rp.next(a.slots);  // the value group
+                    if (C::kExtra) {
+                        if (!(alive = ready(&x_full[xp.slot], xp.phase))) break;
+                        tc_fence_after_sync();
+                        const uint64_t kd = umma_desc_sw128(extra + xp.slot * C::kBoxBytes);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) umma_f16(d, kd + e * 2, qd + VB * (N * 8) + e * 2, kDesc, 1u);
+                        umma_commit(smem_u32(&x_empty[xp.slot]));
+                        xp.next(2);
+                    }
+                    umma_commit(smem_u32(&s_full[sp.slot]));
+                    sp.next(2);
+                }
+                umma_commit(smem_u32(q_free));
+            }
+            umma_commit(smem_u32(drained));
+        }
+        __syncwarp();
+    } else if (warp == 6) {
+        // ---------------- issuer of the products with the values ----------------
+        if (elect_one()) {
+            constexpr uint32_t kDesc = kIdescBase<N> | (1u << 15) | (1u << 16) | (static_cast<uint32_t>(C::kMV >> 4) << 24);
+            int64_t x = ln.x0, base = ln.base;
+            int b = ln.b0, i = 0;
+            AttnSegment sg;
+            bool alive = true;
+            const uint64_t pd = umma_desc_mn_sw128(smem_u32(p_smem), C::kBoxBytes);
+            RingPos rp;
+            while (alive && attn_next_segment(a, ln, x, b, base, sg)) {
+                for (int k = 0; k < sg.n; ++k, ++i) {
+                    alive = attn_wait(smem_u32(p_full), static_cast<uint32_t>(i) & 1u, a.wait_limit_ns, abort_flag, a.err_word);
+                    if (!alive) break;
+                    tc_fence_after_sync();
+                    if (!SHARED) {
+                        rp.next(a.slots);  // the key group
+                        alive = attn_wait(smem_u32(&full[rp.slot]), rp.phase, a.wait_limit_ns, abort_flag, a.err_word);
+                        if (!alive) break;
+                        tc_fence_after_sync();
+                    }
+#pragma unroll
+                    for (int jt = 0; jt < C::kOT; ++jt) {
+                        const uint64_t vd = umma_desc_mn_sw128(ring + rp.slot * C::kGroupBytes, C::kBoxBytes);
+#pragma unroll
+                        for (int e = 0; e < kAttnTile / 16; ++e)
+                            umma_f16(tmem + jt * N, vd + e * 128, pd + e * 128, kDesc, (k | e) != 0 ? 1u : 0u);
+                        umma_commit(smem_u32(&empty[rp.slot]));
+                        rp.next(a.slots);
+                    }
                     umma_commit(smem_u32(pv_done));
                 }
             }
-            // always committed and awaited, so that no product is in flight when the memory goes
+            // always committed and awaited (both issuers'), so that no product is in flight when the memory goes
             umma_commit(smem_u32(drained));
             const uint64_t t0 = global_timer_ns();
             while (!mbar_try_wait(smem_u32(drained), 0u) && global_timer_ns() - t0 < a.wait_limit_ns) {
@@ -477,7 +589,6 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         const int head0 = ht * N;                              // of the group
         const int nheads = min(N, a.group - head0);            // real heads of this tile
         const int all_heads = a.kv_heads * a.group;
-        const __nv_bfloat16 *q = static_cast<const __nv_bfloat16 *>(a.q);
         __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(a.out);
         const int r0 = warp * 16 + (lane >> 2);                // this thread's token rows: r0 and r0 + 8
         const uint32_t lane_base = static_cast<uint32_t>(warp * 32) << 16;
@@ -491,20 +602,6 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         while (attn_next_segment(a, ln, x, b, base, sg)) {
             const int64_t seg_x0 = x - sg.n;
             const bool begins = sg.t0 == 0, ends = sg.t0 + sg.n == sg.tiles;
-            const int64_t qrow = static_cast<int64_t>(sg.b);
-            // queries of this head tile, K-major with the 128-byte swizzle; rows past the heads are zero
-            {
-                const __nv_bfloat16 *qb = q + qrow * a.q_row + static_cast<int64_t>(sg.kv * a.group + head0) * a.q_head;
-#pragma unroll 4
-                for (int e = tid; e < N * KB * 8; e += 128) {
-                    const int r = e / (KB * 8), ch = e - r * (KB * 8);
-                    uint4 v = make_uint4(0, 0, 0, 0);
-                    if (r < nheads) v = *reinterpret_cast<const uint4 *>(qb + r * a.q_head + ch * 8);
-                    *reinterpret_cast<uint4 *>(q_smem + (ch >> 3) * (N * 128) + r * 128 + (((ch & 7) ^ (r & 7)) << 4)) = v;
-                }
-                fence_proxy_async_smem();
-                mbar_arrive(smem_u32(q_full));
-            }
             float m[kS * 2], l[kS * 2];
 #pragma unroll
             for (int e = 0; e < kS * 2; ++e) {
@@ -514,20 +611,26 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             for (int k = 0; k < sg.n; ++k, ++i) {
                 const int64_t tok0 = static_cast<int64_t>(sg.t0 + k) * kAttnTile;
                 const int valid = static_cast<int>(min(static_cast<int64_t>(kAttnTile), sg.len - tok0));
-                attn_wait(smem_u32(&s_full[i & 1]), static_cast<uint32_t>(i >> 1) & 1u, a.wait_limit_ns, abort_flag, a.err_word);
+                softmax_wait(smem_u32(&s_full[i & 1]), static_cast<uint32_t>(i >> 1) & 1u, a.wait_limit_ns, abort_flag, a.err_word);
                 tc_fence_after_sync();
                 float s[kS * 4];
                 tmem_ld_frag<kS>(tmem_s + (i & 1) * N + lane_base, s);
                 if (valid < kAttnTile) {
                     // the last tile: what lies behind the sequence must not reach the product (0 x NaN)
-                    uint8_t *v = smem + (i % a.stages) * C::kStageBytes + C::kVOff;
-                    const int lines = (kAttnTile - valid) * VB;
-                    for (int e = tid; e < lines * 8; e += 128) {
-                        const int ln2 = e >> 3, vb = ln2 / (kAttnTile - valid), r = valid + ln2 - vb * (kAttnTile - valid);
-                        *reinterpret_cast<uint4 *>(v + vb * (kAttnTile * 128) + r * 128 + ((e & 7) << 4)) = make_uint4(0, 0, 0, 0);
+                    const int first = i * C::kGroups + C::kKG;  // its first value group in the ring
+                    if (!SHARED)                                // (a latent tile's scores have waited for it)
+                        softmax_wait(smem_u32(&full[first % a.slots]), static_cast<uint32_t>(first / a.slots) & 1u, a.wait_limit_ns,
+                                     abort_flag, a.err_word);
+                    const int lines = kAttnTile - valid;
+                    for (int e = tid; e < lines * VB * 8; e += 128) {
+                        const int vb = e / (lines * 8), rem = e - vb * (lines * 8);
+                        uint8_t *v = smem + ((first + vb / C::kGB) % a.slots) * C::kGroupBytes + (vb % C::kGB) * C::kBoxBytes;
+                        *reinterpret_cast<uint4 *>(v + (valid + (rem >> 3)) * 128 + ((rem & 7) << 4)) = make_uint4(0, 0, 0, 0);
                     }
                 }
                 tmem_wait_ld();
+                tc_fence_before_sync();
+                mbar_arrive(smem_u32(&s_free[i & 1]));
 #pragma unroll
                 for (int e = 0; e < kS * 4; ++e) s[e] *= a.scale_log2;
                 const bool ok0 = r0 < valid, ok1 = r0 + 8 < valid;
@@ -578,7 +681,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                         if (warp == 0 && lane < 4) *reinterpret_cast<float2 *>(fac + c) = make_float2(f0, f1);
                     }
                     if (k > 0) {
-                        attn_wait(smem_u32(pv_done), static_cast<uint32_t>(i - 1) & 1u, a.wait_limit_ns, abort_flag, a.err_word);
+                        softmax_wait(smem_u32(pv_done), static_cast<uint32_t>(i - 1) & 1u, a.wait_limit_ns, abort_flag, a.err_word);
                         tc_fence_after_sync();
                         softmax_sync();
 #pragma unroll 1
@@ -595,7 +698,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                 }
                 // the probabilities of tile i - 1 have been read before these replace them
                 if (i > 0)
-                    attn_wait(smem_u32(pv_done), static_cast<uint32_t>(i - 1) & 1u, a.wait_limit_ns, abort_flag, a.err_word);
+                    softmax_wait(smem_u32(pv_done), static_cast<uint32_t>(i - 1) & 1u, a.wait_limit_ns, abort_flag, a.err_word);
 #pragma unroll
                 for (int j = 0; j < kS; ++j) {
                     const float p00 = fast_exp2(s[4 * j] - m[2 * j]), p01 = fast_exp2(s[4 * j + 1] - m[2 * j + 1]);
@@ -654,7 +757,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                 e.slot = slot;
                 a.entries[cta] = e;
             }
-            attn_wait(smem_u32(pv_done), static_cast<uint32_t>(i - 1) & 1u, a.wait_limit_ns, abort_flag, a.err_word);
+            softmax_wait(smem_u32(pv_done), static_cast<uint32_t>(i - 1) & 1u, a.wait_limit_ns, abort_flag, a.err_word);
             tc_fence_after_sync();
             softmax_sync();
             const bool good = *abort_flag == 0;
@@ -670,14 +773,15 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                 const int dv = (c0 / N) * C::kMV + warp * rpw + lane;
                 if (lane < rpw && good) {
                     if (whole) {
+                        __nv_bfloat16 *to = out + obase + static_cast<int64_t>(h0) * kDV + dv;
 #pragma unroll
                         for (int e = 0; e < 16; ++e)
-                            if (h0 + e < nheads)
-                                out[obase + static_cast<int64_t>(h0 + e) * kDV + dv] = __float2bfloat16_rn(o[e] * fac[h0 + e]);
+                            if (h0 + e < nheads) to[e * kDV] = __float2bfloat16_rn(o[e] * fac[h0 + e]);
                     } else {
+                        float *to = part + h0 * kDV + dv;
 #pragma unroll
                         for (int e = 0; e < 16; ++e)
-                            if (h0 + e < nheads) part[(h0 + e) * kDV + dv] = o[e];
+                            if (h0 + e < nheads) to[e * kDV] = o[e];
                     }
                 }
             }
@@ -701,14 +805,17 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     griddep_launch_dependents();
     if (*abort_flag != 0 && tid == 0) {
         // copies still in flight land before the shared memory goes
-        const int n = *issued;
-        for (int j = max(0, n - a.stages); j < n; ++j) {
-            if (j == a.skip_tile) continue;
+        const int n = issued[0], nx = issued[1];
+        auto land = [&](uint64_t *bar, int phase) {
             const uint64_t t0 = global_timer_ns();
-            while (!mbar_try_wait(smem_u32(&full[j % a.stages]), static_cast<uint32_t>(j / a.stages) & 1u) &&
-                   global_timer_ns() - t0 < a.wait_limit_ns / 16 + 1) {
+            while (!mbar_try_wait(smem_u32(bar), static_cast<uint32_t>(phase) & 1u) && global_timer_ns() - t0 < a.wait_limit_ns / 16 + 1) {
             }
-        }
+        };
+        for (int j = max(0, n - a.slots); j < n; ++j)
+            if (j / C::kGroups != a.skip_tile) land(&full[j % a.slots], j / a.slots);
+        for (int j = max(0, nx - 2); j < nx; ++j)
+            if (j != a.skip_tile) land(&x_full[j & 1], j >> 1);
+        if (issued[2] > 0) land(q_full, issued[2] - 1);
     }
     if (warp == 5) {
         tc_fence_after_sync();
@@ -720,10 +827,13 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
 // ---- join ------------------------------------------------------------------------------
 //
 // Sequences cut over several CTAs: out = sum_i 2^(m_i - M) O_i / sum_i 2^(m_i - M) l_i, the
-// parts in CTA order.  A unit is one head and 128 value columns; eight warps take the parts
-// in turn and add their sums in warp order.
+// parts in CTA order.  A unit is one head and 128 value columns.  Few parts (a batch: most
+// sequences lie on two or three CTAs) are a warp's work, one round of loads; many parts (one
+// long sequence) are taken in turn by the eight warps of a CTA, whose sums are added in warp
+// order.  Which of the two depends on the number of parts only.
 
 constexpr int kJoinThreads = 256;
+constexpr int kJoinFew = 16;
 
 template <int DV, int N>
 __global__ void __launch_bounds__(kJoinThreads) hsp_attn_join_kernel(const __grid_constant__ AttnArgs a) {
@@ -731,74 +841,179 @@ __global__ void __launch_bounds__(kJoinThreads) hsp_attn_join_kernel(const __gri
     constexpr int kParts = DV / kCols;
     constexpr int kPart = N * DV + 2 * N;       // floats of one partial
     __shared__ float4 acc_s[8][32];
-    __shared__ int list[kAttnMaxCtas];
-    __shared__ uint32_t begun[kAttnMaxCtas / 32];  // bit c: CTA c began a part
+    __shared__ float weight[kAttnMaxCtas], red_s[16];
+    __shared__ AttnEntry few[kAttnMaxCtas], many[kAttnMaxCtas];  // .slot: first CTA * 2 + its slot
+    __shared__ uint32_t bits[2][kAttnMaxCtas / 32];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     griddep_wait();
-    // the parts to join, in CTA order in every CTA of this kernel: its units are shared out by their place
-    for (int c = tid; c < kAttnMaxCtas; c += kJoinThreads) {
-        const uint32_t m = __ballot_sync(0xffffffffu, c < a.ctas && a.entries[c].batch >= 0);
-        if (lane == 0) begun[c >> 5] = m;
+    // the sequences to join, in CTA order in every CTA of this kernel: its units are shared out by their place
+    AttnEntry mine[kAttnMaxCtas / kJoinThreads];
+#pragma unroll
+    for (int k = 0; k < kAttnMaxCtas / kJoinThreads; ++k) {
+        const int c = tid + k * kJoinThreads;
+        mine[k].batch = -1;
+        mine[k].last = 0;
+        if (c < a.ctas) mine[k] = a.entries[c];
+        mine[k].last = min(mine[k].last, a.ctas - 1);
+        const bool begun = mine[k].batch >= 0, f = begun && mine[k].last - c < kJoinFew;
+        const uint32_t mf = __ballot_sync(0xffffffffu, f), mm = __ballot_sync(0xffffffffu, begun && !f);
+        if (lane == 0) {
+            bits[0][c >> 5] = mf;
+            bits[1][c >> 5] = mm;
+        }
     }
     __syncthreads();
-    int n = 0;
-    for (int w = 0; w < kAttnMaxCtas / 32; ++w) {
-        if (warp == (w & 7) && ((begun[w] >> lane) & 1u)) list[n + __popc(begun[w] & ((1u << lane) - 1u))] = w * 32 + lane;
-        n += __popc(begun[w]);
+    int nfew = 0, nmany = 0;
+    for (int w = 0; w * 32 < a.ctas; ++w) {
+        const uint32_t f = bits[0][w], m = bits[1][w];
+        if (warp == (w & 7)) {
+            AttnEntry e = mine[0];
+#pragma unroll
+            for (int k = 1; k < kAttnMaxCtas / kJoinThreads; ++k)
+                if ((w >> 3) == k) e = mine[k];
+            e.slot += (w * 32 + lane) * 2;
+            const uint32_t low = (1u << lane) - 1u;
+            if ((f >> lane) & 1u) few[nfew + __popc(f & low)] = e;
+            if ((m >> lane) & 1u) many[nmany + __popc(m & low)] = e;
+        }
+        nfew += __popc(f);
+        nmany += __popc(m);
     }
     __syncthreads();
-    const int64_t units = static_cast<int64_t>(n) * a.group * kParts;
-    for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
-        const int item = static_cast<int>(u / (a.group * kParts));
-        const int rem = static_cast<int>(u - static_cast<int64_t>(item) * (a.group * kParts));
-        const int h = rem / kParts, dp = rem - h * kParts;
-        const int c0 = list[item];
-        const AttnEntry e = a.entries[c0];
-        const int ht = h / N, col = h - ht * N;
-        const float *first = a.parts + ((static_cast<int64_t>(ht) * a.ctas + c0) * 2 + e.slot) * kPart;
-        const float *next = a.parts + (static_cast<int64_t>(ht) * a.ctas + c0 + 1) * 2 * kPart;  // slot 0 of CTA c0 + 1
-        const int parts = min(e.last, a.ctas - 1) - c0 + 1;
-        auto part = [&](int p) { return p == 0 ? first : next + static_cast<int64_t>(p - 1) * 2 * kPart; };
-        float M = -3.0e38f;
-        for (int p = lane; p < parts; p += 32) M = fmaxf(M, part(p)[N * DV + col]);
+    const int per_item = a.group * kParts;
+    auto store = [&](const AttnEntry &e, int h, int dp, float4 acc, float M, float L) {
+        const int64_t oh = (static_cast<int64_t>(e.batch) * a.kv_heads + e.kv_head) * a.group + h;
+        const float inv = L == 0.f ? 0.f : 1.f / L;
+        if (lane * 4 < kCols) {
+            const __nv_bfloat162 lo = __floats2bfloat162_rn(acc.x * inv, acc.y * inv);
+            const __nv_bfloat162 hi = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
+            uint2 o;
+            o.x = *reinterpret_cast<const uint32_t *>(&lo);
+            o.y = *reinterpret_cast<const uint32_t *>(&hi);
+            *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(a.out) + oh * DV + dp * kCols + lane * 4) = o;
+        }
+        if (a.lse && dp == 0 && lane == 0) a.lse[oh] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
+    };
+    // part p of head h of an entry: CTA c0's slot, then slot 0 of the CTAs behind it
+    auto part = [&](const AttnEntry &e, int h, int p) {
+        const int ht = h / N;
+        const int at = p == 0 ? e.slot : ((e.slot >> 1) + p) * 2;
+        return a.parts + (static_cast<int64_t>(ht) * a.ctas * 2 + at) * kPart;
+    };
+    for (int u = blockIdx.x * 8 + warp; u < nfew * per_item; u += gridDim.x * 8) {
+        const AttnEntry e = few[u / per_item];
+        const int rem = u % per_item, h = rem / kParts, dp = rem % kParts, col = h % N;
+        const int parts = e.last - (e.slot >> 1) + 1;
+        float m = -3.0e38f, l = 0.f;
+        if (lane < parts) {
+            const float *pp = part(e, h, lane);
+            m = pp[N * DV + col];
+            l = pp[N * DV + N + col];
+        }
+        float4 v[4];
+        auto load = [&](int p0) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                if (p0 + k < parts && lane * 4 < kCols)
+                    v[k] = *reinterpret_cast<const float4 *>(part(e, h, p0 + k) + col * DV + dp * kCols + lane * 4);
+        };
+        load(0);
+        float M = m;
 #pragma unroll
         for (int d = 16; d > 0; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
-        float L = 0.f;
-        for (int p = lane; p < parts; p += 32) L += part(p)[N * DV + N + col] * fast_exp2(part(p)[N * DV + col] - M);
+        const float w = lane < parts ? fast_exp2(m - M) : 0.f;
+        float L = w * l;
 #pragma unroll
         for (int d = 16; d > 0; d >>= 1) L += __shfl_xor_sync(0xffffffffu, L, d);
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (lane * 4 < kCols) {
-#pragma unroll 4
-            for (int p = warp; p < parts; p += 8) {
-                const float *pp = part(p);
-                const float w = fast_exp2(pp[N * DV + col] - M);
-                const float4 v = *reinterpret_cast<const float4 *>(pp + col * DV + dp * kCols + lane * 4);
-                acc.x += w * v.x;
-                acc.y += w * v.y;
-                acc.z += w * v.z;
-                acc.w += w * v.w;
+        for (int p0 = 0; p0 < parts; p0 += 4) {
+            if (p0 > 0) load(p0);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const float wk = __shfl_sync(0xffffffffu, w, (p0 + k) & 31);
+                if (p0 + k < parts) {
+                    acc.x += wk * v[k].x;
+                    acc.y += wk * v[k].y;
+                    acc.z += wk * v[k].z;
+                    acc.w += wk * v[k].w;
+                }
             }
+        }
+        store(e, h, dp, acc, M, L);
+    }
+    for (int u = blockIdx.x; u < nmany * per_item; u += gridDim.x) {
+        const AttnEntry e = many[u / per_item];
+        const int rem = u % per_item, h = rem / kParts, dp = rem % kParts, col = h % N;
+        const int parts = e.last - (e.slot >> 1) + 1;
+        // the first rows of values are on their way while the weights are made
+        constexpr int kAhead = 10;
+        float4 v[kAhead];
+        auto load = [&](int p0) {
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k)
+                if (p0 + 8 * k < parts && lane * 4 < kCols)
+                    v[k] = *reinterpret_cast<const float4 *>(part(e, h, p0 + 8 * k) + col * DV + dp * kCols + lane * 4);
+        };
+        load(warp);
+        float m[kAttnMaxCtas / kJoinThreads], lw[kAttnMaxCtas / kJoinThreads];
+        float M = -3.0e38f;
+#pragma unroll
+        for (int k = 0; k < kAttnMaxCtas / kJoinThreads; ++k) {
+            const int p = tid + k * kJoinThreads;
+            m[k] = -3.0e38f;
+            lw[k] = 0.f;
+            if (p < parts) {
+                m[k] = part(e, h, p)[N * DV + col];
+                lw[k] = part(e, h, p)[N * DV + N + col];
+            }
+            M = fmaxf(M, m[k]);
+        }
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
+        if (lane == 0) red_s[warp] = M;
+        __syncthreads();
+#pragma unroll
+        for (int k = 0; k < 8; ++k) M = fmaxf(M, red_s[k]);
+        float L = 0.f;
+#pragma unroll
+        for (int k = 0; k < kAttnMaxCtas / kJoinThreads; ++k) {
+            const int p = tid + k * kJoinThreads;
+            const float w = fast_exp2(m[k] - M);
+            if (p < parts) weight[p] = w;
+            L += lw[k] * w;
+        }
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) L += __shfl_xor_sync(0xffffffffu, L, d);
+        if (lane == 0) red_s[8 + warp] = L;
+        __syncthreads();
+        L = 0.f;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) L += red_s[8 + k];
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int p0 = warp; p0 < parts; p0 += 8 * kAhead) {
+            if (p0 != warp) load(p0);
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k)
+                if (p0 + 8 * k < parts) {
+                    const float w = weight[p0 + 8 * k];
+                    acc.x += w * v[k].x;
+                    acc.y += w * v[k].y;
+                    acc.z += w * v[k].z;
+                    acc.w += w * v[k].w;
+                }
         }
         acc_s[warp][lane] = acc;
         __syncthreads();
-        const int64_t oh = static_cast<int64_t>(e.batch) * a.kv_heads * a.group + e.kv_head * a.group + h;
-        if (warp == 0 && lane * 4 < kCols) {
+        if (warp == 0) {
 #pragma unroll
-            for (int w = 1; w < 8; ++w) {
-                const float4 v = acc_s[w][lane];
+            for (int k = 1; k < 8; ++k) {
+                const float4 v = acc_s[k][lane];
                 acc.x += v.x;
                 acc.y += v.y;
                 acc.z += v.z;
                 acc.w += v.w;
             }
-            const float inv = L == 0.f ? 0.f : 1.f / L;
-            __nv_bfloat162 lo = __floats2bfloat162_rn(acc.x * inv, acc.y * inv), hi = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
-            uint2 o;
-            o.x = *reinterpret_cast<uint32_t *>(&lo);
-            o.y = *reinterpret_cast<uint32_t *>(&hi);
-            *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(a.out) + oh * DV + dp * kCols + lane * 4) = o;
-            if (a.lse && dp == 0 && lane == 0) a.lse[oh] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
+            store(e, h, dp, acc, M, L);
         }
         __syncthreads();
     }

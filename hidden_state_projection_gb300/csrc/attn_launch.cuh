@@ -36,7 +36,7 @@ cudaError_t launch_attn_variant(const AttnLaunchReq &r) {
     cfg.stream = r.stream;
     cfg.attrs = attrs;
     cfg.numAttrs = n;
-    e = cudaLaunchKernelEx(&cfg, kern, r.tmap_k, r.tmap_v, r.args);
+    e = cudaLaunchKernelEx(&cfg, kern, r.tmap_q, r.tmap_k, r.tmap_v, r.args);
     if (e != cudaSuccess) return e;
     cfg.gridDim = dim3(static_cast<unsigned>(r.join_ctas), 1, 1);
     cfg.blockDim = dim3(kJoinThreads, 1, 1);

@@ -44,7 +44,7 @@ proj_status check_index(const proj_page_index *ix, bool counts) {
 
 // Heads and columns the attention kernel serves.
 struct AttnShape {
-    int KB, VB, shared, N, head_tiles, stages, per_sm, smem, min_tiles;
+    int KB, VB, shared, N, head_tiles, slots, per_sm, smem, min_tiles;
 };
 
 proj_status attn_shape(int heads, int kv_heads, int k_dim, int v_dim, bool latent, AttnShape *s) {
@@ -61,14 +61,15 @@ proj_status attn_shape(int heads, int kv_heads, int k_dim, int v_dim, bool laten
     s->shared = latent ? 1 : 0;
     s->N = group <= 16 ? 16 : group <= 32 ? 32 : 64;
     s->head_tiles = (group + s->N - 1) / s->N;
-    const int stage = hsp::attn_stage_bytes(s->KB, s->VB, s->shared), fixed = hsp::attn_fixed_smem(s->KB, s->N);
-    // Latent tiles (73.7 KB) fill an SM with two stages; grouped tiles leave room for two CTAs per
-    // SM, whose softmaxes and products overlap (one of 64 heads: registers allow only one).
+    const int box = hsp::kAttnTile * 128, group_bytes = hsp::attn_group_boxes(s->VB) * box;
+    const int fixed = hsp::attn_fixed_smem(s->KB, s->N) + (latent ? (s->KB - s->VB) * 2 * box : 0);
+    // A latent tile is 73.7 KB: one CTA per SM takes all of its shared memory; grouped tiles leave
+    // room for two CTAs, whose softmaxes and products overlap (64 heads: registers allow one).
     s->per_sm = latent || s->N == 64 ? 1 : 2;
     const int room = s->per_sm == 1 ? kSmemLimit : kSmemPerSm / 2 - kSmemReserved;
-    s->stages = (room - fixed) / stage;
-    if (s->stages > 8) s->stages = 8;
-    s->smem = fixed + s->stages * stage;
+    s->slots = (room - fixed) / group_bytes;
+    if (s->slots > hsp::kAttnMaxSlots) s->slots = hsp::kAttnMaxSlots;
+    s->smem = fixed + s->slots * group_bytes;
     s->min_tiles = 2;
     return PROJ_OK;
 }
@@ -100,7 +101,7 @@ proj_status check_kv(const proj_kv_pages *kv) {
 
 // [pages][heads][64-column boxes][tokens][64]: token lines of 128 bytes as the products read them.
 proj_status encode_pages(const void *p, const proj_page_index *ix, int heads, int dim, int64_t page, int64_t token,
-                         int64_t head, CUtensorMap *out) {
+                         int64_t head, int box_count, CUtensorMap *out) {
     const int boxes = dim / 64;
     const int tile = hsp::kAttnTile;
     const int tok = ix->page_size < tile ? ix->page_size : tile;
@@ -109,7 +110,7 @@ proj_status encode_pages(const void *p, const proj_page_index *ix, int heads, in
     // a stride that no step takes (one head, one page) may be anything: give the map a plain one
     const uint64_t strides[4] = {static_cast<uint64_t>(token) * 2, 128, heads > 1 ? static_cast<uint64_t>(head) * 2 : 128,
                                  ix->num_pages > 1 ? static_cast<uint64_t>(page) * 2 : 128};
-    const uint32_t box[5] = {64, static_cast<uint32_t>(tok), static_cast<uint32_t>(tok == tile ? boxes : 1), 1, 1};
+    const uint32_t box[5] = {64, static_cast<uint32_t>(tok), static_cast<uint32_t>(tok == tile ? box_count : 1), 1, 1};
     return hsp::api_encode_5d(p, dims, strides, box, out);
 }
 
@@ -211,22 +212,33 @@ proj_status proj_paged_attention(const void *q, int64_t q_row_stride, int64_t q_
     if (!q || !out) return api_fail(PROJ_ERR_INVALID_ARG, "q and out must not be NULL");
     if (!aligned(q, 16) || !aligned(out, 16) || q_row_stride % 8 || q_head_stride % 8)
         return api_fail(PROJ_ERR_MISALIGNED, "q and out must be 16-byte aligned, q's strides multiples of 8 elements");
+    if ((heads > 1 && (q_head_stride < 8 || q_head_stride >= (int64_t(1) << 38))) ||
+        (batch > 1 && (q_row_stride < 8 || q_row_stride >= (int64_t(1) << 38))))
+        return api_fail(PROJ_ERR_UNSUPPORTED_SHAPE, "queries must lie apart (strides %lld, %lld)", (long long)q_row_stride,
+                        (long long)q_head_stride);
     if (!aligned(lse, 4) || !aligned(rows, 4)) return api_fail(PROJ_ERR_MISALIGNED, "lse and rows must be 4-byte aligned");
     hsp::ApiDevice dev;
     if ((st = hsp::api_device(&dev)) != PROJ_OK) return st;
     const int ctas = attn_ctas(s, dev.sms);
     if ((st = check_workspace(workspace, workspace_bytes, attn_workspace(s, ctas))) != PROJ_OK) return st;
     hsp::AttnLaunchReq r{};
+    const int boxes = hsp::attn_group_boxes(s.VB);
     if ((st = encode_pages(kv->k, index, kv->kv_heads, kv->k_dim, kv->k_page_stride, kv->k_token_stride, kv->k_head_stride,
-                           &r.tmap_k)) != PROJ_OK)
+                           boxes, &r.tmap_k)) != PROJ_OK)
         return st;
-    if (kv->v) {
-        if ((st = encode_pages(kv->v, index, kv->kv_heads, kv->v_dim, kv->v_page_stride, kv->v_token_stride,
-                               kv->v_head_stride, &r.tmap_v)) != PROJ_OK)
-            return st;
-    } else {
-        r.tmap_v = r.tmap_k;
+    {
+        const uint64_t dims[5] = {64, static_cast<uint64_t>(heads), static_cast<uint64_t>(s.KB), static_cast<uint64_t>(batch), 1};
+        const uint64_t strides[4] = {heads > 1 ? static_cast<uint64_t>(q_head_stride) * 2 : 128, 128,
+                                     batch > 1 ? static_cast<uint64_t>(q_row_stride) * 2 : 128, 128};
+        const uint32_t box[5] = {64, static_cast<uint32_t>(s.N), static_cast<uint32_t>(s.KB), 1, 1};
+        if ((st = hsp::api_encode_5d(q, dims, strides, box, &r.tmap_q)) != PROJ_OK) return st;
     }
+    // the values' map; of a latent cache, the same pages one box at a time (the rotary box)
+    if ((st = kv->v ? encode_pages(kv->v, index, kv->kv_heads, kv->v_dim, kv->v_page_stride, kv->v_token_stride,
+                                   kv->v_head_stride, boxes, &r.tmap_v)
+                    : encode_pages(kv->k, index, kv->kv_heads, kv->k_dim, kv->k_page_stride, kv->k_token_stride,
+                                   kv->k_head_stride, 1, &r.tmap_v)) != PROJ_OK)
+        return st;
     const hsp::ApiOptions opt = hsp::api_options();
     r.KB = s.KB;
     r.VB = s.VB;
@@ -235,12 +247,9 @@ proj_status proj_paged_attention(const void *q, int64_t q_row_stride, int64_t q_
     r.head_tiles = s.head_tiles;
     r.smem_bytes = s.smem;
     r.pdl = opt.pdl;
-    r.join_ctas = dev.sms * 2;
+    r.join_ctas = dev.sms * 4;
     r.stream = reinterpret_cast<cudaStream_t>(stream);
     hsp::AttnArgs &a = r.args;
-    a.q = q;
-    a.q_row = q_row_stride;
-    a.q_head = q_head_stride;
     a.table = index->block_table;
     a.table_stride = index->table_stride;
     a.lens = index->seq_lens;
@@ -254,7 +263,7 @@ proj_status proj_paged_attention(const void *q, int64_t q_row_stride, int64_t q_
     a.group = heads / kv->kv_heads;
     a.ctas = ctas;
     a.min_tiles = s.min_tiles;
-    a.stages = s.stages;
+    a.slots = s.slots;
     a.scale_log2 = scale * 1.4426950408889634f;
     a.out = out;
     a.lse = lse;

@@ -11,7 +11,7 @@ constexpr int kDeviceErrIndex = 8;  // same value as PROJ_ERR_BAD_INDEX
 
 constexpr int kAttnTile = 64;       // tokens per tile
 constexpr int kAttnMaxCtas = 1024; // CTAs along the length (the join lists them in shared memory)
-constexpr int kAttnThreads = 192;   // four softmax warps, the copy producer, the MMA issuer
+constexpr int kAttnThreads = 224;   // four softmax warps, the copy producer, the issuers of S^T and of O^T
 
 // One sequence part that a CTA began and another one finishes: what the join adds up.
 // Entry c belongs to CTA c of the length axis; first < 0: CTA c began no such part.
@@ -23,8 +23,6 @@ struct AttnEntry {
 };
 
 struct AttnArgs {
-    const void *q;               // [batch, heads, KB * 64] bf16, rows at q_row, heads at q_head
-    int64_t q_row, q_head;       // elements
     const int32_t *table;        // [num_rows, max_pages] page ids, rows at table_stride
     int64_t table_stride;
     const int32_t *lens;         // [num_rows]
@@ -34,7 +32,7 @@ struct AttnArgs {
     int32_t batch, kv_heads, group;  // group: query heads per kv head
     int32_t ctas;                // CTAs along the length (grid.y)
     int32_t min_tiles;           // least tiles per CTA
-    int32_t stages;
+    int32_t slots;               // group places in the ring
     float scale_log2;            // softmax scale * log2(e)
     void *out;                   // [batch, heads, VB * 64] bf16
     float *lse;                  // [batch, heads] or null
@@ -52,16 +50,18 @@ struct AttnLaunchReq {
     int pdl;
     int join_ctas;
     cudaStream_t stream;
-    CUtensorMap tmap_k, tmap_v;
+    CUtensorMap tmap_q;          // [batch][boxes][heads][64], a box: the head tile's queries
+    CUtensorMap tmap_k, tmap_v;  // boxes of a group (latent: tmap_v has the single rotary box)
     AttnArgs args;
 };
 // One translation unit per cache kind.
 cudaError_t launch_attn_latent(const AttnLaunchReq &r);
 cudaError_t launch_attn_grouped(const AttnLaunchReq &r);
 // Shared memory of the attention kernel besides its stages: queries, probabilities, reduction
-// buffers, barriers (of at most 16 stages) and the alignment slack.
+// buffers, barriers (of at most kAttnMaxSlots places) and the alignment slack.
+constexpr int kAttnMaxSlots = 12;
 inline int attn_fixed_smem(int KB, int N) { return KB * N * 128 + kAttnTile * 128 + 5 * N * 4 + 512 + 1024; }
-inline int attn_stage_bytes(int KB, int VB, int shared) { return (KB + (shared ? 0 : VB)) * kAttnTile * 128; }
+inline int attn_group_boxes(int VB) { return VB >= 2 ? 2 : 1; }
 
 // ---- append ---------------------------------------------------------------------------
 
