@@ -170,14 +170,6 @@ __device__ __forceinline__ bool attn_wait(uint32_t bar, uint32_t parity, uint64_
     }
 }
 
-// The softmax threads' wait: one of them polls, the others wait at their barrier (threads that
-// poll take issue slots from the thread that issues the products).
-__device__ __forceinline__ void softmax_wait(uint32_t bar, uint32_t parity, uint64_t limit_ns, volatile int *abort_flag,
-                                             int *err_word) {
-    if (threadIdx.x == 0) attn_wait(bar, parity, limit_ns, abort_flag, err_word);
-    softmax_sync();
-}
-
 // ---- the line of tiles ---------------------------------------------------------------
 
 // Length of sequence b, clamped to what its table row can hold; a row outside the table
@@ -198,46 +190,68 @@ __device__ __forceinline__ int attn_len(const AttnArgs &a, int b) {
 }
 __device__ __forceinline__ int attn_tiles(int len) { return static_cast<int>((static_cast<uint32_t>(len) + kAttnTile - 1) / kAttnTile); }
 
-// First tile of CTA c of C over a line of T tiles, and the CTA that holds tile x.
+// The work of all sequences and kv heads forms a line: `weight` units for the start and the
+// end of a sequence part (its queries, the way out of tensor memory), one unit per tile.  CTA c
+// of C takes units [T c / C, T (c + 1) / C); a range that ends inside a sequence's first
+// `weight` units holds none of its tiles.
 __device__ __forceinline__ int64_t line_start(int64_t T, int c, int C) { return T * c / C; }
 __device__ __forceinline__ int line_owner(int64_t T, int64_t x, int C) {
     return static_cast<int>(((x + 1) * C + T - 1) / T) - 1;
 }
 
-// Where a CTA's tiles lie: set up once, then walked by every role alike.
+// Where a CTA's units lie: set up once, then walked by every role alike.
 struct AttnLine {
     int64_t total;    // T
-    int64_t x0, x1;   // this CTA's tiles
-    int64_t base;     // tiles (of one kv head) before sequence b0
+    int64_t x0, x1;   // this CTA's units (unsplit: its first sequence and head, the number of them)
+    int64_t base;     // units (of one kv head) before sequence b0
     int32_t b0;
-    int32_t ctas;     // CTAs that hold tiles
+    int32_t ctas;     // CTAs that hold units
 };
 struct AttnSegment {
     int b, kv, len, t0, n, tiles;  // n tiles from t0 of the sequence's `tiles`
+    int64_t x0, end;               // its first unit on the line, and the end of the sequence's
 };
 
 __device__ __forceinline__ bool attn_next_segment(const AttnArgs &a, const AttnLine &ln, int64_t &x, int &b, int64_t &base,
                                                   AttnSegment &s) {
-    if (x >= ln.x1) return false;
-    int len, tiles;
-    for (;;) {
-        if (b >= a.batch) return false;  // (lengths that changed under the call)
-        len = attn_len(a, b);
-        tiles = attn_tiles(len);
-        if (x < (base + tiles) * a.kv_heads) break;
-        base += tiles;
-        ++b;
+    while (x < ln.x1) {
+        if (!a.split) {  // whole sequences, taken in turn
+            const int item = static_cast<int>(x);
+            x += a.ctas;
+            s.b = item / a.kv_heads;
+            s.kv = item - s.b * a.kv_heads;
+            s.len = attn_len(a, s.b);
+            s.n = s.tiles = attn_tiles(s.len);
+            s.t0 = 0;
+            s.x0 = item;
+            s.end = item + 1;
+            if (s.n > 0) return true;
+            continue;
+        }
+        int len, units;
+        for (;;) {
+            if (b >= a.batch) return false;  // (lengths that changed under the call)
+            len = attn_len(a, b);
+            units = len > 0 ? attn_tiles(len) + a.weight : 0;
+            if (x < (base + units) * a.kv_heads) break;
+            base += units;
+            ++b;
+        }
+        const uint32_t rel = static_cast<uint32_t>(x - base * a.kv_heads);  // (under 2^31: checked on the host)
+        s.kv = static_cast<int>(rel / static_cast<uint32_t>(units));
+        const int p = static_cast<int>(rel - static_cast<uint32_t>(s.kv) * static_cast<uint32_t>(units));
+        const int n = static_cast<int>(min(static_cast<int64_t>(units - p), ln.x1 - x));
+        s.b = b;
+        s.len = len;
+        s.tiles = units - a.weight;
+        s.t0 = max(0, p - a.weight);
+        s.n = max(0, p + n - a.weight) - s.t0;
+        s.x0 = x;
+        s.end = x + (units - p);
+        x += n;
+        if (s.n > 0) return true;
     }
-    const int64_t rel = x - base * a.kv_heads;
-    s.b = b;
-    s.kv = static_cast<int>(rel / tiles);
-    s.t0 = static_cast<int>(rel - static_cast<int64_t>(s.kv) * tiles);
-    s.len = len;
-    s.tiles = tiles;
-    const int64_t left = ln.x1 - x;
-    s.n = static_cast<int>(min(static_cast<int64_t>(tiles - s.t0), left));
-    x += s.n;
-    return true;
+    return false;
 }
 
 // Instruction descriptor: bf16 operands, fp32 accumulator, N columns.
@@ -309,12 +323,12 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     uint64_t *const p_full = q_free + 1;
     uint64_t *const pv_done = p_full + 1;
     uint64_t *const drained = pv_done + 1;
-    AttnLine *const line = reinterpret_cast<AttnLine *>(drained + 1);
-    int *const ints = reinterpret_cast<int *>(line + 1);
+    int *const ints = reinterpret_cast<int *>(drained + 1);
     uint32_t *const tmem_slot = reinterpret_cast<uint32_t *>(ints);
     volatile int *const abort_flag = ints + 1;
     int *const issued = ints + 2;                                       // groups, rotary boxes, queries whose copies were issued
-    int *const warp_sum = ints + 5;                                     // [7]
+    int *const place = ints + 5;                                        // the first sequence of this CTA, units before it
+    int *const warp_sum = ints + 7;                                     // [7]
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int ht = blockIdx.x, cta = blockIdx.y;
@@ -350,51 +364,54 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     }
     griddep_wait();  // everything read below may come from the previous kernel
 
-    // ---- the line: total tiles, and where this CTA's first tile lies ----
-    const int per = (a.batch + kAttnThreads - 1) / kAttnThreads;
-    const int bfirst = min(a.batch, tid * per), blast = min(a.batch, bfirst + per);
-    int mine = 0;
-    for (int b = bfirst; b < blast; ++b) mine += attn_tiles(attn_len(a, b));
-    int incl = mine;
+    // ---- the line: its length, and where this CTA's first unit lies ----
+    AttnLine ln;
+    if (a.split) {
+        const int per = (a.batch + kAttnThreads - 1) / kAttnThreads;
+        const int bfirst = min(a.batch, tid * per), blast = min(a.batch, bfirst + per);
+        int mine = 0;
+        for (int b = bfirst; b < blast; ++b) {
+            const int len = attn_len(a, b);
+            mine += len > 0 ? attn_tiles(len) + a.weight : 0;
+        }
+        int incl = mine;
 #pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-        const int o = __shfl_up_sync(0xffffffffu, incl, d);
-        if (lane >= d) incl += o;
+        for (int d = 1; d < 32; d <<= 1) {
+            const int o = __shfl_up_sync(0xffffffffu, incl, d);
+            if (lane >= d) incl += o;
+        }
+        if (lane == 31) warp_sum[warp] = incl;
+        __syncthreads();
+        int before = 0, all = 0;
+#pragma unroll
+        for (int w = 0; w < kAttnThreads / 32; ++w) {
+            if (w < warp) before += warp_sum[w];
+            all += warp_sum[w];
+        }
+        ln.total = static_cast<int64_t>(all) * a.kv_heads;
+        ln.ctas = static_cast<int>(min((ln.total + a.min_units - 1) / a.min_units, static_cast<int64_t>(a.ctas)));
+        ln.x0 = ln.x1 = 0;
+        if (cta < ln.ctas) {
+            ln.x0 = line_start(ln.total, cta, ln.ctas);
+            ln.x1 = line_start(ln.total, cta + 1, ln.ctas);
+            const int first = before + incl - mine;
+            if (ln.x0 >= static_cast<int64_t>(first) * a.kv_heads && ln.x0 < static_cast<int64_t>(first + mine) * a.kv_heads) {
+                place[0] = bfirst;
+                place[1] = first;
+            }
+        }
+    } else {
+        ln.total = ln.x1 = static_cast<int64_t>(a.batch) * a.kv_heads;
+        ln.x0 = cta;
+        ln.ctas = a.ctas;
     }
-    if (lane == 31) warp_sum[warp] = incl;
     tc_fence_before_sync();
     __syncthreads();
     tc_fence_after_sync();
-    int before = 0, all = 0;
-#pragma unroll
-    for (int w = 0; w < kAttnThreads / 32; ++w) {
-        if (w < warp) before += warp_sum[w];
-        all += warp_sum[w];
-    }
-    const int64_t T = static_cast<int64_t>(all) * a.kv_heads;
-    const int64_t want = (T + a.min_tiles - 1) / a.min_tiles;
-    const int nctas = static_cast<int>(min(want, static_cast<int64_t>(a.ctas)));
-    const int64_t x0 = cta < nctas ? line_start(T, cta, nctas) : T, x1 = cta < nctas ? line_start(T, cta + 1, nctas) : T;
-    {
-        const int64_t first = static_cast<int64_t>(before + incl - mine) * a.kv_heads;
-        if (tid == 0) {
-            line->total = T;
-            line->x0 = x0;
-            line->x1 = x1;
-            line->ctas = nctas;
-            line->b0 = a.batch;
-            line->base = 0;
-        }
-        __syncthreads();
-        if (x0 < x1 && x0 >= first && x0 < first + static_cast<int64_t>(mine) * a.kv_heads) {
-            line->b0 = bfirst;
-            line->base = before + incl - mine;
-        }
-        __syncthreads();
-    }
+    ln.b0 = place[0];
+    ln.base = place[1];
     const uint32_t tmem = *tmem_slot;
     const uint32_t tmem_s = tmem + C::kOT * N;
-    const AttnLine ln = *line;
 
     if (warp == 4) {
         // ---------------- copy producer: one thread reads the table a tile ahead and issues ----------------
@@ -428,10 +445,10 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                     tma_load_5d(smem_u32(q_smem), &tmap_q, 0, sg.kv * a.group + ht * N, 0, sg.b, 0, smem_u32(q_full));
                     issued[2] = static_cast<int>(++seg);
                 };
-                if (seg == 0) queries();
-                const uint32_t seg0 = seg;
                 int next[4];
                 ids_of(sg.t0, next);
+                if (seg == 0) queries();
+                const uint32_t seg0 = seg;
                 for (int k = 0; k < sg.n && alive; ++k, ++i) {
                     int id[4];
 #pragma unroll
@@ -593,14 +610,13 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         const int r0 = warp * 16 + (lane >> 2);                // this thread's token rows: r0 and r0 + 8
         const uint32_t lane_base = static_cast<uint32_t>(warp * 32) << 16;
         constexpr float kFloor = -3.0e38f;
-        if (ht == 0 && tid == 0) {
+        if (a.split && ht == 0 && tid == 0) {
             AttnEntry e;
             e.batch = -1;
             e.kv_head = e.last = e.slot = 0;
             a.entries[cta] = e;
         }
         while (attn_next_segment(a, ln, x, b, base, sg)) {
-            const int64_t seg_x0 = x - sg.n;
             const bool begins = sg.t0 == 0, ends = sg.t0 + sg.n == sg.tiles;
             float m[kS * 2], l[kS * 2];
 #pragma unroll
@@ -611,7 +627,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             for (int k = 0; k < sg.n; ++k, ++i) {
                 const int64_t tok0 = static_cast<int64_t>(sg.t0 + k) * kAttnTile;
                 const int valid = static_cast<int>(min(static_cast<int64_t>(kAttnTile), sg.len - tok0));
-                softmax_wait(smem_u32(&s_full[i & 1]), static_cast<uint32_t>(i >> 1) & 1u, a.wait_limit_ns, abort_flag, a.err_word);
+                attn_wait(smem_u32(&s_full[i & 1]), static_cast<uint32_t>(i >> 1) & 1u, a.wait_limit_ns, abort_flag, a.err_word);
                 tc_fence_after_sync();
                 float s[kS * 4];
                 tmem_ld_frag<kS>(tmem_s + (i & 1) * N + lane_base, s);
@@ -619,7 +635,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                     // the last tile: what lies behind the sequence must not reach the product (0 x NaN)
                     const int first = i * C::kGroups + C::kKG;  // its first value group in the ring
                     if (!SHARED)                                // (a latent tile's scores have waited for it)
-                        softmax_wait(smem_u32(&full[first % a.slots]), static_cast<uint32_t>(first / a.slots) & 1u, a.wait_limit_ns,
+                        attn_wait(smem_u32(&full[first % a.slots]), static_cast<uint32_t>(first / a.slots) & 1u, a.wait_limit_ns,
                                      abort_flag, a.err_word);
                     const int lines = kAttnTile - valid;
                     for (int e = tid; e < lines * VB * 8; e += 128) {
@@ -633,16 +649,21 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                 mbar_arrive(smem_u32(&s_free[i & 1]));
 #pragma unroll
                 for (int e = 0; e < kS * 4; ++e) s[e] *= a.scale_log2;
-                const bool ok0 = r0 < valid, ok1 = r0 + 8 < valid;
-                bool over = (k == 0);
+                if (valid < kAttnTile) {
+#pragma unroll
+                    for (int j = 0; j < kS; ++j)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            if (r0 >= valid) s[4 * j + e] = -INFINITY;
+                            if (r0 + 8 >= valid) s[4 * j + 2 + e] = -INFINITY;
+                        }
+                }
+                float most = -INFINITY;
 #pragma unroll
                 for (int j = 0; j < kS; ++j)
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        if (!ok0) s[4 * j + e] = -INFINITY;
-                        if (!ok1) s[4 * j + 2 + e] = -INFINITY;
-                        over = over || fmaxf(s[4 * j + e], s[4 * j + 2 + e]) > m[2 * j + e] + 8.f;
-                    }
+                    for (int e = 0; e < 2; ++e) most = fmaxf(most, fmaxf(s[4 * j + e], s[4 * j + 2 + e]) - m[2 * j + e]);
+                const bool over = k == 0 || most > 8.f;
                 if (softmax_any(over)) {
                     // column maxima over the tile's 64 tokens, a new reference point, O^T rescaled
                     float mx[kS * 2];
@@ -681,7 +702,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                         if (warp == 0 && lane < 4) *reinterpret_cast<float2 *>(fac + c) = make_float2(f0, f1);
                     }
                     if (k > 0) {
-                        softmax_wait(smem_u32(pv_done), static_cast<uint32_t>(i - 1) & 1u, a.wait_limit_ns, abort_flag, a.err_word);
+                        attn_wait(smem_u32(pv_done), static_cast<uint32_t>(i - 1) & 1u, a.wait_limit_ns, abort_flag, a.err_word);
                         tc_fence_after_sync();
                         softmax_sync();
 #pragma unroll 1
@@ -698,7 +719,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                 }
                 // the probabilities of tile i - 1 have been read before these replace them
                 if (i > 0)
-                    softmax_wait(smem_u32(pv_done), static_cast<uint32_t>(i - 1) & 1u, a.wait_limit_ns, abort_flag, a.err_word);
+                    attn_wait(smem_u32(pv_done), static_cast<uint32_t>(i - 1) & 1u, a.wait_limit_ns, abort_flag, a.err_word);
 #pragma unroll
                 for (int j = 0; j < kS; ++j) {
                     const float p00 = fast_exp2(s[4 * j] - m[2 * j]), p01 = fast_exp2(s[4 * j + 1] - m[2 * j + 1]);
@@ -729,7 +750,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             }
             softmax_sync();
             const bool whole = begins && ends;
-            const int slot = seg_x0 == ln.x0 ? 0 : 1;
+            const int slot = sg.x0 == ln.x0 ? 0 : 1;
             float *part = a.parts + (static_cast<int64_t>(ht) * a.ctas + cta) * 2 * (N * kDV + 2 * N) + slot * (N * kDV + 2 * N);
             if (warp == 0 && lane < 4) {
 #pragma unroll
@@ -753,11 +774,11 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                 AttnEntry e;
                 e.batch = sg.b;
                 e.kv_head = sg.kv;
-                e.last = line_owner(ln.total, seg_x0 + sg.tiles - 1, ln.ctas);
+                e.last = line_owner(ln.total, sg.end - 1, ln.ctas);
                 e.slot = slot;
                 a.entries[cta] = e;
             }
-            softmax_wait(smem_u32(pv_done), static_cast<uint32_t>(i - 1) & 1u, a.wait_limit_ns, abort_flag, a.err_word);
+            attn_wait(smem_u32(pv_done), static_cast<uint32_t>(i - 1) & 1u, a.wait_limit_ns, abort_flag, a.err_word);
             tc_fence_after_sync();
             softmax_sync();
             const bool good = *abort_flag == 0;
@@ -827,36 +848,35 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
 // ---- join ------------------------------------------------------------------------------
 //
 // Sequences cut over several CTAs: out = sum_i 2^(m_i - M) O_i / sum_i 2^(m_i - M) l_i, the
-// parts in CTA order.  A unit is one head and 128 value columns.  Few parts (a batch: most
-// sequences lie on two or three CTAs) are a warp's work, one round of loads; many parts (one
-// long sequence) are taken in turn by the eight warps of a CTA, whose sums are added in warp
-// order.  Which of the two depends on the number of parts only.
+// parts in CTA order.  Few parts (a batch: most
+// sequences lie on two or three CTAs): a warp takes a whole head; many parts (one
+// long sequence): a CTA takes 64 columns of a head, its sixteen half warps take the parts in turn
+// and their sums are added in a fixed order.  Which of the two depends on the number of parts only.
 
 constexpr int kJoinThreads = 256;
 constexpr int kJoinFew = 16;
 
 template <int DV, int N>
-__global__ void __launch_bounds__(kJoinThreads) hsp_attn_join_kernel(const __grid_constant__ AttnArgs a) {
-    constexpr int kCols = DV < 128 ? DV : 128;  // columns of a unit
-    constexpr int kParts = DV / kCols;
+__global__ void __launch_bounds__(kJoinThreads, 3) hsp_attn_join_kernel(const __grid_constant__ AttnArgs a) {
+    constexpr int kParts = DV / 64;             // units of 64 columns of a head with many parts
     constexpr int kPart = N * DV + 2 * N;       // floats of one partial
-    __shared__ float4 acc_s[8][32];
+    __shared__ float4 acc_s[8][16];
     __shared__ float weight[kAttnMaxCtas], red_s[16];
-    __shared__ AttnEntry few[kAttnMaxCtas], many[kAttnMaxCtas];  // .slot: first CTA * 2 + its slot
+    __shared__ uint16_t few[kAttnMaxCtas], many[kAttnMaxCtas];  // the CTAs that began them
     __shared__ uint32_t bits[2][kAttnMaxCtas / 32];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     griddep_wait();
     // the sequences to join, in CTA order in every CTA of this kernel: its units are shared out by their place
-    AttnEntry mine[kAttnMaxCtas / kJoinThreads];
 #pragma unroll
     for (int k = 0; k < kAttnMaxCtas / kJoinThreads; ++k) {
         const int c = tid + k * kJoinThreads;
-        mine[k].batch = -1;
-        mine[k].last = 0;
-        if (c < a.ctas) mine[k] = a.entries[c];
-        mine[k].last = min(mine[k].last, a.ctas - 1);
-        const bool begun = mine[k].batch >= 0, f = begun && mine[k].last - c < kJoinFew;
-        const uint32_t mf = __ballot_sync(0xffffffffu, f), mm = __ballot_sync(0xffffffffu, begun && !f);
+        int begun = -1, last = 0;
+        if (c < a.ctas) {
+            begun = a.entries[c].batch;
+            last = a.entries[c].last;
+        }
+        const uint32_t mf = __ballot_sync(0xffffffffu, begun >= 0 && last - c < kJoinFew);
+        const uint32_t mm = __ballot_sync(0xffffffffu, begun >= 0 && last - c >= kJoinFew);
         if (lane == 0) {
             bits[0][c >> 5] = mf;
             bits[1][c >> 5] = mm;
@@ -867,57 +887,54 @@ __global__ void __launch_bounds__(kJoinThreads) hsp_attn_join_kernel(const __gri
     for (int w = 0; w * 32 < a.ctas; ++w) {
         const uint32_t f = bits[0][w], m = bits[1][w];
         if (warp == (w & 7)) {
-            AttnEntry e = mine[0];
-#pragma unroll
-            for (int k = 1; k < kAttnMaxCtas / kJoinThreads; ++k)
-                if ((w >> 3) == k) e = mine[k];
-            e.slot += (w * 32 + lane) * 2;
             const uint32_t low = (1u << lane) - 1u;
-            if ((f >> lane) & 1u) few[nfew + __popc(f & low)] = e;
-            if ((m >> lane) & 1u) many[nmany + __popc(m & low)] = e;
+            if ((f >> lane) & 1u) few[nfew + __popc(f & low)] = static_cast<uint16_t>(w * 32 + lane);
+            if ((m >> lane) & 1u) many[nmany + __popc(m & low)] = static_cast<uint16_t>(w * 32 + lane);
         }
         nfew += __popc(f);
         nmany += __popc(m);
     }
     __syncthreads();
-    const int per_item = a.group * kParts;
-    auto store = [&](const AttnEntry &e, int h, int dp, float4 acc, float M, float L) {
+    auto store = [&](const AttnEntry &e, int h, int col, float4 acc, float inv) {
         const int64_t oh = (static_cast<int64_t>(e.batch) * a.kv_heads + e.kv_head) * a.group + h;
-        const float inv = L == 0.f ? 0.f : 1.f / L;
-        if (lane * 4 < kCols) {
-            const __nv_bfloat162 lo = __floats2bfloat162_rn(acc.x * inv, acc.y * inv);
-            const __nv_bfloat162 hi = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
-            uint2 o;
-            o.x = *reinterpret_cast<const uint32_t *>(&lo);
-            o.y = *reinterpret_cast<const uint32_t *>(&hi);
-            *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(a.out) + oh * DV + dp * kCols + lane * 4) = o;
-        }
-        if (a.lse && dp == 0 && lane == 0) a.lse[oh] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
+        const __nv_bfloat162 lo = __floats2bfloat162_rn(acc.x * inv, acc.y * inv);
+        const __nv_bfloat162 hi = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
+        uint2 o;
+        o.x = *reinterpret_cast<const uint32_t *>(&lo);
+        o.y = *reinterpret_cast<const uint32_t *>(&hi);
+        *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(a.out) + oh * DV + col) = o;
     };
-    // part p of head h of an entry: CTA c0's slot, then slot 0 of the CTAs behind it
-    auto part = [&](const AttnEntry &e, int h, int p) {
-        const int ht = h / N;
-        const int at = p == 0 ? e.slot : ((e.slot >> 1) + p) * 2;
-        return a.parts + (static_cast<int64_t>(ht) * a.ctas * 2 + at) * kPart;
+    auto store_lse = [&](const AttnEntry &e, int h, float M, float L) {
+        a.lse[(static_cast<int64_t>(e.batch) * a.kv_heads + e.kv_head) * a.group + h] =
+            L == 0.f ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
     };
-    for (int u = blockIdx.x * 8 + warp; u < nfew * per_item; u += gridDim.x * 8) {
-        const AttnEntry e = few[u / per_item];
-        const int rem = u % per_item, h = rem / kParts, dp = rem % kParts, col = h % N;
-        const int parts = e.last - (e.slot >> 1) + 1;
+    // part p of head h of CTA c's sequence: its own slot, then slot 0 of the CTAs behind it
+    auto part = [&](int c, int slot, int h, int p) {
+        const int at = p == 0 ? c * 2 + slot : (c + p) * 2;
+        return a.parts + (static_cast<int64_t>(h / N) * a.ctas * 2 + at) * kPart;
+    };
+    // few parts: a warp takes a head, all of its columns
+    constexpr int kVec = DV >= 128 ? DV / 128 : 1;  // float4 per lane and part
+    for (int u = blockIdx.x * 8 + warp; u < nfew * a.group; u += gridDim.x * 8) {
+        const int c = few[u / a.group], h = u % a.group, col = h % N;
+        const AttnEntry e = a.entries[c];
+        const int parts = min(e.last, a.ctas - 1) - c + 1;
         float m = -3.0e38f, l = 0.f;
         if (lane < parts) {
-            const float *pp = part(e, h, lane);
+            const float *pp = part(c, e.slot, h, lane);
             m = pp[N * DV + col];
             l = pp[N * DV + N + col];
         }
-        float4 v[4];
-        auto load = [&](int p0) {
+        float4 v[2][kVec];
+        auto load = [&](int p, float4 (&to)[kVec]) {
+            if (p < parts && lane * 4 < DV) {
+                const float *pp = part(c, e.slot, h, p) + col * DV + lane * 4;
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-                if (p0 + k < parts && lane * 4 < kCols)
-                    v[k] = *reinterpret_cast<const float4 *>(part(e, h, p0 + k) + col * DV + dp * kCols + lane * 4);
+                for (int k = 0; k < kVec; ++k) to[k] = *reinterpret_cast<const float4 *>(pp + k * 128);
+            }
         };
-        load(0);
+        load(0, v[0]);
+        load(1, v[1]);
         float M = m;
 #pragma unroll
         for (int d = 16; d > 0; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
@@ -925,36 +942,48 @@ __global__ void __launch_bounds__(kJoinThreads) hsp_attn_join_kernel(const __gri
         float L = w * l;
 #pragma unroll
         for (int d = 16; d > 0; d >>= 1) L += __shfl_xor_sync(0xffffffffu, L, d);
-        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int p0 = 0; p0 < parts; p0 += 4) {
-            if (p0 > 0) load(p0);
+        float4 acc[kVec];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const float wk = __shfl_sync(0xffffffffu, w, (p0 + k) & 31);
-                if (p0 + k < parts) {
-                    acc.x += wk * v[k].x;
-                    acc.y += wk * v[k].y;
-                    acc.z += wk * v[k].z;
-                    acc.w += wk * v[k].w;
+        for (int k = 0; k < kVec; ++k) acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int p0 = 0; p0 < parts; p0 += 2) {
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                const float wk = __shfl_sync(0xffffffffu, w, (p0 + q) & 31);
+                if (p0 + q < parts) {
+#pragma unroll
+                    for (int k = 0; k < kVec; ++k) {
+                        acc[k].x += wk * v[q][k].x;
+                        acc[k].y += wk * v[q][k].y;
+                        acc[k].z += wk * v[q][k].z;
+                        acc[k].w += wk * v[q][k].w;
+                    }
                 }
+                load(p0 + q + 2, v[q]);
             }
         }
-        store(e, h, dp, acc, M, L);
+        const float inv = L == 0.f ? 0.f : 1.f / L;
+        if (lane * 4 < DV) {
+#pragma unroll
+            for (int k = 0; k < kVec; ++k) store(e, h, k * 128 + lane * 4, acc[k], inv);
+        }
+        if (a.lse && lane == 0) store_lse(e, h, M, L);
     }
+    const int per_item = a.group * kParts;
     for (int u = blockIdx.x; u < nmany * per_item; u += gridDim.x) {
-        const AttnEntry e = many[u / per_item];
+        const int c = many[u / per_item];
+        const AttnEntry e = a.entries[c];
         const int rem = u % per_item, h = rem / kParts, dp = rem % kParts, col = h % N;
-        const int parts = e.last - (e.slot >> 1) + 1;
-        // the first rows of values are on their way while the weights are made
+        const int parts = min(e.last, a.ctas - 1) - c + 1;
+        // the values are on their way while the weights are made: a half warp per part, 16 at a time
         constexpr int kAhead = 10;
+        const int half = lane >> 4, at = dp * 64 + (lane & 15) * 4, p_first = warp * 2 + half;
         float4 v[kAhead];
         auto load = [&](int p0) {
 #pragma unroll
             for (int k = 0; k < kAhead; ++k)
-                if (p0 + 8 * k < parts && lane * 4 < kCols)
-                    v[k] = *reinterpret_cast<const float4 *>(part(e, h, p0 + 8 * k) + col * DV + dp * kCols + lane * 4);
+                if (p0 + 16 * k < parts) v[k] = *reinterpret_cast<const float4 *>(part(c, e.slot, h, p0 + 16 * k) + col * DV + at);
         };
-        load(warp);
+        load(p_first);
         float m[kAttnMaxCtas / kJoinThreads], lw[kAttnMaxCtas / kJoinThreads];
         float M = -3.0e38f;
 #pragma unroll
@@ -963,8 +992,8 @@ __global__ void __launch_bounds__(kJoinThreads) hsp_attn_join_kernel(const __gri
             m[k] = -3.0e38f;
             lw[k] = 0.f;
             if (p < parts) {
-                m[k] = part(e, h, p)[N * DV + col];
-                lw[k] = part(e, h, p)[N * DV + N + col];
+                m[k] = part(c, e.slot, h, p)[N * DV + col];
+                lw[k] = part(c, e.slot, h, p)[N * DV + N + col];
             }
             M = fmaxf(M, m[k]);
         }
@@ -990,30 +1019,35 @@ __global__ void __launch_bounds__(kJoinThreads) hsp_attn_join_kernel(const __gri
 #pragma unroll
         for (int k = 0; k < 8; ++k) L += red_s[8 + k];
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int p0 = warp; p0 < parts; p0 += 8 * kAhead) {
-            if (p0 != warp) load(p0);
+        for (int p0 = p_first; p0 < parts; p0 += 16 * kAhead) {
+            if (p0 != p_first) load(p0);
 #pragma unroll
             for (int k = 0; k < kAhead; ++k)
-                if (p0 + 8 * k < parts) {
-                    const float w = weight[p0 + 8 * k];
+                if (p0 + 16 * k < parts) {
+                    const float w = weight[p0 + 16 * k];
                     acc.x += w * v[k].x;
                     acc.y += w * v[k].y;
                     acc.z += w * v[k].z;
                     acc.w += w * v[k].w;
                 }
         }
-        acc_s[warp][lane] = acc;
+        acc.x += __shfl_xor_sync(0xffffffffu, acc.x, 16);
+        acc.y += __shfl_xor_sync(0xffffffffu, acc.y, 16);
+        acc.z += __shfl_xor_sync(0xffffffffu, acc.z, 16);
+        acc.w += __shfl_xor_sync(0xffffffffu, acc.w, 16);
+        if (half == 0) acc_s[warp][lane] = acc;
         __syncthreads();
-        if (warp == 0) {
+        if (warp == 0 && half == 0) {
 #pragma unroll
             for (int k = 1; k < 8; ++k) {
-                const float4 v = acc_s[k][lane];
-                acc.x += v.x;
-                acc.y += v.y;
-                acc.z += v.z;
-                acc.w += v.w;
+                const float4 o = acc_s[k][lane];
+                acc.x += o.x;
+                acc.y += o.y;
+                acc.z += o.z;
+                acc.w += o.w;
             }
-            store(e, h, dp, acc, M, L);
+            store(e, h, at, acc, L == 0.f ? 0.f : 1.f / L);
+            if (a.lse && dp == 0 && lane == 0) store_lse(e, h, M, L);
         }
         __syncthreads();
     }

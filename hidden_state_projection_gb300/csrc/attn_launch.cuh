@@ -37,7 +37,7 @@ cudaError_t launch_attn_variant(const AttnLaunchReq &r) {
     cfg.attrs = attrs;
     cfg.numAttrs = n;
     e = cudaLaunchKernelEx(&cfg, kern, r.tmap_q, r.tmap_k, r.tmap_v, r.args);
-    if (e != cudaSuccess) return e;
+    if (e != cudaSuccess || !r.args.split) return e;
     cfg.gridDim = dim3(static_cast<unsigned>(r.join_ctas), 1, 1);
     cfg.blockDim = dim3(kJoinThreads, 1, 1);
     cfg.dynamicSmemBytes = 0;

@@ -42,9 +42,12 @@ proj_status check_index(const proj_page_index *ix, bool counts) {
     return PROJ_OK;
 }
 
+// Sequences of at most so many tiles are not cut.
+constexpr int kAttnWholeTiles = 4;
+
 // Heads and columns the attention kernel serves.
 struct AttnShape {
-    int KB, VB, shared, N, head_tiles, slots, per_sm, smem, min_tiles;
+    int KB, VB, shared, N, head_tiles, slots, per_sm, smem, min_units, weight;
 };
 
 proj_status attn_shape(int heads, int kv_heads, int k_dim, int v_dim, bool latent, AttnShape *s) {
@@ -70,7 +73,11 @@ proj_status attn_shape(int heads, int kv_heads, int k_dim, int v_dim, bool laten
     s->slots = (room - fixed) / group_bytes;
     if (s->slots > hsp::kAttnMaxSlots) s->slots = hsp::kAttnMaxSlots;
     s->smem = fixed + s->slots * group_bytes;
-    s->min_tiles = 2;
+    // What a part's start and end cost, in tiles: a latent part waits for O^T's way out of tensor
+    // memory (64 heads: 6 us, a tile 1.2 us); grouped tiles wait for memory, and another CTA on the
+    // SM uses the pause (no cost in a fit over 304 CTAs).
+    s->weight = latent ? 1 + s->N / 16 : 0;
+    s->min_units = s->weight + 2;
     return PROJ_OK;
 }
 
@@ -199,7 +206,9 @@ proj_status proj_paged_attention(const void *q, int64_t q_row_stride, int64_t q_
     if ((st = attn_shape(heads, kv->kv_heads, kv->k_dim, kv->v_dim, kv->v == nullptr, &s)) != PROJ_OK) return st;
     if (batch < 0) return api_fail(PROJ_ERR_INVALID_ARG, "batch=%d is negative", batch);
     if (!std::isfinite(scale)) return api_fail(PROJ_ERR_INVALID_ARG, "scale must be finite");
-    if (static_cast<int64_t>(batch) * ((static_cast<int64_t>(index->max_pages) * index->page_size + 63) / 64) >= (int64_t(1) << 31))
+    // (units of the line fit 31 bits)
+    const int64_t most_tiles = (static_cast<int64_t>(index->max_pages) * index->page_size + hsp::kAttnTile - 1) / hsp::kAttnTile;
+    if (static_cast<int64_t>(batch) * kv->kv_heads * (most_tiles + s.weight) >= (int64_t(1) << 31))
         return api_fail(PROJ_ERR_UNSUPPORTED_SHAPE, "batch=%d of up to %d pages is too large", batch, index->max_pages);
     if (kv->k_token_stride < 8 || (kv->v && kv->v_token_stride < 8))
         return api_fail(PROJ_ERR_UNSUPPORTED_SHAPE, "tokens of the cache must lie apart (token stride 0)");
@@ -247,7 +256,7 @@ proj_status proj_paged_attention(const void *q, int64_t q_row_stride, int64_t q_
     r.head_tiles = s.head_tiles;
     r.smem_bytes = s.smem;
     r.pdl = opt.pdl;
-    r.join_ctas = dev.sms * 4;
+    r.join_ctas = dev.sms * 3;
     r.stream = reinterpret_cast<cudaStream_t>(stream);
     hsp::AttnArgs &a = r.args;
     a.table = index->block_table;
@@ -262,7 +271,9 @@ proj_status proj_paged_attention(const void *q, int64_t q_row_stride, int64_t q_
     a.kv_heads = kv->kv_heads;
     a.group = heads / kv->kv_heads;
     a.ctas = ctas;
-    a.min_tiles = s.min_tiles;
+    a.split = most_tiles > kAttnWholeTiles ? 1 : 0;
+    a.min_units = s.min_units;
+    a.weight = s.weight;
     a.slots = s.slots;
     a.scale_log2 = scale * 1.4426950408889634f;
     a.out = out;
@@ -274,7 +285,7 @@ proj_status proj_paged_attention(const void *q, int64_t q_row_stride, int64_t q_
     a.err_word = dev.err_word;
     const cudaError_t e = s.shared ? hsp::launch_attn_latent(r) : hsp::launch_attn_grouped(r);
     if (e != cudaSuccess) return hsp::api_cuda_fail(e, "kernel launch (paged attention)");
-    hsp::api_count_launches(2);
+    hsp::api_count_launches(a.split ? 2 : 1);
     return hsp::api_ok();
 }
 

@@ -31,7 +31,8 @@ struct AttnArgs {
     int32_t page_shift;          // log2(page size)
     int32_t batch, kv_heads, group;  // group: query heads per kv head
     int32_t ctas;                // CTAs along the length (grid.y)
-    int32_t min_tiles;           // least tiles per CTA
+    int32_t split;               // 0: no sequence is cut (and nothing is to join)
+    int32_t min_units, weight;   // least units per CTA; units of a part's start and end (one per tile besides)
     int32_t slots;               // group places in the ring
     float scale_log2;            // softmax scale * log2(e)
     void *out;                   // [batch, heads, VB * 64] bf16
