@@ -194,30 +194,38 @@ __device__ __forceinline__ int attn_tiles(int len) { return static_cast<int>((st
 // end of a sequence part (its queries, the way out of tensor memory), one unit per tile.  CTA c
 // of C takes units [T c / C, T (c + 1) / C); a range that ends inside a sequence's first
 // `weight` units holds none of its tiles.
-__device__ __forceinline__ int64_t line_start(int64_t T, int c, int C) { return T * c / C; }
-__device__ __forceinline__ int line_owner(int64_t T, int64_t x, int C) {
-    return static_cast<int>(((x + 1) * C + T - 1) / T) - 1;
+// (T and the products of C stay below 2^31: the host checks T, C is at most kAttnMaxCtas.)
+__device__ __forceinline__ uint32_t line_start(uint32_t T, uint32_t c, uint32_t C) {
+    const uint32_t q = T / C, r = T - q * C;
+    return q * c + r * c / C;
+}
+__device__ __forceinline__ int line_owner(uint32_t T, uint32_t x, uint32_t C) {
+    return static_cast<int>((static_cast<uint64_t>(x + 1) * C + T - 1) / T) - 1;
 }
 
-// Where a CTA's units lie: set up once, then walked by every role alike.
+// Where a CTA's units lie, and a walk over them; every role walks alike.
 struct AttnLine {
-    int64_t total;    // T
-    int64_t x0, x1;   // this CTA's units (unsplit: its first sequence and head, the number of them)
-    int64_t base;     // units (of one kv head) before sequence b0
-    int32_t b0;
-    int32_t ctas;     // CTAs that hold units
+    uint32_t total;    // T
+    uint32_t x0, x1;   // this CTA's units (uncut: its first sequence and head, the number of them)
+    uint32_t base;     // units of all kv heads before sequence b0
+    int32_t b0, len0;  // the sequence that holds x0, its length
+    uint32_t ctas;     // CTAs that hold units
+};
+struct AttnWalk {
+    uint32_t x, base;
+    int b, len;
+    __device__ __forceinline__ explicit AttnWalk(const AttnLine &ln) : x(ln.x0), base(ln.base), b(ln.b0), len(ln.len0) {}
 };
 struct AttnSegment {
     int b, kv, len, t0, n, tiles;  // n tiles from t0 of the sequence's `tiles`
-    int64_t x0, end;               // its first unit on the line, and the end of the sequence's
+    uint32_t x0, end;              // its first unit on the line, and the end of the sequence's (of one kv head)
 };
 
-__device__ __forceinline__ bool attn_next_segment(const AttnArgs &a, const AttnLine &ln, int64_t &x, int &b, int64_t &base,
-                                                  AttnSegment &s) {
-    while (x < ln.x1) {
+__device__ __forceinline__ bool attn_next_segment(const AttnArgs &a, const AttnLine &ln, AttnWalk &w, AttnSegment &s) {
+    while (w.x < ln.x1) {
         if (!a.split) {  // whole sequences, taken in turn
-            const int item = static_cast<int>(x);
-            x += a.ctas;
+            const int item = static_cast<int>(w.x);
+            w.x += a.ctas;
             s.b = item / a.kv_heads;
             s.kv = item - s.b * a.kv_heads;
             s.len = attn_len(a, s.b);
@@ -228,27 +236,26 @@ __device__ __forceinline__ bool attn_next_segment(const AttnArgs &a, const AttnL
             if (s.n > 0) return true;
             continue;
         }
-        int len, units;
+        uint32_t units;
         for (;;) {
-            if (b >= a.batch) return false;  // (lengths that changed under the call)
-            len = attn_len(a, b);
-            units = len > 0 ? attn_tiles(len) + a.weight : 0;
-            if (x < (base + units) * a.kv_heads) break;
-            base += units;
-            ++b;
+            units = w.len > 0 ? attn_tiles(w.len) + a.weight : 0;
+            if (w.x < w.base + units * a.kv_heads) break;
+            w.base += units * a.kv_heads;
+            if (++w.b >= a.batch) return false;  // (lengths that changed under the call)
+            w.len = attn_len(a, w.b);
         }
-        const uint32_t rel = static_cast<uint32_t>(x - base * a.kv_heads);  // (under 2^31: checked on the host)
-        s.kv = static_cast<int>(rel / static_cast<uint32_t>(units));
-        const int p = static_cast<int>(rel - static_cast<uint32_t>(s.kv) * static_cast<uint32_t>(units));
-        const int n = static_cast<int>(min(static_cast<int64_t>(units - p), ln.x1 - x));
-        s.b = b;
-        s.len = len;
-        s.tiles = units - a.weight;
+        const uint32_t rel = w.x - w.base;
+        s.kv = a.kv_heads == 1 ? 0 : static_cast<int>(rel / units);
+        const int p = static_cast<int>(rel - static_cast<uint32_t>(s.kv) * units);
+        const int n = static_cast<int>(min(units - p, ln.x1 - w.x));
+        s.b = w.b;
+        s.len = w.len;
+        s.tiles = static_cast<int>(units) - a.weight;
         s.t0 = max(0, p - a.weight);
         s.n = max(0, p + n - a.weight) - s.t0;
-        s.x0 = x;
-        s.end = x + (units - p);
-        x += n;
+        s.x0 = w.x;
+        s.end = w.x + (units - p);
+        w.x += n;
         if (s.n > 0) return true;
     }
     return false;
@@ -327,8 +334,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     uint32_t *const tmem_slot = reinterpret_cast<uint32_t *>(ints);
     volatile int *const abort_flag = ints + 1;
     int *const issued = ints + 2;                                       // groups, rotary boxes, queries whose copies were issued
-    int *const place = ints + 5;                                        // the first sequence of this CTA, units before it
-    int *const warp_sum = ints + 7;                                     // [7]
+    int *const place = ints + 5;                                        // the first sequence of this CTA, units before it, its length
+    int *const warp_sum = ints + 8;                                     // [7]
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int ht = blockIdx.x, cta = blockIdx.y;
@@ -369,39 +376,50 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     if (a.split) {
         const int per = (a.batch + kAttnThreads - 1) / kAttnThreads;
         const int bfirst = min(a.batch, tid * per), blast = min(a.batch, bfirst + per);
-        int mine = 0;
+        uint32_t mine = 0;
+        int len = 0;
         for (int b = bfirst; b < blast; ++b) {
-            const int len = attn_len(a, b);
+            len = attn_len(a, b);
             mine += len > 0 ? attn_tiles(len) + a.weight : 0;
         }
-        int incl = mine;
+        uint32_t incl = mine;
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
-            const int o = __shfl_up_sync(0xffffffffu, incl, d);
+            const uint32_t o = __shfl_up_sync(0xffffffffu, incl, d);
             if (lane >= d) incl += o;
         }
-        if (lane == 31) warp_sum[warp] = incl;
+        if (lane == 31) warp_sum[warp] = static_cast<int>(incl);
         __syncthreads();
-        int before = 0, all = 0;
+        uint32_t before = 0, all = 0;
 #pragma unroll
         for (int w = 0; w < kAttnThreads / 32; ++w) {
             if (w < warp) before += warp_sum[w];
             all += warp_sum[w];
         }
-        ln.total = static_cast<int64_t>(all) * a.kv_heads;
-        ln.ctas = static_cast<int>(min((ln.total + a.min_units - 1) / a.min_units, static_cast<int64_t>(a.ctas)));
+        ln.total = all * a.kv_heads;
+        ln.ctas = min((ln.total + a.min_units - 1) / a.min_units, static_cast<uint32_t>(a.ctas));
         ln.x0 = ln.x1 = 0;
         if (cta < ln.ctas) {
             ln.x0 = line_start(ln.total, cta, ln.ctas);
             ln.x1 = line_start(ln.total, cta + 1, ln.ctas);
-            const int first = before + incl - mine;
-            if (ln.x0 >= static_cast<int64_t>(first) * a.kv_heads && ln.x0 < static_cast<int64_t>(first + mine) * a.kv_heads) {
-                place[0] = bfirst;
-                place[1] = first;
+            uint32_t first = (before + incl - mine) * a.kv_heads;
+            if (ln.x0 >= first && ln.x0 < first + mine * a.kv_heads) {
+                int b = bfirst;
+                if (per > 1) {  // walk to the sequence
+                    for (;; ++b) {
+                        len = attn_len(a, b);
+                        const uint32_t units = len > 0 ? (attn_tiles(len) + a.weight) * a.kv_heads : 0;
+                        if (ln.x0 < first + units || b + 1 >= blast) break;
+                        first += units;
+                    }
+                }
+                place[0] = b;
+                place[1] = static_cast<int>(first);
+                place[2] = len;
             }
         }
     } else {
-        ln.total = ln.x1 = static_cast<int64_t>(a.batch) * a.kv_heads;
+        ln.total = ln.x1 = static_cast<uint32_t>(a.batch) * a.kv_heads;
         ln.x0 = cta;
         ln.ctas = a.ctas;
     }
@@ -410,14 +428,15 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     tc_fence_after_sync();
     ln.b0 = place[0];
     ln.base = place[1];
+    ln.len0 = place[2];
     const uint32_t tmem = *tmem_slot;
     const uint32_t tmem_s = tmem + C::kOT * N;
 
     if (warp == 4) {
         // ---------------- copy producer: one thread reads the table a tile ahead and issues ----------------
         if (elect_one()) {
-            int64_t x = ln.x0, base = ln.base;
-            int b = ln.b0, i = 0;
+            AttnWalk walk(ln);
+            int i = 0;
             AttnSegment sg;
             RingPos rp, xp;
             int ng = 0;
@@ -426,7 +445,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             const int boxes = kAttnTile / pbox;                     // pages that meet a tile (1, 2 or 4)
             const uint32_t line_bytes = static_cast<uint32_t>(pbox) * 128;
             bool alive = true;
-            while (alive && attn_next_segment(a, ln, x, b, base, sg)) {
+            while (alive && attn_next_segment(a, ln, walk, sg)) {
                 const int row = a.rows ? a.rows[sg.b] : sg.b;
                 const int32_t *tbl = a.table + row * a.table_stride;
                 const int pages = static_cast<int>((static_cast<int64_t>(sg.len) + (1 << a.page_shift) - 1) >> a.page_shift);
@@ -508,8 +527,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         // ---------------- issuer of the scores ----------------
         if (elect_one()) {
             constexpr uint32_t kDesc = kIdescBase<N> | (static_cast<uint32_t>(kAttnTile >> 4) << 24);
-            int64_t x = ln.x0, base = ln.base;
-            int b = ln.b0;
+            AttnWalk walk(ln);
             uint32_t seg = 0;
             AttnSegment sg;
             bool alive = true;
@@ -518,7 +536,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             auto ready = [&](uint64_t *bar, uint32_t phase) {
                 return attn_wait(smem_u32(bar), phase, a.wait_limit_ns, abort_flag, a.err_word);
             };
-            while (alive && attn_next_segment(a, ln, x, b, base, sg)) {
+            while (alive && attn_next_segment(a, ln, walk, sg)) {
                 if (!ready(q_full, seg & 1u)) break;
                 ++seg;
                 for (int k = 0; k < sg.n; ++k) {
@@ -562,13 +580,13 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         // ---------------- issuer of the products with the values ----------------
         if (elect_one()) {
             constexpr uint32_t kDesc = kIdescBase<N> | (1u << 15) | (1u << 16) | (static_cast<uint32_t>(C::kMV >> 4) << 24);
-            int64_t x = ln.x0, base = ln.base;
-            int b = ln.b0, i = 0;
+            AttnWalk walk(ln);
+            int i = 0;
             AttnSegment sg;
             bool alive = true;
             const uint64_t pd = umma_desc_mn_sw128(smem_u32(p_smem), C::kBoxBytes);
             RingPos rp;
-            while (alive && attn_next_segment(a, ln, x, b, base, sg)) {
+            while (alive && attn_next_segment(a, ln, walk, sg)) {
                 for (int k = 0; k < sg.n; ++k, ++i) {
                     alive = attn_wait(smem_u32(p_full), static_cast<uint32_t>(i) & 1u, a.wait_limit_ns, abort_flag, a.err_word);
                     if (!alive) break;
@@ -600,8 +618,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         __syncwarp();
     } else {
         // ---------------- softmax warps ----------------
-        int64_t x = ln.x0, base = ln.base;
-        int b = ln.b0, i = 0;
+        AttnWalk walk(ln);
+        int i = 0;
         AttnSegment sg;
         const int head0 = ht * N;                              // of the group
         const int nheads = min(N, a.group - head0);            // real heads of this tile
@@ -616,7 +634,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             e.kv_head = e.last = e.slot = 0;
             a.entries[cta] = e;
         }
-        while (attn_next_segment(a, ln, x, b, base, sg)) {
+        while (attn_next_segment(a, ln, walk, sg)) {
             const bool begins = sg.t0 == 0, ends = sg.t0 + sg.n == sg.tiles;
             float m[kS * 2], l[kS * 2];
 #pragma unroll

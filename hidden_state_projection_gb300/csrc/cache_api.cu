@@ -206,9 +206,9 @@ proj_status proj_paged_attention(const void *q, int64_t q_row_stride, int64_t q_
     if ((st = attn_shape(heads, kv->kv_heads, kv->k_dim, kv->v_dim, kv->v == nullptr, &s)) != PROJ_OK) return st;
     if (batch < 0) return api_fail(PROJ_ERR_INVALID_ARG, "batch=%d is negative", batch);
     if (!std::isfinite(scale)) return api_fail(PROJ_ERR_INVALID_ARG, "scale must be finite");
-    // (units of the line fit 31 bits)
+    // (units of the line fit 30 bits)
     const int64_t most_tiles = (static_cast<int64_t>(index->max_pages) * index->page_size + hsp::kAttnTile - 1) / hsp::kAttnTile;
-    if (static_cast<int64_t>(batch) * kv->kv_heads * (most_tiles + s.weight) >= (int64_t(1) << 31))
+    if (static_cast<int64_t>(batch) * kv->kv_heads * (most_tiles + s.weight) >= (int64_t(1) << 30))
         return api_fail(PROJ_ERR_UNSUPPORTED_SHAPE, "batch=%d of up to %d pages is too large", batch, index->max_pages);
     if (kv->k_token_stride < 8 || (kv->v && kv->v_token_stride < 8))
         return api_fail(PROJ_ERR_UNSUPPORTED_SHAPE, "tokens of the cache must lie apart (token stride 0)");
