@@ -837,10 +837,10 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                     for (int c = tid; c < nheads; c += 128) a.lse[h + c] = -INFINITY;
             }
         }
-        fence_release_gpu();
     }
     tc_fence_before_sync();
     __syncthreads();
+    if (tid == 0) fence_release_gpu();  // the outputs and partials of this CTA (cumulative over the barrier)
     griddep_launch_dependents();
     if (*abort_flag != 0 && tid == 0) {
         // copies still in flight land before the shared memory goes
@@ -1069,8 +1069,8 @@ __global__ void __launch_bounds__(kJoinThreads, 3) hsp_attn_join_kernel(const __
         }
         __syncthreads();
     }
-    fence_release_gpu();
     __syncthreads();
+    if (tid == 0) fence_release_gpu();  // (cumulative over the barrier)
     griddep_launch_dependents();
 }
 

@@ -362,7 +362,7 @@ proj_status proj_cache_append(const void *k_new, int64_t k_row_stride, const voi
     a.k_dim = kv->k_dim;
     a.v_dim = kv->v_dim;
     a.err_word = dev.err_word;
-    const cudaError_t e = hsp::launch_append(a, hsp::api_options().pdl, reinterpret_cast<cudaStream_t>(stream));
+    const cudaError_t e = hsp::launch_append(a, dev.sms, hsp::api_options().pdl, reinterpret_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return hsp::api_cuda_fail(e, "kernel launch (cache append)");
     hsp::api_count_launches(1);
     return hsp::api_ok();

@@ -83,7 +83,7 @@ struct AppendArgs {
     int32_t tokens, kv_heads, heads, k_dim, v_dim, rot, max_pos, interleaved;
     int *err_word;
 };
-cudaError_t launch_append(const AppendArgs &a, int pdl, cudaStream_t stream);
+cudaError_t launch_append(const AppendArgs &a, int sms, int pdl, cudaStream_t stream);
 
 // ---- pages ------------------------------------------------------------------------------
 
@@ -124,7 +124,7 @@ struct ResizeArgs {
     int32_t *status;                 // [n]
     int32_t n;
     // workspace
-    int32_t *head;                   // [0]: copy pairs, [1]: live pages (compaction)
+    int32_t *head;                   // [0]: copy pairs, [1]: live pages (compaction), [2]: copy units taken
     RowPlan *plan;                   // [n]
     int32_t *claims;                 // [num_rows]
     int32_t *list;                   // [num_pages] free pages (resize) or new places (compaction)

@@ -7,10 +7,12 @@
 //   pairs (2j, 2j + 1) or (j, j + rot / 2); v rows as they are; query rows turned alike.
 //
 // Every value is read once and written once in 16-byte pieces; products and sums in fp32, one
-// rounding to bf16.  A thread takes one piece (a pair of pieces where the pairs lie rot / 2
-// apart); a token's pieces are spread over enough CTAs that a decode step of a few tokens is
-// one round of loads.  The page lookup (row, position, table) is a chain of dependent loads:
-// it bounds the small calls, the copied bytes the large ones.
+// rounding to bf16.  A thread takes pieces (pairs of pieces where the pairs lie rot / 2 apart),
+// two requested before either is stored.  A CTA looks up the places of its tokens first (row and
+// position, then the page: two dependent loads, which bound the small calls): one token, its
+// pieces spread over several CTAs, while that does not fill the GPU, up to eight behind one
+// look-up and one release fence otherwise (2047 tokens of 48 heads of 128: 16.7 us with a CTA
+// per token, 51 MB).
 #include <cuda_bf16.h>
 #include <stdint.h>
 
@@ -19,8 +21,8 @@
 
 namespace hsp {
 
-constexpr int kAppendThreads = 128;
-constexpr int kAppendPieces = 2;  // pieces per thread, all loads before the stores
+constexpr int kAppendThreads = 256;
+constexpr int kAppendTokens = 8;  // most tokens per CTA
 
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
     const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
@@ -45,97 +47,113 @@ __device__ __forceinline__ void turn_halves(uint32_t &a, uint32_t &b, float c0, 
     b = pack_bf16(b0 * c0 + a0 * s0, b1 * c1 + a1 * s1);
 }
 
-__global__ void __launch_bounds__(kAppendThreads) hsp_append_kernel(const __grid_constant__ AppendArgs a) {
+struct AppendPlace {
+    int64_t k, v;      // element offsets of the token's line in the cache, -1: nowhere
+    const float *cs;   // its angles; null: none (or outside the table)
+};
+
+__global__ void __launch_bounds__(kAppendThreads, 4) hsp_append_kernel(const __grid_constant__ AppendArgs a, int per_cta) {
+    __shared__ AppendPlace places[kAppendTokens];
     griddep_wait();
-    const int i = blockIdx.x;
+    const int first = blockIdx.x * per_cta, here = min(per_cta, a.tokens - first);
+    if (threadIdx.x < here) {
+        const int i = first + threadIdx.x;
+        const int row = a.rows ? a.rows[i] : i;
+        const bool row_ok = row >= 0 && row < a.num_rows;
+        const int pos = a.positions ? a.positions[i] : row_ok ? a.lens[row] - 1 : -1;
+        int page = -1;
+        if (row_ok && pos >= 0 && (pos >> a.page_shift) < a.max_pages)
+            page = a.table[row * a.table_stride + (pos >> a.page_shift)];
+        const bool angle = a.rot > 0 && pos >= 0 && pos < a.max_pos;
+        const int64_t line = pos & ((1 << a.page_shift) - 1);
+        AppendPlace p;
+        p.k = p.v = -1;
+        p.cs = angle ? a.cos_sin + static_cast<int64_t>(pos) * a.rot : nullptr;
+        if (page >= 0 && page < a.num_pages && (angle || a.rot == 0)) {
+            p.k = page * a.k_page + line * a.k_token;
+            p.v = page * a.v_page + line * a.v_token;
+        } else if (blockIdx.y == 0) {
+            atomicCAS(a.err_word, 0, kDeviceErrIndex);
+        }
+        places[threadIdx.x] = p;
+    }
+    __syncthreads();
     const int plain = (a.k_dim - a.rot) / 8;                               // pieces of a k or q row that are copied
     const int turned = a.rot / (a.interleaved ? 8 : 16);                   // and those that are turned
     const int per_row = plain + turned, per_v = a.v_new ? a.v_dim / 8 : 0;
     const int nk = a.kv_heads * per_row, nv = a.kv_heads * per_v, nq = a.q ? a.heads * per_row : 0;
-    const int row = a.rows ? a.rows[i] : i;
-    const bool row_ok = row >= 0 && row < a.num_rows;
-    const int pos = a.positions ? a.positions[i] : (row_ok ? a.lens[row] - 1 : -1);
-    const bool pos_ok = pos >= 0 && (pos >> a.page_shift) < a.max_pages;
-    int page = -1;
-    if (row_ok && pos_ok) page = a.table[row * a.table_stride + (pos >> a.page_shift)];
-    const bool write = page >= 0 && page < a.num_pages;
-    const bool turn = a.rot > 0;
-    const bool angle = !turn || (pos >= 0 && pos < a.max_pos);
-    if ((!write || !angle) && threadIdx.x == 0 && blockIdx.y == 0) atomicCAS(a.err_word, 0, kDeviceErrIndex);
-    if (!angle) return;
-    const int64_t line = pos & ((1 << a.page_shift) - 1);
-    const float *cs = turn ? a.cos_sin + static_cast<int64_t>(pos) * a.rot : nullptr;
-    const int total = nk + nv + nq;
+    const int total = nk + nv + nq, half = a.rot / 2;
     const int step = gridDim.y * kAppendThreads;
-    for (int e0 = blockIdx.y * kAppendThreads + threadIdx.x; e0 < total; e0 += step * kAppendPieces) {
-        uint4 v[kAppendPieces], w[kAppendPieces];
-        __nv_bfloat16 *to[kAppendPieces], *to2[kAppendPieces];
+    for (int e0 = blockIdx.y * kAppendThreads + threadIdx.x; e0 < total * here; e0 += 2 * step) {
+        uint4 v[2], w[2];
+        __nv_bfloat16 *to[2];
+        const float *cs[2];  // angles of a piece that is turned
 #pragma unroll
-        for (int u = 0; u < kAppendPieces; ++u) {
+        for (int u = 0; u < 2; ++u) {
             const int e = e0 + u * step;
-            to[u] = to2[u] = nullptr;
-            if (e >= total) continue;
+            to[u] = nullptr;
+            cs[u] = nullptr;
+            if (e >= total * here) continue;
+            const int tok = e / total, x = e - tok * total, i = first + tok;
+            const AppendPlace p = places[tok];
+            // piece t of head h of k (kind 0), v (1) or q (2)
+            const int kind = x < nk ? 0 : x < nk + nv ? 1 : 2;
+            const int r = x - (kind == 0 ? 0 : kind == 1 ? nk : nk + nv), per = kind == 1 ? per_v : per_row;
+            const int h = r / per, t = r - h * per;
             const __nv_bfloat16 *from;
-            __nv_bfloat16 *dst;
-            int t;
-            bool is_v = false;
-            if (e < nk) {
-                const int h = e / per_row;
-                t = e - h * per_row;
-                from = static_cast<const __nv_bfloat16 *>(a.k_new) + i * a.k_row + static_cast<int64_t>(h) * a.k_dim;
-                dst = write ? static_cast<__nv_bfloat16 *>(a.k) + page * a.k_page + line * a.k_token + h * a.k_head : nullptr;
-            } else if (e < nk + nv) {
-                const int h = (e - nk) / per_v;
-                t = e - nk - h * per_v;
-                is_v = true;
-                from = static_cast<const __nv_bfloat16 *>(a.v_new) + i * a.v_row + static_cast<int64_t>(h) * a.v_dim;
-                dst = write ? static_cast<__nv_bfloat16 *>(a.v) + page * a.v_page + line * a.v_token + h * a.v_head : nullptr;
+            if (kind == 0) {
+                from = static_cast<const __nv_bfloat16 *>(a.k_new) + i * a.k_row + h * a.k_dim;
+                if (p.k >= 0) to[u] = static_cast<__nv_bfloat16 *>(a.k) + p.k + h * a.k_head + t * 8;
+            } else if (kind == 1) {
+                from = static_cast<const __nv_bfloat16 *>(a.v_new) + i * a.v_row + h * a.v_dim;
+                if (p.v >= 0) to[u] = static_cast<__nv_bfloat16 *>(a.v) + p.v + h * a.v_head + t * 8;
             } else {
-                const int h = (e - nk - nv) / per_row;
-                t = e - nk - nv - h * per_row;
                 from = static_cast<const __nv_bfloat16 *>(a.q) + i * a.q_row + h * a.q_head;
-                dst = static_cast<__nv_bfloat16 *>(a.q_out) + i * a.qo_row + h * a.qo_head;
+                if (p.cs) to[u] = static_cast<__nv_bfloat16 *>(a.q_out) + i * a.qo_row + h * a.qo_head + t * 8;
             }
-            if (!dst) continue;
+            if (!to[u]) continue;
             v[u] = *reinterpret_cast<const uint4 *>(from + t * 8);
-            to[u] = dst + t * 8;
-            if (is_v || t < plain) continue;
-            const int j = t - plain;  // piece of the turned columns
-            if (a.interleaved) {
-                const float4 c = *reinterpret_cast<const float4 *>(cs + 4 * j);
-                const float4 s = *reinterpret_cast<const float4 *>(cs + a.rot / 2 + 4 * j);
-                v[u] = turn_pairs(v[u], c, s);
-            } else {
-                const int half = a.rot / 2;
-                w[u] = *reinterpret_cast<const uint4 *>(from + t * 8 + half);
-                to2[u] = dst + t * 8 + half;
-                const float4 c0 = *reinterpret_cast<const float4 *>(cs + 8 * j), c1 = *reinterpret_cast<const float4 *>(cs + 8 * j + 4);
-                const float4 s0 = *reinterpret_cast<const float4 *>(cs + half + 8 * j);
-                const float4 s1 = *reinterpret_cast<const float4 *>(cs + half + 8 * j + 4);
-                turn_halves(v[u].x, w[u].x, c0.x, c0.y, s0.x, s0.y);
-                turn_halves(v[u].y, w[u].y, c0.z, c0.w, s0.z, s0.w);
-                turn_halves(v[u].z, w[u].z, c1.x, c1.y, s1.x, s1.y);
-                turn_halves(v[u].w, w[u].w, c1.z, c1.w, s1.z, s1.w);
+            if (kind != 1 && t >= plain) {
+                cs[u] = p.cs + (t - plain) * (a.interleaved ? 4 : 8);
+                if (!a.interleaved) w[u] = *reinterpret_cast<const uint4 *>(from + t * 8 + half);
             }
         }
 #pragma unroll
-        for (int u = 0; u < kAppendPieces; ++u) {
-            if (to[u]) *reinterpret_cast<uint4 *>(to[u]) = v[u];
-            if (to2[u]) *reinterpret_cast<uint4 *>(to2[u]) = w[u];
+        for (int u = 0; u < 2; ++u) {
+            if (!to[u]) continue;
+            if (cs[u]) {
+                const float4 c0 = *reinterpret_cast<const float4 *>(cs[u]), s0 = *reinterpret_cast<const float4 *>(cs[u] + half);
+                if (a.interleaved) {
+                    v[u] = turn_pairs(v[u], c0, s0);
+                } else {
+                    const float4 c1 = *reinterpret_cast<const float4 *>(cs[u] + 4);
+                    const float4 s1 = *reinterpret_cast<const float4 *>(cs[u] + half + 4);
+                    turn_halves(v[u].x, w[u].x, c0.x, c0.y, s0.x, s0.y);
+                    turn_halves(v[u].y, w[u].y, c0.z, c0.w, s0.z, s0.w);
+                    turn_halves(v[u].z, w[u].z, c1.x, c1.y, s1.x, s1.y);
+                    turn_halves(v[u].w, w[u].w, c1.z, c1.w, s1.z, s1.w);
+                    *reinterpret_cast<uint4 *>(to[u] + half) = w[u];
+                }
+            }
+            *reinterpret_cast<uint4 *>(to[u]) = v[u];
         }
     }
-    fence_release_gpu();
     __syncthreads();
+    if (threadIdx.x == 0) fence_release_gpu();  // (cumulative over the barrier)
     griddep_launch_dependents();
 }
 
-cudaError_t launch_append(const AppendArgs &a, int pdl, cudaStream_t stream) {
+cudaError_t launch_append(const AppendArgs &a, int sms, int pdl, cudaStream_t stream) {
     const int per_row = (a.k_dim - a.rot) / 8 + a.rot / (a.interleaved ? 8 : 16);
     const int total = a.kv_heads * (per_row + (a.v_new ? a.v_dim / 8 : 0)) + (a.q ? a.heads * per_row : 0);
-    int y = (total + kAppendThreads * kAppendPieces - 1) / (kAppendThreads * kAppendPieces);
+    // one token per CTA and a thread per piece while the CTAs fit the GPU at once, else more tokens
+    int y = (total + kAppendThreads - 1) / kAppendThreads;
     if (y > 65535) y = 65535;
+    int per_cta = 1;
+    while (per_cta < kAppendTokens && static_cast<int64_t>(a.tokens) * y > static_cast<int64_t>(sms) * 4 * per_cta) per_cta *= 2;
+    if (per_cta > 1) y = 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(a.tokens), static_cast<unsigned>(y), 1);
+    cfg.gridDim = dim3(static_cast<unsigned>((a.tokens + per_cta - 1) / per_cta), static_cast<unsigned>(y), 1);
     cfg.blockDim = dim3(kAppendThreads, 1, 1);
     cfg.stream = stream;
     cudaLaunchAttribute attrs[1];
@@ -147,7 +165,7 @@ cudaError_t launch_append(const AppendArgs &a, int pdl, cudaStream_t stream) {
     }
     cfg.attrs = attrs;
     cfg.numAttrs = n;
-    return cudaLaunchKernelEx(&cfg, hsp_append_kernel, a);
+    return cudaLaunchKernelEx(&cfg, hsp_append_kernel, a, per_cta);
 }
 
 }  // namespace hsp

@@ -18,7 +18,10 @@
 //
 // The plan kernels are bound by latency: a warp takes a contiguous share of the counts, four
 // 16-byte loads of every lane in flight, one block-wide prefix sum per pass.  The moves are
-// bound by memory: 16 KB pieces, four 16-byte loads per thread before the stores.
+// bound by memory: 16 KB pieces, four 16-byte loads per thread before the stores, and CTAs that
+// take the pieces in order as they get free: 6000 pages of 73,728 bytes took 144 us with a fixed
+// stride over a resident grid (6.1 TB/s), 133 us in order (6.67 TB/s, the rate of a plain
+// device copy).
 #include <stdint.h>
 
 #include "cache_args.h"
@@ -34,6 +37,14 @@ constexpr int kPagesThreads = 256;
 
 __device__ __forceinline__ int pages_of(int len, int shift) {
     return static_cast<int>((static_cast<int64_t>(len) + (1 << shift) - 1) >> shift);
+}
+
+// The end of every kernel here: the CTA's stores are performed (one fence, cumulative over the
+// barrier), then the dependent launch is triggered.
+__device__ __forceinline__ void done() {
+    __syncthreads();
+    if (threadIdx.x == 0) fence_release_gpu();
+    griddep_launch_dependents();
 }
 
 // Exclusive prefix of v over the CTA's threads, and the sum.
@@ -89,6 +100,24 @@ __device__ __forceinline__ void copy_unit(const PoolList &pl, int64_t u, Pair pa
     }
 }
 
+// The same over all units, taken in order from a counter that starts at zero.  All threads call.
+template <typename Pair>
+__device__ __forceinline__ void copy_in_order(const PoolList &pl, int64_t units, int *counter, Pair pair) {
+    __shared__ int64_t next;
+    if (units == 0) return;
+    int mine = 0;
+    if (threadIdx.x == 0) mine = atomicAdd(counter, 1);
+    for (;;) {
+        if (threadIdx.x == 0) next = mine;
+        __syncthreads();
+        const int64_t u = next;
+        if (u >= units) return;
+        if (threadIdx.x == 0) mine = atomicAdd(counter, 1);  // on its way during the copy
+        copy_unit(pl, u, pair);
+        __syncthreads();
+    }
+}
+
 template <int PAIRS>
 struct CopyArgs {
     PoolList pools;
@@ -102,9 +131,7 @@ __global__ void __launch_bounds__(kPagesThreads) hsp_copy_pages_kernel(const __g
     const int64_t units = static_cast<int64_t>(a.n) * a.pools.pieces_total;
     for (int64_t u = blockIdx.x; u < units; u += gridDim.x)
         copy_unit(a.pools, u, [&](int64_t k) { return make_int2(a.src[k], a.dst[k]); });
-    fence_release_gpu();
-    __syncthreads();
-    griddep_launch_dependents();
+    done();
 }
 
 // ---- resize ---------------------------------------------------------------------------
@@ -224,10 +251,11 @@ __global__ void __launch_bounds__(kPlanThreads) hsp_resize_plan_kernel(const __g
         a.status[i] = st;
     }
     __syncthreads();
-    if (tid == 0) a.head[0] = pair_count;
-    fence_release_gpu();
-    __syncthreads();
-    griddep_launch_dependents();
+    if (tid == 0) {
+        a.head[0] = pair_count;
+        a.head[2] = 0;
+    }
+    done();
 }
 
 __device__ __forceinline__ void release_page(const IndexArgs &ix, int id) {
@@ -266,10 +294,8 @@ __global__ void __launch_bounds__(kPagesThreads) hsp_resize_apply_kernel(const _
         }
     }
     const int64_t units = static_cast<int64_t>(a.head[0]) * a.pools.pieces_total;
-    for (int64_t u = blockIdx.x; u < units; u += gridDim.x) copy_unit(a.pools, u, [&](int64_t k) { return a.pairs[k]; });
-    fence_release_gpu();
-    __syncthreads();
-    griddep_launch_dependents();
+    copy_in_order(a.pools, units, &a.head[2], [&](int64_t k) { return a.pairs[k]; });
+    done();
 }
 
 // ---- fork -----------------------------------------------------------------------------
@@ -317,9 +343,7 @@ __global__ void __launch_bounds__(kPagesThreads) hsp_fork_kernel(const __grid_co
         if (threadIdx.x == 0) ix.lens[c] = len;
     }
     if (threadIdx.x == 0) a.status[i] = st;
-    fence_release_gpu();
-    __syncthreads();
-    griddep_launch_dependents();
+    done();
 }
 
 // ---- compact --------------------------------------------------------------------------
@@ -403,11 +427,10 @@ __global__ void __launch_bounds__(kPlanThreads) hsp_compact_plan_kernel(const __
     if (tid == 0) {
         a.head[0] = moves;
         a.head[1] = L;
+        a.head[2] = 0;
         a.live[0] = L;
     }
-    fence_release_gpu();
-    __syncthreads();
-    griddep_launch_dependents();
+    done();
 }
 
 __global__ void __launch_bounds__(kPagesThreads) hsp_compact_apply_kernel(const __grid_constant__ CompactArgs a) {
@@ -437,12 +460,9 @@ __global__ void __launch_bounds__(kPagesThreads) hsp_compact_apply_kernel(const 
             ix.refs[p.x] = 0;
         }
         const int64_t units = static_cast<int64_t>(moves) * a.pools.pieces_total;
-        for (int64_t u = blockIdx.x; u < units; u += gridDim.x)
-            copy_unit(a.pools, u, [&](int64_t k) { return a.pairs[k]; });
+        copy_in_order(a.pools, units, &a.head[2], [&](int64_t k) { return a.pairs[k]; });
     }
-    fence_release_gpu();
-    __syncthreads();
-    griddep_launch_dependents();
+    done();
 }
 
 // ---- launches -------------------------------------------------------------------------
@@ -475,8 +495,9 @@ cudaError_t launch_copy(const PoolList &pools, const int32_t *src, const int32_t
         a.src[i] = src[i];
         a.dst[i] = dst[i];
     }
-    int64_t ctas = static_cast<int64_t>(n) * pools.pieces_total;
-    if (ctas > sms * 8) ctas = sms * 8;
+    (void)sms;
+    int64_t ctas = static_cast<int64_t>(n) * pools.pieces_total;  // one each: they start in order
+    if (ctas > 0x7fffffff) ctas = 0x7fffffff;
     return launch_one(hsp_copy_pages_kernel<PAIRS>, a, ctas, kPagesThreads, pdl, stream);
 }
 
