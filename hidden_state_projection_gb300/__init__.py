@@ -30,6 +30,7 @@ STATUS_NAMES = {0: "PROJ_OK", 1: "PROJ_ERR_INVALID_ARG", 2: "PROJ_ERR_UNSUPPORTE
 STATUS = {v: k for k, v in STATUS_NAMES.items()}
 MAX_SPLITS = 8
 MAX_M = 64
+UNCUT_TOKENS = 256  # PROJ_UNCUT_TOKENS
 
 EXPORTED = ("proj_fused_gemm", "proj_fused_gemm_prefetch", "proj_fused_gemm_host",
             "proj_host_plan_create", "proj_host_plan_launch", "proj_host_plan_destroy", "proj_fused_gemm_rmsnorm", "proj_rmsnorm_workspace_bytes",
@@ -424,6 +425,9 @@ def pack_check(w: torch.Tensor, w_cat: torch.Tensor, row_off: int) -> bool:
 _BF16, _I32, _F32 = torch.bfloat16, torch.int32, torch.float32
 
 
+_empty = torch.empty
+
+
 def _device(*tensors) -> int:
     """Index of the CUDA device that every given tensor (None is left out) lies on: the current one."""
     dev = tensors[0].get_device()
@@ -439,11 +443,9 @@ def _raw_stream(stream, dev: int) -> int:
     return torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream_ptr(stream)
 
 
-def _ints(name: str, t: Optional[torch.Tensor], n: int):
-    """Device pointer of a dense 1-D int32 tensor of n elements; None stays None."""
-    if t is None:
-        return None
-    if t.dtype != _I32 or t.shape != (n,) or not t.is_contiguous():
+def _ints(name: str, t: torch.Tensor, n: int) -> int:
+    """Device pointer of a dense 1-D int32 tensor of n elements."""
+    if t.dtype is not _I32 or t.shape != (n,) or (n > 1 and t.stride() != (1,)):
         raise ProjError(1, f"{name} must be a dense 1-D int32 tensor of {n} elements")
     return t.data_ptr()
 
@@ -455,9 +457,10 @@ _pack_rotary = struct.Struct("Piiii").pack        # proj_rotary
 
 
 def _page_index(block_table, seq_lens, ref_counts, num_pages: int, page_size: int) -> bytes:
-    if block_table.dtype != _I32 or block_table.dim() != 2:
+    shape = block_table.shape
+    if block_table.dtype is not _I32 or len(shape) != 2:
         raise ProjError(1, "block_table must be a 2-D int32 tensor with dense rows")
-    rows, width = block_table.shape
+    rows, width = shape
     st, one = block_table.stride()
     if one != 1 and width > 1:
         raise ProjError(1, "block_table must be a 2-D int32 tensor with dense rows")
@@ -468,13 +471,11 @@ def _page_index(block_table, seq_lens, ref_counts, num_pages: int, page_size: in
 
 def _kv_pages(k_pages: torch.Tensor, v_pages: Optional[torch.Tensor], v_dim: Optional[int]):
     """(packed proj_kv_pages, shape of the keys, columns of the values)"""
-    if k_pages.dim() != 4:
-        raise ProjError(1, "k_pages must be a [num_pages, page_size, kv_heads, k_dim] tensor with dense columns")
     shape = k_pages.shape
-    sp, st, sh, one = k_pages.stride()
-    if one != 1:
+    if len(shape) != 4 or k_pages.stride(3) != 1:
         raise ProjError(1, "k_pages must be a [num_pages, page_size, kv_heads, k_dim] tensor with dense columns")
-    if k_pages.dtype != _BF16 or (v_pages is not None and v_pages.dtype != _BF16):
+    sp, st, sh, _ = k_pages.stride()
+    if k_pages.dtype is not _BF16 or (v_pages is not None and v_pages.dtype is not _BF16):
         raise ProjError(4, "the cache holds bf16")
     if v_pages is None:
         dv = 512 if v_dim is None else int(v_dim)
@@ -520,7 +521,8 @@ def _made(t: torch.Tensor, stream) -> torch.Tensor:
 def _work(t: Optional[torch.Tensor], need: int, dev: int, stream) -> torch.Tensor:
     """The caller's workspace, or one from torch for this call."""
     if t is None:
-        return _made(torch.empty(need, dtype=torch.uint8, device=dev), stream)
+        t = _empty(need, dtype=torch.uint8, device=dev)
+        return t if stream is None else _made(t, stream)
     if not t.is_contiguous():
         raise ProjError(1, "workspace must be dense")
     return t
@@ -548,33 +550,45 @@ def paged_attention(q: torch.Tensor, k_pages: torch.Tensor, v_pages: Optional[to
     return_lse.  `workspace` (paged_attention_workspace_bytes) is taken from torch per call if not given."""
     dev = _device(q, k_pages, v_pages, block_table, seq_lens, rows, out, lse, workspace)
     kv, kshape, dv = _kv_pages(k_pages, v_pages, v_dim)
-    if q.dim() != 3 or q.shape[2] != kshape[3] or q.stride(2) != 1:
+    pages, page, kv_heads, k_dim = kshape
+    shape = q.shape
+    if len(shape) != 3 or shape[2] != k_dim or q.stride(2) != 1:
         raise ProjError(1, "q must be a [batch, heads, k_dim] tensor with dense columns")
-    if q.dtype != _BF16:
+    if q.dtype is not _BF16:
         raise ProjError(4, f"unsupported tensor dtype {q.dtype}")
-    batch, heads, k_dim = q.shape
-    index = _page_index(block_table, seq_lens, None, kshape[0], kshape[1])
+    batch, heads, _ = shape
+    index = _page_index(block_table, seq_lens, None, pages, page)
     if out is None:
-        out = _made(torch.empty((batch, heads, dv), dtype=_BF16, device=dev), stream)
-    elif out.shape != (batch, heads, dv) or out.dtype != _BF16 or not out.is_contiguous():
+        out = _empty((batch, heads, dv), dtype=_BF16, device=dev)
+        if stream is not None:
+            _made(out, stream)
+    elif out.shape != (batch, heads, dv) or out.dtype is not _BF16 or not out.is_contiguous():
         raise ProjError(1, f"out must be a dense [{batch}, {heads}, {dv}] {q.dtype} tensor")
-    if lse is None:
-        if return_lse:
-            lse = _made(torch.empty((batch, heads), dtype=_F32, device=dev), stream)
-    elif lse.shape != (batch, heads) or lse.dtype != _F32 or not lse.is_contiguous():
-        raise ProjError(1, f"lse must be a dense [{batch}, {heads}] float32 tensor")
-    if workspace is None:
-        key = (heads, kshape[2], k_dim, dv, v_pages is None, dev)
-        need = _attn_workspace.get(key)
-        if need is None:
-            need = _attn_workspace[key] = paged_attention_workspace_bytes(heads, kshape[2], k_dim, dv, v_pages is None)
-        workspace = _work(None, need, dev, stream)
-    elif not workspace.is_contiguous():
-        raise ProjError(1, "workspace must be dense")
+    lse_ptr = None
+    if lse is not None:
+        if lse.shape != (batch, heads) or lse.dtype is not _F32 or not lse.is_contiguous():
+            raise ProjError(1, f"lse must be a dense [{batch}, {heads}] float32 tensor")
+        lse_ptr = lse.data_ptr()
+    elif return_lse:
+        lse = _empty((batch, heads), dtype=_F32, device=dev)
+        if stream is not None:
+            _made(lse, stream)
+        lse_ptr = lse.data_ptr()
+    ws_ptr, ws_bytes = None, 0
+    if workspace is not None or block_table.shape[1] * page > UNCUT_TOKENS:
+        if workspace is None:
+            key = (heads, kv_heads, k_dim, dv, v_pages is None, dev)
+            need = _attn_workspace.get(key)
+            if need is None:
+                need = _attn_workspace[key] = paged_attention_workspace_bytes(heads, kv_heads, k_dim, dv, v_pages is None)
+            workspace = _work(None, need, dev, stream)
+        elif not workspace.is_contiguous():
+            raise ProjError(1, "workspace must be dense")
+        ws_ptr, ws_bytes = workspace.data_ptr(), workspace.nbytes
     qb, qh, _ = q.stride()
-    rc = lib().proj_paged_attention(q.data_ptr(), qb, qh, kv, index, None if rows is None else _ints("rows", rows, batch), batch,
-                                    heads, scale, out.data_ptr(), None if lse is None else lse.data_ptr(), workspace.data_ptr(),
-                                    workspace.nbytes, _raw_stream(stream, dev))
+    rc = (_lib or lib()).proj_paged_attention(q.data_ptr(), qb, qh, kv, index, None if rows is None else _ints("rows", rows, batch),
+                                              batch, heads, scale, out.data_ptr(), lse_ptr, ws_ptr, ws_bytes,
+                                              _raw_stream(stream, dev))
     if rc != 0:
         _check(rc)
     return (out, lse) if return_lse else out
@@ -582,7 +596,7 @@ def paged_attention(q: torch.Tensor, k_pages: torch.Tensor, v_pages: Optional[to
 
 def _new_rows(name: str, t: torch.Tensor, tokens: int, heads: int, dim: int):
     """(pointer, token stride) of the new rows of a cache: [tokens, heads, dim] or [tokens, heads * dim]."""
-    if t.dtype != _BF16:
+    if t.dtype is not _BF16:
         raise ProjError(4, f"unsupported tensor dtype {t.dtype}")
     shape, st = t.shape, t.stride()
     if not (len(shape) == 2 and shape == (tokens, heads * dim) and st[1] == 1) and \
@@ -608,7 +622,7 @@ def cache_append(k_new: torch.Tensor, v_new: Optional[torch.Tensor], k_pages: to
     index = _page_index(block_table, seq_lens, None, kshape[0], kshape[1])
     rot = None
     if cos_sin is not None:
-        if cos_sin.dtype != _F32 or cos_sin.dim() != 2 or not cos_sin.is_contiguous():
+        if cos_sin.dtype is not _F32 or cos_sin.dim() != 2 or not cos_sin.is_contiguous():
             raise ProjError(1, "cos_sin must be a dense [max_pos, rot] float32 tensor")
         most, dim = cos_sin.shape
         rot = _pack_rotary(cos_sin.data_ptr(), most, dim, 1 if interleaved else 0, 0)
@@ -616,17 +630,18 @@ def cache_append(k_new: torch.Tensor, v_new: Optional[torch.Tensor], k_pages: to
     if q is not None:
         if q_out is None:
             q_out = _made(torch.empty(q.shape, dtype=q.dtype, device=dev), stream)
-        if q.dim() != 3 or q.shape[0] != tokens or q.shape[2] != k_dim or q_out.shape != q.shape:
+        shape = q.shape
+        if len(shape) != 3 or shape[0] != tokens or shape[2] != k_dim or q_out.shape != shape:
             raise ProjError(1, f"q and q_out must be [tokens, heads, {k_dim}] with dense columns")
-        if q.dtype != _BF16 or q_out.dtype != _BF16:
+        if q.dtype is not _BF16 or q_out.dtype is not _BF16:
             raise ProjError(4, f"unsupported tensor dtype {q.dtype}, {q_out.dtype}")
-        heads = q.shape[1]
+        heads = shape[1]
         qs, qh, one = q.stride()
         os_, oh, two = q_out.stride()
         if one != 1 or two != 1:
             raise ProjError(1, f"q and q_out must be [tokens, heads, {k_dim}] with dense columns")
         qp, op = q.data_ptr(), q_out.data_ptr()
-    rc = lib().proj_cache_append(kp, ks, vp, vs, kv, index, None if rows is None else _ints("rows", rows, tokens),
+    rc = (_lib or lib()).proj_cache_append(kp, ks, vp, vs, kv, index, None if rows is None else _ints("rows", rows, tokens),
                                  None if positions is None else _ints("positions", positions, tokens), tokens, rot, qp, qs, qh,
                                  op, os_, oh, heads, _raw_stream(stream, dev))
     if rc != 0:
@@ -641,7 +656,7 @@ def cache_workspace_bytes(block_table: torch.Tensor, num_pages: int, n: int) -> 
 
 
 def _cache_need(index: bytes, n: int) -> int:
-    need = lib().proj_cache_workspace_bytes(index, n)
+    need = (_lib or lib()).proj_cache_workspace_bytes(index, n)
     if need == 0:
         raise ProjError(2, lib().proj_last_error_string().decode())
     return need
@@ -650,7 +665,8 @@ def _cache_need(index: bytes, n: int) -> int:
 def _result(name: str, t: Optional[torch.Tensor], n: int, dev: int, stream) -> torch.Tensor:
     """The caller's int32 output of n elements, or a new one."""
     if t is None:
-        return _made(torch.empty(n, dtype=_I32, device=dev), stream)
+        t = _empty(n, dtype=_I32, device=dev)
+        return t if stream is None else _made(t, stream)
     _ints(name, t, n)
     return t
 
@@ -667,7 +683,7 @@ def cache_resize(block_table: torch.Tensor, seq_lens: torch.Tensor, ref_counts: 
     n = rows.shape[0]
     status = _result("status", status, n, dev, stream)
     workspace = _work(workspace, _cache_need(index, n) if workspace is None else 0, dev, stream)
-    rc = lib().proj_cache_resize(index, _ints("rows", rows, n), _ints("new_lens", new_lens, n), n, packed, len(pools),
+    rc = (_lib or lib()).proj_cache_resize(index, _ints("rows", rows, n), _ints("new_lens", new_lens, n), n, packed, len(pools),
                                  status.data_ptr(), workspace.data_ptr(), workspace.nbytes, _raw_stream(stream, dev))
     if rc != 0:
         _check(rc)
@@ -681,7 +697,7 @@ def cache_fork(block_table: torch.Tensor, seq_lens: torch.Tensor, ref_counts: to
     index = _page_index(block_table, seq_lens, ref_counts, ref_counts.shape[0], page_size)
     n = parents.shape[0]
     status = _result("status", status, n, dev, stream)
-    rc = lib().proj_cache_fork(index, _ints("parents", parents, n), _ints("children", children, n), n, status.data_ptr(),
+    rc = (_lib or lib()).proj_cache_fork(index, _ints("parents", parents, n), _ints("children", children, n), n, status.data_ptr(),
                                _raw_stream(stream, dev))
     if rc != 0:
         _check(rc)
@@ -698,7 +714,7 @@ def cache_compact(block_table: torch.Tensor, seq_lens: torch.Tensor, ref_counts:
     index = _page_index(block_table, seq_lens, ref_counts, num_pages, page_size)
     live = _result("live", live, 1, dev, stream)
     workspace = _work(workspace, _cache_need(index, 0) if workspace is None else 0, dev, stream)
-    rc = lib().proj_cache_compact(index, packed, len(pools), live.data_ptr(), workspace.data_ptr(), workspace.nbytes,
+    rc = (_lib or lib()).proj_cache_compact(index, packed, len(pools), live.data_ptr(), workspace.data_ptr(), workspace.nbytes,
                                   _raw_stream(stream, dev))
     if rc != 0:
         _check(rc)
@@ -714,7 +730,7 @@ def cache_copy_pages(pools: Sequence[torch.Tensor], src, dst, stream=None) -> No
     if src.is_cuda or dst.is_cuda:
         raise ProjError(1, "src and dst must be on the host")
     n = src.shape[0]
-    rc = lib().proj_cache_copy_pages(packed, len(pools), num_pages, _ints("src", src, n), _ints("dst", dst, n), n,
+    rc = (_lib or lib()).proj_cache_copy_pages(packed, len(pools), num_pages, _ints("src", src, n), _ints("dst", dst, n), n,
                                      _raw_stream(stream, dev))
     if rc != 0:
         _check(rc)

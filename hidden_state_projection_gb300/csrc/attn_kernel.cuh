@@ -203,6 +203,9 @@ __device__ __forceinline__ int line_owner(uint32_t T, uint32_t x, uint32_t C) {
     return static_cast<int>((static_cast<uint64_t>(x + 1) * C + T - 1) / T) - 1;
 }
 
+// Up to so many tiles per CTA the line is cut by tiles alone.
+constexpr uint32_t kAttnFewTiles = 2;
+
 // Where a CTA's units lie, and a walk over them; every role walks alike.
 struct AttnLine {
     uint32_t total;    // T
@@ -210,6 +213,7 @@ struct AttnLine {
     uint32_t base;     // units of all kv heads before sequence b0
     int32_t b0, len0;  // the sequence that holds x0, its length
     uint32_t ctas;     // CTAs that hold units
+    int32_t weight;    // units besides the tiles
 };
 struct AttnWalk {
     uint32_t x, base;
@@ -238,7 +242,7 @@ __device__ __forceinline__ bool attn_next_segment(const AttnArgs &a, const AttnL
         }
         uint32_t units;
         for (;;) {
-            units = w.len > 0 ? attn_tiles(w.len) + a.weight : 0;
+            units = w.len > 0 ? attn_tiles(w.len) + ln.weight : 0;
             if (w.x < w.base + units * a.kv_heads) break;
             w.base += units * a.kv_heads;
             if (++w.b >= a.batch) return false;  // (lengths that changed under the call)
@@ -250,9 +254,9 @@ __device__ __forceinline__ bool attn_next_segment(const AttnArgs &a, const AttnL
         const int n = static_cast<int>(min(units - p, ln.x1 - w.x));
         s.b = w.b;
         s.len = w.len;
-        s.tiles = static_cast<int>(units) - a.weight;
-        s.t0 = max(0, p - a.weight);
-        s.n = max(0, p + n - a.weight) - s.t0;
+        s.tiles = static_cast<int>(units) - ln.weight;
+        s.t0 = max(0, p - ln.weight);
+        s.n = max(0, p + n - ln.weight) - s.t0;
         s.x0 = w.x;
         s.end = w.x + (units - p);
         w.x += n;
@@ -304,7 +308,7 @@ struct RingPos {
 };
 
 template <int KB, int VB, bool SHARED, int N>
-__global__ void __launch_bounds__(kAttnThreads, 1)
+__global__ void __launch_bounds__(kAttnThreads, attn_ctas_per_sm(KB, SHARED, N))
     hsp_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ CUtensorMap tmap_k,
                     const __grid_constant__ CUtensorMap tmap_v, const __grid_constant__ AttnArgs a) {
     using C = AttnCfg<KB, VB, SHARED, N>;
@@ -335,7 +339,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     volatile int *const abort_flag = ints + 1;
     int *const issued = ints + 2;                                       // groups, rotary boxes, queries whose copies were issued
     int *const place = ints + 5;                                        // the first sequence of this CTA, units before it, its length
-    int *const warp_sum = ints + 8;                                     // [7]
+    int *const warp_sum = ints + 8;                                     // [7][2]
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int ht = blockIdx.x, cta = blockIdx.y;
@@ -376,39 +380,52 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     if (a.split) {
         const int per = (a.batch + kAttnThreads - 1) / kAttnThreads;
         const int bfirst = min(a.batch, tid * per), blast = min(a.batch, bfirst + per);
-        uint32_t mine = 0;
+        uint32_t mine = 0, seqs = 0;  // tiles, and sequences that have any
         int len = 0;
         for (int b = bfirst; b < blast; ++b) {
             len = attn_len(a, b);
-            mine += len > 0 ? attn_tiles(len) + a.weight : 0;
+            mine += attn_tiles(len);
+            seqs += len > 0 ? 1 : 0;
         }
-        uint32_t incl = mine;
+        uint32_t incl = mine, iseq = seqs;
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
-            const uint32_t o = __shfl_up_sync(0xffffffffu, incl, d);
-            if (lane >= d) incl += o;
+            const uint32_t o = __shfl_up_sync(0xffffffffu, incl, d), q = __shfl_up_sync(0xffffffffu, iseq, d);
+            if (lane >= d) {
+                incl += o;
+                iseq += q;
+            }
         }
-        if (lane == 31) warp_sum[warp] = static_cast<int>(incl);
+        if (lane == 31) *reinterpret_cast<uint2 *>(warp_sum + 2 * warp) = make_uint2(incl, iseq);
         __syncthreads();
-        uint32_t before = 0, all = 0;
+        uint32_t before = 0, all = 0, bseq = 0, aseq = 0;
 #pragma unroll
         for (int w = 0; w < kAttnThreads / 32; ++w) {
-            if (w < warp) before += warp_sum[w];
-            all += warp_sum[w];
+            const uint2 t = *reinterpret_cast<const uint2 *>(warp_sum + 2 * w);
+            if (w < warp) {
+                before += t.x;
+                bseq += t.y;
+            }
+            all += t.x;
+            aseq += t.y;
         }
-        ln.total = all * a.kv_heads;
-        ln.ctas = min((ln.total + a.min_units - 1) / a.min_units, static_cast<uint32_t>(a.ctas));
+        // while a CTA gets a few tiles only, every part's start and end run side by side: cut by tiles alone
+        ln.weight = all * a.kv_heads <= kAttnFewTiles * static_cast<uint32_t>(a.ctas) ? 0 : a.weight;
+        mine += seqs * ln.weight;
+        before += incl - (mine - seqs * ln.weight) + (bseq + iseq - seqs) * ln.weight;
+        ln.total = (all + aseq * ln.weight) * a.kv_heads;
+        ln.ctas = min(ln.total, static_cast<uint32_t>(a.ctas));
         ln.x0 = ln.x1 = 0;
         if (cta < ln.ctas) {
             ln.x0 = line_start(ln.total, cta, ln.ctas);
             ln.x1 = line_start(ln.total, cta + 1, ln.ctas);
-            uint32_t first = (before + incl - mine) * a.kv_heads;
+            uint32_t first = before * a.kv_heads;
             if (ln.x0 >= first && ln.x0 < first + mine * a.kv_heads) {
                 int b = bfirst;
                 if (per > 1) {  // walk to the sequence
                     for (;; ++b) {
                         len = attn_len(a, b);
-                        const uint32_t units = len > 0 ? (attn_tiles(len) + a.weight) * a.kv_heads : 0;
+                        const uint32_t units = len > 0 ? (attn_tiles(len) + ln.weight) * a.kv_heads : 0;
                         if (ln.x0 < first + units || b + 1 >= blast) break;
                         first += units;
                     }
@@ -422,6 +439,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         ln.total = ln.x1 = static_cast<uint32_t>(a.batch) * a.kv_heads;
         ln.x0 = cta;
         ln.ctas = a.ctas;
+        ln.weight = 0;
     }
     tc_fence_before_sync();
     __syncthreads();
@@ -866,13 +884,13 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
 // ---- join ------------------------------------------------------------------------------
 //
 // Sequences cut over several CTAs: out = sum_i 2^(m_i - M) O_i / sum_i 2^(m_i - M) l_i, the
-// parts in CTA order.  Few parts (a batch: most
-// sequences lie on two or three CTAs): a warp takes a whole head; many parts (one
-// long sequence): a CTA takes 64 columns of a head, its sixteen half warps take the parts in turn
-// and their sums are added in a fixed order.  Which of the two depends on the number of parts only.
+// parts in a fixed order.  Few parts, or heads enough for all warps: a warp takes a head, part
+// after part.  Else (one long sequence): a CTA takes 64 columns of a head, its sixteen half warps
+// take the parts in turn and their sums are added in a fixed order.  Which of the two depends on
+// the lengths only.
 
 constexpr int kJoinThreads = 256;
-constexpr int kJoinFew = 16;
+constexpr int kJoinWarpParts = 32;  // most parts of a head that one warp joins
 
 template <int DV, int N>
 __global__ void __launch_bounds__(kJoinThreads, 3) hsp_attn_join_kernel(const __grid_constant__ AttnArgs a) {
@@ -885,6 +903,7 @@ __global__ void __launch_bounds__(kJoinThreads, 3) hsp_attn_join_kernel(const __
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     griddep_wait();
     // the sequences to join, in CTA order in every CTA of this kernel: its units are shared out by their place
+    int parts_of[kAttnMaxCtas / kJoinThreads];
 #pragma unroll
     for (int k = 0; k < kAttnMaxCtas / kJoinThreads; ++k) {
         const int c = tid + k * kJoinThreads;
@@ -893,17 +912,26 @@ __global__ void __launch_bounds__(kJoinThreads, 3) hsp_attn_join_kernel(const __
             begun = a.entries[c].batch;
             last = a.entries[c].last;
         }
-        const uint32_t mf = __ballot_sync(0xffffffffu, begun >= 0 && last - c < kJoinFew);
-        const uint32_t mm = __ballot_sync(0xffffffffu, begun >= 0 && last - c >= kJoinFew);
-        if (lane == 0) {
-            bits[0][c >> 5] = mf;
-            bits[1][c >> 5] = mm;
-        }
+        parts_of[k] = begun >= 0 ? last - c + 1 : 0;
+        const uint32_t mm = __ballot_sync(0xffffffffu, begun >= 0);
+        if (lane == 0) bits[1][c >> 5] = mm;
+    }
+    __syncthreads();
+    // A warp joins a head in about half as many steps as it has parts, a CTA 64 columns of one in
+    // about five; with R such units for every CTA, up to 5 R parts are a warp's.
+    int items = 0;
+    for (int w = 0; w * 32 < a.ctas; ++w) items += __popc(bits[1][w]);
+    const int units = static_cast<int>(min(static_cast<int64_t>(1) << 20, static_cast<int64_t>(items) * a.group * kParts / gridDim.x));
+    const int by_warp = min(kJoinWarpParts, 5 * max(1, units));
+#pragma unroll
+    for (int k = 0; k < kAttnMaxCtas / kJoinThreads; ++k) {
+        const uint32_t mf = __ballot_sync(0xffffffffu, parts_of[k] > 0 && parts_of[k] <= by_warp);
+        if (lane == 0) bits[0][(tid + k * kJoinThreads) >> 5] = mf;
     }
     __syncthreads();
     int nfew = 0, nmany = 0;
     for (int w = 0; w * 32 < a.ctas; ++w) {
-        const uint32_t f = bits[0][w], m = bits[1][w];
+        const uint32_t f = bits[0][w], m = bits[1][w] & ~f;
         if (warp == (w & 7)) {
             const uint32_t low = (1u << lane) - 1u;
             if ((f >> lane) & 1u) few[nfew + __popc(f & low)] = static_cast<uint16_t>(w * 32 + lane);

@@ -42,12 +42,12 @@ proj_status check_index(const proj_page_index *ix, bool counts) {
     return PROJ_OK;
 }
 
-// Sequences of at most so many tiles are not cut.
-constexpr int kAttnWholeTiles = 4;
+// Tables of at most so many tiles per row: no sequence is cut, no workspace is used.
+constexpr int kAttnWholeTiles = PROJ_UNCUT_TOKENS / hsp::kAttnTile;
 
 // Heads and columns the attention kernel serves.
 struct AttnShape {
-    int KB, VB, shared, N, head_tiles, slots, per_sm, smem, min_units, weight;
+    int KB, VB, shared, N, head_tiles, slots, per_sm, smem, weight;
 };
 
 proj_status attn_shape(int heads, int kv_heads, int k_dim, int v_dim, bool latent, AttnShape *s) {
@@ -66,10 +66,8 @@ proj_status attn_shape(int heads, int kv_heads, int k_dim, int v_dim, bool laten
     s->head_tiles = (group + s->N - 1) / s->N;
     const int box = hsp::kAttnTile * 128, group_bytes = hsp::attn_group_boxes(s->VB) * box;
     const int fixed = hsp::attn_fixed_smem(s->KB, s->N) + (latent ? (s->KB - s->VB) * 2 * box : 0);
-    // A latent tile is 73.7 KB: one CTA per SM takes all of its shared memory; grouped tiles leave
-    // room for two CTAs, whose softmaxes and products overlap (64 heads: registers allow one).
-    s->per_sm = latent || s->N == 64 ? 1 : 2;
-    const int room = s->per_sm == 1 ? kSmemLimit : kSmemPerSm / 2 - kSmemReserved;
+    s->per_sm = hsp::attn_ctas_per_sm(s->KB, latent, s->N);
+    const int room = s->per_sm == 1 ? kSmemLimit : kSmemPerSm / s->per_sm - kSmemReserved;
     s->slots = (room - fixed) / group_bytes;
     if (s->slots > hsp::kAttnMaxSlots) s->slots = hsp::kAttnMaxSlots;
     s->smem = fixed + s->slots * group_bytes;
@@ -77,7 +75,6 @@ proj_status attn_shape(int heads, int kv_heads, int k_dim, int v_dim, bool laten
     // memory (64 heads: 6 us, a tile 1.2 us); grouped tiles wait for memory, and another CTA on the
     // SM uses the pause (no cost in a fit over 304 CTAs).
     s->weight = latent ? 1 + s->N / 16 : 0;
-    s->min_units = s->weight + 2;
     return PROJ_OK;
 }
 
@@ -229,7 +226,8 @@ proj_status proj_paged_attention(const void *q, int64_t q_row_stride, int64_t q_
     hsp::ApiDevice dev;
     if ((st = hsp::api_device(&dev)) != PROJ_OK) return st;
     const int ctas = attn_ctas(s, dev.sms);
-    if ((st = check_workspace(workspace, workspace_bytes, attn_workspace(s, ctas))) != PROJ_OK) return st;
+    const bool split = most_tiles > kAttnWholeTiles;
+    if (split && (st = check_workspace(workspace, workspace_bytes, attn_workspace(s, ctas))) != PROJ_OK) return st;
     hsp::AttnLaunchReq r{};
     const int boxes = hsp::attn_group_boxes(s.VB);
     if ((st = encode_pages(kv->k, index, kv->kv_heads, kv->k_dim, kv->k_page_stride, kv->k_token_stride, kv->k_head_stride,
@@ -243,11 +241,16 @@ proj_status proj_paged_attention(const void *q, int64_t q_row_stride, int64_t q_
         if ((st = hsp::api_encode_5d(q, dims, strides, box, &r.tmap_q)) != PROJ_OK) return st;
     }
     // the values' map; of a latent cache, the same pages one box at a time (the rotary box)
-    if ((st = kv->v ? encode_pages(kv->v, index, kv->kv_heads, kv->v_dim, kv->v_page_stride, kv->v_token_stride,
-                                   kv->v_head_stride, boxes, &r.tmap_v)
-                    : encode_pages(kv->k, index, kv->kv_heads, kv->k_dim, kv->k_page_stride, kv->k_token_stride,
-                                   kv->k_head_stride, 1, &r.tmap_v)) != PROJ_OK)
-        return st;
+    st = PROJ_OK;
+    if (kv->v)
+        st = encode_pages(kv->v, index, kv->kv_heads, kv->v_dim, kv->v_page_stride, kv->v_token_stride, kv->v_head_stride, boxes,
+                          &r.tmap_v);
+    else if (s.KB > s.VB)
+        st = encode_pages(kv->k, index, kv->kv_heads, kv->k_dim, kv->k_page_stride, kv->k_token_stride, kv->k_head_stride, 1,
+                          &r.tmap_v);
+    else
+        r.tmap_v = r.tmap_k;
+    if (st != PROJ_OK) return st;
     const hsp::ApiOptions opt = hsp::api_options();
     r.KB = s.KB;
     r.VB = s.VB;
@@ -271,15 +274,16 @@ proj_status proj_paged_attention(const void *q, int64_t q_row_stride, int64_t q_
     a.kv_heads = kv->kv_heads;
     a.group = heads / kv->kv_heads;
     a.ctas = ctas;
-    a.split = most_tiles > kAttnWholeTiles ? 1 : 0;
-    a.min_units = s.min_units;
+    a.split = split ? 1 : 0;
     a.weight = s.weight;
     a.slots = s.slots;
     a.scale_log2 = scale * 1.4426950408889634f;
     a.out = out;
     a.lse = lse;
-    a.entries = static_cast<hsp::AttnEntry *>(workspace);
-    a.parts = reinterpret_cast<float *>(static_cast<char *>(workspace) + up256(static_cast<size_t>(ctas) * sizeof(hsp::AttnEntry)));
+    if (split) {
+        a.entries = static_cast<hsp::AttnEntry *>(workspace);
+        a.parts = reinterpret_cast<float *>(static_cast<char *>(workspace) + up256(static_cast<size_t>(ctas) * sizeof(hsp::AttnEntry)));
+    }
     a.skip_tile = opt.skip_stage;
     a.wait_limit_ns = opt.wait_limit_ns;
     a.err_word = dev.err_word;
@@ -305,6 +309,9 @@ proj_status proj_cache_append(const void *k_new, int64_t k_row_stride, const voi
     if ((kv->v != nullptr) != (v_new != nullptr) && tokens > 0)
         return api_fail(PROJ_ERR_INVALID_ARG, "v_new goes with a cache that has values of its own");
     if (q && (heads < 1 || heads > 65536)) return api_fail(PROJ_ERR_INVALID_ARG, "heads=%d (1..65536)", heads);
+    const int64_t columns = static_cast<int64_t>(kv->kv_heads) * (kv->k_dim + (kv->v ? kv->v_dim : 0)) +
+                            (q ? static_cast<int64_t>(heads) * kv->k_dim : 0);
+    if (columns > (1 << 24)) return api_fail(PROJ_ERR_UNSUPPORTED_SHAPE, "%lld columns of a token exceed 2^24", (long long)columns);
     if (q && !rotary) return api_fail(PROJ_ERR_INVALID_ARG, "queries are only turned: q needs rotary");
     if (rotary) {
         if (!rotary->cos_sin || rotary->max_pos < 1) return api_fail(PROJ_ERR_INVALID_ARG, "rotary without a table");
@@ -401,6 +408,7 @@ proj_status proj_cache_resize(const proj_page_index *index, const int32_t *rows,
     a.n = n;
     char *ws = static_cast<char *>(workspace);
     a.head = reinterpret_cast<int32_t *>(ws);
+    a.taken = reinterpret_cast<unsigned long long *>(ws + 16);
     a.claims = reinterpret_cast<int32_t *>(ws + w.claims);
     a.list = reinterpret_cast<int32_t *>(ws + w.list);
     a.pairs = reinterpret_cast<int2 *>(ws + w.pairs);
@@ -451,6 +459,7 @@ proj_status proj_cache_compact(const proj_page_index *index, const proj_page_poo
     a.live = live;
     char *ws = static_cast<char *>(workspace);
     a.head = reinterpret_cast<int32_t *>(ws);
+    a.taken = reinterpret_cast<unsigned long long *>(ws + 16);
     a.list = reinterpret_cast<int32_t *>(ws + w.list);
     a.pairs = reinterpret_cast<int2 *>(ws + w.pairs);
     const cudaError_t e = hsp::launch_compact(a, dev.sms, hsp::api_options().pdl, reinterpret_cast<cudaStream_t>(stream));

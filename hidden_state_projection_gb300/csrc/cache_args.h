@@ -32,7 +32,7 @@ struct AttnArgs {
     int32_t batch, kv_heads, group;  // group: query heads per kv head
     int32_t ctas;                // CTAs along the length (grid.y)
     int32_t split;               // 0: no sequence is cut (and nothing is to join)
-    int32_t min_units, weight;   // least units per CTA; units of a part's start and end (one per tile besides)
+    int32_t weight;              // units of a part's start and end (one per tile besides)
     int32_t slots;               // group places in the ring
     float scale_log2;            // softmax scale * log2(e)
     void *out;                   // [batch, heads, VB * 64] bf16
@@ -62,6 +62,11 @@ cudaError_t launch_attn_grouped(const AttnLaunchReq &r);
 // buffers, barriers (of at most kAttnMaxSlots places) and the alignment slack.
 constexpr int kAttnMaxSlots = 12;
 inline int attn_fixed_smem(int KB, int N) { return KB * N * 128 + kAttnTile * 128 + 5 * N * 4 + 512 + 1024; }
+// CTAs per SM.  A latent tile is 73.7 KB, one CTA takes the shared memory of an SM; grouped tiles
+// are 32 or 16 KB, and the softmaxes and products of two or three CTAs overlap (32 sequences of
+// up to 4096 tokens, 8 heads of 64 columns: 38.4 us with two, 33.0 with three).  64 heads: registers
+// allow one.
+constexpr int attn_ctas_per_sm(int KB, bool shared, int N) { return shared || N == 64 ? 1 : KB == 1 && N == 16 ? 3 : 2; }
 inline int attn_group_boxes(int VB) { return VB >= 2 ? 2 : 1; }
 
 // ---- append ---------------------------------------------------------------------------
@@ -124,7 +129,8 @@ struct ResizeArgs {
     int32_t *status;                 // [n]
     int32_t n;
     // workspace
-    int32_t *head;                   // [0]: copy pairs, [1]: live pages (compaction), [2]: copy units taken
+    int32_t *head;                   // [0]: copy pairs, [1]: live pages (compaction)
+    unsigned long long *taken;       // copy units taken so far
     RowPlan *plan;                   // [n]
     int32_t *claims;                 // [num_rows]
     int32_t *list;                   // [num_pages] free pages (resize) or new places (compaction)
@@ -145,6 +151,7 @@ struct CompactArgs {
     IndexArgs ix;
     int32_t *live;                   // [1]
     int32_t *head, *list;            // workspace, as in ResizeArgs
+    unsigned long long *taken;
     int2 *pairs;
     PoolList pools;
 };

@@ -102,17 +102,17 @@ __device__ __forceinline__ void copy_unit(const PoolList &pl, int64_t u, Pair pa
 
 // The same over all units, taken in order from a counter that starts at zero.  All threads call.
 template <typename Pair>
-__device__ __forceinline__ void copy_in_order(const PoolList &pl, int64_t units, int *counter, Pair pair) {
+__device__ __forceinline__ void copy_in_order(const PoolList &pl, int64_t units, unsigned long long *counter, Pair pair) {
     __shared__ int64_t next;
     if (units == 0) return;
-    int mine = 0;
-    if (threadIdx.x == 0) mine = atomicAdd(counter, 1);
+    int64_t mine = 0;
+    if (threadIdx.x == 0) mine = static_cast<int64_t>(atomicAdd(counter, 1ull));
     for (;;) {
         if (threadIdx.x == 0) next = mine;
         __syncthreads();
         const int64_t u = next;
         if (u >= units) return;
-        if (threadIdx.x == 0) mine = atomicAdd(counter, 1);  // on its way during the copy
+        if (threadIdx.x == 0) mine = static_cast<int64_t>(atomicAdd(counter, 1ull));  // on its way during the copy
         copy_unit(pl, u, pair);
         __syncthreads();
     }
@@ -253,7 +253,7 @@ __global__ void __launch_bounds__(kPlanThreads) hsp_resize_plan_kernel(const __g
     __syncthreads();
     if (tid == 0) {
         a.head[0] = pair_count;
-        a.head[2] = 0;
+        *a.taken = 0;
     }
     done();
 }
@@ -294,7 +294,7 @@ __global__ void __launch_bounds__(kPagesThreads) hsp_resize_apply_kernel(const _
         }
     }
     const int64_t units = static_cast<int64_t>(a.head[0]) * a.pools.pieces_total;
-    copy_in_order(a.pools, units, &a.head[2], [&](int64_t k) { return a.pairs[k]; });
+    copy_in_order(a.pools, units, a.taken, [&](int64_t k) { return a.pairs[k]; });
     done();
 }
 
@@ -427,7 +427,7 @@ __global__ void __launch_bounds__(kPlanThreads) hsp_compact_plan_kernel(const __
     if (tid == 0) {
         a.head[0] = moves;
         a.head[1] = L;
-        a.head[2] = 0;
+        *a.taken = 0;
         a.live[0] = L;
     }
     done();
@@ -460,7 +460,7 @@ __global__ void __launch_bounds__(kPagesThreads) hsp_compact_apply_kernel(const 
             ix.refs[p.x] = 0;
         }
         const int64_t units = static_cast<int64_t>(moves) * a.pools.pieces_total;
-        copy_in_order(a.pools, units, &a.head[2], [&](int64_t k) { return a.pairs[k]; });
+        copy_in_order(a.pools, units, a.taken, [&](int64_t k) { return a.pairs[k]; });
     }
     done();
 }

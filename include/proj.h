@@ -69,6 +69,7 @@ typedef enum {
 #define PROJ_MAX_PREFETCH 4
 #define PROJ_MAX_POOLS 4
 #define PROJ_MAX_COPY_PAIRS 2048
+#define PROJ_UNCUT_TOKENS 256
 
 /* A global range to bring into L2 (proj_fused_gemm_prefetch). */
 typedef struct {
@@ -431,8 +432,9 @@ typedef struct {
  *   lse        device [batch, heads] fp32, or NULL
  *   workspace  device, 16-byte aligned, at least proj_paged_attention_workspace_bytes
  *              bytes; needs no initialisation and keeps nothing.  Calls that share one
- *              must not overlap on the GPU.
- * Two kernel launches.  batch = 0 succeeds and touches nothing.
+ *              must not overlap on the GPU.  Not used (and may be NULL) where a table row
+ *              holds at most PROJ_UNCUT_TOKENS tokens: then no sequence is cut.
+ * Two kernel launches, one for such a table.  batch = 0 succeeds and touches nothing.
  */
 proj_status proj_paged_attention(const void *q, int64_t q_row_stride, int64_t q_head_stride,
                                  const proj_kv_pages *kv, const proj_page_index *index,

@@ -137,6 +137,55 @@ def test_many_sequences(hsp, latent):
 
 
 @pytest.mark.parametrize("latent", [True, False])
+def test_many_short_sequences_are_not_cut(hsp, latent):
+    """Tables of at most 256 tokens per row: one launch, no workspace."""
+    lens = [(37 * i) % 241 for i in range(700)]
+    dk, dv, heads, kv = (512, 512, 70, 1) if latent else (64, 64, 6, 3)
+    args = make(lens, heads, kv, dk, latent, 16, 13)
+    assert args[3].shape[1] * 16 == 256
+    n = hsp.launch_count()
+    check(hsp, args, dk ** -0.5, dv)
+    assert hsp.launch_count() == n + 1
+
+
+@pytest.mark.parametrize("latent", [True, False])
+def test_a_cache_past_four_gigabytes(hsp, latent):
+    """Pages whose offsets do not fit 32 bits, neither in bytes nor in elements."""
+    dk, dv, kv, heads, page = (576, 512, 1, 16, 64) if latent else (128, 128, 4, 8, 64)
+    lens = [200, 129]
+    q, k, v, table, ln = make(lens, heads, kv, dk, latent, page, 17)
+    pages = 2 ** 32 // (page * kv * dk) + 40                        # more than 2^32 elements
+    at = pages - 1 - torch.arange(7, device="cuda") * 3
+    move = {}
+
+    def far(t):
+        big = torch.empty((pages,) + tuple(t.shape[1:]), dtype=BF, device="cuda")
+        big[at] = t[:7]
+        return big
+
+    assert k.shape[0] <= 9 and int(table[table < 2 ** 30].max()) < 9
+    used = sorted(set(table[table < 2 ** 30].tolist()))
+    move = {u: int(at[i]) for i, u in enumerate(used)}
+    order = torch.tensor(used, device="cuda")
+    big_k, big_v = far(k[order]), None if latent else far(v[order])
+    far_table = table.clone()
+    for b, n in enumerate(lens):
+        for j in range(-(-n // page)):
+            far_table[b, j] = move[int(table[b, j])]
+    want = hsp.paged_attention(q, k, v, table, ln, 0.07)
+    assert torch.equal(hsp.paged_attention(q, big_k, big_v, far_table, ln, 0.07), want)
+    # and the new tokens of the next step land there
+    kn = torch.randn(2, kv, dk, device="cuda").to(BF)
+    hsp.cache_append(kn, None if latent else kn, big_k, big_v, far_table, ln)
+    hsp.check_device_error()
+    for b, n in enumerate(lens):
+        p = int(far_table[b, (n - 1) // page])
+        assert p * page * kv * dk >= 2 ** 32 - 40 * page * kv * dk
+        assert torch.equal(big_k[p, (n - 1) % page], kn[b])
+        assert latent or torch.equal(big_v[p, (n - 1) % page], kn[b])
+
+
+@pytest.mark.parametrize("latent", [True, False])
 def test_heads_before_tokens_and_strided_queries(hsp, latent):
     """Pages that hold head after head, queries and keys that are columns of wider tensors."""
     dk, dv, kv = (576, 512, 2) if latent else (128, 128, 2)
@@ -295,12 +344,13 @@ def test_bad_pages_rows_and_lengths_are_reported(hsp):
 
 @pytest.mark.parametrize("latent", [True, False])
 def test_bounded_waits_report_a_timeout(hsp, latent):
-    """The test hook leaves one tile of every CTA unloaded: the waits run out, and the next call is right again."""
+    """The test hook leaves the first tile of every CTA unloaded (the only one that every CTA has): the waits run out,
+    and the next call is right again."""
     import hidden_state_projection_gb300 as m
     dk, dv = (576, 512) if latent else (128, 128)
     args = make([3000], 16, 1, dk, latent, 64, 12)
     want = hsp.paged_attention(*args, 0.07)
-    hsp.set_options(pdl=True, wait_limit_us=20000, skip_stage=1)
+    hsp.set_options(pdl=True, wait_limit_us=20000, skip_stage=0)
     try:
         hsp.paged_attention(*args, 0.07)
         with pytest.raises(m.ProjError) as ei:

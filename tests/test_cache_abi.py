@@ -53,6 +53,10 @@ def test_attention_refusals(hsp):
                      (dict(ix=index(table=A + 2)), 2)]:
         assert attend(hsp, **kw) == bad[want], kw
         assert hsp.lib().proj_last_error_string()
+    for ws in (dict(ws=None), dict(ws_bytes=1000), dict(ws=A + 8)):   # a table row of 512 tokens: sequences may be cut
+        assert attend(hsp, **ws) in (*bad, S["PROJ_ERR_DEVICE"], S["PROJ_ERR_CUDA"])
+    for qs in ((0, 576), (9216, 0), (-9216, 576), (9216, 1 << 39)):
+        assert attend(hsp, qs=qs) == bad[1], qs
     assert attend(hsp, batch=0) == S["PROJ_OK"]
     assert hsp.launch_count() == n
 
@@ -87,7 +91,8 @@ def test_append_refusals(hsp):
                      (dict(kvp=kv(heads=0)), "UNSUPPORTED_SHAPE"), (dict(r=rot(table=A + 4)), "MISALIGNED"),
                      (dict(k=A + 2), "MISALIGNED"), (dict(ks=577), "MISALIGNED"), (dict(q=A, qo=A + 8), "MISALIGNED"),
                      (dict(q=A, qo=A, qs=(9216, 4)), "MISALIGNED"), (dict(pos=A + 2), "MISALIGNED"),
-                     (dict(ix=index(page=20)), "UNSUPPORTED_SHAPE")]:
+                     (dict(ix=index(page=20)), "UNSUPPORTED_SHAPE"), (dict(q=A, qo=A, heads=65536), "UNSUPPORTED_SHAPE"),
+                     (dict(kvp=kv(heads=65536, dk=512)), "UNSUPPORTED_SHAPE")]:
         assert call(**kw) == S["PROJ_ERR_" + want], (kw, hsp.lib().proj_last_error_string())
     assert call(tokens=0) == S["PROJ_OK"]
     assert hsp.launch_count() == n

@@ -275,6 +275,23 @@ def test_copy_pages(hsp, n):
     hsp.cache_copy_pages([pool], [], [])
 
 
+def test_pages_past_four_gigabytes(hsp):
+    pages, page = 36000, 64
+    pool = torch.empty(1, pages, page, 1024, dtype=BF, device="cuda")        # 4.7 GB, 2^31 elements and more
+    pool[0, [3, pages - 1]] = torch.randn(2, page, 1024, device="cuda").to(BF)
+    hsp.cache_copy_pages([pool], [3, pages - 1], [pages - 7, 5])
+    assert torch.equal(pool[0, pages - 7], pool[0, 3]) and torch.equal(pool[0, 5], pool[0, pages - 1])
+    table = torch.tensor([[pages - 1, pages - 7, -1]], dtype=torch.int32, device="cuda")
+    lens = torch.tensor([100], dtype=torch.int32, device="cuda")
+    refs = torch.zeros(pages, dtype=torch.int32, device="cuda")
+    refs[pages - 1] = refs[pages - 7] = 1
+    kept = pool[0, [pages - 1, pages - 7]].clone()
+    assert hsp.cache_compact(table, lens, refs, page, [pool]).tolist() == [2]
+    assert sorted(table[0, :2].tolist()) == [0, 1] and torch.equal(pool[0, table[0, :2].long()], kept)
+    assert refs.nonzero().flatten().tolist() == [0, 1]
+    hsp.check_device_error()
+
+
 def test_page_calls_captured_and_replayed(hsp):
     """A beam step captured once: free the children, fork, grow; replayed with other parents."""
     c = Cache(hsp, 10, 8, 60, 16, 9)
