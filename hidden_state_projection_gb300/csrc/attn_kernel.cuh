@@ -151,6 +151,8 @@ __device__ __forceinline__ float fast_exp2(float x) {
     return y;
 }
 
+__device__ __forceinline__ void prefetch_l1(const void *p) { asm volatile("prefetch.global.L1 [%0];" ::"l"(p)); }
+
 // Bounded wait.  Once any thread of the CTA has given up, waits that are not yet satisfied
 // return at once; the roles keep their barrier pattern and store nothing.
 __device__ __forceinline__ bool attn_wait(uint32_t bar, uint32_t parity, uint64_t limit_ns, volatile int *abort_flag,
@@ -433,6 +435,11 @@ __global__ void __launch_bounds__(kAttnThreads, attn_ctas_per_sm(KB, SHARED, N))
                 place[0] = b;
                 place[1] = static_cast<int>(first);
                 place[2] = len;
+                // its first page id, on its way before the copy producer asks for it
+                const uint32_t units = attn_tiles(len) + ln.weight;
+                const uint32_t t = (ln.x0 - first) % units;
+                const int64_t page = (static_cast<int64_t>(max(0, static_cast<int>(t) - ln.weight)) * kAttnTile) >> a.page_shift;
+                prefetch_l1(a.table + (a.rows ? a.rows[b] : b) * a.table_stride + page);
             }
         }
     } else {
@@ -858,6 +865,8 @@ __global__ void __launch_bounds__(kAttnThreads, attn_ctas_per_sm(KB, SHARED, N))
     }
     tc_fence_before_sync();
     __syncthreads();
+    // (Triggered at the start, the join's CTAs crowded on the SMs that were free first: 43 -> 47 us
+    // for one sequence of 131071 tokens and 64 heads.)
     if (tid == 0) fence_release_gpu();  // the outputs and partials of this CTA (cumulative over the barrier)
     griddep_launch_dependents();
     if (*abort_flag != 0 && tid == 0) {
@@ -899,6 +908,7 @@ __global__ void __launch_bounds__(kJoinThreads, 3) hsp_attn_join_kernel(const __
     __shared__ float4 acc_s[8][16];
     __shared__ float weight[kAttnMaxCtas], red_s[16];
     __shared__ uint16_t few[kAttnMaxCtas], many[kAttnMaxCtas];  // the CTAs that began them
+    __shared__ AttnEntry entries[kAttnMaxCtas];
     __shared__ uint32_t bits[2][kAttnMaxCtas / 32];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     griddep_wait();
@@ -909,8 +919,10 @@ __global__ void __launch_bounds__(kJoinThreads, 3) hsp_attn_join_kernel(const __
         const int c = tid + k * kJoinThreads;
         int begun = -1, last = 0;
         if (c < a.ctas) {
-            begun = a.entries[c].batch;
-            last = a.entries[c].last;
+            const AttnEntry e = a.entries[c];
+            entries[c] = e;
+            begun = e.batch;
+            last = e.last;
         }
         parts_of[k] = begun >= 0 ? last - c + 1 : 0;
         const uint32_t mm = __ballot_sync(0xffffffffu, begun >= 0);
@@ -963,7 +975,7 @@ __global__ void __launch_bounds__(kJoinThreads, 3) hsp_attn_join_kernel(const __
     constexpr int kVec = DV >= 128 ? DV / 128 : 1;  // float4 per lane and part
     for (int u = blockIdx.x * 8 + warp; u < nfew * a.group; u += gridDim.x * 8) {
         const int c = few[u / a.group], h = u % a.group, col = h % N;
-        const AttnEntry e = a.entries[c];
+        const AttnEntry e = entries[c];
         const int parts = min(e.last, a.ctas - 1) - c + 1;
         float m = -3.0e38f, l = 0.f;
         if (lane < parts) {
@@ -1017,7 +1029,7 @@ __global__ void __launch_bounds__(kJoinThreads, 3) hsp_attn_join_kernel(const __
     const int per_item = a.group * kParts;
     for (int u = blockIdx.x; u < nmany * per_item; u += gridDim.x) {
         const int c = many[u / per_item];
-        const AttnEntry e = a.entries[c];
+        const AttnEntry e = entries[c];
         const int rem = u % per_item, h = rem / kParts, dp = rem % kParts, col = h % N;
         const int parts = min(e.last, a.ctas - 1) - c + 1;
         // the values are on their way while the weights are made: a half warp per part, 16 at a time

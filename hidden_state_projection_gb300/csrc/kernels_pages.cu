@@ -143,6 +143,7 @@ __global__ void __launch_bounds__(kPlanThreads) hsp_resize_plan_kernel(const __g
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const IndexArgs &ix = a.ix;
     const int64_t most = static_cast<int64_t>(ix.max_pages) << ix.page_shift;
+    griddep_launch_dependents();  // (the apply kernel, which waits for this one's end)
     griddep_wait();
     // a row named twice counts once: the first of them
     for (int i = tid; i < a.n; i += kPlanThreads) {
@@ -255,7 +256,6 @@ __global__ void __launch_bounds__(kPlanThreads) hsp_resize_plan_kernel(const __g
         a.head[0] = pair_count;
         *a.taken = 0;
     }
-    done();
 }
 
 __device__ __forceinline__ void release_page(const IndexArgs &ix, int id) {
@@ -353,6 +353,7 @@ __global__ void __launch_bounds__(kPlanThreads) hsp_compact_plan_kernel(const __
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const IndexArgs &ix = a.ix;
     const int N = ix.num_pages;
+    griddep_launch_dependents();  // (the apply kernel, which waits for this one's end)
     griddep_wait();
     const int share = ((N + kPlanWarps - 1) / kPlanWarps + 127) / 128 * 128;
     const int lo = min(N, warp * share), hi = min(N, lo + share);
@@ -430,7 +431,6 @@ __global__ void __launch_bounds__(kPlanThreads) hsp_compact_plan_kernel(const __
         *a.taken = 0;
         a.live[0] = L;
     }
-    done();
 }
 
 __global__ void __launch_bounds__(kPagesThreads) hsp_compact_apply_kernel(const __grid_constant__ CompactArgs a) {
