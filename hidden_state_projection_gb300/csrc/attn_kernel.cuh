@@ -205,9 +205,6 @@ __device__ __forceinline__ int line_owner(uint32_t T, uint32_t x, uint32_t C) {
     return static_cast<int>((static_cast<uint64_t>(x + 1) * C + T - 1) / T) - 1;
 }
 
-// Up to so many tiles per CTA the line is cut by tiles alone.
-constexpr uint32_t kAttnFewTiles = 2;
-
 // Where a CTA's units lie, and a walk over them; every role walks alike.
 struct AttnLine {
     uint32_t total;    // T
@@ -215,7 +212,6 @@ struct AttnLine {
     uint32_t base;     // units of all kv heads before sequence b0
     int32_t b0, len0;  // the sequence that holds x0, its length
     uint32_t ctas;     // CTAs that hold units
-    int32_t weight;    // units besides the tiles
 };
 struct AttnWalk {
     uint32_t x, base;
@@ -244,7 +240,7 @@ __device__ __forceinline__ bool attn_next_segment(const AttnArgs &a, const AttnL
         }
         uint32_t units;
         for (;;) {
-            units = w.len > 0 ? attn_tiles(w.len) + ln.weight : 0;
+            units = w.len > 0 ? attn_tiles(w.len) + a.weight : 0;
             if (w.x < w.base + units * a.kv_heads) break;
             w.base += units * a.kv_heads;
             if (++w.b >= a.batch) return false;  // (lengths that changed under the call)
@@ -256,9 +252,9 @@ __device__ __forceinline__ bool attn_next_segment(const AttnArgs &a, const AttnL
         const int n = static_cast<int>(min(units - p, ln.x1 - w.x));
         s.b = w.b;
         s.len = w.len;
-        s.tiles = static_cast<int>(units) - ln.weight;
-        s.t0 = max(0, p - ln.weight);
-        s.n = max(0, p + n - ln.weight) - s.t0;
+        s.tiles = static_cast<int>(units) - a.weight;
+        s.t0 = max(0, p - a.weight);
+        s.n = max(0, p + n - a.weight) - s.t0;
         s.x0 = w.x;
         s.end = w.x + (units - p);
         w.x += n;
@@ -341,7 +337,7 @@ __global__ void __launch_bounds__(kAttnThreads, attn_ctas_per_sm(KB, SHARED, N))
     volatile int *const abort_flag = ints + 1;
     int *const issued = ints + 2;                                       // groups, rotary boxes, queries whose copies were issued
     int *const place = ints + 5;                                        // the first sequence of this CTA, units before it, its length
-    int *const warp_sum = ints + 8;                                     // [7][2]
+    int *const warp_sum = ints + 8;                                     // [7]
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int ht = blockIdx.x, cta = blockIdx.y;
@@ -382,40 +378,27 @@ __global__ void __launch_bounds__(kAttnThreads, attn_ctas_per_sm(KB, SHARED, N))
     if (a.split) {
         const int per = (a.batch + kAttnThreads - 1) / kAttnThreads;
         const int bfirst = min(a.batch, tid * per), blast = min(a.batch, bfirst + per);
-        uint32_t mine = 0, seqs = 0;  // tiles, and sequences that have any
+        uint32_t mine = 0;
         int len = 0;
         for (int b = bfirst; b < blast; ++b) {
             len = attn_len(a, b);
-            mine += attn_tiles(len);
-            seqs += len > 0 ? 1 : 0;
+            mine += len > 0 ? attn_tiles(len) + a.weight : 0;
         }
-        uint32_t incl = mine, iseq = seqs;
+        uint32_t incl = mine;
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
-            const uint32_t o = __shfl_up_sync(0xffffffffu, incl, d), q = __shfl_up_sync(0xffffffffu, iseq, d);
-            if (lane >= d) {
-                incl += o;
-                iseq += q;
-            }
+            const uint32_t o = __shfl_up_sync(0xffffffffu, incl, d);
+            if (lane >= d) incl += o;
         }
-        if (lane == 31) *reinterpret_cast<uint2 *>(warp_sum + 2 * warp) = make_uint2(incl, iseq);
+        if (lane == 31) warp_sum[warp] = static_cast<int>(incl);
         __syncthreads();
-        uint32_t before = 0, all = 0, bseq = 0, aseq = 0;
+        uint32_t before = incl - mine, all = 0;
 #pragma unroll
         for (int w = 0; w < kAttnThreads / 32; ++w) {
-            const uint2 t = *reinterpret_cast<const uint2 *>(warp_sum + 2 * w);
-            if (w < warp) {
-                before += t.x;
-                bseq += t.y;
-            }
-            all += t.x;
-            aseq += t.y;
+            if (w < warp) before += warp_sum[w];
+            all += warp_sum[w];
         }
-        // while a CTA gets a few tiles only, every part's start and end run side by side: cut by tiles alone
-        ln.weight = all * a.kv_heads <= kAttnFewTiles * static_cast<uint32_t>(a.ctas) ? 0 : a.weight;
-        mine += seqs * ln.weight;
-        before += incl - (mine - seqs * ln.weight) + (bseq + iseq - seqs) * ln.weight;
-        ln.total = (all + aseq * ln.weight) * a.kv_heads;
+        ln.total = all * a.kv_heads;
         ln.ctas = min(ln.total, static_cast<uint32_t>(a.ctas));
         ln.x0 = ln.x1 = 0;
         if (cta < ln.ctas) {
@@ -427,7 +410,7 @@ __global__ void __launch_bounds__(kAttnThreads, attn_ctas_per_sm(KB, SHARED, N))
                 if (per > 1) {  // walk to the sequence
                     for (;; ++b) {
                         len = attn_len(a, b);
-                        const uint32_t units = len > 0 ? (attn_tiles(len) + ln.weight) * a.kv_heads : 0;
+                        const uint32_t units = len > 0 ? (attn_tiles(len) + a.weight) * a.kv_heads : 0;
                         if (ln.x0 < first + units || b + 1 >= blast) break;
                         first += units;
                     }
@@ -436,9 +419,9 @@ __global__ void __launch_bounds__(kAttnThreads, attn_ctas_per_sm(KB, SHARED, N))
                 place[1] = static_cast<int>(first);
                 place[2] = len;
                 // its first page id, on its way before the copy producer asks for it
-                const uint32_t units = attn_tiles(len) + ln.weight;
+                const uint32_t units = attn_tiles(len) + a.weight;
                 const uint32_t t = (ln.x0 - first) % units;
-                const int64_t page = (static_cast<int64_t>(max(0, static_cast<int>(t) - ln.weight)) * kAttnTile) >> a.page_shift;
+                const int64_t page = (static_cast<int64_t>(max(0, static_cast<int>(t) - a.weight)) * kAttnTile) >> a.page_shift;
                 prefetch_l1(a.table + (a.rows ? a.rows[b] : b) * a.table_stride + page);
             }
         }
@@ -446,7 +429,6 @@ __global__ void __launch_bounds__(kAttnThreads, attn_ctas_per_sm(KB, SHARED, N))
         ln.total = ln.x1 = static_cast<uint32_t>(a.batch) * a.kv_heads;
         ln.x0 = cta;
         ln.ctas = a.ctas;
-        ln.weight = 0;
     }
     tc_fence_before_sync();
     __syncthreads();
@@ -894,18 +876,23 @@ __global__ void __launch_bounds__(kAttnThreads, attn_ctas_per_sm(KB, SHARED, N))
 //
 // Sequences cut over several CTAs: out = sum_i 2^(m_i - M) O_i / sum_i 2^(m_i - M) l_i, the
 // parts in a fixed order.  Few parts, or heads enough for all warps: a warp takes a head, part
-// after part.  Else (one long sequence): a CTA takes 64 columns of a head, its sixteen half warps
-// take the parts in turn and their sums are added in a fixed order.  Which of the two depends on
+// after part.  Else (one long sequence): a CTA takes 64 or 128 columns of a head, its half warps
+// or warps take the parts in turn and their sums are added in a fixed order.  Which of the two depends on
 // the lengths only.
 
 constexpr int kJoinThreads = 256;
 constexpr int kJoinWarpParts = 32;  // most parts of a head that one warp joins
 
+template <int W>
+struct JoinWidth {
+    static constexpr int value = W;
+};
+
 template <int DV, int N>
-__global__ void __launch_bounds__(kJoinThreads, 3) hsp_attn_join_kernel(const __grid_constant__ AttnArgs a) {
+__global__ void __launch_bounds__(kJoinThreads, 2) hsp_attn_join_kernel(const __grid_constant__ AttnArgs a) {
     constexpr int kParts = DV / 64;             // units of 64 columns of a head with many parts
     constexpr int kPart = N * DV + 2 * N;       // floats of one partial
-    __shared__ float4 acc_s[8][16];
+    __shared__ float4 acc_s[8][32];
     __shared__ float weight[kAttnMaxCtas], red_s[16];
     __shared__ uint16_t few[kAttnMaxCtas], many[kAttnMaxCtas];  // the CTAs that began them
     __shared__ AttnEntry entries[kAttnMaxCtas];
@@ -1026,20 +1013,19 @@ __global__ void __launch_bounds__(kJoinThreads, 3) hsp_attn_join_kernel(const __
         }
         if (a.lse && lane == 0) store_lse(e, h, M, L);
     }
-    const int per_item = a.group * kParts;
-    for (int u = blockIdx.x; u < nmany * per_item; u += gridDim.x) {
-        const int c = many[u / per_item];
+    // one head, `width` columns from dp * width on
+    auto join_cta = [&](int c, int h, int dp, auto width) {
         const AttnEntry e = entries[c];
-        const int rem = u % per_item, h = rem / kParts, dp = rem % kParts, col = h % N;
+        const int col = h % N;
         const int parts = min(e.last, a.ctas - 1) - c + 1;
-        // the values are on their way while the weights are made: a half warp per part, 16 at a time
-        constexpr int kAhead = 10;
-        const int half = lane >> 4, at = dp * 64 + (lane & 15) * 4, p_first = warp * 2 + half;
+        // the values are on their way while the weights are made
+        constexpr int kAhead = 10, kLanes = decltype(width)::value / 4, kRows = kJoinThreads / kLanes;
+        const int at = dp * (kLanes * 4) + tid % kLanes * 4, p_first = tid / kLanes;
         float4 v[kAhead];
         auto load = [&](int p0) {
 #pragma unroll
             for (int k = 0; k < kAhead; ++k)
-                if (p0 + 16 * k < parts) v[k] = *reinterpret_cast<const float4 *>(part(c, e.slot, h, p0 + 16 * k) + col * DV + at);
+                if (p0 + kRows * k < parts) v[k] = *reinterpret_cast<const float4 *>(part(c, e.slot, h, p0 + kRows * k) + col * DV + at);
         };
         load(p_first);
         float m[kAttnMaxCtas / kJoinThreads], lw[kAttnMaxCtas / kJoinThreads];
@@ -1077,25 +1063,27 @@ __global__ void __launch_bounds__(kJoinThreads, 3) hsp_attn_join_kernel(const __
 #pragma unroll
         for (int k = 0; k < 8; ++k) L += red_s[8 + k];
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int p0 = p_first; p0 < parts; p0 += 16 * kAhead) {
+        for (int p0 = p_first; p0 < parts; p0 += kRows * kAhead) {
             if (p0 != p_first) load(p0);
 #pragma unroll
             for (int k = 0; k < kAhead; ++k)
-                if (p0 + 16 * k < parts) {
-                    const float w = weight[p0 + 16 * k];
+                if (p0 + kRows * k < parts) {
+                    const float w = weight[p0 + kRows * k];
                     acc.x += w * v[k].x;
                     acc.y += w * v[k].y;
                     acc.z += w * v[k].z;
                     acc.w += w * v[k].w;
                 }
         }
-        acc.x += __shfl_xor_sync(0xffffffffu, acc.x, 16);
-        acc.y += __shfl_xor_sync(0xffffffffu, acc.y, 16);
-        acc.z += __shfl_xor_sync(0xffffffffu, acc.z, 16);
-        acc.w += __shfl_xor_sync(0xffffffffu, acc.w, 16);
-        if (half == 0) acc_s[warp][lane] = acc;
+        if (kLanes == 16) {
+            acc.x += __shfl_xor_sync(0xffffffffu, acc.x, 16);
+            acc.y += __shfl_xor_sync(0xffffffffu, acc.y, 16);
+            acc.z += __shfl_xor_sync(0xffffffffu, acc.z, 16);
+            acc.w += __shfl_xor_sync(0xffffffffu, acc.w, 16);
+        }
+        if (lane < kLanes) acc_s[warp][lane] = acc;
         __syncthreads();
-        if (warp == 0 && half == 0) {
+        if (tid < kLanes) {
 #pragma unroll
             for (int k = 1; k < 8; ++k) {
                 const float4 o = acc_s[k][lane];
@@ -1108,6 +1096,14 @@ __global__ void __launch_bounds__(kJoinThreads, 3) hsp_attn_join_kernel(const __
             if (a.lse && dp == 0 && lane == 0) store_lse(e, h, M, L);
         }
         __syncthreads();
+    };
+    // 64 columns while that leaves CTAs without any work, else 128
+    const bool wide = DV >= 128 && static_cast<int64_t>(nmany) * a.group * (DV / 128) >= gridDim.x;
+    const int pieces = wide ? DV / 128 : DV / 64, per_item = a.group * pieces;
+    for (int u = blockIdx.x; u < nmany * per_item; u += gridDim.x) {
+        const int c = many[u / per_item], rem = u % per_item, h = rem / pieces, dp = rem % pieces;
+        if (wide) join_cta(c, h, dp, JoinWidth<DV >= 128 ? 128 : 64>{});
+        else join_cta(c, h, dp, JoinWidth<64>{});
     }
     __syncthreads();
     if (tid == 0) fence_release_gpu();  // (cumulative over the barrier)
