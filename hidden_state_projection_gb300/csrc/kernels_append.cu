@@ -9,10 +9,10 @@
 // Every value is read once and written once in 16-byte pieces; products and sums in fp32, one
 // rounding to bf16.  A thread takes pieces (pairs of pieces where the pairs lie rot / 2 apart),
 // two requested before either is stored.  A CTA looks up the places of its tokens first (row and
-// position, then the page: two dependent loads, which bound the small calls): one token, its
-// pieces spread over several CTAs, while that does not fill the GPU, up to eight behind one
-// look-up and one release fence otherwise (2047 tokens of 48 heads of 128: 16.7 us with a CTA
-// per token, 51 MB).
+// position, then the page: two dependent loads, which bound the small calls).  On a GB300, graph
+// replay: 8 latent tokens with 16 query heads 2.4 us; 2047 tokens of 8 + 8 + 32 heads of 128
+// (51 MB) 15.1 us with a CTA per token and a fence per thread, 9.9 with up to eight tokens behind
+// one look-up and one fence, 8.5 with multiplications for the divisions by the rows' pieces.
 #include <cuda_bf16.h>
 #include <stdint.h>
 
@@ -47,12 +47,32 @@ __device__ __forceinline__ void turn_halves(uint32_t &a, uint32_t &b, float c0, 
     b = pack_bf16(b0 * c0 + a0 * s0, b1 * c1 + a1 * s1);
 }
 
+// n / d for n < 2^31: multiply by floor(2^(32 + s) / d) + 1, s = floor(log2 d), and shift (the
+// product is too large by at most n d <= 2^(32 + s), so the quotient is exact); a power of two
+// only shifts.
+struct FastDiv {
+    uint32_t mul, shift;
+    explicit FastDiv(int d) {
+        shift = 0;
+        while (d >> (shift + 1)) ++shift;
+        mul = (d & (d - 1)) == 0 ? 0u : static_cast<uint32_t>((1ull << (32 + shift)) / static_cast<uint32_t>(d)) + 1u;
+    }
+    __device__ __forceinline__ int operator()(int n) const {
+        return static_cast<int>(mul ? __umulhi(static_cast<uint32_t>(n), mul) >> shift : static_cast<uint32_t>(n) >> shift);
+    }
+};
+struct AppendShape {  // pieces of a token
+    int plain, per_row, per_v, nk, nv, total;
+    FastDiv by_total, by_row, by_v;
+};
+
 struct AppendPlace {
     int64_t k, v;      // element offsets of the token's line in the cache, -1: nowhere
     const float *cs;   // its angles; null: none (or outside the table)
 };
 
-__global__ void __launch_bounds__(kAppendThreads, 4) hsp_append_kernel(const __grid_constant__ AppendArgs a, int per_cta) {
+__global__ void __launch_bounds__(kAppendThreads, 4) hsp_append_kernel(const __grid_constant__ AppendArgs a, const __grid_constant__ AppendShape g,
+                                                                     int per_cta) {
     __shared__ AppendPlace places[kAppendTokens];
     griddep_wait();
     const int first = blockIdx.x * per_cta, here = min(per_cta, a.tokens - first);
@@ -78,11 +98,7 @@ __global__ void __launch_bounds__(kAppendThreads, 4) hsp_append_kernel(const __g
         places[threadIdx.x] = p;
     }
     __syncthreads();
-    const int plain = (a.k_dim - a.rot) / 8;                               // pieces of a k or q row that are copied
-    const int turned = a.rot / (a.interleaved ? 8 : 16);                   // and those that are turned
-    const int per_row = plain + turned, per_v = a.v_new ? a.v_dim / 8 : 0;
-    const int nk = a.kv_heads * per_row, nv = a.kv_heads * per_v, nq = a.q ? a.heads * per_row : 0;
-    const int total = nk + nv + nq, half = a.rot / 2;
+    const int half = a.rot / 2, total = g.total;
     const int step = gridDim.y * kAppendThreads;
     for (int e0 = blockIdx.y * kAppendThreads + threadIdx.x; e0 < total * here; e0 += 2 * step) {
         uint4 v[2], w[2];
@@ -94,12 +110,12 @@ __global__ void __launch_bounds__(kAppendThreads, 4) hsp_append_kernel(const __g
             to[u] = nullptr;
             cs[u] = nullptr;
             if (e >= total * here) continue;
-            const int tok = e / total, x = e - tok * total, i = first + tok;
+            const int tok = g.by_total(e), x = e - tok * total, i = first + tok;
             const AppendPlace p = places[tok];
             // piece t of head h of k (kind 0), v (1) or q (2)
-            const int kind = x < nk ? 0 : x < nk + nv ? 1 : 2;
-            const int r = x - (kind == 0 ? 0 : kind == 1 ? nk : nk + nv), per = kind == 1 ? per_v : per_row;
-            const int h = r / per, t = r - h * per;
+            const int kind = x < g.nk ? 0 : x < g.nk + g.nv ? 1 : 2;
+            const int r = x - (kind == 0 ? 0 : kind == 1 ? g.nk : g.nk + g.nv);
+            const int h = kind == 1 ? g.by_v(r) : g.by_row(r), t = r - h * (kind == 1 ? g.per_v : g.per_row);
             const __nv_bfloat16 *from;
             if (kind == 0) {
                 from = static_cast<const __nv_bfloat16 *>(a.k_new) + i * a.k_row + h * a.k_dim;
@@ -113,8 +129,8 @@ __global__ void __launch_bounds__(kAppendThreads, 4) hsp_append_kernel(const __g
             }
             if (!to[u]) continue;
             v[u] = *reinterpret_cast<const uint4 *>(from + t * 8);
-            if (kind != 1 && t >= plain) {
-                cs[u] = p.cs + (t - plain) * (a.interleaved ? 4 : 8);
+            if (kind != 1 && t >= g.plain) {
+                cs[u] = p.cs + (t - g.plain) * (a.interleaved ? 4 : 8);
                 if (!a.interleaved) w[u] = *reinterpret_cast<const uint4 *>(from + t * 8 + half);
             }
         }
@@ -144,14 +160,19 @@ __global__ void __launch_bounds__(kAppendThreads, 4) hsp_append_kernel(const __g
 }
 
 cudaError_t launch_append(const AppendArgs &a, int sms, int pdl, cudaStream_t stream) {
-    const int per_row = (a.k_dim - a.rot) / 8 + a.rot / (a.interleaved ? 8 : 16);
-    const int total = a.kv_heads * (per_row + (a.v_new ? a.v_dim / 8 : 0)) + (a.q ? a.heads * per_row : 0);
-    // one token per CTA and a thread per piece while the CTAs fit the GPU at once, else more tokens
-    int y = (total + kAppendThreads - 1) / kAppendThreads;
+    // pieces of a k or q row: copied ones, then turned ones (a pair of pieces each where the pairs lie apart)
+    const int plain = (a.k_dim - a.rot) / 8, per_row = plain + a.rot / (a.interleaved ? 8 : 16);
+    const int per_v = a.v_new ? a.v_dim / 8 : 0, nk = a.kv_heads * per_row, nv = a.kv_heads * per_v;
+    const int total = nk + nv + (a.q ? a.heads * per_row : 0);
+    const AppendShape g{plain, per_row, per_v, nk, nv, total, FastDiv(total), FastDiv(per_row), FastDiv(per_v > 0 ? per_v : 1)};
+    // as many CTAs as fit the GPU at once (four per SM): few tokens are spread over several CTAs each,
+    // a piece per thread at least; of many, a CTA takes up to kAppendTokens
+    const int fit = sms * 4;
+    int y = (total + kAppendThreads - 1) / kAppendThreads, per_cta = 1;
+    if (static_cast<int64_t>(a.tokens) * y > fit) y = fit / a.tokens > 1 ? fit / a.tokens : 1;
+    if (a.tokens > fit) per_cta = (a.tokens + fit - 1) / fit;
+    if (per_cta > kAppendTokens) per_cta = kAppendTokens;
     if (y > 65535) y = 65535;
-    int per_cta = 1;
-    while (per_cta < kAppendTokens && static_cast<int64_t>(a.tokens) * y > static_cast<int64_t>(sms) * 4 * per_cta) per_cta *= 2;
-    if (per_cta > 1) y = 1;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>((a.tokens + per_cta - 1) / per_cta), static_cast<unsigned>(y), 1);
     cfg.blockDim = dim3(kAppendThreads, 1, 1);
@@ -165,7 +186,7 @@ cudaError_t launch_append(const AppendArgs &a, int sms, int pdl, cudaStream_t st
     }
     cfg.attrs = attrs;
     cfg.numAttrs = n;
-    return cudaLaunchKernelEx(&cfg, hsp_append_kernel, a, per_cta);
+    return cudaLaunchKernelEx(&cfg, hsp_append_kernel, a, g, per_cta);
 }
 
 }  // namespace hsp
