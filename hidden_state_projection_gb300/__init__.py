@@ -14,6 +14,7 @@ TensorRT-LLM PR #20636 (DeepSeek-V4.1 wq_a/wkv via tinygemm2), Description.
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import os
 import struct
 from typing import List, Optional, Sequence
@@ -30,7 +31,6 @@ STATUS_NAMES = {0: "PROJ_OK", 1: "PROJ_ERR_INVALID_ARG", 2: "PROJ_ERR_UNSUPPORTE
 STATUS = {v: k for k, v in STATUS_NAMES.items()}
 MAX_SPLITS = 8
 MAX_M = 64
-UNCUT_TOKENS = 256  # PROJ_UNCUT_TOKENS
 
 EXPORTED = ("proj_fused_gemm", "proj_fused_gemm_prefetch", "proj_fused_gemm_host",
             "proj_host_plan_create", "proj_host_plan_launch", "proj_host_plan_destroy", "proj_fused_gemm_rmsnorm", "proj_rmsnorm_workspace_bytes",
@@ -419,116 +419,40 @@ def pack_check(w: torch.Tensor, w_cat: torch.Tensor, row_off: int) -> bool:
 
 # ---- the paged cache ------------------------------------------------------------
 #
-# A decode step makes a handful of these calls per layer, so the checks are written to cost
-# little: plain comparisons, packed structs, the raw stream.
+# A decode step makes a handful of these calls per layer; their tensors are checked and
+# marshalled by _lib/hsp_cache_py.so (csrc/py_cache.cpp), which calls the C ABI.
 
-_BF16, _I32, _F32 = torch.bfloat16, torch.int32, torch.float32
-
-
-_empty = torch.empty
+PY_PATH = os.path.join(_HERE, "_lib", "hsp_cache_py.so")
+_cache = None
 
 
-def _device(*tensors) -> int:
-    """Index of the CUDA device that every given tensor (None is left out) lies on: the current one."""
-    dev = tensors[0].get_device()
-    for t in tensors:
-        if t is not None and t.get_device() != dev:
-            raise ProjError(1, f"every tensor must be on the current CUDA device (one is on {t.device})")
-    if dev < 0 or dev != torch._C._cuda_getDevice():
-        raise ProjError(1, f"every tensor must be on the current CUDA device (they are on {tensors[0].device})")
-    return dev
-
-
-def _raw_stream(stream, dev: int) -> int:
-    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream_ptr(stream)
-
-
-def _ints(name: str, t: torch.Tensor, n: int) -> int:
-    """Device pointer of a dense 1-D int32 tensor of n elements."""
-    if t.dtype is not _I32 or t.shape != (n,) or (n > 1 and t.stride() != (1,)):
-        raise ProjError(1, f"{name} must be a dense 1-D int32 tensor of {n} elements")
-    return t.data_ptr()
-
-
-_pack_index = struct.Struct("PqPPiiii").pack      # proj_page_index
-_pack_kv = struct.Struct("PPiiiiqqqqqq").pack     # proj_kv_pages
-_pack_pool = struct.Struct("Pqqqii").pack         # proj_page_pool
-_pack_rotary = struct.Struct("Piiii").pack        # proj_rotary
-
-
-def _page_index(block_table, seq_lens, ref_counts, num_pages: int, page_size: int) -> bytes:
-    shape = block_table.shape
-    if block_table.dtype is not _I32 or len(shape) != 2:
-        raise ProjError(1, "block_table must be a 2-D int32 tensor with dense rows")
-    rows, width = shape
-    st, one = block_table.stride()
-    if one != 1 and width > 1:
-        raise ProjError(1, "block_table must be a 2-D int32 tensor with dense rows")
-    return _pack_index(block_table.data_ptr(), st if rows > 1 else max(st, width), _ints("seq_lens", seq_lens, rows),
-                       0 if ref_counts is None else _ints("ref_counts", ref_counts, num_pages), rows, width, num_pages,
-                       page_size)
-
-
-def _kv_pages(k_pages: torch.Tensor, v_pages: Optional[torch.Tensor], v_dim: Optional[int]):
-    """(packed proj_kv_pages, shape of the keys, columns of the values)"""
-    shape = k_pages.shape
-    if len(shape) != 4 or k_pages.stride(3) != 1:
-        raise ProjError(1, "k_pages must be a [num_pages, page_size, kv_heads, k_dim] tensor with dense columns")
-    sp, st, sh, _ = k_pages.stride()
-    if k_pages.dtype is not _BF16 or (v_pages is not None and v_pages.dtype is not _BF16):
-        raise ProjError(4, "the cache holds bf16")
-    if v_pages is None:
-        dv = 512 if v_dim is None else int(v_dim)
-        return _pack_kv(k_pages.data_ptr(), 0, shape[2], shape[3], dv, 0, sp, st, sh, 0, 0, 0), shape, dv
-    if v_pages.dim() != 4 or v_pages.stride(3) != 1 or v_pages.shape[:3] != shape[:3]:
-        raise ProjError(1, "v_pages must be a [num_pages, page_size, kv_heads, v_dim] tensor like k_pages")
-    dv = v_pages.shape[3]
-    if v_dim is not None and int(v_dim) != dv:
-        raise ProjError(1, f"v_dim={v_dim}, but v_pages has {dv} columns")
-    vp, vt, vh, _ = v_pages.stride()
-    return _pack_kv(k_pages.data_ptr(), v_pages.data_ptr(), shape[2], shape[3], dv, 0, sp, st, sh, vp, vt, vh), shape, dv
-
-
-def _pools(pools: Sequence[torch.Tensor], num_pages: Optional[int]):
-    packed = []
-    for t in pools:
-        shape = t.shape
-        if len(shape) < 3 or (num_pages is not None and shape[1] != num_pages):
-            raise ProjError(1, "a pool is a [layers, num_pages, ...] tensor")
-        num_pages, strides, e = shape[1], t.stride(), t.element_size()
-        want = 1
-        for d in range(len(shape) - 1, 1, -1):
-            if shape[d] != 1 and strides[d] != want:
-                raise ProjError(1, "the pages of a pool must be dense")
-            want *= shape[d]
-        page = want * e
-        packed.append(_pack_pool(t.data_ptr(), strides[0] * e if shape[0] > 1 else page, strides[1] * e if num_pages > 1 else page,
-                                 page, shape[0], 0))
-    return b"".join(packed), num_pages
+def _cache_py():
+    """Load hsp_cache_py.so (raises if it has not been built)."""
+    global _cache
+    if _cache is None:
+        lib()  # first: the module is linked to the same libhsp_proj.so
+        if not os.path.exists(PY_PATH):
+            raise RuntimeError(f"{PY_PATH} is missing: build it first (python -m hidden_state_projection_gb300.build)")
+        spec = importlib.util.spec_from_file_location("hsp_cache_py", PY_PATH)
+        module = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(module)
+        module.set_error(ProjError)
+        _cache = module
+    return _cache
 
 
 def _made(t: torch.Tensor, stream) -> torch.Tensor:
     """A tensor allocated on the current stream for use on `stream`: its memory is not used before the current
     stream has left it, nor given away before `stream` has."""
-    if stream is not None:
-        s = torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream
-        if s.cuda_stream != torch.cuda.current_stream().cuda_stream:
-            s.wait_stream(torch.cuda.current_stream())
-            t.record_stream(s)
+    s = torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream
+    if s.cuda_stream != torch.cuda.current_stream().cuda_stream:
+        s.wait_stream(torch.cuda.current_stream())
+        t.record_stream(s)
     return t
 
 
-def _work(t: Optional[torch.Tensor], need: int, dev: int, stream) -> torch.Tensor:
-    """The caller's workspace, or one from torch for this call."""
-    if t is None:
-        t = _empty(need, dtype=torch.uint8, device=dev)
-        return t if stream is None else _made(t, stream)
-    if not t.is_contiguous():
-        raise ProjError(1, "workspace must be dense")
-    return t
-
-
-_attn_workspace = {}  # bytes by shape and device: the library's answer depends on nothing else
+def _new(like: torch.Tensor, shape, dtype, stream) -> torch.Tensor:
+    return _made(torch.empty(shape, dtype=dtype, device=like.device), stream)
 
 
 def paged_attention_workspace_bytes(heads: int, kv_heads: int, k_dim: int, v_dim: int, latent: bool) -> int:
@@ -548,61 +472,19 @@ def paged_attention(q: torch.Tensor, k_pages: torch.Tensor, v_pages: Optional[to
     cache, the values are the first v_dim = 512 columns of the keys); block_table [rows, max_pages] and seq_lens
     [rows] int32; `rows` maps batch entries to table rows.  Returns out [batch, heads, v_dim], or (out, lse) with
     return_lse.  `workspace` (paged_attention_workspace_bytes) is taken from torch per call if not given."""
-    dev = _device(q, k_pages, v_pages, block_table, seq_lens, rows, out, lse, workspace)
-    kv, kshape, dv = _kv_pages(k_pages, v_pages, v_dim)
-    pages, page, kv_heads, k_dim = kshape
-    shape = q.shape
-    if len(shape) != 3 or shape[2] != k_dim or q.stride(2) != 1:
-        raise ProjError(1, "q must be a [batch, heads, k_dim] tensor with dense columns")
-    if q.dtype is not _BF16:
-        raise ProjError(4, f"unsupported tensor dtype {q.dtype}")
-    batch, heads, _ = shape
-    index = _page_index(block_table, seq_lens, None, pages, page)
-    if out is None:
-        out = _empty((batch, heads, dv), dtype=_BF16, device=dev)
-        if stream is not None:
-            _made(out, stream)
-    elif out.shape != (batch, heads, dv) or out.dtype is not _BF16 or not out.is_contiguous():
-        raise ProjError(1, f"out must be a dense [{batch}, {heads}, {dv}] {q.dtype} tensor")
-    lse_ptr = None
-    if lse is not None:
-        if lse.shape != (batch, heads) or lse.dtype is not _F32 or not lse.is_contiguous():
-            raise ProjError(1, f"lse must be a dense [{batch}, {heads}] float32 tensor")
-        lse_ptr = lse.data_ptr()
-    elif return_lse:
-        lse = _empty((batch, heads), dtype=_F32, device=dev)
-        if stream is not None:
-            _made(lse, stream)
-        lse_ptr = lse.data_ptr()
-    ws_ptr, ws_bytes = None, 0
-    if workspace is not None or block_table.shape[1] * page > UNCUT_TOKENS:
+    if stream is not None:
+        batch, heads, k_dim = q.shape
+        dv = v_pages.shape[3] if v_pages is not None else 512 if v_dim is None else v_dim
+        if out is None:
+            out = _new(q, (batch, heads, dv), torch.bfloat16, stream)
+        if lse is None and return_lse:
+            lse = _new(q, (batch, heads), torch.float32, stream)
         if workspace is None:
-            key = (heads, kv_heads, k_dim, dv, v_pages is None, dev)
-            need = _attn_workspace.get(key)
-            if need is None:
-                need = _attn_workspace[key] = paged_attention_workspace_bytes(heads, kv_heads, k_dim, dv, v_pages is None)
-            workspace = _work(None, need, dev, stream)
-        elif not workspace.is_contiguous():
-            raise ProjError(1, "workspace must be dense")
-        ws_ptr, ws_bytes = workspace.data_ptr(), workspace.nbytes
-    qb, qh, _ = q.stride()
-    rc = (_lib or lib()).proj_paged_attention(q.data_ptr(), qb, qh, kv, index, None if rows is None else _ints("rows", rows, batch),
-                                              batch, heads, scale, out.data_ptr(), lse_ptr, ws_ptr, ws_bytes,
-                                              _raw_stream(stream, dev))
-    if rc != 0:
-        _check(rc)
-    return (out, lse) if return_lse else out
-
-
-def _new_rows(name: str, t: torch.Tensor, tokens: int, heads: int, dim: int):
-    """(pointer, token stride) of the new rows of a cache: [tokens, heads, dim] or [tokens, heads * dim]."""
-    if t.dtype is not _BF16:
-        raise ProjError(4, f"unsupported tensor dtype {t.dtype}")
-    shape, st = t.shape, t.stride()
-    if not (len(shape) == 2 and shape == (tokens, heads * dim) and st[1] == 1) and \
-            not (len(shape) == 3 and shape == (tokens, heads, dim) and st[2] == 1 and (heads == 1 or st[1] == dim)):
-        raise ProjError(1, f"{name} must be [tokens, {heads}, {dim}] with dense tokens")
-    return t.data_ptr(), st[0] if tokens > 1 else heads * dim
+            workspace = _new(q, paged_attention_workspace_bytes(heads, k_pages.shape[2], k_dim, dv, v_pages is None),
+                             torch.uint8, stream)
+        stream = _stream_ptr(stream)
+    return (_cache or _cache_py()).paged_attention(q, k_pages, v_pages, block_table, seq_lens, scale, -1 if v_dim is None else v_dim,
+                                                   rows, out, lse, return_lse, workspace, stream)
 
 
 def cache_append(k_new: torch.Tensor, v_new: Optional[torch.Tensor], k_pages: torch.Tensor, v_pages: Optional[torch.Tensor],
@@ -612,63 +494,22 @@ def cache_append(k_new: torch.Tensor, v_new: Optional[torch.Tensor], k_pages: to
     """The new tokens' keys [tokens, (kv_heads,) k_dim] and values into their pages, at positions[i] of row rows[i]
     (default: the last place of row i).  cos_sin [max_pos, rot] fp32 turns the last `rot` columns of the keys and
     of the queries q [tokens, heads, k_dim] on the way; returns the turned queries (q_out; may be q), or None."""
-    dev = _device(k_new, v_new, k_pages, v_pages, block_table, seq_lens, rows, positions, cos_sin, q, q_out)
-    kv, kshape, dv = _kv_pages(k_pages, v_pages, None)
-    tokens, k_dim = k_new.shape[0], kshape[3]
-    if (v_new is None) != (v_pages is None):
-        raise ProjError(1, "v_new goes with a cache that has values of its own")
-    kp, ks = _new_rows("k_new", k_new, tokens, kshape[2], k_dim)
-    vp, vs = (None, 0) if v_new is None else _new_rows("v_new", v_new, tokens, kshape[2], dv)
-    index = _page_index(block_table, seq_lens, None, kshape[0], kshape[1])
-    rot = None
-    if cos_sin is not None:
-        if cos_sin.dtype is not _F32 or cos_sin.dim() != 2 or not cos_sin.is_contiguous():
-            raise ProjError(1, "cos_sin must be a dense [max_pos, rot] float32 tensor")
-        most, dim = cos_sin.shape
-        rot = _pack_rotary(cos_sin.data_ptr(), most, dim, 1 if interleaved else 0, 0)
-    heads, qp, qs, qh, op, os_, oh = 0, None, 0, 0, None, 0, 0
-    if q is not None:
-        if q_out is None:
-            q_out = _made(torch.empty(q.shape, dtype=q.dtype, device=dev), stream)
-        shape = q.shape
-        if len(shape) != 3 or shape[0] != tokens or shape[2] != k_dim or q_out.shape != shape:
-            raise ProjError(1, f"q and q_out must be [tokens, heads, {k_dim}] with dense columns")
-        if q.dtype is not _BF16 or q_out.dtype is not _BF16:
-            raise ProjError(4, f"unsupported tensor dtype {q.dtype}, {q_out.dtype}")
-        heads = shape[1]
-        qs, qh, one = q.stride()
-        os_, oh, two = q_out.stride()
-        if one != 1 or two != 1:
-            raise ProjError(1, f"q and q_out must be [tokens, heads, {k_dim}] with dense columns")
-        qp, op = q.data_ptr(), q_out.data_ptr()
-    rc = (_lib or lib()).proj_cache_append(kp, ks, vp, vs, kv, index, None if rows is None else _ints("rows", rows, tokens),
-                                 None if positions is None else _ints("positions", positions, tokens), tokens, rot, qp, qs, qh,
-                                 op, os_, oh, heads, _raw_stream(stream, dev))
-    if rc != 0:
-        _check(rc)
-    return q_out if q is not None else None
+    if stream is not None:
+        if q is not None and q_out is None:
+            q_out = _new(q, q.shape, torch.bfloat16, stream)
+        stream = _stream_ptr(stream)
+    return (_cache or _cache_py()).cache_append(k_new, v_new, k_pages, v_pages, block_table, seq_lens, rows, positions, cos_sin,
+                                                interleaved, q, q_out, stream)
 
 
 def cache_workspace_bytes(block_table: torch.Tensor, num_pages: int, n: int) -> int:
     """Workspace bytes of cache_resize over n rows (cache_compact: n = 0)."""
     rows, width = block_table.shape
-    return _cache_need(_pack_index(16, width, 16, 16, rows, width, num_pages, 16), n)
-
-
-def _cache_need(index: bytes, n: int) -> int:
-    need = (_lib or lib()).proj_cache_workspace_bytes(index, n)
+    index = struct.pack("PqPPiiii", 16, width, 16, 16, rows, width, num_pages, 16)  # a proj_page_index of these sizes
+    need = int(lib().proj_cache_workspace_bytes(index, n))
     if need == 0:
         raise ProjError(2, lib().proj_last_error_string().decode())
     return need
-
-
-def _result(name: str, t: Optional[torch.Tensor], n: int, dev: int, stream) -> torch.Tensor:
-    """The caller's int32 output of n elements, or a new one."""
-    if t is None:
-        t = _empty(n, dtype=_I32, device=dev)
-        return t if stream is None else _made(t, stream)
-    _ints(name, t, n)
-    return t
 
 
 def cache_resize(block_table: torch.Tensor, seq_lens: torch.Tensor, ref_counts: torch.Tensor, rows: torch.Tensor,
@@ -677,31 +518,25 @@ def cache_resize(block_table: torch.Tensor, seq_lens: torch.Tensor, ref_counts: 
     """Rows get new lengths: growing takes the lowest free pages (and a private copy of a shared, partly filled last
     page, over all pools [layers, num_pages, ...]), shrinking gives pages back, 0 frees the row.  Returns the status
     per row: 0 done, 1 not enough free pages, 2 refused."""
-    dev = _device(block_table, seq_lens, ref_counts, rows, new_lens, status, workspace, *pools)
-    packed, num_pages = _pools(pools, ref_counts.shape[0])
-    index = _page_index(block_table, seq_lens, ref_counts, num_pages, page_size)
-    n = rows.shape[0]
-    status = _result("status", status, n, dev, stream)
-    workspace = _work(workspace, _cache_need(index, n) if workspace is None else 0, dev, stream)
-    rc = (_lib or lib()).proj_cache_resize(index, _ints("rows", rows, n), _ints("new_lens", new_lens, n), n, packed, len(pools),
-                                 status.data_ptr(), workspace.data_ptr(), workspace.nbytes, _raw_stream(stream, dev))
-    if rc != 0:
-        _check(rc)
-    return status
+    if stream is not None:
+        n = rows.shape[0]
+        if status is None:
+            status = _new(rows, n, torch.int32, stream)
+        if workspace is None:
+            workspace = _new(rows, cache_workspace_bytes(block_table, ref_counts.shape[0], n), torch.uint8, stream)
+        stream = _stream_ptr(stream)
+    return (_cache or _cache_py()).cache_resize(block_table, seq_lens, ref_counts, rows, new_lens, page_size, pools, status,
+                                                workspace, stream)
 
 
 def cache_fork(block_table: torch.Tensor, seq_lens: torch.Tensor, ref_counts: torch.Tensor, parents: torch.Tensor,
                children: torch.Tensor, page_size: int, status: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """children[i], an empty row, shares every page of parents[i].  Returns the status per child: 0 done, 2 refused."""
-    dev = _device(block_table, seq_lens, ref_counts, parents, children, status)
-    index = _page_index(block_table, seq_lens, ref_counts, ref_counts.shape[0], page_size)
-    n = parents.shape[0]
-    status = _result("status", status, n, dev, stream)
-    rc = (_lib or lib()).proj_cache_fork(index, _ints("parents", parents, n), _ints("children", children, n), n, status.data_ptr(),
-                               _raw_stream(stream, dev))
-    if rc != 0:
-        _check(rc)
-    return status
+    if stream is not None:
+        if status is None:
+            status = _new(parents, parents.shape[0], torch.int32, stream)
+        stream = _stream_ptr(stream)
+    return (_cache or _cache_py()).cache_fork(block_table, seq_lens, ref_counts, parents, children, page_size, status, stream)
 
 
 def cache_compact(block_table: torch.Tensor, seq_lens: torch.Tensor, ref_counts: torch.Tensor, page_size: int,
@@ -709,31 +544,23 @@ def cache_compact(block_table: torch.Tensor, seq_lens: torch.Tensor, ref_counts:
                   workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """Moves the live pages into the first places of the pools; tables and counts follow.  Returns `live` [1], the
     number of live pages."""
-    dev = _device(block_table, seq_lens, ref_counts, live, workspace, *pools)
-    packed, num_pages = _pools(pools, ref_counts.shape[0])
-    index = _page_index(block_table, seq_lens, ref_counts, num_pages, page_size)
-    live = _result("live", live, 1, dev, stream)
-    workspace = _work(workspace, _cache_need(index, 0) if workspace is None else 0, dev, stream)
-    rc = (_lib or lib()).proj_cache_compact(index, packed, len(pools), live.data_ptr(), workspace.data_ptr(), workspace.nbytes,
-                                  _raw_stream(stream, dev))
-    if rc != 0:
-        _check(rc)
-    return live
+    if stream is not None:
+        if live is None:
+            live = _new(ref_counts, 1, torch.int32, stream)
+        if workspace is None:
+            workspace = _new(ref_counts, cache_workspace_bytes(block_table, ref_counts.shape[0], 0), torch.uint8, stream)
+        stream = _stream_ptr(stream)
+    return (_cache or _cache_py()).cache_compact(block_table, seq_lens, ref_counts, page_size, pools, live, workspace, stream)
 
 
 def cache_copy_pages(pools: Sequence[torch.Tensor], src, dst, stream=None) -> None:
     """Copies page src[i] to page dst[i] in every layer of every pool [layers, num_pages, ...].  src and dst live on
     the host (CPU int32 tensors or sequences of ints); destinations differ and are no sources of the call."""
-    dev = _device(*pools)
-    packed, num_pages = _pools(pools, None)
-    src, dst = (t if isinstance(t, torch.Tensor) else torch.tensor(t, dtype=_I32) for t in (src, dst))
-    if src.is_cuda or dst.is_cuda:
-        raise ProjError(1, "src and dst must be on the host")
-    n = src.shape[0]
-    rc = (_lib or lib()).proj_cache_copy_pages(packed, len(pools), num_pages, _ints("src", src, n), _ints("dst", dst, n), n,
-                                     _raw_stream(stream, dev))
-    if rc != 0:
-        _check(rc)
+    if not isinstance(src, torch.Tensor):
+        src = torch.tensor(src, dtype=torch.int32)
+    if not isinstance(dst, torch.Tensor):
+        dst = torch.tensor(dst, dtype=torch.int32)
+    (_cache or _cache_py()).cache_copy_pages(pools, src, dst, None if stream is None else _stream_ptr(stream))
 
 
 def supported(M: int, K: int, n_total: int, dtype: int) -> bool:
