@@ -371,13 +371,24 @@ __global__ void __launch_bounds__(kAttnThreads, attn_ctas_per_sm(KB, SHARED, N))
         tmem_alloc(smem_u32(tmem_slot), C::kTmemCols);
         tmem_relinquish();
     }
+    tc_fence_before_sync();
+    __syncthreads();
+    tc_fence_after_sync();
     griddep_wait();  // everything read below may come from the previous kernel
 
     // ---- the line: its length, and where this CTA's first unit lies ----
+    // Up to 128 sequences: every warp for itself (no thread waits for another warp); more: the CTA.
     AttnLine ln;
+    ln.total = ln.x1 = static_cast<uint32_t>(a.batch) * a.kv_heads;  // uncut: the items
+    ln.x0 = cta;
+    ln.ctas = a.ctas;
+    ln.base = 0;
+    ln.b0 = ln.len0 = 0;
     if (a.split) {
-        const int per = (a.batch + kAttnThreads - 1) / kAttnThreads;
-        const int bfirst = min(a.batch, tid * per), blast = min(a.batch, bfirst + per);
+        const bool by_warp = a.batch <= 128;
+        const int tn = by_warp ? 32 : kAttnThreads, tno = by_warp ? lane : tid;
+        const int per = (a.batch + tn - 1) / tn;
+        const int bfirst = min(a.batch, tno * per), blast = min(a.batch, bfirst + per);
         uint32_t mine = 0;
         int len = 0;
         for (int b = bfirst; b < blast; ++b) {
@@ -390,52 +401,61 @@ __global__ void __launch_bounds__(kAttnThreads, attn_ctas_per_sm(KB, SHARED, N))
             const uint32_t o = __shfl_up_sync(0xffffffffu, incl, d);
             if (lane >= d) incl += o;
         }
-        if (lane == 31) warp_sum[warp] = static_cast<int>(incl);
-        __syncthreads();
-        uint32_t before = incl - mine, all = 0;
+        uint32_t before = incl - mine, all = __shfl_sync(0xffffffffu, incl, 31);
+        if (!by_warp) {
+            if (lane == 31) warp_sum[warp] = static_cast<int>(incl);
+            __syncthreads();
+            all = 0;
 #pragma unroll
-        for (int w = 0; w < kAttnThreads / 32; ++w) {
-            if (w < warp) before += warp_sum[w];
-            all += warp_sum[w];
+            for (int w = 0; w < kAttnThreads / 32; ++w) {
+                if (w < warp) before += warp_sum[w];
+                all += warp_sum[w];
+            }
         }
         ln.total = all * a.kv_heads;
         ln.ctas = min(ln.total, static_cast<uint32_t>(a.ctas));
         ln.x0 = ln.x1 = 0;
+        bool here = false;  // this thread's sequences hold the CTA's first unit
+        uint32_t first = before * a.kv_heads;
+        int b = bfirst;
         if (cta < ln.ctas) {
             ln.x0 = line_start(ln.total, cta, ln.ctas);
             ln.x1 = line_start(ln.total, cta + 1, ln.ctas);
-            uint32_t first = before * a.kv_heads;
-            if (ln.x0 >= first && ln.x0 < first + mine * a.kv_heads) {
-                int b = bfirst;
-                if (per > 1) {  // walk to the sequence
-                    for (;; ++b) {
-                        len = attn_len(a, b);
-                        const uint32_t units = len > 0 ? (attn_tiles(len) + a.weight) * a.kv_heads : 0;
-                        if (ln.x0 < first + units || b + 1 >= blast) break;
-                        first += units;
-                    }
+            here = ln.x0 >= first && ln.x0 < first + mine * a.kv_heads;
+        }
+        if (here) {
+            if (per > 1) {  // walk to the sequence
+                for (;; ++b) {
+                    len = attn_len(a, b);
+                    const uint32_t units = len > 0 ? (attn_tiles(len) + a.weight) * a.kv_heads : 0;
+                    if (ln.x0 < first + units || b + 1 >= blast) break;
+                    first += units;
                 }
+            }
+            // its first page id, on its way before the copy producer asks for it
+            const uint32_t units = attn_tiles(len) + a.weight;
+            const uint32_t t = (ln.x0 - first) % units;
+            const int64_t page = (static_cast<int64_t>(max(0, static_cast<int>(t) - a.weight)) * kAttnTile) >> a.page_shift;
+            prefetch_l1(a.table + (a.rows ? a.rows[b] : b) * a.table_stride + page);
+        }
+        if (by_warp) {
+            const uint32_t who = __ballot_sync(0xffffffffu, here);
+            const int from = who ? __ffs(who) - 1 : 0;
+            ln.b0 = __shfl_sync(0xffffffffu, b, from);
+            ln.base = __shfl_sync(0xffffffffu, first, from);
+            ln.len0 = __shfl_sync(0xffffffffu, len, from);
+        } else {
+            if (here) {
                 place[0] = b;
                 place[1] = static_cast<int>(first);
                 place[2] = len;
-                // its first page id, on its way before the copy producer asks for it
-                const uint32_t units = attn_tiles(len) + a.weight;
-                const uint32_t t = (ln.x0 - first) % units;
-                const int64_t page = (static_cast<int64_t>(max(0, static_cast<int>(t) - a.weight)) * kAttnTile) >> a.page_shift;
-                prefetch_l1(a.table + (a.rows ? a.rows[b] : b) * a.table_stride + page);
             }
+            __syncthreads();
+            ln.b0 = place[0];
+            ln.base = static_cast<uint32_t>(place[1]);
+            ln.len0 = place[2];
         }
-    } else {
-        ln.total = ln.x1 = static_cast<uint32_t>(a.batch) * a.kv_heads;
-        ln.x0 = cta;
-        ln.ctas = a.ctas;
     }
-    tc_fence_before_sync();
-    __syncthreads();
-    tc_fence_after_sync();
-    ln.b0 = place[0];
-    ln.base = place[1];
-    ln.len0 = place[2];
     const uint32_t tmem = *tmem_slot;
     const uint32_t tmem_s = tmem + C::kOT * N;
 
