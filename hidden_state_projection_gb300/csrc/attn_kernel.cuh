@@ -874,7 +874,8 @@ __global__ void __launch_bounds__(kAttnThreads, attn_ctas_per_sm(KB, SHARED, N))
             if (attn_len(a, e) != 0) continue;
             for (int kv = 0; kv < a.kv_heads; ++kv) {
                 const int64_t h = static_cast<int64_t>(e) * all_heads + kv * a.group + head0;
-                for (int c = tid; c < nheads * kDV; c += 128) out[h * kDV + c] = __float2bfloat16_rn(0.f);
+                uint4 *to = reinterpret_cast<uint4 *>(out + h * kDV);  // (its heads lie one after another)
+                for (int c = tid; c < nheads * kDV / 8; c += 128) to[c] = make_uint4(0, 0, 0, 0);
                 if (a.lse)
                     for (int c = tid; c < nheads; c += 128) a.lse[h + c] = -INFINITY;
             }

@@ -202,7 +202,8 @@ proj_status proj_paged_attention(const void *q, int64_t q_row_stride, int64_t q_
     AttnShape s;
     if ((st = attn_shape(heads, kv->kv_heads, kv->k_dim, kv->v_dim, kv->v == nullptr, &s)) != PROJ_OK) return st;
     if (batch < 0) return api_fail(PROJ_ERR_INVALID_ARG, "batch=%d is negative", batch);
-    if (!std::isfinite(scale)) return api_fail(PROJ_ERR_INVALID_ARG, "scale must be finite");
+    const float scale_log2 = scale * 1.4426950408889634f;  // log2(e)
+    if (!std::isfinite(scale_log2)) return api_fail(PROJ_ERR_INVALID_ARG, "scale (times log2 e) must be finite");
     // (units of the line fit 30 bits)
     const int64_t most_tiles = (static_cast<int64_t>(index->max_pages) * index->page_size + hsp::kAttnTile - 1) / hsp::kAttnTile;
     if (static_cast<int64_t>(batch) * kv->kv_heads * (most_tiles + s.weight) >= (int64_t(1) << 30))
@@ -277,7 +278,7 @@ proj_status proj_paged_attention(const void *q, int64_t q_row_stride, int64_t q_
     a.split = split ? 1 : 0;
     a.weight = s.weight;
     a.slots = s.slots;
-    a.scale_log2 = scale * 1.4426950408889634f;
+    a.scale_log2 = scale_log2;
     a.out = out;
     a.lse = lse;
     if (split) {

@@ -149,6 +149,19 @@ def test_many_short_sequences_are_not_cut(hsp, latent):
 
 
 @pytest.mark.parametrize("latent", [True, False])
+def test_a_padded_batch(hsp, latent):
+    """A batch padded with empty sequences, before, between and behind the others: zeros there, and the others as
+    without them (the CTAs and their cuts are the same)."""
+    dk, dv, kv = (576, 512, 1) if latent else (128, 128, 2)
+    q, k, v, table, lens = make([900, 0, 77] + [0] * 250 + [1500], 16, kv, dk, latent, 64, 23)
+    out, lse = check(hsp, (q, k, v, table, lens), 0.07, dv)
+    assert (out[lens == 0] == 0).all() and torch.isneginf(lse[lens == 0]).all()
+    rows = torch.tensor([0, 2, 253], dtype=torch.int32, device="cuda")
+    packed = hsp.paged_attention(q[rows.long()], k, v, table, lens, 0.07, rows=rows)
+    assert torch.equal(packed, out[rows.long()])
+
+
+@pytest.mark.parametrize("latent", [True, False])
 def test_a_cache_past_four_gigabytes(hsp, latent):
     """Pages whose offsets do not fit 32 bits, neither in bytes nor in elements."""
     dk, dv, kv, heads, page = (576, 512, 1, 16, 64) if latent else (128, 128, 4, 8, 64)

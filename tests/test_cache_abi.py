@@ -39,7 +39,7 @@ def test_attention_refusals(hsp):
     S, n = hsp.STATUS, hsp.launch_count()
     bad = S["PROJ_ERR_INVALID_ARG"], S["PROJ_ERR_UNSUPPORTED_SHAPE"], S["PROJ_ERR_MISALIGNED"]
     for kw, want in [(dict(q=None), 0), (dict(out=None), 0), (dict(batch=-1), 0), (dict(heads=0), 0), (dict(scale=float("nan")), 0),
-                     (dict(scale=float("inf")), 0), (dict(batch=5), 0), (dict(kvp=kv(k=0)), 0), (dict(ix=index(table=0)), 0),
+                     (dict(scale=float("inf")), 0), (dict(scale=3e38), 0), (dict(batch=5), 0), (dict(kvp=kv(k=0)), 0), (dict(ix=index(table=0)), 0),
                      (dict(ix=index(lens=0)), 0), (dict(ix=index(rows=-1)), 0), (dict(ix=index(stride=7)), 0),
                      (dict(kvp=kv(dk=575)), 1), (dict(kvp=kv(dk=640)), 1), (dict(kvp=kv(dv=576)), 1), (dict(kvp=kv(dk=128, dv=128)), 1),
                      (dict(kvp=kv(v=A, vs=(36864, 576, 576))), 1), (dict(kvp=kv(heads=3)), 1), (dict(heads=70000), 1),
