@@ -916,7 +916,7 @@ __global__ void __launch_bounds__(kAttnThreads, attn_ctas_per_sm(KB, SHARED, N))
 // or warps take the parts in turn and their sums are added in a fixed order.  Which of the two depends on
 // the lengths only.
 
-constexpr int kJoinThreads = 256;
+constexpr int kJoinThreads = 128, kJoinWarps = kJoinThreads / 32, kJoinPerSm = 4;
 constexpr int kJoinWarpParts = 32;  // most parts of a head that one warp joins
 
 template <int W>
@@ -925,11 +925,11 @@ struct JoinWidth {
 };
 
 template <int DV, int N>
-__global__ void __launch_bounds__(kJoinThreads, 2) hsp_attn_join_kernel(const __grid_constant__ AttnArgs a) {
+__global__ void __launch_bounds__(kJoinThreads, kJoinPerSm) hsp_attn_join_kernel(const __grid_constant__ AttnArgs a) {
     constexpr int kParts = DV / 64;             // units of 64 columns of a head with many parts
     constexpr int kPart = N * DV + 2 * N;       // floats of one partial
-    __shared__ float4 acc_s[8][32];
-    __shared__ float weight[kAttnMaxCtas], red_s[16];
+    __shared__ float4 acc_s[kJoinWarps][32];
+    __shared__ float weight[kAttnMaxCtas], red_s[2 * kJoinWarps];
     __shared__ uint16_t few[kAttnMaxCtas], many[kAttnMaxCtas];  // the CTAs that began them
     __shared__ AttnEntry entries[kAttnMaxCtas];
     __shared__ uint32_t bits[2][kAttnMaxCtas / 32];
@@ -967,7 +967,7 @@ __global__ void __launch_bounds__(kJoinThreads, 2) hsp_attn_join_kernel(const __
     int nfew = 0, nmany = 0;
     for (int w = 0; w * 32 < a.ctas; ++w) {
         const uint32_t f = bits[0][w], m = bits[1][w] & ~f;
-        if (warp == (w & 7)) {
+        if (warp == w % kJoinWarps) {
             const uint32_t low = (1u << lane) - 1u;
             if ((f >> lane) & 1u) few[nfew + __popc(f & low)] = static_cast<uint16_t>(w * 32 + lane);
             if ((m >> lane) & 1u) many[nmany + __popc(m & low)] = static_cast<uint16_t>(w * 32 + lane);
@@ -996,7 +996,7 @@ __global__ void __launch_bounds__(kJoinThreads, 2) hsp_attn_join_kernel(const __
     };
     // few parts: a warp takes a head, all of its columns
     constexpr int kVec = DV >= 128 ? DV / 128 : 1;  // float4 per lane and part
-    for (int u = blockIdx.x * 8 + warp; u < nfew * a.group; u += gridDim.x * 8) {
+    for (int u = blockIdx.x * kJoinWarps + warp; u < nfew * a.group; u += gridDim.x * kJoinWarps) {
         const int c = few[u / a.group], h = u % a.group, col = h % N;
         const AttnEntry e = entries[c];
         const int parts = min(e.last, a.ctas - 1) - c + 1;
@@ -1082,7 +1082,7 @@ __global__ void __launch_bounds__(kJoinThreads, 2) hsp_attn_join_kernel(const __
         if (lane == 0) red_s[warp] = M;
         __syncthreads();
 #pragma unroll
-        for (int k = 0; k < 8; ++k) M = fmaxf(M, red_s[k]);
+        for (int k = 0; k < kJoinWarps; ++k) M = fmaxf(M, red_s[k]);
         float L = 0.f;
 #pragma unroll
         for (int k = 0; k < kAttnMaxCtas / kJoinThreads; ++k) {
@@ -1093,11 +1093,11 @@ __global__ void __launch_bounds__(kJoinThreads, 2) hsp_attn_join_kernel(const __
         }
 #pragma unroll
         for (int d = 16; d > 0; d >>= 1) L += __shfl_xor_sync(0xffffffffu, L, d);
-        if (lane == 0) red_s[8 + warp] = L;
+        if (lane == 0) red_s[kJoinWarps + warp] = L;
         __syncthreads();
         L = 0.f;
 #pragma unroll
-        for (int k = 0; k < 8; ++k) L += red_s[8 + k];
+        for (int k = 0; k < kJoinWarps; ++k) L += red_s[kJoinWarps + k];
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
         for (int p0 = p_first; p0 < parts; p0 += kRows * kAhead) {
             if (p0 != p_first) load(p0);
@@ -1121,7 +1121,7 @@ __global__ void __launch_bounds__(kJoinThreads, 2) hsp_attn_join_kernel(const __
         __syncthreads();
         if (tid < kLanes) {
 #pragma unroll
-            for (int k = 1; k < 8; ++k) {
+            for (int k = 1; k < kJoinWarps; ++k) {
                 const float4 o = acc_s[k][lane];
                 acc.x += o.x;
                 acc.y += o.y;

@@ -38,7 +38,7 @@ cudaError_t launch_attn_variant(const AttnLaunchReq &r) {
     cfg.numAttrs = n;
     e = cudaLaunchKernelEx(&cfg, kern, r.tmap_q, r.tmap_k, r.tmap_v, r.args);
     if (e != cudaSuccess || !r.args.split) return e;
-    cfg.gridDim = dim3(static_cast<unsigned>(r.join_ctas), 1, 1);
+    cfg.gridDim = dim3(static_cast<unsigned>(r.sms * kJoinPerSm), 1, 1);
     cfg.blockDim = dim3(kJoinThreads, 1, 1);
     cfg.dynamicSmemBytes = 0;
     return cudaLaunchKernelEx(&cfg, hsp_attn_join_kernel<VB * 64, N>, r.args);

@@ -260,7 +260,7 @@ proj_status proj_paged_attention(const void *q, int64_t q_row_stride, int64_t q_
     r.head_tiles = s.head_tiles;
     r.smem_bytes = s.smem;
     r.pdl = opt.pdl;
-    r.join_ctas = dev.sms * 2;
+    r.sms = dev.sms;
     r.stream = reinterpret_cast<cudaStream_t>(stream);
     hsp::AttnArgs &a = r.args;
     a.table = index->block_table;

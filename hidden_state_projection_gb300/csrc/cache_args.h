@@ -10,7 +10,7 @@ namespace hsp {
 constexpr int kDeviceErrIndex = 8;  // same value as PROJ_ERR_BAD_INDEX
 
 constexpr int kAttnTile = 64;       // tokens per tile
-constexpr int kAttnMaxCtas = 1024; // CTAs along the length (the join lists them in shared memory)
+constexpr int kAttnMaxCtas = 512;  // CTAs along the length (the join lists them in shared memory)
 constexpr int kAttnThreads = 224;   // four softmax warps, the copy producer, the issuers of S^T and of O^T
 
 // One sequence part that a CTA began and another one finishes: what the join adds up.
@@ -49,7 +49,7 @@ struct AttnLaunchReq {
     int head_tiles;              // grid.x
     int smem_bytes;
     int pdl;
-    int join_ctas;
+    int sms;
     cudaStream_t stream;
     CUtensorMap tmap_q;          // [batch][boxes][heads][64], a box: the head tile's queries
     CUtensorMap tmap_k, tmap_v;  // boxes of a group (latent: tmap_v has the single rotary box)
