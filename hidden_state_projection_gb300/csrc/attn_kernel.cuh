@@ -287,7 +287,11 @@ constexpr uint32_t kIdescBase = (1u << 4) | (1u << 7) | (1u << 10) | (static_cas
 // place is free as soon as the product that reads it last is done.
 //   latent:  the value groups 0 .. 3 (read by the scores and by one O^T tile each), and for 576
 //            columns the rotary box in a small ring of its own (read by the scores only)
-//   grouped: the key group (scores only), then the value group
+//   grouped: the key group (scores only), then the value group.  The number of places is even and at least four:
+//            the issuer of the scores waits for key groups only, and a barrier's parity tells it
+//            one use of a place from the next, not from the one after; with an odd number a
+//            place would hold keys and values in turn, and a wait for keys could pass on the
+//            phase before the values that are still to come.
 template <int KB, int VB, bool SHARED, int N>
 struct AttnCfg {
     static constexpr int kDV = VB * 64;

@@ -70,6 +70,7 @@ proj_status attn_shape(int heads, int kv_heads, int k_dim, int v_dim, bool laten
     const int room = s->per_sm == 1 ? kSmemLimit : kSmemPerSm / s->per_sm - kSmemReserved;
     s->slots = (room - fixed) / group_bytes;
     if (s->slots > hsp::kAttnMaxSlots) s->slots = hsp::kAttnMaxSlots;
+    if (!latent) s->slots &= ~1;  // keys and values take turns: each kind keeps its places (attn_kernel.cuh)
     s->smem = fixed + s->slots * group_bytes;
     // What a part's start and end cost, in tiles: a latent part waits for O^T's way out of tensor
     // memory (64 heads: 6 us, a tile 1.2 us); grouped tiles wait for memory, and another CTA on the

@@ -5,6 +5,7 @@
 namespace hsp {
 
 cudaError_t launch_attn_grouped(const AttnLaunchReq &r) {
+    if (r.args.slots < 4 || r.args.slots % 2 != 0) return cudaErrorInvalidConfiguration;
     if (r.KB == 2) {
         if (r.N == 16) return launch_attn_variant<2, 2, false, 16>(r);
         if (r.N == 32) return launch_attn_variant<2, 2, false, 32>(r);

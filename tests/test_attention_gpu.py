@@ -129,6 +129,34 @@ def test_grouped(hsp, lens, heads, kv, page, d):
     check(hsp, make(lens, heads, kv, d, False, page, 7 + heads), d ** -0.5, d)
 
 
+# Every shape of the copy ring (columns, head tiles), over sequences long enough for each CTA to go around it
+# several times, next to short ones: what each warp waits for has to be the use of a place that it means.
+RAGGED = [64, 64, 63, 1, 1, 63, 7560, 0, 64, 0, 7122, 64, 0, 7560, 2569, 276, 7560, 0, 1, 2123, 65, 1, 65, 2814, 6038, 1954,
+          1793, 0, 65, 0, 2096, 1, 6664, 7484, 1, 1930, 63, 4785, 4611]
+
+
+@pytest.mark.parametrize("page", [16, 128])
+@pytest.mark.parametrize("d,kv,group", [(128, 3, 16), (128, 3, 17), (128, 3, 40), (64, 3, 5), (64, 3, 17), (64, 3, 64)])
+def test_grouped_rings(hsp, d, kv, group, page):
+    args = make(RAGGED, kv * group, kv, d, False, page, 616 + group)
+    first = check(hsp, args, -0.1, d)
+    for _ in range(20):                                     # other timings, the same bits
+        out, lse = hsp.paged_attention(*args, -0.1, v_dim=d, return_lse=True)
+        assert torch.equal(out, first[0]) and torch.equal(lse, first[1])
+    hsp.check_device_error()
+
+
+@pytest.mark.parametrize("page", [16, 128])
+@pytest.mark.parametrize("dk,heads", [(576, 16), (576, 32), (576, 64), (576, 100), (512, 16), (512, 32), (512, 64)])
+def test_latent_rings(hsp, dk, heads, page):
+    args = make(RAGGED, heads, 1, dk, True, page, 617 + heads)
+    first = check(hsp, args, 0.06, 512)
+    for _ in range(20):
+        out, lse = hsp.paged_attention(*args, 0.06, return_lse=True)
+        assert torch.equal(out, first[0]) and torch.equal(lse, first[1])
+    hsp.check_device_error()
+
+
 @pytest.mark.parametrize("latent", [True, False])
 def test_many_sequences(hsp, latent):
     lens = [(37 * i) % 301 for i in range(391)]            # more sequences than threads, empty ones among them
