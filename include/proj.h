@@ -469,7 +469,7 @@ typedef struct {
  *   positions  device [tokens], or NULL for the last place of the row, seq_lens[row] - 1
  *   rotary     NULL: rows are copied as they are
  *   q, q_out   device [tokens, heads, k_dim], turned at the same positions; q_out may be q.
- *              NULL q: no queries.  Strides in elements, multiples of 8.
+ *              NULL q: no queries (and none without rotary).  Strides in elements, multiples of 8.
  * Pages must already hold the positions (proj_cache_resize) and be the row's own.  Two
  * tokens of one call must not name the same row and position (which one stays is not
  * defined).  One kernel launch; tokens = 0 succeeds and touches nothing.
