@@ -104,6 +104,16 @@ proj_status check_kv(const proj_kv_pages *kv) {
     return PROJ_OK;
 }
 
+// Tokens, heads and pages that steps can reach lie apart.
+proj_status check_apart(const proj_kv_pages *kv, const proj_page_index *ix) {
+    if (kv->k_token_stride < 8 || (kv->v && kv->v_token_stride < 8))
+        return api_fail(PROJ_ERR_UNSUPPORTED_SHAPE, "tokens of the cache must lie apart (token stride 0)");
+    if ((kv->kv_heads > 1 && (kv->k_head_stride < 8 || (kv->v && kv->v_head_stride < 8))) ||
+        (ix->num_pages > 1 && (kv->k_page_stride < 8 || (kv->v && kv->v_page_stride < 8))))
+        return api_fail(PROJ_ERR_UNSUPPORTED_SHAPE, "heads and pages of the cache must lie apart (stride 0)");
+    return PROJ_OK;
+}
+
 // [pages][heads][64-column boxes][tokens][64]: token lines of 128 bytes as the products read them.
 proj_status encode_pages(const void *p, const proj_page_index *ix, int heads, int dim, int64_t page, int64_t token,
                          int64_t head, int box_count, CUtensorMap *out) {
@@ -209,11 +219,7 @@ proj_status proj_paged_attention(const void *q, int64_t q_row_stride, int64_t q_
     const int64_t most_tiles = (static_cast<int64_t>(index->max_pages) * index->page_size + hsp::kAttnTile - 1) / hsp::kAttnTile;
     if (static_cast<int64_t>(batch) * kv->kv_heads * (most_tiles + s.weight) >= (int64_t(1) << 30))
         return api_fail(PROJ_ERR_UNSUPPORTED_SHAPE, "batch=%d of up to %d pages is too large", batch, index->max_pages);
-    if (kv->k_token_stride < 8 || (kv->v && kv->v_token_stride < 8))
-        return api_fail(PROJ_ERR_UNSUPPORTED_SHAPE, "tokens of the cache must lie apart (token stride 0)");
-    if ((kv->kv_heads > 1 && (kv->k_head_stride < 8 || (kv->v && kv->v_head_stride < 8))) ||
-        (index->num_pages > 1 && (kv->k_page_stride < 8 || (kv->v && kv->v_page_stride < 8))))
-        return api_fail(PROJ_ERR_UNSUPPORTED_SHAPE, "heads and pages of the cache must lie apart (stride 0)");
+    if ((st = check_apart(kv, index)) != PROJ_OK) return st;
     if (batch == 0) return hsp::api_ok();
     if (!rows && batch > index->num_rows)
         return api_fail(PROJ_ERR_INVALID_ARG, "batch=%d exceeds the table's %d rows", batch, index->num_rows);
@@ -314,6 +320,7 @@ proj_status proj_cache_append(const void *k_new, int64_t k_row_stride, const voi
     const int64_t columns = static_cast<int64_t>(kv->kv_heads) * (kv->k_dim + (kv->v ? kv->v_dim : 0)) +
                             (q ? static_cast<int64_t>(heads) * kv->k_dim : 0);
     if (columns > (1 << 24)) return api_fail(PROJ_ERR_UNSUPPORTED_SHAPE, "%lld columns of a token exceed 2^24", (long long)columns);
+    if ((st = check_apart(kv, index)) != PROJ_OK) return st;
     if (q && !rotary) return api_fail(PROJ_ERR_INVALID_ARG, "queries are only turned: q needs rotary");
     if (rotary) {
         if (!rotary->cos_sin || rotary->max_pos < 1) return api_fail(PROJ_ERR_INVALID_ARG, "rotary without a table");

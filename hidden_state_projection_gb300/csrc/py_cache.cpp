@@ -76,6 +76,11 @@ double number(PyObject *o) {
     if (v == -1.0 && PyErr_Occurred()) throw PythonError();
     return v;
 }
+bool truth(PyObject *o) {
+    const int v = PyObject_IsTrue(o);
+    if (v < 0) throw PythonError();
+    return v != 0;
+}
 // Sizes that the C ABI takes as 32 bits: what does not fit is out of its range anyway.
 int32_t narrow(int64_t v) { return v > INT32_MAX ? INT32_MAX : static_cast<int32_t>(v); }
 
@@ -256,7 +261,7 @@ PyObject *paged_attention(PyObject *, PyObject *const *args, Py_ssize_t nargs) {
         const float scale = static_cast<float>(number(args[5]));
         const at::Tensor rows = optional(args[7], "rows");
         at::Tensor out = optional(args[8], "out"), lse = optional(args[9], "lse");
-        const bool return_lse = PyObject_IsTrue(args[10]) == 1;
+        const bool return_lse = truth(args[10]);
         const at::Tensor given = optional(args[11], "workspace");
         const int dev = device_of({&q, &k, &v, &table, &lens, &rows, &out, &lse, &given});
         const proj_kv_pages kv = kv_pages(k, v, integer(args[6]));
@@ -332,7 +337,7 @@ PyObject *cache_append(PyObject *, PyObject *const *args, Py_ssize_t nargs) {
             rot.cos_sin = static_cast<const float *>(cs.data_ptr());
             rot.max_pos = narrow(cs.size(0));
             rot.dim = narrow(cs.size(1));
-            rot.interleaved = PyObject_IsTrue(args[9]) == 1;
+            rot.interleaved = truth(args[9]);
         }
         int64_t heads = 0, qs = 0, qh = 0, os = 0, oh = 0;
         if (q.defined()) {

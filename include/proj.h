@@ -434,7 +434,8 @@ typedef struct {
  *              bytes; needs no initialisation and keeps nothing.  Calls that share one
  *              must not overlap on the GPU.  Not used (and may be NULL) where a table row
  *              holds at most PROJ_UNCUT_TOKENS tokens: then no sequence is cut.
- * Two kernel launches, one for such a table.  batch = 0 succeeds and touches nothing.
+ * out and lse overlap none of the inputs.  Two kernel launches, one for such a table.
+ * batch = 0 succeeds and touches nothing.
  */
 proj_status proj_paged_attention(const void *q, int64_t q_row_stride, int64_t q_head_stride,
                                  const proj_kv_pages *kv, const proj_page_index *index,
@@ -489,7 +490,8 @@ proj_status proj_cache_append(const void *k_new, int64_t k_row_stride, const voi
  * rows too gets a copy of that page (over all pools) first, so what is appended next
  * belongs to it alone.  Shrinking gives the pages past the new length back (their counts
  * drop, the table entries become -1); length 0 frees the row.
- *   status     device [n]: 0 done; 1 not enough free pages (the row is left as it was);
+ *   status     device [n]: 0 done; 1 not enough free pages (the row is left as it was, but the
+ *              pages it wanted count for the rows named behind it);
  *              2 refused: a row outside the table, named before in the call, or a length
  *              outside 0 .. max_pages * page_size
  *   pools      host [num_pools], 1..PROJ_MAX_POOLS
@@ -507,7 +509,7 @@ proj_status proj_cache_resize(const proj_page_index *index, const int32_t *rows,
  * same length, same pages, counts raised.  A parent may have several children.  Nothing
  * is copied until one of them grows (proj_cache_resize).
  *   status     device [n]: 0 done; 2 refused: a row outside the table, a child that is not
- *              empty, is named before in the call or is itself a parent in it
+ *              empty or is named before in the call, a parent that is a child in it
  * One kernel launch.
  */
 proj_status proj_cache_fork(const proj_page_index *index, const int32_t *parents,

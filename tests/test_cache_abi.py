@@ -95,6 +95,9 @@ def test_append_refusals(hsp):
                      (dict(kvp=kv(heads=65536, dk=512)), "UNSUPPORTED_SHAPE")]:
         assert call(**kw) == S["PROJ_ERR_" + want], (kw, hsp.lib().proj_last_error_string())
     assert call(tokens=0) == S["PROJ_OK"]
+    for strides in ((0, 576, 576), (36864, 0, 576)):               # places that would be written twice
+        assert call(kvp=kv(ks=strides)) == S["PROJ_ERR_UNSUPPORTED_SHAPE"], strides
+    assert call(kvp=kv(v=A, dk=64, dv=64, heads=2, ks=(8192, 128, 64), vs=(8192, 128, 0)), v=A, r=None) == S["PROJ_ERR_UNSUPPORTED_SHAPE"]
     assert hsp.launch_count() == n
 
 
@@ -147,6 +150,13 @@ def test_copy_refusals(hsp):
     assert copy(src, dst, pages=5000) == bad
     assert copy([], []) == S["PROJ_OK"]
     assert hsp.launch_count() == n
+
+
+def test_a_flag_that_has_no_truth_value(hsp):
+    q, k = torch.zeros(1, 16, 576, dtype=torch.bfloat16), torch.zeros(4, 64, 1, 576, dtype=torch.bfloat16)
+    table, lens = torch.zeros(1, 4, dtype=torch.int32), torch.zeros(1, dtype=torch.int32)
+    with pytest.raises(RuntimeError, match="ambiguous"):
+        hsp.paged_attention(q, k, None, table, lens, 0.1, return_lse=torch.zeros(2))
 
 
 def test_python_checks(hsp):
