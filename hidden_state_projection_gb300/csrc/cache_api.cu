@@ -424,7 +424,7 @@ proj_status proj_cache_resize(const proj_page_index *index, const int32_t *rows,
     a.plan = reinterpret_cast<hsp::RowPlan *>(ws + w.plan);
     const cudaError_t e = hsp::launch_resize(a, dev.sms, hsp::api_options().pdl, reinterpret_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return hsp::api_cuda_fail(e, "kernel launch (cache resize)");
-    hsp::api_count_launches(2);
+    hsp::api_count_launches(hsp::team_resize(a) ? 1 : 2);
     return hsp::api_ok();
 }
 

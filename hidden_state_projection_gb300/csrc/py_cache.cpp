@@ -228,20 +228,21 @@ void run(Call call) {
 }
 
 struct Workspace {
-    at::Tensor t;
+    c10::DataPtr own;  // (torch's allocator, on the current stream, like a tensor of its own but quicker to have)
     void *ptr = nullptr;
     size_t bytes = 0;
 };
-void use(Workspace *w, const at::Tensor &given, size_t need, int dev) {
-    w->t = given;
+void use(Workspace *w, const at::Tensor &given, size_t need) {
     if (!given.defined()) {
         if (need == 0) refuse(PROJ_ERR_UNSUPPORTED_SHAPE, "%s", proj_last_error_string());
-        w->t = make({static_cast<int64_t>(need)}, at::kByte, dev);
-    } else if (!given.is_contiguous()) {
-        refuse(PROJ_ERR_INVALID_ARG, "workspace must be dense");
+        w->own = c10::GetAllocator(c10::kCUDA)->allocate(need);
+        w->ptr = w->own.get();
+        w->bytes = need;
+        return;
     }
-    w->ptr = w->t.data_ptr();
-    w->bytes = w->t.nbytes();
+    if (!given.is_contiguous()) refuse(PROJ_ERR_INVALID_ARG, "workspace must be dense");
+    w->ptr = given.data_ptr();
+    w->bytes = given.nbytes();
 }
 
 void arguments(Py_ssize_t have, Py_ssize_t want) {
@@ -281,7 +282,7 @@ PyObject *paged_attention(PyObject *, PyObject *const *args, Py_ssize_t nargs) {
         const int32_t *rp = rows.defined() ? ints("rows", rows, batch) : nullptr;
         Workspace ws;
         if (given.defined() || static_cast<int64_t>(ix.max_pages) * ix.page_size > PROJ_UNCUT_TOKENS)
-            use(&ws, given, given.defined() ? 0 : proj_paged_attention_workspace_bytes(narrow(heads), kv.kv_heads, kv.k_dim, kv.v_dim, !v.defined()), dev);
+            use(&ws, given, given.defined() ? 0 : proj_paged_attention_workspace_bytes(narrow(heads), kv.kv_heads, kv.k_dim, kv.v_dim, !v.defined()));
         const proj_stream_t stream = stream_of(args[12], dev);
         const void *qp = q.data_ptr();
         void *op = out.data_ptr();
@@ -387,7 +388,7 @@ PyObject *cache_resize(PyObject *, PyObject *const *args, Py_ssize_t nargs) {
         int32_t *sp = ints_out("status", status, n);
         const int32_t *rp = ints("rows", rows, n), *wp = ints("new_lens", want, n);
         Workspace ws;
-        use(&ws, given, given.defined() ? 0 : proj_cache_workspace_bytes(&ix, narrow(n)), dev);
+        use(&ws, given, given.defined() ? 0 : proj_cache_workspace_bytes(&ix, narrow(n)));
         const proj_stream_t stream = stream_of(args[9], dev);
         run([&] {
             return proj_cache_resize(&ix, rp, wp, narrow(n), pools.pools.data(), narrow(static_cast<int64_t>(pools.pools.size())), sp,
@@ -432,7 +433,7 @@ PyObject *cache_compact(PyObject *, PyObject *const *args, Py_ssize_t nargs) {
         if (!live.defined()) live = make({1}, at::kInt, dev);
         int32_t *lp = ints_out("live", live, 1);
         Workspace ws;
-        use(&ws, given, given.defined() ? 0 : proj_cache_workspace_bytes(&ix, 0), dev);
+        use(&ws, given, given.defined() ? 0 : proj_cache_workspace_bytes(&ix, 0));
         const proj_stream_t stream = stream_of(args[7], dev);
         run([&] {
             return proj_cache_compact(&ix, pools.pools.data(), narrow(static_cast<int64_t>(pools.pools.size())), lp, ws.ptr, ws.bytes, stream);

@@ -497,7 +497,8 @@ proj_status proj_cache_append(const void *k_new, int64_t k_row_stride, const voi
  *   pools      host [num_pools], 1..PROJ_MAX_POOLS
  *   workspace  device, 16-byte aligned, proj_cache_workspace_bytes(index, n) bytes, as for
  *              proj_paged_attention
- * Two kernel launches; n = 0 succeeds and touches nothing.
+ * Two kernel launches, or one for a small call (at most 256 rows, 4096 pages and 1 MB in n
+ * pages of the pools); n = 0 succeeds and touches nothing.
  */
 proj_status proj_cache_resize(const proj_page_index *index, const int32_t *rows,
                               const int32_t *new_lens, int32_t n, const proj_page_pool *pools,

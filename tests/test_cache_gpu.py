@@ -231,6 +231,47 @@ def test_random_runs_of_all_of_them(hsp, rows, width, pages, page, seed):
     hsp.check_device_error()
 
 
+@pytest.mark.parametrize("n", [255, 256, 257])
+@pytest.mark.parametrize("pages", [4095, 4096, 4097])
+def test_one_launch_or_two(hsp, pages, n):
+    """Requests and pools on both sides of the sizes that one launch serves: the same rules, rows named twice and
+    rows outside the table among them, a pool that runs out."""
+    import hidden_state_projection_gb300 as m
+    c = Cache(hsp, 400, 30, pages, 16, pages + n)
+    rng = np.random.RandomState(n)
+    small = n <= 256 and pages <= 4096
+    for step in range(6):
+        who = rng.randint(-1, 401, n)
+        before = hsp.launch_count()
+        c.resize(who, np.where(rng.rand(n) < 0.2, 0, rng.randint(-1, 30 * 16 + 2, n)))
+        assert hsp.launch_count() - before == (1 if small else 2)
+        c.check()
+        empty, full = np.flatnonzero(c.model.lens == 0), np.flatnonzero(c.model.lens > 0)
+        c.fork(rng.choice(full, len(empty) // 2), empty[:len(empty) // 2])
+        held = rng.permutation(np.flatnonzero(c.model.lens > 0))[:n]
+        c.resize(held, np.minimum(c.model.lens[held] + 1, 480))
+        c.check()
+        if step % 2:
+            c.compact()
+            c.check()
+    with pytest.raises(m.ProjError) as ei:
+        hsp.check_device_error()
+    assert ei.value.status_name == "PROJ_ERR_BAD_INDEX"
+
+
+def test_one_launch_moves_as_much_as_two(hsp):
+    """Pages of 196,608 bytes over two pools: five copies at most in one launch."""
+    for n in (1, 4, 5, 6, 40):
+        c = Cache(hsp, 80, 6, 100, 16, n, cols=(2048, 2048))
+        c.resize(range(0, 2 * n, 2), [17 + i for i in range(n)])
+        c.fork(range(0, 2 * n, 2), range(1, 2 * n, 2))
+        before = hsp.launch_count()
+        c.resize(range(1, 2 * n, 2), [18 + i for i in range(n)])
+        assert hsp.launch_count() - before == (1 if n <= 5 else 2)
+        c.check()
+    hsp.check_device_error()
+
+
 def test_compact_an_empty_a_full_and_a_sparse_cache(hsp):
     for pages in (1, 127, 128, 129, 5000):
         c = Cache(hsp, 70, 40, pages, 16, pages, layers=(1,), cols=(8,))
