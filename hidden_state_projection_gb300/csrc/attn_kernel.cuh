@@ -674,7 +674,7 @@ __global__ void __launch_bounds__(kAttnThreads, attn_ctas_per_sm(KB, SHARED, N))
         const int r0 = warp * 16 + (lane >> 2);                // this thread's token rows: r0 and r0 + 8
         const uint32_t lane_base = static_cast<uint32_t>(warp * 32) << 16;
         constexpr float kFloor = -3.0e38f;
-        if (a.split && ht == 0 && tid == 0) {
+        if (a.split && ht == 0 && tid == 96) {
             AttnEntry e;
             e.batch = -1;
             e.kv_head = e.last = e.slot = 0;
@@ -695,19 +695,6 @@ __global__ void __launch_bounds__(kAttnThreads, attn_ctas_per_sm(KB, SHARED, N))
                 tc_fence_after_sync();
                 float s[kS * 4];
                 tmem_ld_frag<kS>(tmem_s + (i & 1) * N + lane_base, s);
-                if (valid < kAttnTile) {
-                    // the last tile: what lies behind the sequence must not reach the product (0 x NaN)
-                    const int first = i * C::kGroups + C::kKG;  // its first value group in the ring
-                    if (!SHARED)                                // (a latent tile's scores have waited for it)
-                        attn_wait(smem_u32(&full[first % a.slots]), static_cast<uint32_t>(first / a.slots) & 1u, a.wait_limit_ns,
-                                     abort_flag, a.err_word);
-                    const int lines = kAttnTile - valid;
-                    for (int e = tid; e < lines * VB * 8; e += 128) {
-                        const int vb = e / (lines * 8), rem = e - vb * (lines * 8);
-                        uint8_t *v = smem + ((first + vb / C::kGB) % a.slots) * C::kGroupBytes + (vb % C::kGB) * C::kBoxBytes;
-                        *reinterpret_cast<uint4 *>(v + (valid + (rem >> 3)) * 128 + ((rem & 7) << 4)) = make_uint4(0, 0, 0, 0);
-                    }
-                }
                 tmem_wait_ld();
                 tc_fence_before_sync();
                 mbar_arrive(smem_u32(&s_free[i & 1]));
@@ -781,6 +768,20 @@ __global__ void __launch_bounds__(kAttnThreads, attn_ctas_per_sm(KB, SHARED, N))
                         tmem_wait_st();
                     }
                 }
+                if (valid < kAttnTile) {
+                    // the last tile: what lies behind the sequence must not reach the product (0 x NaN)
+                    const int first = i * C::kGroups + C::kKG;  // its first value group in the ring
+                    if (!SHARED)                                // (a latent tile's scores have waited for it)
+                        attn_wait(smem_u32(&full[first % a.slots]), static_cast<uint32_t>(first / a.slots) & 1u, a.wait_limit_ns,
+                                     abort_flag, a.err_word);
+                    const int pieces = (kAttnTile - valid) * 8;
+#pragma unroll 1
+                    for (int vb = 0; vb < VB; ++vb) {
+                        uint8_t *v = smem + ((first + vb / C::kGB) % a.slots) * C::kGroupBytes + (vb % C::kGB) * C::kBoxBytes +
+                                     valid * 128;
+                        for (int e = tid; e < pieces; e += 128) *reinterpret_cast<uint4 *>(v + e * 16) = make_uint4(0, 0, 0, 0);
+                    }
+                }
                 // the probabilities of tile i - 1 have been read before these replace them
                 if (i > 0)
                     attn_wait(smem_u32(pv_done), static_cast<uint32_t>(i - 1) & 1u, a.wait_limit_ns, abort_flag, a.err_word);
@@ -806,35 +807,32 @@ __global__ void __launch_bounds__(kAttnThreads, attn_ctas_per_sm(KB, SHARED, N))
                 l[e] += __shfl_xor_sync(0xffffffffu, l[e], 8);
                 l[e] += __shfl_xor_sync(0xffffffffu, l[e], 16);
             }
-            softmax_sync();  // the last tile's maxima have been read
+            softmax_sync();  // the last tile's maxima and factors have been read
             if (lane < 4) {
 #pragma unroll
-                for (int j = 0; j < kS; ++j)
-                    *reinterpret_cast<float2 *>(red + warp * N + 8 * j + 2 * lane) = make_float2(l[2 * j], l[2 * j + 1]);
+                for (int j = 0; j < kS; ++j) {
+                    const int c = 8 * j + 2 * lane;
+                    *reinterpret_cast<float2 *>(red + warp * N + c) = make_float2(l[2 * j], l[2 * j + 1]);
+                    if (warp == 0) *reinterpret_cast<float2 *>(fac + c) = make_float2(m[2 * j], m[2 * j + 1]);
+                }
             }
             softmax_sync();
             const bool whole = begins && ends;
             const int slot = sg.x0 == ln.x0 ? 0 : 1;
             float *part = a.parts + (static_cast<int64_t>(ht) * a.ctas + cta) * 2 * (N * kDV + 2 * N) + slot * (N * kDV + 2 * N);
-            if (warp == 0 && lane < 4) {
-#pragma unroll
-                for (int j = 0; j < kS; ++j)
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const int c = 8 * j + 2 * lane + e;
-                        const float t = red[c] + red[N + c] + red[2 * N + c] + red[3 * N + c];
-                        if (whole) {
-                            fac[c] = t == 0.f ? 0.f : 1.f / t;
-                            if (a.lse && c < nheads && *abort_flag == 0)
-                                a.lse[static_cast<int64_t>(sg.b) * all_heads + sg.kv * a.group + head0 + c] =
-                                    t == 0.f ? -INFINITY : (m[2 * j + e] + log2f(t)) * 0.6931471805599453f;
-                        } else {
-                            part[N * kDV + c] = m[2 * j + e];
-                            part[N * kDV + N + c] = t;
-                        }
-                    }
+            if (tid < N) {  // a column per thread
+                const float t = red[tid] + red[N + tid] + red[2 * N + tid] + red[3 * N + tid], top = fac[tid];
+                if (whole) {
+                    fac[tid] = t == 0.f ? 0.f : 1.f / t;
+                    if (a.lse && tid < nheads && *abort_flag == 0)
+                        a.lse[static_cast<int64_t>(sg.b) * all_heads + sg.kv * a.group + head0 + tid] =
+                            t == 0.f ? -INFINITY : (top + log2f(t)) * 0.6931471805599453f;
+                } else {
+                    part[N * kDV + tid] = top;
+                    part[N * kDV + N + tid] = t;
+                }
             }
-            if (ht == 0 && tid == 0 && begins && !ends) {
+            if (ht == 0 && tid == 96 && begins && !ends) {
                 AttnEntry e;
                 e.batch = sg.b;
                 e.kv_head = sg.kv;
