@@ -634,6 +634,7 @@ __global__ void __launch_bounds__(kAttnThreads, attn_ctas_per_sm(KB, SHARED, N))
             RingPos rp;
             while (alive && attn_next_segment(a, ln, walk, sg)) {
                 for (int k = 0; k < sg.n; ++k, ++i) {
+                    const int valid = min(kAttnTile, sg.len - (sg.t0 + k) * kAttnTile);  // tokens of this tile
                     alive = attn_wait(smem_u32(p_full), static_cast<uint32_t>(i) & 1u, a.wait_limit_ns, abort_flag, a.err_word);
                     if (!alive) break;
                     tc_fence_after_sync();
@@ -648,7 +649,7 @@ __global__ void __launch_bounds__(kAttnThreads, attn_ctas_per_sm(KB, SHARED, N))
                         const uint64_t vd = umma_desc_mn_sw128(ring + rp.slot * C::kGroupBytes, C::kBoxBytes);
 #pragma unroll
                         for (int e = 0; e < kAttnTile / 16; ++e)
-                            umma_f16(tmem + jt * N, vd + e * 128, pd + e * 128, kDesc, (k | e) != 0 ? 1u : 0u);
+                            if (e * 16 < valid) umma_f16(tmem + jt * N, vd + e * 128, pd + e * 128, kDesc, (k | e) != 0 ? 1u : 0u);
                         umma_commit(smem_u32(&empty[rp.slot]));
                         rp.next(a.slots);
                     }
@@ -769,17 +770,22 @@ __global__ void __launch_bounds__(kAttnThreads, attn_ctas_per_sm(KB, SHARED, N))
                     }
                 }
                 if (valid < kAttnTile) {
-                    // the last tile: what lies behind the sequence must not reach the product (0 x NaN)
+                    // the last tile: what lies behind the sequence must not reach the product (0 x NaN).  Its last
+                    // step of 16 tokens is filled up with zeros; the steps behind that are not taken.
                     const int first = i * C::kGroups + C::kKG;  // its first value group in the ring
                     if (!SHARED)                                // (a latent tile's scores have waited for it)
                         attn_wait(smem_u32(&full[first % a.slots]), static_cast<uint32_t>(first / a.slots) & 1u, a.wait_limit_ns,
                                      abort_flag, a.err_word);
-                    const int pieces = (kAttnTile - valid) * 8;
-#pragma unroll 1
-                    for (int vb = 0; vb < VB; ++vb) {
-                        uint8_t *v = smem + ((first + vb / C::kGB) % a.slots) * C::kGroupBytes + (vb % C::kGB) * C::kBoxBytes +
-                                     valid * 128;
-                        for (int e = tid; e < pieces; e += 128) *reinterpret_cast<uint4 *>(v + e * 16) = make_uint4(0, 0, 0, 0);
+                    if (tid < (-valid & 15) * 8) {
+                        int at = first % a.slots;
+#pragma unroll
+                        for (int g = 0; g < C::kVG; ++g) {
+#pragma unroll
+                            for (int e = 0; e < C::kGB; ++e)
+                                *reinterpret_cast<uint4 *>(smem + at * C::kGroupBytes + e * C::kBoxBytes + valid * 128 + tid * 16) =
+                                    make_uint4(0, 0, 0, 0);
+                            at = at + 1 == a.slots ? 0 : at + 1;
+                        }
                     }
                 }
                 // the probabilities of tile i - 1 have been read before these replace them
