@@ -166,6 +166,13 @@ __device__ __forceinline__ float fast_exp2(float x) {
     return y;
 }
 
+// A box of a tensor on its way to L2.
+__device__ __forceinline__ void tma_prefetch_5d(const CUtensorMap *map, int c0, int c1, int c2, int c3, int c4) {
+    asm volatile("cp.async.bulk.prefetch.tensor.5d.L2.global.tile [%0, {%1, %2, %3, %4, %5}];" ::"l"(reinterpret_cast<uint64_t>(map)),
+                 "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(c4)
+                 : "memory");
+}
+
 __device__ __forceinline__ void prefetch_l1(const void *p) { asm volatile("prefetch.global.L1 [%0];" ::"l"(p)); }
 
 // Bounded wait.  Once any thread of the CTA has given up, waits that are not yet satisfied
@@ -541,6 +548,18 @@ __global__ void __launch_bounds__(kAttnThreads, attn_ctas_per_sm(KB, SHARED, N))
                                         tma_load_5d(dst + kb * C::kBoxBytes + e * line_bytes, map, 0, 0, box + kb, sg.kv, id[e], fb);
                         }
                     };
+                    // Two tiles are all that shared memory holds beside 64 latent queries, too few to hide DRAM
+                    // behind the products: with several head tiles one of them sends the next tile to L2
+                    // (48 ragged sequences, 128 heads: 66.4 -> 62.8 us; two tiles ahead 65.5; one head tile,
+                    // 16 to 64 heads: mostly 1 us slower).
+                    if (SHARED && N == 64 && gridDim.x > 1 && boxes == 1 && k + 1 < sg.n && (k + 1) % static_cast<int>(gridDim.x) == ht && next[0] >= 0 &&
+                        next[0] < a.num_pages) {
+                        const int to = static_cast<int>((tok + kAttnTile) & ((1 << a.page_shift) - 1));
+#pragma unroll
+                        for (int g = 0; g < C::kGroups; ++g)
+                            tma_prefetch_5d(SHARED || g < C::kKG ? &tmap_k : &tmap_v, 0, to, SHARED ? g * C::kGB : 0, sg.kv, next[0]);
+                        if (C::kExtra) tma_prefetch_5d(&tmap_v, 0, to, VB, sg.kv, next[0]);
+                    }
                     const bool skip = i == a.skip_tile;
 #pragma unroll 1
                     for (int g = 0; g < C::kGroups; ++g) {
