@@ -882,14 +882,30 @@ __global__ void __launch_bounds__(kAttnThreads, attn_ctas_per_sm(KB, SHARED, N))
                 if (lane < rpw && good) {
                     if (whole) {
                         __nv_bfloat16 *to = out + obase + static_cast<int64_t>(h0) * kDV + dv;
+                        if (h0 + 16 <= nheads) {  // (16 tests take longer than the stores)
 #pragma unroll
-                        for (int e = 0; e < 16; ++e)
-                            if (h0 + e < nheads) to[e * kDV] = __float2bfloat16_rn(o[e] * fac[h0 + e]);
+                            for (int e = 0; e < 16; e += 4) {
+                                const float4 f = *reinterpret_cast<const float4 *>(fac + h0 + e);
+                                to[e * kDV] = __float2bfloat16_rn(o[e] * f.x);
+                                to[(e + 1) * kDV] = __float2bfloat16_rn(o[e + 1] * f.y);
+                                to[(e + 2) * kDV] = __float2bfloat16_rn(o[e + 2] * f.z);
+                                to[(e + 3) * kDV] = __float2bfloat16_rn(o[e + 3] * f.w);
+                            }
+                        } else {
+#pragma unroll
+                            for (int e = 0; e < 15; ++e)
+                                if (h0 + e < nheads) to[e * kDV] = __float2bfloat16_rn(o[e] * fac[h0 + e]);
+                        }
                     } else {
                         float *to = part + h0 * kDV + dv;
+                        if (h0 + 16 <= nheads) {
 #pragma unroll
-                        for (int e = 0; e < 16; ++e)
-                            if (h0 + e < nheads) to[e * kDV] = o[e];
+                            for (int e = 0; e < 16; ++e) to[e * kDV] = o[e];
+                        } else {
+#pragma unroll
+                            for (int e = 0; e < 15; ++e)
+                                if (h0 + e < nheads) to[e * kDV] = o[e];
+                        }
                     }
                 }
             }
