@@ -39,12 +39,13 @@
 // sequence cut over several CTAs leaves fp32 partials (O^T, m, l) in the workspace, and the
 // join kernel adds them; the cut depends on the lengths and the grid only.
 //
-// On a GB300 (graph replay): one sequence of 131071 tokens and 64 heads over 512 columns 43 us
-// (134 MB, 19.8 us at the copy rate): 4 us until the first tile is there, 23 us at 5.7 TB/s, 4 us
+// On a GB300 (graph replay): one sequence of 131071 tokens and 64 heads over 512 columns 40.7 us
+// (134 MB, 19.8 us at the copy rate): 4 us until the first tile is there, 24 us at 5.6 TB/s, 3 us
 // for 128 KB of partial per CTA (an SM stores 21 bytes per cycle), 7 us for the join with its
-// launch.  48 sequences up to 6001 tokens, 128 heads: 66 us, 1.17 us per tile of the 1.06 that the
-// products take, 5 us per part.  61 sequences up to 4099, 32 heads over 8 of 128: 91-94 us (515 MB,
-// 75.8): 70 us at the memory's limit, the rest start, the spread of the CTAs' ends and the join.
+// launch.  48 sequences up to 6001 tokens, 128 heads: 59.6 us, the products (1.06 us per tile) and
+// 3.5 us per part, 7 us for the join.  61 sequences up to 4099, 32 heads over 8 of 128: 90-93 us
+// (515 MB, 75.8): 70 us at the memory's limit, the rest start, the spread of the CTAs' ends and the
+// join.  One sequence of 77 tokens, 16 heads: 6.7 us, dependent loads and two tiles in turn.
 #pragma once
 
 #include <cuda.h>

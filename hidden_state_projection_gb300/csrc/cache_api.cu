@@ -73,11 +73,11 @@ proj_status attn_shape(int heads, int kv_heads, int k_dim, int v_dim, bool laten
     if (!latent) s->slots &= ~1;  // keys and values take turns: each kind keeps its places (attn_kernel.cuh)
     s->smem = fixed + s->slots * group_bytes;
     // What a part's start and end cost, in tiles: its pipeline fills, and O^T finds its way out of tensor
-    // memory (64 latent heads: 6 us, a tile 1.2 us).  Weights of 0 to 10 in turn, sequences of mixed
-    // lengths, us: 200 x 8 kv heads of 128 columns, 4 heads each, up to 600 tokens 74.9 (0), 59.7 (2),
-    // 60.2 (4); 20 heads each 67.6 (1), 53.6 (4); 32 x 4 kv heads with 64 heads each, up to 4096
-    // tokens 70.5 (0), 50.5 (3), 39.9 (7), 40.8 (10).
-    s->weight = latent ? 1 + s->N / 16 : 1 + s->N / 10;
+    // memory.  Weights in turn, sequences of mixed lengths, us: 200 x 8 kv heads of 128 columns with 4 heads
+    // each, up to 600 tokens 60.2 (0), 53.3 (1), 54.5 (3); 100 x 4 kv heads of 64 columns with 20 heads each
+    // 49.3 (1), 47.0 (2), 48.0 (5); 64 x 4 with 64 each 40.3 (2), 37.4 (3), 39.6 (8); latent heads: 100 x 16
+    // 23.7 (0), 22.9 (1), 24.5 (4); 64 x 128 72.2 (2), 70.4 (3), 75.0 (8).
+    s->weight = 1 + s->N / 32;
     return PROJ_OK;
 }
 
