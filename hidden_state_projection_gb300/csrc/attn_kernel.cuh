@@ -31,12 +31,15 @@
 // fp32 and bf16 keeps its relative precision), so most tiles need no exchange between the
 // threads but one barrier with an OR; a tile that exceeds it takes the column maxima over
 // all warps and rescales O^T.  P is rounded to bf16 for the product (at most 2^-8 relative per
-// weight, the sum l adds the unrounded values); all sums and statistics are fp32.
+// weight; the values are bf16, and one instruction takes one type).  O^T is divided by the sum l
+// of the rounded weights, so the rounding that all of a row's weight has in common cancels and a
+// token with nearly all the weight comes out as it is; lse takes the sum u of the unrounded
+// ones.  All sums and statistics are fp32.
 //
 // The tiles of all sequences form one line that is cut over the CTAs (grid.y), so ragged
 // batches balance; CTAs of one y and different x take the different head tiles of the same
 // tokens at the same time (DRAM reads of 128 heads in two tiles: 158 MB for 157 MB of cache).  A
-// sequence cut over several CTAs leaves fp32 partials (O^T, m, l) in the workspace, and the
+// sequence cut over several CTAs leaves fp32 partials (O^T, m, l, u) in the workspace, and the
 // join kernel adds them; the cut depends on the lengths and the grid only.
 //
 // On a GB300 (graph replay): one sequence of 131071 tokens and 64 heads over 512 columns 40.7 us
@@ -165,6 +168,13 @@ __device__ __forceinline__ float fast_exp2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
+}
+
+// a += b, both columns in one instruction.
+__device__ __forceinline__ void add2(float2 &a, float2 b) {
+    asm("{\n\t.reg .b64 x, y;\n\tmov.b64 x, {%0, %1};\n\tmov.b64 y, {%2, %3};\n\tadd.rn.f32x2 x, x, y;\n\tmov.b64 {%0, %1}, x;\n\t}"
+        : "+f"(a.x), "+f"(a.y)
+        : "f"(b.x), "f"(b.y));
 }
 
 // A box of a tensor on its way to L2.
@@ -703,12 +713,12 @@ __global__ void __launch_bounds__(kAttnThreads, attn_ctas_per_sm(KB, SHARED, N))
         }
         while (attn_next_segment(a, ln, walk, sg)) {
             const bool begins = sg.t0 == 0, ends = sg.t0 + sg.n == sg.tiles;
-            float m[kS * 2], l[kS * 2];
+            float m[kS * 2];     // reference point
+            float2 l[kS], u[kS];  // sums of the rounded and the unrounded weights
 #pragma unroll
-            for (int e = 0; e < kS * 2; ++e) {
-                m[e] = kFloor;
-                l[e] = 0.f;
-            }
+            for (int e = 0; e < kS * 2; ++e) m[e] = kFloor;
+#pragma unroll
+            for (int j = 0; j < kS; ++j) l[j] = u[j] = make_float2(0.f, 0.f);
             for (int k = 0; k < sg.n; ++k, ++i) {
                 const int64_t tok0 = static_cast<int64_t>(sg.t0 + k) * kAttnTile;
                 const int valid = static_cast<int>(min(static_cast<int64_t>(kAttnTile), sg.len - tok0));
@@ -761,16 +771,16 @@ __global__ void __launch_bounds__(kAttnThreads, attn_ctas_per_sm(KB, SHARED, N))
                         float2 t = *reinterpret_cast<const float2 *>(red + c);
 #pragma unroll
                         for (int w = 1; w < 4; ++w) {
-                            const float2 u = *reinterpret_cast<const float2 *>(red + w * N + c);
-                            t.x = fmaxf(t.x, u.x);
-                            t.y = fmaxf(t.y, u.y);
+                            const float2 o = *reinterpret_cast<const float2 *>(red + w * N + c);
+                            t.x = fmaxf(t.x, o.x);
+                            t.y = fmaxf(t.y, o.y);
                         }
                         const float n0 = fmaxf(m[2 * j], t.x), n1 = fmaxf(m[2 * j + 1], t.y);
                         const float f0 = fast_exp2(m[2 * j] - n0), f1 = fast_exp2(m[2 * j + 1] - n1);
                         m[2 * j] = n0;
                         m[2 * j + 1] = n1;
-                        l[2 * j] *= f0;
-                        l[2 * j + 1] *= f1;
+                        l[j] = make_float2(l[j].x * f0, l[j].y * f1);
+                        u[j] = make_float2(u[j].x * f0, u[j].y * f1);
                         if (warp == 0 && lane < 4) *reinterpret_cast<float2 *>(fac + c) = make_float2(f0, f1);
                     }
                     if (k > 0) {
@@ -811,51 +821,75 @@ __global__ void __launch_bounds__(kAttnThreads, attn_ctas_per_sm(KB, SHARED, N))
                 // the probabilities of tile i - 1 have been read before these replace them
                 if (i > 0)
                     attn_wait(smem_u32(pv_done), static_cast<uint32_t>(i - 1) & 1u, a.wait_limit_ns, abort_flag, a.err_word);
+                uint32_t pb[kS * 2];  // the rounded weights, two columns each
 #pragma unroll
                 for (int j = 0; j < kS; ++j) {
-                    const float p00 = fast_exp2(s[4 * j] - m[2 * j]), p01 = fast_exp2(s[4 * j + 1] - m[2 * j + 1]);
-                    const float p10 = fast_exp2(s[4 * j + 2] - m[2 * j]), p11 = fast_exp2(s[4 * j + 3] - m[2 * j + 1]);
-                    l[2 * j] += p00 + p10;
-                    l[2 * j + 1] += p01 + p11;
-                    const __nv_bfloat162 u = __floats2bfloat162_rn(p00, p01), w = __floats2bfloat162_rn(p10, p11);
-                    uint8_t *pr = p_smem + r0 * 128 + ((j ^ (r0 & 7)) << 4) + (lane & 3) * 4;
-                    *reinterpret_cast<__nv_bfloat162 *>(pr) = u;
-                    *reinterpret_cast<__nv_bfloat162 *>(pr + 8 * 128) = w;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) s[4 * j + e] = fast_exp2(s[4 * j + e] - m[2 * j + (e & 1)]);
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const __nv_bfloat162 b = __floats2bfloat162_rn(s[4 * j + 2 * e], s[4 * j + 2 * e + 1]);
+                        pb[2 * j + e] = *reinterpret_cast<const uint32_t *>(&b);
+                        *reinterpret_cast<uint32_t *>(p_smem + (r0 + 8 * e) * 128 + ((j ^ (r0 & 7)) << 4) + (lane & 3) * 4) = pb[2 * j + e];
+                    }
                 }
                 fence_proxy_async_smem();
                 tc_fence_before_sync();
                 mbar_arrive(smem_u32(p_full));
-            }
-            // ---- the part is done: l over the tokens, then O^T out of tensor memory ----
+                // the sums, beside the product (48 sequences with 128 heads: 61.5 us before the arrival, 60.2 behind it)
 #pragma unroll
-            for (int e = 0; e < kS * 2; ++e) {
-                l[e] += __shfl_xor_sync(0xffffffffu, l[e], 4);
-                l[e] += __shfl_xor_sync(0xffffffffu, l[e], 8);
-                l[e] += __shfl_xor_sync(0xffffffffu, l[e], 16);
-            }
-            softmax_sync();  // the last tile's maxima and factors have been read
-            if (lane < 4) {
+                for (int j = 0; j < kS; ++j)
 #pragma unroll
-                for (int j = 0; j < kS; ++j) {
-                    const int c = 8 * j + 2 * lane;
-                    *reinterpret_cast<float2 *>(red + warp * N + c) = make_float2(l[2 * j], l[2 * j + 1]);
-                    if (warp == 0) *reinterpret_cast<float2 *>(fac + c) = make_float2(m[2 * j], m[2 * j + 1]);
+                    for (int e = 0; e < 2; ++e) {
+                        add2(u[j], make_float2(s[4 * j + 2 * e], s[4 * j + 2 * e + 1]));
+                        add2(l[j], make_float2(__uint_as_float(pb[2 * j + e] << 16), __uint_as_float(pb[2 * j + e] & 0xffff0000u)));
+                    }
+            }
+            // ---- the part is done: l (and u) over the tokens, then O^T out of tensor memory ----
+            auto over_tokens = [&](float2 (&v)[kS]) {  // a warp's sums to `red`
+#pragma unroll
+                for (int j = 0; j < kS; ++j)
+#pragma unroll
+                    for (int d = 4; d < 32; d <<= 1) {
+                        v[j].x += __shfl_xor_sync(0xffffffffu, v[j].x, d);
+                        v[j].y += __shfl_xor_sync(0xffffffffu, v[j].y, d);
+                    }
+                softmax_sync();  // the last tile's maxima and factors (l), the sums l (u) have been read
+                if (lane < 4) {
+#pragma unroll
+                    for (int j = 0; j < kS; ++j) *reinterpret_cast<float2 *>(red + warp * N + 8 * j + 2 * lane) = v[j];
                 }
+            };
+            over_tokens(l);
+            if (warp == 0 && lane < 4) {
+#pragma unroll
+                for (int j = 0; j < kS; ++j) *reinterpret_cast<float2 *>(fac + 8 * j + 2 * lane) = make_float2(m[2 * j], m[2 * j + 1]);
             }
             softmax_sync();
             const bool whole = begins && ends;
             const int slot = sg.x0 == ln.x0 ? 0 : 1;
-            float *part = a.parts + (static_cast<int64_t>(ht) * a.ctas + cta) * 2 * (N * kDV + 2 * N) + slot * (N * kDV + 2 * N);
+            float *part = a.parts + (static_cast<int64_t>(ht) * a.ctas + cta) * 2 * attn_part(kDV, N) + slot * attn_part(kDV, N);
+            float top = 0.f;
             if (tid < N) {  // a column per thread
-                const float t = red[tid] + red[N + tid] + red[2 * N + tid] + red[3 * N + tid], top = fac[tid];
+                const float t = red[tid] + red[N + tid] + red[2 * N + tid] + red[3 * N + tid];
+                top = fac[tid];
                 if (whole) {
                     fac[tid] = t == 0.f ? 0.f : 1.f / t;
-                    if (a.lse && tid < nheads && *abort_flag == 0)
-                        a.lse[static_cast<int64_t>(sg.b) * all_heads + sg.kv * a.group + head0 + tid] =
-                            t == 0.f ? -INFINITY : (top + log2f(t)) * 0.6931471805599453f;
                 } else {
                     part[N * kDV + tid] = top;
                     part[N * kDV + N + tid] = t;
+                }
+            }
+            if (a.lse) {
+                over_tokens(u);
+                softmax_sync();
+                if (tid < N) {
+                    const float t = red[tid] + red[N + tid] + red[2 * N + tid] + red[3 * N + tid];
+                    if (!whole)
+                        part[N * kDV + 2 * N + tid] = t;
+                    else if (tid < nheads && *abort_flag == 0)
+                        a.lse[static_cast<int64_t>(sg.b) * all_heads + sg.kv * a.group + head0 + tid] =
+                            t == 0.f ? -INFINITY : (top + log2f(t)) * 0.6931471805599453f;
                 }
             }
             if (ht == 0 && tid == 96 && begins && !ends) {
@@ -954,8 +988,8 @@ __global__ void __launch_bounds__(kAttnThreads, attn_ctas_per_sm(KB, SHARED, N))
 
 // ---- join ------------------------------------------------------------------------------
 //
-// Sequences cut over several CTAs: out = sum_i 2^(m_i - M) O_i / sum_i 2^(m_i - M) l_i, the
-// parts in a fixed order.  Few parts, or heads enough for all warps: a warp takes a head, part
+// Sequences cut over several CTAs: out = sum_i 2^(m_i - M) O_i / sum_i 2^(m_i - M) l_i, and with u_i
+// for l_i the sum of lse, the parts in a fixed order.  Few parts, or heads enough for all warps: a warp takes a head, part
 // after part.  Else (one long sequence): a CTA takes 64 or 128 columns of a head, its half warps
 // or warps take the parts in turn and their sums are added in a fixed order.  Which of the two depends on
 // the lengths only.
@@ -971,9 +1005,9 @@ struct JoinWidth {
 template <int DV, int N>
 __global__ void __launch_bounds__(kJoinThreads, kJoinPerSm) hsp_attn_join_kernel(const __grid_constant__ AttnArgs a) {
     constexpr int kParts = DV / 64;             // units of 64 columns of a head with many parts
-    constexpr int kPart = N * DV + 2 * N;       // floats of one partial
+    constexpr int kPart = attn_part(DV, N);     // floats of one partial
     __shared__ float4 acc_s[kJoinWarps][32];
-    __shared__ float weight[kAttnMaxCtas], red_s[2 * kJoinWarps];
+    __shared__ float weight[kAttnMaxCtas], red_s[3 * kJoinWarps];
     __shared__ uint16_t few[kAttnMaxCtas], many[kAttnMaxCtas];  // the CTAs that began them
     __shared__ AttnEntry entries[kAttnMaxCtas];
     __shared__ uint32_t bits[2][kAttnMaxCtas / 32];
@@ -1029,9 +1063,9 @@ __global__ void __launch_bounds__(kJoinThreads, kJoinPerSm) hsp_attn_join_kernel
         o.y = *reinterpret_cast<const uint32_t *>(&hi);
         *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(a.out) + oh * DV + col) = o;
     };
-    auto store_lse = [&](const AttnEntry &e, int h, float M, float L) {
+    auto store_lse = [&](const AttnEntry &e, int h, float M, float U) {
         a.lse[(static_cast<int64_t>(e.batch) * a.kv_heads + e.kv_head) * a.group + h] =
-            L == 0.f ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
+            U == 0.f ? -INFINITY : (M + log2f(U)) * 0.6931471805599453f;
     };
     // part p of head h of CTA c's sequence: its own slot, then slot 0 of the CTAs behind it
     auto part = [&](int c, int slot, int h, int p) {
@@ -1044,11 +1078,12 @@ __global__ void __launch_bounds__(kJoinThreads, kJoinPerSm) hsp_attn_join_kernel
         const int c = few[u / a.group], h = u % a.group, col = h % N;
         const AttnEntry e = entries[c];
         const int parts = min(e.last, a.ctas - 1) - c + 1;
-        float m = -3.0e38f, l = 0.f;
+        float m = -3.0e38f, l = 0.f, un = 0.f;
         if (lane < parts) {
             const float *pp = part(c, e.slot, h, lane);
             m = pp[N * DV + col];
             l = pp[N * DV + N + col];
+            if (a.lse) un = pp[N * DV + 2 * N + col];
         }
         float4 v[2][kVec];
         auto load = [&](int p, float4 (&to)[kVec]) {
@@ -1064,9 +1099,12 @@ __global__ void __launch_bounds__(kJoinThreads, kJoinPerSm) hsp_attn_join_kernel
 #pragma unroll
         for (int d = 16; d > 0; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
         const float w = lane < parts ? fast_exp2(m - M) : 0.f;
-        float L = w * l;
+        float L = w * l, U = w * un;
 #pragma unroll
-        for (int d = 16; d > 0; d >>= 1) L += __shfl_xor_sync(0xffffffffu, L, d);
+        for (int d = 16; d > 0; d >>= 1) {
+            L += __shfl_xor_sync(0xffffffffu, L, d);
+            U += __shfl_xor_sync(0xffffffffu, U, d);
+        }
         float4 acc[kVec];
 #pragma unroll
         for (int k = 0; k < kVec; ++k) acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -1091,7 +1129,7 @@ __global__ void __launch_bounds__(kJoinThreads, kJoinPerSm) hsp_attn_join_kernel
 #pragma unroll
             for (int k = 0; k < kVec; ++k) store(e, h, k * 128 + lane * 4, acc[k], inv);
         }
-        if (a.lse && lane == 0) store_lse(e, h, M, L);
+        if (a.lse && lane == 0) store_lse(e, h, M, U);
     }
     // one head, `width` columns from dp * width on
     auto join_cta = [&](int c, int h, int dp, auto width) {
@@ -1108,16 +1146,19 @@ __global__ void __launch_bounds__(kJoinThreads, kJoinPerSm) hsp_attn_join_kernel
                 if (p0 + kRows * k < parts) v[k] = *reinterpret_cast<const float4 *>(part(c, e.slot, h, p0 + kRows * k) + col * DV + at);
         };
         load(p_first);
-        float m[kAttnMaxCtas / kJoinThreads], lw[kAttnMaxCtas / kJoinThreads];
+        float m[kAttnMaxCtas / kJoinThreads], lw[kAttnMaxCtas / kJoinThreads], uw[kAttnMaxCtas / kJoinThreads];
+        const bool sums_u = a.lse && dp == 0;  // (one CTA of a head stores its lse)
         float M = -3.0e38f;
 #pragma unroll
         for (int k = 0; k < kAttnMaxCtas / kJoinThreads; ++k) {
             const int p = tid + k * kJoinThreads;
             m[k] = -3.0e38f;
-            lw[k] = 0.f;
+            lw[k] = uw[k] = 0.f;
             if (p < parts) {
-                m[k] = part(c, e.slot, h, p)[N * DV + col];
-                lw[k] = part(c, e.slot, h, p)[N * DV + N + col];
+                const float *pp = part(c, e.slot, h, p) + N * DV + col;
+                m[k] = pp[0];
+                lw[k] = pp[N];
+                if (sums_u) uw[k] = pp[2 * N];
             }
             M = fmaxf(M, m[k]);
         }
@@ -1127,21 +1168,31 @@ __global__ void __launch_bounds__(kJoinThreads, kJoinPerSm) hsp_attn_join_kernel
         __syncthreads();
 #pragma unroll
         for (int k = 0; k < kJoinWarps; ++k) M = fmaxf(M, red_s[k]);
-        float L = 0.f;
+        float L = 0.f, U = 0.f;
 #pragma unroll
         for (int k = 0; k < kAttnMaxCtas / kJoinThreads; ++k) {
             const int p = tid + k * kJoinThreads;
             const float w = fast_exp2(m[k] - M);
             if (p < parts) weight[p] = w;
             L += lw[k] * w;
+            U += uw[k] * w;
         }
 #pragma unroll
-        for (int d = 16; d > 0; d >>= 1) L += __shfl_xor_sync(0xffffffffu, L, d);
-        if (lane == 0) red_s[kJoinWarps + warp] = L;
+        for (int d = 16; d > 0; d >>= 1) {
+            L += __shfl_xor_sync(0xffffffffu, L, d);
+            U += __shfl_xor_sync(0xffffffffu, U, d);
+        }
+        if (lane == 0) {
+            red_s[kJoinWarps + warp] = L;
+            red_s[2 * kJoinWarps + warp] = U;
+        }
         __syncthreads();
-        L = 0.f;
+        L = U = 0.f;
 #pragma unroll
-        for (int k = 0; k < kJoinWarps; ++k) L += red_s[kJoinWarps + k];
+        for (int k = 0; k < kJoinWarps; ++k) {
+            L += red_s[kJoinWarps + k];
+            U += red_s[2 * kJoinWarps + k];
+        }
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
         for (int p0 = p_first; p0 < parts; p0 += kRows * kAhead) {
             if (p0 != p_first) load(p0);
@@ -1173,7 +1224,7 @@ __global__ void __launch_bounds__(kJoinThreads, kJoinPerSm) hsp_attn_join_kernel
                 acc.w += o.w;
             }
             store(e, h, at, acc, L == 0.f ? 0.f : 1.f / L);
-            if (a.lse && dp == 0 && lane == 0) store_lse(e, h, M, L);
+            if (sums_u && lane == 0) store_lse(e, h, M, U);
         }
         __syncthreads();
     };

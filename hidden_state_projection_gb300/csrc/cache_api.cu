@@ -91,7 +91,7 @@ size_t up256(size_t b) { return (b + 255) / 256 * 256; }
 
 size_t attn_workspace(const AttnShape &s, int ctas) {
     return up256(static_cast<size_t>(ctas) * sizeof(hsp::AttnEntry)) +
-           static_cast<size_t>(s.head_tiles) * ctas * 2 * (static_cast<size_t>(s.N) * s.VB * 64 + 2 * s.N) * 4;
+           static_cast<size_t>(s.head_tiles) * ctas * 2 * hsp::attn_part(s.VB * 64, s.N) * 4;
 }
 
 proj_status check_kv(const proj_kv_pages *kv) {

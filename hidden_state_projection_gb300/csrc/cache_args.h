@@ -12,6 +12,8 @@ constexpr int kDeviceErrIndex = 8;  // same value as PROJ_ERR_BAD_INDEX
 constexpr int kAttnTile = 64;       // tokens per tile
 constexpr int kAttnMaxCtas = 512;  // CTAs along the length (the join lists them in shared memory)
 constexpr int kAttnThreads = 224;   // four softmax warps, the copy producer, the issuers of S^T and of O^T
+// Floats of one partial: O^T, and per head the reference point m, the sums l and u.
+__host__ __device__ constexpr int attn_part(int dv, int N) { return N * dv + 3 * N; }
 
 // One sequence part that a CTA began and another one finishes: what the join adds up.
 // Entry c belongs to CTA c of the length axis; first < 0: CTA c began no such part.
@@ -38,7 +40,7 @@ struct AttnArgs {
     void *out;                   // [batch, heads, VB * 64] bf16
     float *lse;                  // [batch, heads] or null
     AttnEntry *entries;          // [ctas]
-    float *parts;                // [head tiles][ctas][2][N * DV + 2 N]
+    float *parts;                // [head tiles][ctas][2][attn_part]
     int32_t skip_tile;           // test hook: this tile of every CTA is never loaded (-1: off)
     uint64_t wait_limit_ns;
     int *err_word;

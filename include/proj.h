@@ -419,7 +419,8 @@ typedef struct {
  *     lse[b, h] = log sum_t exp(scale * q[b, h] . k[t])
  * for sequence rows[b] (or b), query heads h sharing kv head h / (heads / kv_heads).
  * fp32 scores, maxima and sums; the softmax weights are rounded to bf16 for the product
- * with the values and the result once.  A sequence of length 0 gives zeros and lse =
+ * with the values (which is divided by the sum of the rounded weights; lse is the logarithm of
+ * the unrounded sum) and the result once.  A sequence of length 0 gives zeros and lse =
  * -infinity; what lies in a page behind a sequence's last token is never used, NaN
  * included.  Sequences are cut over the GPU by their lengths and joined in a fixed order:
  * the same lengths give the same bits, run to run and under CUDA-graph replay; another
