@@ -960,11 +960,9 @@ __global__ void __launch_bounds__(kAttnThreads, attn_ctas_per_sm(KB, SHARED, N))
         }
     }
     tc_fence_before_sync();
-    __syncthreads();
     // (Triggered at the start, the join's CTAs crowded on the SMs that were free first: 43 -> 47 us
     // for one sequence of 131071 tokens and 64 heads.)
-    if (tid == 0) fence_release_gpu();  // the outputs and partials of this CTA (cumulative over the barrier)
-    griddep_launch_dependents();
+    cta_release_and_trigger();
     if (*abort_flag != 0 && tid == 0) {
         // copies still in flight land before the shared memory goes
         const int n = issued[0], nx = issued[1];
@@ -1236,9 +1234,7 @@ __global__ void __launch_bounds__(kJoinThreads, kJoinPerSm) hsp_attn_join_kernel
         if (wide) join_cta(c, h, dp, JoinWidth<DV >= 128 ? 128 : 64>{});
         else join_cta(c, h, dp, JoinWidth<64>{});
     }
-    __syncthreads();
-    if (tid == 0) fence_release_gpu();  // (cumulative over the barrier)
-    griddep_launch_dependents();
+    cta_release_and_trigger();
 }
 
 }  // namespace hsp

@@ -154,9 +154,7 @@ __global__ void __launch_bounds__(kAppendThreads, 4) hsp_append_kernel(const __g
             *reinterpret_cast<uint4 *>(to[u]) = v[u];
         }
     }
-    __syncthreads();
-    if (threadIdx.x == 0) fence_release_gpu();  // (cumulative over the barrier)
-    griddep_launch_dependents();
+    cta_release_and_trigger();
 }
 
 cudaError_t launch_append(const AppendArgs &a, int sms, int pdl, cudaStream_t stream) {

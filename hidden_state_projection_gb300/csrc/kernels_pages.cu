@@ -40,14 +40,6 @@ __device__ __forceinline__ int pages_of(int len, int shift) {
     return static_cast<int>((static_cast<int64_t>(len) + (1 << shift) - 1) >> shift);
 }
 
-// The end of every kernel here: the CTA's stores are performed (one fence, cumulative over the
-// barrier), then the dependent launch is triggered.
-__device__ __forceinline__ void done() {
-    __syncthreads();
-    if (threadIdx.x == 0) fence_release_gpu();
-    griddep_launch_dependents();
-}
-
 // Exclusive prefix of v over the CTA's threads, and the sum.
 __device__ __forceinline__ int64_t block_prefix(int64_t v, int64_t *warp_sums, int64_t *sum) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -168,7 +160,7 @@ __global__ void __launch_bounds__(kPagesThreads) hsp_copy_pages_kernel(const __g
     const int64_t units = static_cast<int64_t>(a.n) * a.pools.pieces_total;
     for (int64_t u = blockIdx.x; u < units; u += gridDim.x)
         copy_unit(a.pools, u, [&](int64_t k) { return make_int2(a.src[k], a.dst[k]); });
-    done();
+    cta_release_and_trigger();
 }
 
 // ---- resize ---------------------------------------------------------------------------
@@ -332,7 +324,7 @@ __global__ void __launch_bounds__(kPagesThreads) hsp_resize_apply_kernel(const _
     }
     const int64_t units = static_cast<int64_t>(a.head[0]) * a.pools.pieces_total;
     copy_in_order(a.pools, units, a.taken, [&](int64_t k) { return a.pairs[k]; });
-    done();
+    cta_release_and_trigger();
 }
 
 // A table of the rows named in a request, in shared memory: the first place that names a row.
@@ -475,7 +467,7 @@ __global__ void __launch_bounds__(kPlanThreads) hsp_resize_team_kernel(const __g
         }
     }
     copy_by_team(a.pools, pair_count, rank, [&](uint32_t k) { return pairs[k]; });
-    done();
+    cta_release_and_trigger();
 }
 
 // ---- fork -----------------------------------------------------------------------------
@@ -523,7 +515,7 @@ __global__ void __launch_bounds__(kPagesThreads) hsp_fork_kernel(const __grid_co
         if (threadIdx.x == 0) ix.lens[c] = len;
     }
     if (threadIdx.x == 0) a.status[i] = st;
-    done();
+    cta_release_and_trigger();
 }
 
 // ---- compact --------------------------------------------------------------------------
@@ -642,7 +634,7 @@ __global__ void __launch_bounds__(kPagesThreads) hsp_compact_apply_kernel(const 
         const int64_t units = static_cast<int64_t>(moves) * a.pools.pieces_total;
         copy_in_order(a.pools, units, a.taken, [&](int64_t k) { return a.pairs[k]; });
     }
-    done();
+    cta_release_and_trigger();
 }
 
 // ---- launches -------------------------------------------------------------------------

@@ -282,6 +282,17 @@ __device__ __forceinline__ void griddep_launch_dependents() {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
+// All threads of a CTA, after their last stores: the stores are performed at GPU scope (one fence,
+// cumulative over the barrier), then the dependent launch is triggered.  Fence and trigger belong to the
+// same thread: the trigger of any thread counts for its CTA.
+__device__ __forceinline__ void cta_release_and_trigger() {
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        fence_release_gpu();
+        griddep_launch_dependents();
+    }
+}
+
 // ---- clusters -------------------------------------------------------------
 
 __device__ __forceinline__ void cluster_sync_all() {
