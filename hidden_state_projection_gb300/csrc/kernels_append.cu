@@ -80,10 +80,12 @@ __global__ void __launch_bounds__(kAppendThreads, 4) hsp_append_kernel(const __g
         const int i = first + threadIdx.x;
         const int row = a.rows ? a.rows[i] : i;
         const bool row_ok = row >= 0 && row < a.num_rows;
-        const int pos = a.positions ? a.positions[i] : row_ok ? a.lens[row] - 1 : -1;
+        const int len = row_ok ? a.lens[row] : 0;
+        const int pos = a.positions ? a.positions[i] : len - 1;
         int page = -1;
         if (row_ok && pos >= 0 && (pos >> a.page_shift) < a.max_pages)
             page = a.table[row * a.table_stride + (pos >> a.page_shift)];
+        if (pos >= len) page = -1;  // behind the row's end, as where its growth found no free page (on the way with the table's entry)
         const bool angle = a.rot > 0 && pos >= 0 && pos < a.max_pos;
         const int64_t line = pos & ((1 << a.page_shift) - 1);
         AppendPlace p;

@@ -468,11 +468,16 @@ typedef struct {
  *              heads dense: a fused projection's output as it is
  *   v_new      device [tokens, kv_heads, v_dim] (NULL for a latent cache)
  *   rows       device [tokens] table rows, or NULL for token i = row i
- *   positions  device [tokens], or NULL for the last place of the row, seq_lens[row] - 1
+ *   positions  device [tokens], each below its row's seq_lens, or NULL for the last place of the
+ *              row, seq_lens[row] - 1
  *   rotary     NULL: rows are copied as they are
  *   q, q_out   device [tokens, heads, k_dim], turned at the same positions; q_out may be q.
  *              NULL q: no queries (and none without rotary).  Strides in elements, multiples of 8.
- * Pages must already hold the positions (proj_cache_resize) and be the row's own.  Two
+ * Pages must already hold the positions (proj_cache_resize) and be the row's own.  A token
+ * whose position is not below seq_lens[row] is written nowhere and reported (PROJ_ERR_BAD_INDEX):
+ * so a step that passes the positions of a growth leaves alone a row that found no free page
+ * (status 1), on whose last page other rows may still be.  Without positions the call takes the
+ * growth to have succeeded: it writes the row's last token whatever that is.  Two
  * tokens of one call must not name the same row and position (which one stays is not
  * defined).  One kernel launch; tokens = 0 succeeds and touches nothing.
  */
