@@ -1,4 +1,5 @@
 // cache_api.cu -- the C entry points of the paged cache: checks of arguments, plans, launches.
+#include <algorithm>
 #include <cmath>
 #include <cstring>
 
@@ -106,6 +107,33 @@ proj_status check_kv(const proj_kv_pages *kv) {
     return PROJ_OK;
 }
 
+// Steps through what a call writes: `extent` places, `stride` apart.
+struct Dim {
+    int64_t extent, stride;
+};
+// Whether places of `inner` units lie apart, as they do where every step (in the order of their strides) is at
+// least as long as all that lies inside it.
+template <size_t N>
+bool nested(Dim (&dims)[N], int64_t inner) {
+    std::sort(dims, dims + N, [](const Dim &x, const Dim &y) { return x.stride < y.stride; });
+    __int128 reach = inner;
+    for (const Dim &d : dims) {
+        if (d.extent <= 1) continue;
+        if (d.stride < reach) return false;
+        reach += static_cast<__int128>(d.stride) * (d.extent - 1);
+    }
+    return true;
+}
+
+// The same of a cache that is written.
+proj_status check_writable(const proj_kv_pages *kv, const proj_page_index *ix) {
+    Dim k[3] = {{ix->num_pages, kv->k_page_stride}, {ix->page_size, kv->k_token_stride}, {kv->kv_heads, kv->k_head_stride}};
+    Dim v[3] = {{ix->num_pages, kv->v_page_stride}, {ix->page_size, kv->v_token_stride}, {kv->kv_heads, kv->v_head_stride}};
+    if (!nested(k, kv->k_dim) || (kv->v && !nested(v, kv->v_dim)))
+        return api_fail(PROJ_ERR_UNSUPPORTED_SHAPE, "pages, tokens and heads of a cache that is written must not overlap");
+    return PROJ_OK;
+}
+
 // Tokens, heads and pages that steps can reach lie apart.
 proj_status check_apart(const proj_kv_pages *kv, const proj_page_index *ix) {
     if (kv->k_token_stride < 8 || (kv->v && kv->v_token_stride < 8))
@@ -156,6 +184,15 @@ proj_status check_pools(const proj_page_pool *pools, int num_pools, hsp::PoolLis
         out->page_bytes[i] = p.page_bytes;
     }
     out->pieces_total = static_cast<int32_t>(total);
+    return PROJ_OK;
+}
+
+// Pages of different layers do not overlap either.
+proj_status check_layers(const proj_page_pool *pools, int num_pools, int num_pages) {
+    for (int i = 0; i < num_pools; ++i) {
+        Dim dims[2] = {{pools[i].layers, pools[i].layer_stride}, {num_pages, pools[i].page_stride}};
+        if (!nested(dims, pools[i].page_bytes)) return api_fail(PROJ_ERR_INVALID_ARG, "pools[%d]: layers overlap", i);
+    }
     return PROJ_OK;
 }
 
@@ -322,7 +359,7 @@ proj_status proj_cache_append(const void *k_new, int64_t k_row_stride, const voi
     const int64_t columns = static_cast<int64_t>(kv->kv_heads) * (kv->k_dim + (kv->v ? kv->v_dim : 0)) +
                             (q ? static_cast<int64_t>(heads) * kv->k_dim : 0);
     if (columns > (1 << 24)) return api_fail(PROJ_ERR_UNSUPPORTED_SHAPE, "%lld columns of a token exceed 2^24", (long long)columns);
-    if ((st = check_apart(kv, index)) != PROJ_OK) return st;
+    if ((st = check_writable(kv, index)) != PROJ_OK) return st;
     if (q && !rotary) return api_fail(PROJ_ERR_INVALID_ARG, "queries are only turned: q needs rotary");
     if (rotary) {
         if (!rotary->cos_sin || rotary->max_pos < 1) return api_fail(PROJ_ERR_INVALID_ARG, "rotary without a table");
@@ -339,6 +376,12 @@ proj_status proj_cache_append(const void *k_new, int64_t k_row_stride, const voi
         return api_fail(PROJ_ERR_MISALIGNED, "k_new, v_new, q and q_out: 16-byte aligned, strides multiples of 8 elements");
     if (!aligned(rows, 4) || !aligned(positions, 4))
         return api_fail(PROJ_ERR_MISALIGNED, "rows and positions must be 4-byte aligned");
+    if (q) {
+        Dim dims[2] = {{tokens, q_out_row_stride}, {heads, q_out_head_stride}};
+        if (!nested(dims, kv->k_dim)) return api_fail(PROJ_ERR_UNSUPPORTED_SHAPE, "tokens and heads of q_out must not overlap");
+        if (q == q_out && ((tokens > 1 && q_row_stride != q_out_row_stride) || (heads > 1 && q_head_stride != q_out_head_stride)))
+            return api_fail(PROJ_ERR_INVALID_ARG, "q_out may be q, with the same strides");
+    }
     hsp::ApiDevice dev;
     if ((st = hsp::api_device(&dev)) != PROJ_OK) return st;
     hsp::AppendArgs a;
@@ -403,6 +446,7 @@ proj_status proj_cache_resize(const proj_page_index *index, const int32_t *rows,
     hsp::ResizeArgs a;
     memset(&a, 0, sizeof a);
     if ((st = check_pools(pools, num_pools, &a.pools)) != PROJ_OK) return st;
+    if ((st = check_layers(pools, num_pools, index->num_pages)) != PROJ_OK) return st;
     if (n < 0) return api_fail(PROJ_ERR_INVALID_ARG, "n=%d is negative", n);
     if (n == 0) return hsp::api_ok();
     if (!rows || !new_lens || !status) return api_fail(PROJ_ERR_INVALID_ARG, "rows, new_lens and status must not be NULL");
@@ -460,6 +504,7 @@ proj_status proj_cache_compact(const proj_page_index *index, const proj_page_poo
     hsp::CompactArgs a;
     memset(&a, 0, sizeof a);
     if ((st = check_pools(pools, num_pools, &a.pools)) != PROJ_OK) return st;
+    if ((st = check_layers(pools, num_pools, index->num_pages)) != PROJ_OK) return st;
     if (!live) return api_fail(PROJ_ERR_INVALID_ARG, "live must not be NULL");
     if (!aligned(live, 4)) return api_fail(PROJ_ERR_MISALIGNED, "live must be 4-byte aligned");
     const CacheWorkspace w = cache_workspace(index, 0);
@@ -486,6 +531,7 @@ proj_status proj_cache_copy_pages(const proj_page_pool *pools, int32_t num_pools
     if (st != PROJ_OK) return st;
     if (n < 0 || num_pages < 0) return api_fail(PROJ_ERR_INVALID_ARG, "negative size (n=%d num_pages=%d)", n, num_pages);
     if (n > PROJ_MAX_COPY_PAIRS) return api_fail(PROJ_ERR_UNSUPPORTED_SHAPE, "n=%d exceeds %d pairs", n, PROJ_MAX_COPY_PAIRS);
+    if ((st = check_layers(pools, num_pools, num_pages)) != PROJ_OK) return st;
     if (n == 0) return hsp::api_ok();
     if (!src || !dst) return api_fail(PROJ_ERR_INVALID_ARG, "src and dst must not be NULL");
     // destinations in a table of their own: a second one, or a source among them, is refused

@@ -390,7 +390,8 @@ typedef struct {
 
 /* The keys and values of one layer, bf16.  Token `t` of page `p`, kv head `h`: k_dim
  * consecutive elements at k + p * k_page_stride + t * k_token_stride + h * k_head_stride
- * (elements; multiples of 8, so either order of tokens and heads in a page will do).
+ * (elements; multiples of 8, so either order of tokens and heads in a page will do; where the
+ * cache is written, each step at least as long as all that lies inside it).
  *   latent cache: v = NULL, k_dim 576 or 512, v_dim 512: the values are the first 512
  *                 columns of the keys (compressed KV ++ k_pe, or the wkv projection);
  *   grouped cache: v of its own, k_dim = v_dim = 64 or 128. */
@@ -405,7 +406,8 @@ typedef struct {
 
 /* Page data for the calls that move whole pages: `layers` arrays of num_pages pages.
  * Page p of layer l is page_bytes consecutive bytes at base + l * layer_stride +
- * p * page_stride (bytes, all multiples of 16; base 16-byte aligned). */
+ * p * page_stride (bytes, all multiples of 16; base 16-byte aligned; pages and layers do not
+ * overlap, the shorter step inside the longer one). */
 typedef struct {
     void *base;
     int64_t layer_stride, page_stride, page_bytes;
@@ -471,7 +473,8 @@ typedef struct {
  *   positions  device [tokens], each below its row's seq_lens, or NULL for the last place of the
  *              row, seq_lens[row] - 1
  *   rotary     NULL: rows are copied as they are
- *   q, q_out   device [tokens, heads, k_dim], turned at the same positions; q_out may be q.
+ *   q, q_out   device [tokens, heads, k_dim], turned at the same positions; q_out may be q (with
+ *              its strides), its own tokens and heads do not overlap.
  *              NULL q: no queries (and none without rotary).  Strides in elements, multiples of 8.
  * Pages must already hold the positions (proj_cache_resize) and be the row's own.  A token
  * whose position is not below seq_lens[row] is written nowhere and reported (PROJ_ERR_BAD_INDEX):
