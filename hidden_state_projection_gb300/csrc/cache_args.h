@@ -120,6 +120,7 @@ struct IndexArgs {
 // One row of a resize (workspace).
 struct RowPlan {
     int32_t row;                     // -1: nothing to do
+    int32_t len;                     // its new length
     int32_t have, want;              // pages before and after
     int32_t first;                   // its first entry in the free list
     int32_t cow_src;                 // the shared last page to copy, -1: none

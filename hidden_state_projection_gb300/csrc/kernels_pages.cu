@@ -191,7 +191,7 @@ __global__ void __launch_bounds__(kPlanThreads) hsp_resize_plan_kernel(const __g
         const int i = i0 + tid;
         RowPlan p;
         p.row = -1;
-        p.have = p.want = p.first = 0;
+        p.len = p.have = p.want = p.first = 0;
         p.cow_src = -1;
         int need = 0;
         if (i < a.n) {
@@ -202,6 +202,7 @@ __global__ void __launch_bounds__(kPlanThreads) hsp_resize_plan_kernel(const __g
                 const int old = ix.lens[r];
                 if (old >= 0 && old <= most) {
                     p.row = r;
+                    p.len = want;
                     p.have = pages_of(old, ix.page_shift);
                     p.want = pages_of(want, ix.page_shift);
                     if (want > old && (old & ((1 << ix.page_shift) - 1)) != 0) {
@@ -263,7 +264,8 @@ __global__ void __launch_bounds__(kPlanThreads) hsp_resize_plan_kernel(const __g
         }
     }
     __syncthreads();
-    // rows whose pages were found change, in the order of the call; the others stay as they are
+    // rows whose pages were found change, in the order of the call; the others stay as they are (all of the
+    // request has been read: new_lens may be seq_lens, or a part of it)
     for (int i = tid; i < a.n; i += kPlanThreads) {
         RowPlan p = a.plan[i];
         int st = 2;
@@ -271,7 +273,7 @@ __global__ void __launch_bounds__(kPlanThreads) hsp_resize_plan_kernel(const __g
             const int need = max(0, p.want - p.have) + (p.cow_src >= 0 ? 1 : 0);
             if (need == 0 || static_cast<int64_t>(p.first) + need <= found) {
                 st = 0;
-                ix.lens[p.row] = a.new_lens[i];
+                ix.lens[p.row] = p.len;
                 if (p.cow_src >= 0) a.pairs[atomicAdd(&pair_count, 1)] = make_int2(p.cow_src, a.list[p.first]);
             } else {
                 st = 1;
@@ -392,7 +394,7 @@ __global__ void __launch_bounds__(kPlanThreads) hsp_resize_team_kernel(const __g
     __syncthreads();
     RowPlan p;
     p.row = p.cow_src = -1;
-    p.have = p.want = p.first = 0;
+    p.len = p.have = p.want = p.first = 0;
     int need = 0;
     if (in && named.first[h] == tid && want >= 0 && want <= most) {
         if (old >= 0 && old <= most) {

@@ -493,7 +493,8 @@ proj_status proj_cache_append(const void *k_new, int64_t k_row_stride, const voi
                               int32_t heads, proj_stream_t stream);
 
 /*
- * proj_cache_resize -- sets the lengths of n rows: rows[i] gets new_lens[i] tokens.
+ * proj_cache_resize -- sets the lengths of n rows: rows[i] gets new_lens[i] tokens (new_lens may
+ * lie in seq_lens: the lengths are those before the call).
  * Growing takes the lowest free pages, in the order of the call (the pages free when the
  * call starts); a row that grows and whose last page is partly filled and held by other
  * rows too gets a copy of that page (over all pools) first, so what is appended next

@@ -78,3 +78,18 @@ def test_append_at_and_behind_the_end(hsp):  # noqa: F811
     hsp.cache_append(kn, None, k, None, table, ints([16, 3]), rows=ints([0, 1]), positions=ints([16, 3]))
     expect_bad_index(hsp)
     assert not k.any()
+
+
+@pytest.mark.parametrize("rows,pages", [(200, 900), (3000, 9000)])
+def test_new_lengths_that_lie_in_the_lengths(hsp, rows, pages):  # noqa: F811
+    """rows[i] gets the length that row i had: every length is read before any is changed, in one launch and in two."""
+    c = Cache(hsp, rows, 4, pages, 16, rows)
+    rng = np.random.RandomState(rows)
+    c.resize(range(rows), rng.randint(0, 65, rows))
+    for step in range(8):
+        who = rng.permutation(rows)
+        n = rows if step % 2 else rows - 1
+        st = hsp.cache_resize(c.table, c.lens, c.refs, c.t(who[:n]), c.lens[:n], 16, c.pools)
+        assert st.tolist() == c.model.resize(list(who[:n]), list(c.model.lens[:n]))
+        c.check()
+    hsp.check_device_error()
