@@ -455,11 +455,19 @@ def _new(like: torch.Tensor, shape, dtype, stream) -> torch.Tensor:
     return _made(torch.empty(shape, dtype=dtype, device=like.device), stream)
 
 
+def _ranks(*pairs) -> bool:
+    """Whether these are CUDA tensors of these ranks (what is not, the call itself refuses)."""
+    return all(isinstance(t, torch.Tensor) and t.is_cuda and t.dim() == d for t, d in pairs)
+
+
 def paged_attention_workspace_bytes(heads: int, kv_heads: int, k_dim: int, v_dim: int, latent: bool) -> int:
     """Workspace bytes of proj_paged_attention (raises if the heads and columns are not supported)."""
     n = int(lib().proj_paged_attention_workspace_bytes(heads, kv_heads, k_dim, v_dim, int(latent)))
-    if n == 0:
-        raise ProjError(2, lib().proj_last_error_string().decode())
+    if n == 0:  # the same heads and columns in a call without sequences: refused with the status that goes with the text
+        kv = struct.pack("PPiiiiqqqqqq", 16, 0 if latent else 16, kv_heads, k_dim, v_dim, 0, *[1 << 20, 1 << 10, 8] * 2)
+        index = struct.pack("PqPPiiii", 16, 1, 16, 16, 1, 1, 1, 16)
+        _check(lib().proj_paged_attention(None, 0, 0, kv, index, None, 0, heads, 1.0, None, None, None, 0, None))
+        raise ProjError(2, "unsupported heads and columns")
     return n
 
 
@@ -473,15 +481,16 @@ def paged_attention(q: torch.Tensor, k_pages: torch.Tensor, v_pages: Optional[to
     [rows] int32; `rows` maps batch entries to table rows.  Returns out [batch, heads, v_dim], or (out, lse) with
     return_lse.  `workspace` (paged_attention_workspace_bytes) is taken from torch per call if not given."""
     if stream is not None:
-        batch, heads, k_dim = q.shape
-        dv = v_pages.shape[3] if v_pages is not None else 512 if v_dim is None else v_dim
-        if out is None:
-            out = _new(q, (batch, heads, dv), torch.bfloat16, stream)
-        if lse is None and return_lse:
-            lse = _new(q, (batch, heads), torch.float32, stream)
-        if workspace is None:
-            workspace = _new(q, paged_attention_workspace_bytes(heads, k_pages.shape[2], k_dim, dv, v_pages is None),
-                             torch.uint8, stream)
+        if _ranks((q, 3), (k_pages, 4)) and (v_pages is None or _ranks((v_pages, 4))):
+            batch, heads, k_dim = q.shape
+            dv = v_pages.shape[3] if v_pages is not None else 512 if v_dim is None else v_dim
+            if workspace is None:
+                workspace = _new(q, paged_attention_workspace_bytes(heads, k_pages.shape[2], k_dim, dv, v_pages is None),
+                                 torch.uint8, stream)
+            if out is None:
+                out = _new(q, (batch, heads, dv), torch.bfloat16, stream)
+            if lse is None and return_lse:
+                lse = _new(q, (batch, heads), torch.float32, stream)
         stream = _stream_ptr(stream)
     return (_cache or _cache_py()).paged_attention(q, k_pages, v_pages, block_table, seq_lens, scale, -1 if v_dim is None else v_dim,
                                                    rows, out, lse, return_lse, workspace, stream)
@@ -496,7 +505,7 @@ def cache_append(k_new: torch.Tensor, v_new: Optional[torch.Tensor], k_pages: to
     page, is written nowhere and reported; without positions the row is taken to have grown.  cos_sin [max_pos, rot] fp32 turns the last `rot` columns of the keys and
     of the queries q [tokens, heads, k_dim] on the way; returns the turned queries (q_out; may be q), or None."""
     if stream is not None:
-        if q is not None and q_out is None:
+        if q is not None and q_out is None and _ranks((q, 3)):
             q_out = _new(q, q.shape, torch.bfloat16, stream)
         stream = _stream_ptr(stream)
     return (_cache or _cache_py()).cache_append(k_new, v_new, k_pages, v_pages, block_table, seq_lens, rows, positions, cos_sin,
@@ -508,8 +517,9 @@ def cache_workspace_bytes(block_table: torch.Tensor, num_pages: int, n: int) -> 
     rows, width = block_table.shape
     index = struct.pack("PqPPiiii", 16, width, 16, 16, rows, width, num_pages, 16)  # a proj_page_index of these sizes
     need = int(lib().proj_cache_workspace_bytes(index, n))
-    if need == 0:
-        raise ProjError(2, lib().proj_last_error_string().decode())
+    if need == 0:  # (see paged_attention_workspace_bytes)
+        _check(lib().proj_cache_fork(index, None, None, min(n, 0), None, None))
+        raise ProjError(2, "unsupported sizes")
     return need
 
 
@@ -520,11 +530,12 @@ def cache_resize(block_table: torch.Tensor, seq_lens: torch.Tensor, ref_counts: 
     page, over all pools [layers, num_pages, ...]), shrinking gives pages back, 0 frees the row.  Returns the status
     per row: 0 done, 1 not enough free pages, 2 refused."""
     if stream is not None:
-        n = rows.shape[0]
-        if status is None:
-            status = _new(rows, n, torch.int32, stream)
-        if workspace is None:
-            workspace = _new(rows, cache_workspace_bytes(block_table, ref_counts.shape[0], n), torch.uint8, stream)
+        if _ranks((block_table, 2), (ref_counts, 1), (rows, 1)):
+            n = rows.shape[0]
+            if workspace is None:
+                workspace = _new(rows, cache_workspace_bytes(block_table, ref_counts.shape[0], n), torch.uint8, stream)
+            if status is None:
+                status = _new(rows, n, torch.int32, stream)
         stream = _stream_ptr(stream)
     return (_cache or _cache_py()).cache_resize(block_table, seq_lens, ref_counts, rows, new_lens, page_size, pools, status,
                                                 workspace, stream)
@@ -534,7 +545,7 @@ def cache_fork(block_table: torch.Tensor, seq_lens: torch.Tensor, ref_counts: to
                children: torch.Tensor, page_size: int, status: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """children[i], an empty row, shares every page of parents[i].  Returns the status per child: 0 done, 2 refused."""
     if stream is not None:
-        if status is None:
+        if status is None and _ranks((parents, 1)):
             status = _new(parents, parents.shape[0], torch.int32, stream)
         stream = _stream_ptr(stream)
     return (_cache or _cache_py()).cache_fork(block_table, seq_lens, ref_counts, parents, children, page_size, status, stream)
@@ -546,10 +557,11 @@ def cache_compact(block_table: torch.Tensor, seq_lens: torch.Tensor, ref_counts:
     """Moves the live pages into the first places of the pools; tables and counts follow.  Returns `live` [1], the
     number of live pages."""
     if stream is not None:
-        if live is None:
-            live = _new(ref_counts, 1, torch.int32, stream)
-        if workspace is None:
-            workspace = _new(ref_counts, cache_workspace_bytes(block_table, ref_counts.shape[0], 0), torch.uint8, stream)
+        if _ranks((block_table, 2), (ref_counts, 1)):
+            if workspace is None:
+                workspace = _new(ref_counts, cache_workspace_bytes(block_table, ref_counts.shape[0], 0), torch.uint8, stream)
+            if live is None:
+                live = _new(ref_counts, 1, torch.int32, stream)
         stream = _stream_ptr(stream)
     return (_cache or _cache_py()).cache_compact(block_table, seq_lens, ref_counts, page_size, pools, live, workspace, stream)
 

@@ -232,9 +232,10 @@ struct Workspace {
     void *ptr = nullptr;
     size_t bytes = 0;
 };
+// `need` of 0: sizes that the C call refuses, which then says why.
 void use(Workspace *w, const at::Tensor &given, size_t need) {
     if (!given.defined()) {
-        if (need == 0) refuse(PROJ_ERR_UNSUPPORTED_SHAPE, "%s", proj_last_error_string());
+        if (need == 0) return;
         w->own = c10::GetAllocator(c10::kCUDA)->allocate(need);
         w->ptr = w->own.get();
         w->bytes = need;
