@@ -455,6 +455,11 @@ def _new(like: torch.Tensor, shape, dtype, stream) -> torch.Tensor:
     return _made(torch.empty(shape, dtype=dtype, device=like.device), stream)
 
 
+def _i32(v: int) -> int:
+    """A size for a 32-bit argument: what does not fit is out of its range anyway."""
+    return max(-2 ** 31, min(int(v), 2 ** 31 - 1))
+
+
 def _ranks(*pairs) -> bool:
     """Whether these are CUDA tensors of these ranks (what is not, the call itself refuses)."""
     return all(isinstance(t, torch.Tensor) and t.is_cuda and t.dim() == d for t, d in pairs)
@@ -462,6 +467,7 @@ def _ranks(*pairs) -> bool:
 
 def paged_attention_workspace_bytes(heads: int, kv_heads: int, k_dim: int, v_dim: int, latent: bool) -> int:
     """Workspace bytes of proj_paged_attention (raises if the heads and columns are not supported)."""
+    heads, kv_heads, k_dim, v_dim = _i32(heads), _i32(kv_heads), _i32(k_dim), _i32(v_dim)
     n = int(lib().proj_paged_attention_workspace_bytes(heads, kv_heads, k_dim, v_dim, int(latent)))
     if n == 0:  # the same heads and columns in a call without sequences: refused with the status that goes with the text
         kv = struct.pack("PPiiiiqqqqqq", 16, 0 if latent else 16, kv_heads, k_dim, v_dim, 0, *[1 << 20, 1 << 10, 8] * 2)
@@ -492,7 +498,7 @@ def paged_attention(q: torch.Tensor, k_pages: torch.Tensor, v_pages: Optional[to
             if lse is None and return_lse:
                 lse = _new(q, (batch, heads), torch.float32, stream)
         stream = _stream_ptr(stream)
-    return (_cache or _cache_py()).paged_attention(q, k_pages, v_pages, block_table, seq_lens, scale, -1 if v_dim is None else v_dim,
+    return (_cache or _cache_py()).paged_attention(q, k_pages, v_pages, block_table, seq_lens, scale, v_dim,
                                                    rows, out, lse, return_lse, workspace, stream)
 
 
@@ -515,6 +521,7 @@ def cache_append(k_new: torch.Tensor, v_new: Optional[torch.Tensor], k_pages: to
 def cache_workspace_bytes(block_table: torch.Tensor, num_pages: int, n: int) -> int:
     """Workspace bytes of cache_resize over n rows (cache_compact: n = 0)."""
     rows, width = block_table.shape
+    num_pages, n = _i32(num_pages), _i32(n)
     index = struct.pack("PqPPiiii", 16, width, 16, 16, rows, width, num_pages, 16)  # a proj_page_index of these sizes
     need = int(lib().proj_cache_workspace_bytes(index, n))
     if need == 0:  # (see paged_attention_workspace_bytes)

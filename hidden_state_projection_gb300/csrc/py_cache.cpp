@@ -10,6 +10,7 @@
 
 #include <ATen/ATen.h>
 
+#include <algorithm>
 #include <cstdarg>
 #include <cstdio>
 #include <exception>
@@ -82,7 +83,7 @@ bool truth(PyObject *o) {
     return v != 0;
 }
 // Sizes that the C ABI takes as 32 bits: what does not fit is out of its range anyway.
-int32_t narrow(int64_t v) { return v > INT32_MAX ? INT32_MAX : static_cast<int32_t>(v); }
+int32_t narrow(int64_t v) { return static_cast<int32_t>(std::min<int64_t>(std::max<int64_t>(v, INT32_MIN), INT32_MAX)); }
 
 // The current CUDA device, which every tensor must be on.
 int device_of(std::initializer_list<const at::Tensor *> tensors) {
@@ -146,7 +147,10 @@ proj_page_index page_index(const at::Tensor &table, const at::Tensor &lens, cons
     return ix;
 }
 
-proj_kv_pages kv_pages(const at::Tensor &k, const at::Tensor &v, int64_t v_dim) {
+// v_dim None: the values' columns, or 512 of a latent cache.
+proj_kv_pages kv_pages(const at::Tensor &k, const at::Tensor &v, PyObject *v_dim_or_none) {
+    const bool given = v_dim_or_none != Py_None;
+    const int64_t v_dim = given ? integer(v_dim_or_none) : 512;
     if (k.dim() != 4 || k.stride(3) != 1)
         refuse(PROJ_ERR_INVALID_ARG, "k_pages must be a [num_pages, page_size, kv_heads, k_dim] tensor with dense columns");
     if (k.scalar_type() != at::kBFloat16 || (v.defined() && v.scalar_type() != at::kBFloat16))
@@ -159,12 +163,12 @@ proj_kv_pages kv_pages(const at::Tensor &k, const at::Tensor &v, int64_t v_dim) 
     p.k_token_stride = k.stride(1);
     p.k_head_stride = k.stride(2);
     if (!v.defined()) {
-        p.v_dim = narrow(v_dim < 0 ? 512 : v_dim);
+        p.v_dim = narrow(v_dim);
         return p;
     }
     if (v.dim() != 4 || v.stride(3) != 1 || v.size(0) != k.size(0) || v.size(1) != k.size(1) || v.size(2) != k.size(2))
         refuse(PROJ_ERR_INVALID_ARG, "v_pages must be a [num_pages, page_size, kv_heads, v_dim] tensor like k_pages");
-    if (v_dim >= 0 && v_dim != v.size(3))
+    if (given && v_dim != v.size(3))
         refuse(PROJ_ERR_INVALID_ARG, "v_dim=%lld, but v_pages has %lld columns", (long long)v_dim, (long long)v.size(3));
     p.v = v.data_ptr();
     p.v_dim = narrow(v.size(3));
@@ -253,7 +257,7 @@ void arguments(Py_ssize_t have, Py_ssize_t want) {
     }
 }
 
-// (q, k_pages, v_pages, block_table, seq_lens, scale, v_dim or -1, rows, out, lse, return_lse, workspace, stream)
+// (q, k_pages, v_pages, block_table, seq_lens, scale, v_dim, rows, out, lse, return_lse, workspace, stream)
 PyObject *paged_attention(PyObject *, PyObject *const *args, Py_ssize_t nargs) {
     return guarded([&]() -> PyObject * {
         arguments(nargs, 13);
@@ -266,11 +270,13 @@ PyObject *paged_attention(PyObject *, PyObject *const *args, Py_ssize_t nargs) {
         const bool return_lse = truth(args[10]);
         const at::Tensor given = optional(args[11], "workspace");
         const int dev = device_of({&q, &k, &v, &table, &lens, &rows, &out, &lse, &given});
-        const proj_kv_pages kv = kv_pages(k, v, integer(args[6]));
+        const proj_kv_pages kv = kv_pages(k, v, args[6]);
         if (q.dim() != 3 || q.size(2) != kv.k_dim || q.stride(2) != 1)
             refuse(PROJ_ERR_INVALID_ARG, "q must be a [batch, heads, k_dim] tensor with dense columns");
         if (q.scalar_type() != at::kBFloat16) refuse(PROJ_ERR_UNSUPPORTED_DTYPE, "unsupported tensor dtype %s", c10::toString(q.scalar_type()));
         const int64_t batch = q.size(0), heads = q.size(1), dv = kv.v_dim;
+        if (dv < 1 || dv > kv.k_dim)  // (before out is made)
+            refuse(PROJ_ERR_UNSUPPORTED_SHAPE, "k_dim=%d, v_dim=%d: the values are at most as wide as the keys", kv.k_dim, kv.v_dim);
         const proj_page_index ix = page_index(table, lens, at::Tensor(), k.size(0), k.size(1));
         if (!out.defined()) out = make({batch, heads, dv}, at::kBFloat16, dev);
         else if (out.sizes() != at::IntArrayRef({batch, heads, dv}) || out.scalar_type() != at::kBFloat16 || !out.is_contiguous())
@@ -324,7 +330,7 @@ PyObject *cache_append(PyObject *, PyObject *const *args, Py_ssize_t nargs) {
         const at::Tensor q = optional(args[10], "q");
         at::Tensor q_out = optional(args[11], "q_out");
         const int dev = device_of({&kn, &vn, &k, &v, &table, &lens, &rows, &pos, &cs, &q, &q_out});
-        const proj_kv_pages kv = kv_pages(k, v, -1);
+        const proj_kv_pages kv = kv_pages(k, v, Py_None);
         if (kn.dim() < 1) refuse(PROJ_ERR_INVALID_ARG, "k_new must be [tokens, ...]");
         const int64_t tokens = kn.size(0), dim = kv.k_dim;
         if (vn.defined() != v.defined()) refuse(PROJ_ERR_INVALID_ARG, "v_new goes with a cache that has values of its own");

@@ -94,3 +94,23 @@ def test_what_is_wrong_with_a_workspace(hsp):  # noqa: F811
                                               None) == hsp.STATUS["PROJ_ERR_" + want]
     assert hsp.launch_count() == n
     hsp.check_device_error()
+
+
+def test_sizes_that_do_not_fit_32_bits(hsp):  # noqa: F811
+    """Sizes far outside their range are refused, not cut to 32 bits; a negative v_dim is none of the defaults."""
+    q, k = torch.zeros(1, 16, 576, dtype=BF, device="cuda"), torch.zeros(4, 16, 1, 576, dtype=BF, device="cuda")
+    table, lens, refs, pool = ints(1, 4), ints(1), ints(4), torch.zeros(1, 4, 16, 8, dtype=BF, device="cuda")
+    for big in (2 ** 32, -2 ** 32, 2 ** 40, -2 ** 40):
+        want = "PROJ_ERR_UNSUPPORTED_SHAPE"
+        for stream in (None, torch.cuda.Stream()):
+            assert refusal(hsp, lambda: hsp.paged_attention(q, k, None, table, lens, 0.1, v_dim=512 + big, stream=stream))[0] == want
+        assert refusal(hsp, lambda: hsp.cache_resize(table, lens, refs, lens, lens, 16 + big, [pool]))[0] == want
+        assert refusal(hsp, lambda: hsp.cache_fork(table, lens, refs, lens, lens, 16 + big))[0] == want
+        assert refusal(hsp, lambda: hsp.cache_compact(table, lens, refs, 16 + big, [pool]))[0] == want
+    for v_dim in (-1, -2, 0, 576):
+        assert refusal(hsp, lambda: hsp.paged_attention(q, k, None, table, lens, 0.1, v_dim=v_dim))[0] == "PROJ_ERR_UNSUPPORTED_SHAPE"
+    g = torch.zeros(4, 16, 1, 64, dtype=BF, device="cuda")
+    for v_dim in (-1, 63, 64 + 2 ** 32):
+        assert refusal(hsp, lambda: hsp.paged_attention(q[..., :64], g, g, table, lens, 0.1, v_dim=v_dim))[0] == "PROJ_ERR_INVALID_ARG"
+    assert not hsp.paged_attention(q, k, None, table, lens, 0.1, v_dim=512).any()
+    hsp.check_device_error()
