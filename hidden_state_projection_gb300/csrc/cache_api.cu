@@ -557,8 +557,7 @@ proj_status proj_cache_copy_pages(const proj_page_pool *pools, int32_t num_pools
             return api_fail(PROJ_ERR_INVALID_ARG, "page %d is a source and a destination", src[i]);
     hsp::ApiDevice dev;
     if ((st = hsp::api_device(&dev)) != PROJ_OK) return st;
-    const cudaError_t e = hsp::launch_copy_pages(pl, src, dst, n, dev.sms, hsp::api_options().pdl,
-                                                 reinterpret_cast<cudaStream_t>(stream));
+    const cudaError_t e = hsp::launch_copy_pages(pl, src, dst, n, hsp::api_options().pdl, reinterpret_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return hsp::api_cuda_fail(e, "kernel launch (cache copy)");
     hsp::api_count_launches(1);
     return hsp::api_ok();

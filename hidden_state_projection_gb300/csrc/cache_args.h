@@ -16,7 +16,7 @@ constexpr int kAttnThreads = 224;   // four softmax warps, the copy producer, th
 __host__ __device__ constexpr int attn_part(int dv, int N) { return N * dv + 3 * N; }
 
 // One sequence part that a CTA began and another one finishes: what the join adds up.
-// Entry c belongs to CTA c of the length axis; first < 0: CTA c began no such part.
+// Entry c belongs to CTA c of the length axis; batch < 0: CTA c began no such part.
 struct AttnEntry {
     int32_t batch;   // sequence (row of q), -1: none
     int32_t kv_head;
@@ -173,7 +173,6 @@ struct CompactArgs {
 cudaError_t launch_compact(const CompactArgs &a, int sms, int pdl, cudaStream_t stream);
 
 // n pairs of host arrays (n <= kMaxCopyPairs), passed by value.
-cudaError_t launch_copy_pages(const PoolList &pools, const int32_t *src, const int32_t *dst, int n, int sms, int pdl,
-                              cudaStream_t stream);
+cudaError_t launch_copy_pages(const PoolList &pools, const int32_t *src, const int32_t *dst, int n, int pdl, cudaStream_t stream);
 
 }  // namespace hsp

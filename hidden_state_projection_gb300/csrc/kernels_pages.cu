@@ -17,8 +17,10 @@
 //           meet) and hsp_compact_apply_kernel
 //   copy    hsp_copy_pages_kernel (pairs by value, checked on the host)
 //
-// The plan kernels are bound by latency: a warp takes a contiguous share of the counts, four
-// 16-byte loads of every lane in flight, one block-wide prefix sum per pass.  The moves are
+// The plan kernels are bound by latency: a warp takes a contiguous share of the counts, 128 at a
+// time (four 4-byte loads of every lane in flight), sums by shuffles, the warps' sums in shared
+// memory; resize reads the counts twice (how many are free, which), compaction three times (how
+// many are live, how many holes and tails lie in front of a warp's share, which).  The moves are
 // bound by memory: 16 KB pieces, four 16-byte loads per thread before the stores, and CTAs that
 // take the pieces in order as they get free: 6000 pages of 73,728 bytes took 144 us with a fixed
 // stride over a resident grid (6.1 TB/s), 133 us in order (6.67 TB/s, the rate of a plain
@@ -543,13 +545,9 @@ __global__ void __launch_bounds__(kPlanThreads) hsp_compact_plan_kernel(const __
     for (int d = 16; d > 0; d >>= 1) live += __shfl_xor_sync(0xffffffffu, live, d);
     if (lane == 0) warp_live[warp] = live;
     __syncthreads();
-    int L = 0, before = 0;
-    for (int w = 0; w < kPlanWarps; ++w) {
-        if (w < warp) before += warp_live[w];
-        L += warp_live[w];
-    }
-    // free pages before L in front of this warp's share, and live pages at or past L in front of it: all
-    // but the warp that L falls into know both from the counts
+    int L = 0;
+    for (int w = 0; w < kPlanWarps; ++w) L += warp_live[w];
+    // free pages before L, and live pages at or past L, in this warp's share (read again, now that L is known)
     int holes = 0, tails = 0;
     for (int j0 = lo; j0 < hi; j0 += 128) {
 #pragma unroll
@@ -667,8 +665,7 @@ cudaError_t launch_one(void (*kern)(Args), const Args &a, int64_t ctas, int thre
 }
 
 template <int PAIRS>
-cudaError_t launch_copy(const PoolList &pools, const int32_t *src, const int32_t *dst, int n, int sms, int pdl,
-                        cudaStream_t stream) {
+cudaError_t launch_copy(const PoolList &pools, const int32_t *src, const int32_t *dst, int n, int pdl, cudaStream_t stream) {
     CopyArgs<PAIRS> a;
     a.pools = pools;
     a.n = n;
@@ -676,7 +673,6 @@ cudaError_t launch_copy(const PoolList &pools, const int32_t *src, const int32_t
         a.src[i] = src[i];
         a.dst[i] = dst[i];
     }
-    (void)sms;
     int64_t ctas = static_cast<int64_t>(n) * pools.pieces_total;  // one each: they start in order
     if (ctas > 0x7fffffff) ctas = 0x7fffffff;
     return launch_one(hsp_copy_pages_kernel<PAIRS>, a, ctas, kPagesThreads, pdl, stream);
@@ -684,10 +680,9 @@ cudaError_t launch_copy(const PoolList &pools, const int32_t *src, const int32_t
 
 }  // namespace
 
-cudaError_t launch_copy_pages(const PoolList &pools, const int32_t *src, const int32_t *dst, int n, int sms, int pdl,
-                              cudaStream_t stream) {
-    if (n <= 64) return launch_copy<64>(pools, src, dst, n, sms, pdl, stream);
-    return launch_copy<kMaxCopyPairs>(pools, src, dst, n, sms, pdl, stream);
+cudaError_t launch_copy_pages(const PoolList &pools, const int32_t *src, const int32_t *dst, int n, int pdl, cudaStream_t stream) {
+    if (n <= 64) return launch_copy<64>(pools, src, dst, n, pdl, stream);
+    return launch_copy<kMaxCopyPairs>(pools, src, dst, n, pdl, stream);
 }
 
 cudaError_t launch_resize(const ResizeArgs &a, int sms, int pdl, cudaStream_t stream) {
