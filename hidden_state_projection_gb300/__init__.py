@@ -509,7 +509,8 @@ def cache_append(k_new: torch.Tensor, v_new: Optional[torch.Tensor], k_pages: to
     """The new tokens' keys [tokens, (kv_heads,) k_dim] and values into their pages, at positions[i] of row rows[i]
     (default: the last place of row i).  A position at or past seq_lens[row], as where cache_resize found no free
     page, is written nowhere and reported; without positions the row is taken to have grown.  cos_sin [max_pos, rot] fp32 turns the last `rot` columns of the keys and
-    of the queries q [tokens, heads, k_dim] on the way; returns the turned queries (q_out; may be q), or None."""
+    of the queries q [tokens, heads, k_dim] on the way (a model that turns the first ones: lay out the rows of its query
+    and key weights rolled by `rot` within each head; scores stay the same); returns the turned queries (q_out; may be q), or None."""
     if stream is not None:
         if q is not None and q_out is None and _ranks((q, 3)):
             q_out = _new(q, q.shape, torch.bfloat16, stream)

@@ -454,7 +454,10 @@ size_t proj_paged_attention_workspace_bytes(int32_t heads, int32_t kv_heads, int
 /* Rotary turn of proj_cache_append: the last `dim` columns of a key or query row, in pairs
  * (2j, 2j + 1) if interleaved, else (j, j + dim / 2):
  *     (a, b) -> (a cos - b sin, b cos + a sin)
- * with the cosines in cos_sin[pos][0 .. dim / 2) and the sines behind them. */
+ * with the cosines in cos_sin[pos][0 .. dim / 2) and the sines behind them.
+ * Scores do not depend on the order of columns that queries and keys share.  So where a model
+ * turns the FIRST dim columns of a head, its query and key projections give their rows of each
+ * head rolled by dim (the columns that are not turned first), once, when the weights are laid out. */
 typedef struct {
     const float *cos_sin;  /* device [max_pos, dim] fp32, 16-byte aligned */
     int32_t max_pos;

@@ -67,3 +67,48 @@ def test_layouts(hsp, kind, n, heads, kv, dk, latent, rot, inter):  # noqa: F811
     q0[..., 8:8 + dk] = qw[..., 8:8 + dk]
     assert torch.equal(qw, q0)
     hsp.check_device_error()
+
+
+@pytest.mark.parametrize("heads,kv,dk,rot,inter", [(8, 2, 128, 64, False), (4, 4, 64, 32, True), (6, 1, 128, 32, False)])
+def test_models_that_turn_the_first_columns(hsp, heads, kv, dk, rot, inter):  # noqa: F811
+    """Weights whose rows are rolled by `rot` within each head put the columns to turn last; the attention is that of
+    the model as it is written, which turns the first columns."""
+    g = torch.Generator(device="cuda").manual_seed(heads)
+    K, n, page = 256, 70, 16
+    wq, wk, wv = ((torch.randn(h, dk, K, generator=g, device="cuda") * K ** -0.5).to(BF) for h in (heads, kv, kv))
+    x = torch.randn(n, K, generator=g, device="cuda").to(BF)
+    ang = torch.rand(n, rot // 2, generator=g, device="cuda") * 6.3
+    cs = torch.cat([ang.cos(), ang.sin()], 1).contiguous()
+    laid_out = torch.cat([w.roll(-rot, 1).reshape(-1, K) for w in (wq, wk)] + [wv.reshape(-1, K)])
+    k, v = (torch.zeros(8, page, kv, dk, dtype=BF, device="cuda") for _ in range(2))
+    table = torch.tensor([[5, 2, 7, 0, 4]], dtype=torch.int32, device="cuda")
+    out = []
+    for t in range(n):                                      # decode, token by token
+        lens = torch.tensor([t + 1], dtype=torch.int32, device="cuda")
+        q, kn, vn = hsp.fused_gemm(x[t:t + 1], laid_out, [heads * dk, kv * dk, kv * dk])
+        q = hsp.cache_append(kn, vn, k, v, table, lens, cos_sin=cs, interleaved=inter, q=q.view(1, heads, dk))
+        out.append(hsp.paged_attention(q, k, v, table, lens, dk ** -0.5))
+    hsp.check_device_error()
+    # the model in 64 bits, its projections rounded as the library's are
+
+    def project(w):
+        return torch.stack([hsp.fused_gemm(x[t:t + 1], w.reshape(-1, K), [w.shape[0] * dk])[0][0] for t in range(n)]).view(n, -1, dk)
+
+    def first(y):
+        half, c, s = rot // 2, ang.double().cos()[:, None], ang.double().sin()[:, None]
+        y = y.double().clone()
+        one, two = (slice(0, rot, 2), slice(1, rot, 2)) if inter else (slice(0, half), slice(half, rot))
+        a, b = y[..., one].clone(), y[..., two].clone()
+        y[..., one], y[..., two] = a * c - b * s, b * c + a * s
+        return y
+
+    qq, kk, vv = first(project(wq)), first(project(wk)), project(wv).double()
+    for t in range(n):
+        for h in range(heads):
+            keys, vals = kk[:t + 1, h * kv // heads], vv[:t + 1, h * kv // heads]
+            sc = keys @ qq[t, h] * dk ** -0.5
+            p = torch.softmax(sc, 0)
+            # turned queries and keys are rounded once more: scores off by 2^-7 of their terms' sum, weights by e^that
+            off = 2.0 ** -7 * float((keys.abs() @ qq[t, h].abs()).max()) * dk ** -0.5 + 2.0 ** -7
+            tol = (p @ vals.abs()) * (torch.tensor(2 * off).exp() - 1 + 2.0 ** -7).cuda() + 2.0 ** -8 * (p @ vals).abs()
+            assert ((out[t][0, h].double() - p @ vals).abs() <= tol).all(), (t, h)
