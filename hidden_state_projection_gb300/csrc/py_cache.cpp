@@ -21,6 +21,7 @@
 namespace {
 
 PyObject *g_error = nullptr;       // ProjError
+PyObject *g_no_memory = nullptr;   // torch.OutOfMemoryError
 PyObject *g_get_device = nullptr;  // torch._C._cuda_getDevice
 PyObject *g_get_stream = nullptr;  // torch._C._cuda_getCurrentRawStream
 
@@ -52,6 +53,10 @@ PyObject *guarded(Body body) {
             Py_DECREF(e);
         }
     } catch (const PythonError &) {
+    } catch (const c10::OutOfMemoryError &e) {
+        PyErr_SetString(g_no_memory, e.what_without_backtrace());
+    } catch (const c10::Error &e) {
+        PyErr_SetString(PyExc_RuntimeError, e.what_without_backtrace());
     } catch (const std::exception &e) {
         PyErr_SetString(PyExc_RuntimeError, e.what());
     } catch (...) {
@@ -498,8 +503,9 @@ PyMODINIT_FUNC PyInit_hsp_cache_py() {
     if (!c) return nullptr;
     g_get_device = PyObject_GetAttrString(c, "_cuda_getDevice");
     g_get_stream = PyObject_GetAttrString(c, "_cuda_getCurrentRawStream");
+    g_no_memory = PyObject_GetAttrString(c, "OutOfMemoryError");
     Py_DECREF(c);
-    if (!g_get_device || !g_get_stream) return nullptr;
+    if (!g_get_device || !g_get_stream || !g_no_memory) return nullptr;
     g_error = Py_NewRef(PyExc_RuntimeError);
     return PyModule_Create(&kModule);
 }

@@ -114,3 +114,12 @@ def test_sizes_that_do_not_fit_32_bits(hsp):  # noqa: F811
         assert refusal(hsp, lambda: hsp.paged_attention(q[..., :64], g, g, table, lens, 0.1, v_dim=v_dim))[0] == "PROJ_ERR_INVALID_ARG"
     assert not hsp.paged_attention(q, k, None, table, lens, 0.1, v_dim=512).any()
     hsp.check_device_error()
+
+
+def test_no_memory_for_an_output_is_torchs_own_error(hsp):  # noqa: F811
+    """The output of so many (expanded) queries does not fit any GPU: the error that a server catches to make room."""
+    q, k = torch.zeros(1, 1, 576, dtype=BF, device="cuda").expand(2 ** 22, 256, 576), torch.zeros(4, 16, 1, 576, dtype=BF, device="cuda")
+    n = hsp.launch_count()
+    with pytest.raises(torch.OutOfMemoryError):
+        hsp.paged_attention(q, k, None, ints(1, 4), ints(1), 0.1)
+    assert hsp.launch_count() == n
