@@ -962,7 +962,12 @@ __global__ void __launch_bounds__(kAttnThreads, attn_ctas_per_sm(KB, SHARED, N))
     tc_fence_before_sync();
     // (Triggered at the start, the join's CTAs crowded on the SMs that were free first: 43 -> 47 us
     // for one sequence of 131071 tokens and 64 heads.)
-    cta_release_and_trigger();
+    if (a.split) {  // the join waits for the end of this grid: no fence
+        __syncthreads();
+        griddep_launch_dependents();
+    } else {
+        cta_release_and_trigger();
+    }
     if (*abort_flag != 0 && tid == 0) {
         // copies still in flight land before the shared memory goes
         const int n = issued[0], nx = issued[1];
