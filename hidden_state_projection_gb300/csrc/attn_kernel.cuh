@@ -187,41 +187,33 @@ __device__ __forceinline__ void tma_prefetch_5d(const CUtensorMap *map, int c0, 
 __device__ __forceinline__ void prefetch_l1(const void *p) { asm volatile("prefetch.global.L1 [%0];" ::"l"(p)); }
 
 // Bounded wait.  Once any thread of the CTA has given up, waits that are not yet satisfied
-// return at once; the roles keep their barrier pattern and store nothing.
-__device__ __forceinline__ bool attn_wait(uint32_t bar, uint32_t parity, uint64_t limit_ns, volatile int *abort_flag,
-                                          int *err_word) {
-    if (mbar_try_wait(bar, parity)) return true;
-    const uint64_t t0 = global_timer_ns();
-    for (uint32_t it = 0;; ++it) {
-        if (mbar_try_wait(bar, parity)) return true;
-        if ((it & 7u) == 7u) {
-            if (*abort_flag != 0) return false;
-            if (global_timer_ns() - t0 > limit_ns) {
-                atomicCAS(err_word, 0, kDeviceErrTimeout);
-                *abort_flag = 1;
-                return false;
-            }
-        }
+// return at once; the roles keep their barrier pattern and store nothing, and the CTA reports it at its
+// end.  (Inlined at every wait of every role: short, for the sake of the instruction cache.)
+__device__ __forceinline__ bool attn_wait(uint32_t bar, uint32_t parity, uint64_t limit_ns, volatile int *abort_flag) {
+    uint64_t t0 = 0;
+    for (uint32_t it = 1; !mbar_try_wait(bar, parity); ++it) {
+        if ((it & 7u) != 0) continue;
+        const uint64_t now = global_timer_ns();
+        if (t0 == 0) t0 = now;
+        if (now - t0 > limit_ns) *abort_flag = 1;
+        if (*abort_flag != 0) return false;
     }
+    return true;
 }
 
 // ---- the line of tiles ---------------------------------------------------------------
 
 // Length of sequence b, clamped to what its table row can hold; a row outside the table
-// is an empty sequence.  Both are reported.
+// is an empty sequence.  Both are reported where the CTA looks for empty sequences (REPORT),
+// which meets each of them once.
+template <bool REPORT = false>
 __device__ __forceinline__ int attn_len(const AttnArgs &a, int b) {
     const int row = a.rows ? a.rows[b] : b;
-    if (row < 0 || row >= a.num_rows) {
-        atomicCAS(a.err_word, 0, kDeviceErrIndex);
-        return 0;
-    }
-    const int n = a.lens[row];
-    const int64_t most = static_cast<int64_t>(a.max_pages) << a.page_shift;
-    if (n < 0 || n > most) {
-        atomicCAS(a.err_word, 0, kDeviceErrIndex);
-        return n < 0 ? 0 : static_cast<int>(most);
-    }
-    return n;
+    const bool in = row >= 0 && row < a.num_rows;
+    const int n = in ? a.lens[row] : 0;
+    const int most = a.max_pages << a.page_shift;  // (the host checks that it fits)
+    if (REPORT && (!in || n < 0 || n > most)) atomicCAS(a.err_word, 0, kDeviceErrIndex);
+    return min(max(n, 0), most);
 }
 __device__ __forceinline__ int attn_tiles(int len) { return static_cast<int>((static_cast<uint32_t>(len) + kAttnTile - 1) / kAttnTile); }
 
@@ -522,7 +514,7 @@ __global__ void __launch_bounds__(kAttnThreads, attn_ctas_per_sm(KB, SHARED, N))
                 // with theirs (heads past the group are another group's, or zero past the last: columns
                 // that nothing reads); behind the first tile, which does not have to wait for that
                 auto queries = [&]() {
-                    alive = attn_wait(smem_u32(q_free), (seg & 1u) ^ 1u, a.wait_limit_ns, abort_flag, a.err_word);
+                    alive = attn_wait(smem_u32(q_free), (seg & 1u) ^ 1u, a.wait_limit_ns, abort_flag);
                     if (!alive) return;
                     mbar_arrive_expect_tx(smem_u32(q_full), C::kQBytes);
                     tma_load_5d(smem_u32(q_smem), &tmap_q, 0, sg.kv * a.group + ht * N, 0, sg.b, 0, smem_u32(q_full));
@@ -575,7 +567,7 @@ __global__ void __launch_bounds__(kAttnThreads, attn_ctas_per_sm(KB, SHARED, N))
 #pragma unroll 1
                     for (int g = 0; g < C::kGroups; ++g) {
                         // (a fresh barrier's phase before the first counts as complete)
-                        alive = attn_wait(smem_u32(&empty[rp.slot]), rp.phase ^ 1u, a.wait_limit_ns, abort_flag, a.err_word);
+                        alive = attn_wait(smem_u32(&empty[rp.slot]), rp.phase ^ 1u, a.wait_limit_ns, abort_flag);
                         if (!alive) break;
                         ++ng;
                         if (!skip) {
@@ -586,7 +578,7 @@ __global__ void __launch_bounds__(kAttnThreads, attn_ctas_per_sm(KB, SHARED, N))
                         rp.next(a.slots);
                     }
                     if (C::kExtra && alive) {
-                        alive = attn_wait(smem_u32(&x_empty[xp.slot]), xp.phase ^ 1u, a.wait_limit_ns, abort_flag, a.err_word);
+                        alive = attn_wait(smem_u32(&x_empty[xp.slot]), xp.phase ^ 1u, a.wait_limit_ns, abort_flag);
                         if (!alive) break;
                         if (!skip) {
                             load(&tmap_v, VB, 1, extra + xp.slot * C::kBoxBytes, smem_u32(&x_full[xp.slot]));
@@ -610,7 +602,7 @@ __global__ void __launch_bounds__(kAttnThreads, attn_ctas_per_sm(KB, SHARED, N))
             const uint64_t qd = umma_desc_sw128(smem_u32(q_smem));
             RingPos rp, xp, sp;
             auto ready = [&](uint64_t *bar, uint32_t phase) {
-                return attn_wait(smem_u32(bar), phase, a.wait_limit_ns, abort_flag, a.err_word);
+                return attn_wait(smem_u32(bar), phase, a.wait_limit_ns, abort_flag);
             };
             while (alive && attn_next_segment(a, ln, walk, sg)) {
                 if (!ready(q_full, seg & 1u)) break;
@@ -665,12 +657,12 @@ __global__ void __launch_bounds__(kAttnThreads, attn_ctas_per_sm(KB, SHARED, N))
             while (alive && attn_next_segment(a, ln, walk, sg)) {
                 for (int k = 0; k < sg.n; ++k, ++i) {
                     const int valid = min(kAttnTile, sg.len - (sg.t0 + k) * kAttnTile);  // tokens of this tile
-                    alive = attn_wait(smem_u32(p_full), static_cast<uint32_t>(i) & 1u, a.wait_limit_ns, abort_flag, a.err_word);
+                    alive = attn_wait(smem_u32(p_full), static_cast<uint32_t>(i) & 1u, a.wait_limit_ns, abort_flag);
                     if (!alive) break;
                     tc_fence_after_sync();
                     if (!SHARED) {
                         rp.next(a.slots);  // the key group
-                        alive = attn_wait(smem_u32(&full[rp.slot]), rp.phase, a.wait_limit_ns, abort_flag, a.err_word);
+                        alive = attn_wait(smem_u32(&full[rp.slot]), rp.phase, a.wait_limit_ns, abort_flag);
                         if (!alive) break;
                         tc_fence_after_sync();
                     }
@@ -722,7 +714,7 @@ __global__ void __launch_bounds__(kAttnThreads, attn_ctas_per_sm(KB, SHARED, N))
             for (int k = 0; k < sg.n; ++k, ++i) {
                 const int64_t tok0 = static_cast<int64_t>(sg.t0 + k) * kAttnTile;
                 const int valid = static_cast<int>(min(static_cast<int64_t>(kAttnTile), sg.len - tok0));
-                attn_wait(smem_u32(&s_full[i & 1]), static_cast<uint32_t>(i >> 1) & 1u, a.wait_limit_ns, abort_flag, a.err_word);
+                attn_wait(smem_u32(&s_full[i & 1]), static_cast<uint32_t>(i >> 1) & 1u, a.wait_limit_ns, abort_flag);
                 tc_fence_after_sync();
                 float s[kS * 4];
                 tmem_ld_frag<kS>(tmem_s + (i & 1) * N + lane_base, s);
@@ -784,7 +776,7 @@ __global__ void __launch_bounds__(kAttnThreads, attn_ctas_per_sm(KB, SHARED, N))
                         if (warp == 0 && lane < 4) *reinterpret_cast<float2 *>(fac + c) = make_float2(f0, f1);
                     }
                     if (k > 0) {
-                        attn_wait(smem_u32(pv_done), static_cast<uint32_t>(i - 1) & 1u, a.wait_limit_ns, abort_flag, a.err_word);
+                        attn_wait(smem_u32(pv_done), static_cast<uint32_t>(i - 1) & 1u, a.wait_limit_ns, abort_flag);
                         tc_fence_after_sync();
                         softmax_sync();
 #pragma unroll 1
@@ -804,8 +796,7 @@ __global__ void __launch_bounds__(kAttnThreads, attn_ctas_per_sm(KB, SHARED, N))
                     // step of 16 tokens is filled up with zeros; the steps behind that are not taken.
                     const int first = i * C::kGroups + C::kKG;  // its first value group in the ring
                     if (!SHARED)                                // (a latent tile's scores have waited for it)
-                        attn_wait(smem_u32(&full[first % a.slots]), static_cast<uint32_t>(first / a.slots) & 1u, a.wait_limit_ns,
-                                     abort_flag, a.err_word);
+                        attn_wait(smem_u32(&full[first % a.slots]), static_cast<uint32_t>(first / a.slots) & 1u, a.wait_limit_ns, abort_flag);
                     if (tid < (-valid & 15) * 8) {
                         int at = first % a.slots;
 #pragma unroll
@@ -820,7 +811,7 @@ __global__ void __launch_bounds__(kAttnThreads, attn_ctas_per_sm(KB, SHARED, N))
                 }
                 // the probabilities of tile i - 1 have been read before these replace them
                 if (i > 0)
-                    attn_wait(smem_u32(pv_done), static_cast<uint32_t>(i - 1) & 1u, a.wait_limit_ns, abort_flag, a.err_word);
+                    attn_wait(smem_u32(pv_done), static_cast<uint32_t>(i - 1) & 1u, a.wait_limit_ns, abort_flag);
                 uint32_t pb[kS * 2];  // the rounded weights, two columns each
 #pragma unroll
                 for (int j = 0; j < kS; ++j) {
@@ -900,7 +891,7 @@ __global__ void __launch_bounds__(kAttnThreads, attn_ctas_per_sm(KB, SHARED, N))
                 e.slot = slot;
                 a.entries[cta] = e;
             }
-            attn_wait(smem_u32(pv_done), static_cast<uint32_t>(i - 1) & 1u, a.wait_limit_ns, abort_flag, a.err_word);
+            attn_wait(smem_u32(pv_done), static_cast<uint32_t>(i - 1) & 1u, a.wait_limit_ns, abort_flag);
             tc_fence_after_sync();
             softmax_sync();
             const bool good = *abort_flag == 0;
@@ -949,7 +940,7 @@ __global__ void __launch_bounds__(kAttnThreads, attn_ctas_per_sm(KB, SHARED, N))
         }
         // sequences without a token: zeros, and no weight at all
         for (int e = cta; e < a.batch; e += a.ctas) {
-            if (attn_len(a, e) != 0) continue;
+            if (attn_len<true>(a, e) != 0) continue;
             for (int kv = 0; kv < a.kv_heads; ++kv) {
                 const int64_t h = static_cast<int64_t>(e) * all_heads + kv * a.group + head0;
                 uint4 *to = reinterpret_cast<uint4 *>(out + h * kDV);  // (its heads lie one after another)
@@ -969,6 +960,7 @@ __global__ void __launch_bounds__(kAttnThreads, attn_ctas_per_sm(KB, SHARED, N))
         cta_release_and_trigger();
     }
     if (*abort_flag != 0 && tid == 0) {
+        atomicCAS(a.err_word, 0, kDeviceErrTimeout);
         // copies still in flight land before the shared memory goes
         const int n = issued[0], nx = issued[1];
         auto land = [&](uint64_t *bar, int phase) {
