@@ -19,7 +19,7 @@
 // 64 x 64 x 16 33, 128 x 64 x 16 49, 128 x 16 x 16 40; a latent tile of 64 heads is 36 of the
 // first and 16 of the second, 1970 cycles, against 3140 that its bytes take at 1/152 of the
 // device's bandwidth, so up to 64 heads wait for memory and 128 (two CTAs sharing the bytes)
-// for the tensor cores.
+// for the chain of a tile's copy, products and softmax.
 //
 // Seven warps: a copy producer (one thread: page ids a tile ahead, one tensor copy per group of
 // 128 columns, or per page and 64 columns where pages are smaller than a tile), an issuer of
@@ -42,13 +42,15 @@
 // sequence cut over several CTAs leaves fp32 partials (O^T, m, l, u) in the workspace, and the
 // join kernel adds them; the cut depends on the lengths and the grid only.
 //
-// On a GB300 (graph replay): one sequence of 131071 tokens and 64 heads over 512 columns 40.7 us
+// On a GB300 (graph replay): one sequence of 131071 tokens and 64 heads over 512 columns 41.0 us
 // (134 MB, 19.8 us at the copy rate): 4 us until the first tile is there, 24 us at 5.6 TB/s, 3 us
 // for 128 KB of partial per CTA (an SM stores 21 bytes per cycle), 7 us for the join with its
-// launch.  48 sequences up to 6001 tokens, 128 heads: 59.6 us, the products (1.06 us per tile) and
-// 3.5 us per part, 7 us for the join.  61 sequences up to 4099, 32 heads over 8 of 128: 90-93 us
+// launch.  48 sequences up to 6001 tokens, 128 heads: 61.4 us: 1.5 us per tile (two tiles, all that
+// shared memory holds, take turns at copy, scores, softmax and values; the products alone are 0.95),
+// 3.2 us per part, 7 us for the join.  61 sequences up to 4099, 32 heads over 8 of 128: 91.5 us
 // (515 MB, 75.8): 70 us at the memory's limit, the rest start, the spread of the CTAs' ends and the
-// join.  One sequence of 77 tokens, 16 heads: 6.7 us, dependent loads and two tiles in turn.
+// join.  One sequence of 77 tokens, 16 heads: 7.1 us in a table of at most 256 tokens (one launch:
+// dependent loads and two tiles in turn), 9.4 in one of 2048 pages (cut over three CTAs and joined).
 #pragma once
 
 #include <cuda.h>

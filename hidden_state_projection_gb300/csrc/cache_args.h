@@ -66,8 +66,8 @@ constexpr int kAttnMaxSlots = 12;
 inline int attn_fixed_smem(int KB, int N) { return KB * N * 128 + kAttnTile * 128 + 5 * N * 4 + 512 + 1024; }
 // CTAs per SM.  A latent tile is 73.7 KB, one CTA takes the shared memory of an SM; grouped tiles
 // are 32 or 16 KB, and the softmaxes and products of two or three CTAs overlap (32 sequences of
-// up to 4096 tokens, 8 heads of 64 columns: 38.4 us with two, 33.0 with three).  64 heads: registers
-// allow one.
+// up to 4096 tokens, 8 kv heads of 64 columns: 38.4 us with two, 33.0 with three; its bytes take 19
+// to 20 at the copy rate).  64 heads: registers allow one.
 constexpr int attn_ctas_per_sm(int KB, bool shared, int N) { return shared || N == 64 ? 1 : KB == 1 && N == 16 ? 3 : 2; }
 inline int attn_group_boxes(int VB) { return VB >= 2 ? 2 : 1; }
 

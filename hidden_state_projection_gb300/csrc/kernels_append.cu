@@ -9,10 +9,12 @@
 // Every value is read once and written once in 16-byte pieces; products and sums in fp32, one
 // rounding to bf16.  A thread takes pieces (pairs of pieces where the pairs lie rot / 2 apart),
 // two requested before either is stored.  A CTA looks up the places of its tokens first (row and
-// position, then the page: two dependent loads, which bound the small calls).  On a GB300, graph
-// replay: 8 latent tokens with 16 query heads 2.4 us; 2047 tokens of 8 + 8 + 32 heads of 128
-// (51 MB) 15.1 us with a CTA per token and a fence per thread, 9.9 with up to eight tokens behind
-// one look-up and one fence, 8.5 with multiplications for the divisions by the rows' pieces.
+// position, then the page and the length: two dependent loads, which bound the small calls, and
+// the large ones where their rows come from DRAM: none is requested before).  On a GB300, graph
+// replay: 8 latent tokens with 16 query heads 2.3 us; 2047 tokens of 8 + 8 + 32 heads of 128
+// (51 MB) held by L2 15.1 us with a CTA per token and a fence per thread, 9.9 with up to eight
+// tokens behind one look-up and one fence, 8.5 with multiplications for the divisions by the rows'
+// pieces; 8.7 with the rows' lengths read too and the trigger behind the fence, 11.8 from DRAM.
 #include <cuda_bf16.h>
 #include <stdint.h>
 
