@@ -505,10 +505,12 @@ def paged_attention(q: torch.Tensor, k_pages: torch.Tensor, v_pages: Optional[to
 def cache_append(k_new: torch.Tensor, v_new: Optional[torch.Tensor], k_pages: torch.Tensor, v_pages: Optional[torch.Tensor],
                  block_table: torch.Tensor, seq_lens: torch.Tensor, rows: Optional[torch.Tensor] = None,
                  positions: Optional[torch.Tensor] = None, cos_sin: Optional[torch.Tensor] = None, interleaved: bool = True,
-                 q: Optional[torch.Tensor] = None, q_out: Optional[torch.Tensor] = None, stream=None):
+                 q: Optional[torch.Tensor] = None, q_out: Optional[torch.Tensor] = None, stream=None,
+                 ref_counts: Optional[torch.Tensor] = None):
     """The new tokens' keys [tokens, (kv_heads,) k_dim] and values into their pages, at positions[i] of row rows[i]
     (default: the last place of row i).  A position at or past seq_lens[row], as where cache_resize found no free
-    page, is written nowhere and reported; without positions the row is taken to have grown.  cos_sin [max_pos, rot] fp32 turns the last `rot` columns of the keys and
+    page, is written nowhere and reported; without positions the row is taken to have grown.  With ref_counts
+    [num_pages] a token whose page other rows hold too is written nowhere and reported likewise.  cos_sin [max_pos, rot] fp32 turns the last `rot` columns of the keys and
     of the queries q [tokens, heads, k_dim] on the way (a model that turns the first ones: lay out the rows of its query
     and key weights rolled by `rot` within each head; scores stay the same); returns the turned queries (q_out; may be q), or None."""
     if stream is not None:
@@ -516,7 +518,7 @@ def cache_append(k_new: torch.Tensor, v_new: Optional[torch.Tensor], k_pages: to
             q_out = _new(q, q.shape, torch.bfloat16, stream)
         stream = _stream_ptr(stream)
     return (_cache or _cache_py()).cache_append(k_new, v_new, k_pages, v_pages, block_table, seq_lens, rows, positions, cos_sin,
-                                                interleaved, q, q_out, stream)
+                                                interleaved, q, q_out, stream, ref_counts)
 
 
 def cache_workspace_bytes(block_table: torch.Tensor, num_pages: int, n: int) -> int:

@@ -401,6 +401,7 @@ proj_status proj_cache_append(const void *k_new, int64_t k_row_stride, const voi
     a.table = index->block_table;
     a.table_stride = index->table_stride;
     a.lens = index->seq_lens;
+    a.refs = index->ref_counts;
     a.rows = rows;
     a.positions = positions;
     a.cos_sin = rotary ? rotary->cos_sin : nullptr;

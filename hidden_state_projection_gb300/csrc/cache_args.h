@@ -82,6 +82,7 @@ struct AppendArgs {
     const int32_t *table;
     int64_t table_stride;
     const int32_t *lens, *rows, *positions;  // rows, positions may be null
+    const int32_t *refs;             // [num_pages] or null: pages are not checked to be the row's own
     const float *cos_sin;            // [max_pos, rot] or null
     const void *q;                   // [tokens, heads, k_dim] or null, tokens at q_row, heads at q_head
     void *q_out;

@@ -88,6 +88,7 @@ __global__ void __launch_bounds__(kAppendThreads, 4) hsp_append_kernel(const __g
         if (row_ok && pos >= 0 && (pos >> a.page_shift) < a.max_pages)
             page = a.table[row * a.table_stride + (pos >> a.page_shift)];
         if (pos >= len) page = -1;  // behind the row's end, as where its growth found no free page (on the way with the table's entry)
+        if (a.refs && page >= 0 && page < a.num_pages && a.refs[page] > 1) page = -1;  // others hold it too
         const bool angle = a.rot > 0 && pos >= 0 && pos < a.max_pos;
         const int64_t line = pos & ((1 << a.page_shift) - 1);
         AppendPlace p;

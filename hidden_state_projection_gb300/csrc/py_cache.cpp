@@ -324,17 +324,18 @@ const void *new_rows(const char *name, const at::Tensor &t, int64_t tokens, int6
     return t.data_ptr();
 }
 
-// (k_new, v_new, k_pages, v_pages, block_table, seq_lens, rows, positions, cos_sin, interleaved, q, q_out, stream)
+// (k_new, v_new, k_pages, v_pages, block_table, seq_lens, rows, positions, cos_sin, interleaved, q, q_out, stream, ref_counts)
 PyObject *cache_append(PyObject *, PyObject *const *args, Py_ssize_t nargs) {
     return guarded([&]() -> PyObject * {
-        arguments(nargs, 13);
+        arguments(nargs, 14);
         const at::Tensor &kn = tensor(args[0], "k_new"), &k = tensor(args[2], "k_pages");
         const at::Tensor vn = optional(args[1], "v_new"), v = optional(args[3], "v_pages");
         const at::Tensor &table = tensor(args[4], "block_table"), &lens = tensor(args[5], "seq_lens");
         const at::Tensor rows = optional(args[6], "rows"), pos = optional(args[7], "positions"), cs = optional(args[8], "cos_sin");
         const at::Tensor q = optional(args[10], "q");
         at::Tensor q_out = optional(args[11], "q_out");
-        const int dev = device_of({&kn, &vn, &k, &v, &table, &lens, &rows, &pos, &cs, &q, &q_out});
+        const at::Tensor refs = optional(args[13], "ref_counts");
+        const int dev = device_of({&kn, &vn, &k, &v, &table, &lens, &rows, &pos, &cs, &q, &q_out, &refs});
         const proj_kv_pages kv = kv_pages(k, v, Py_None);
         if (kn.dim() < 1) refuse(PROJ_ERR_INVALID_ARG, "k_new must be [tokens, ...]");
         const int64_t tokens = kn.size(0), dim = kv.k_dim;
@@ -342,7 +343,7 @@ PyObject *cache_append(PyObject *, PyObject *const *args, Py_ssize_t nargs) {
         int64_t ks = 0, vs = 0;
         const void *kp = new_rows("k_new", kn, tokens, kv.kv_heads, dim, &ks);
         const void *vp = vn.defined() ? new_rows("v_new", vn, tokens, kv.kv_heads, kv.v_dim, &vs) : nullptr;
-        const proj_page_index ix = page_index(table, lens, at::Tensor(), k.size(0), k.size(1));
+        const proj_page_index ix = page_index(table, lens, refs, k.size(0), k.size(1));
         proj_rotary rot = {};
         if (cs.defined()) {
             if (cs.scalar_type() != at::kFloat || cs.dim() != 2 || !cs.is_contiguous())

@@ -381,7 +381,7 @@ typedef struct {
     int32_t *block_table;  /* [num_rows, max_pages] page ids, rows at table_stride */
     int64_t table_stride;  /* elements, >= max_pages */
     int32_t *seq_lens;     /* [num_rows] */
-    int32_t *ref_counts;   /* [num_pages]; NULL where only tokens are read or written */
+    int32_t *ref_counts;   /* [num_pages]; may be NULL where only tokens are read or written */
     int32_t num_rows;
     int32_t max_pages;     /* table entries per row; max_pages * page_size < 2^31 - 1024 */
     int32_t num_pages;
@@ -483,7 +483,9 @@ typedef struct {
  * whose position is not below seq_lens[row] is written nowhere and reported (PROJ_ERR_BAD_INDEX):
  * so a step that passes the positions of a growth leaves alone a row that found no free page
  * (status 1), on whose last page other rows may still be.  Without positions the call takes the
- * growth to have succeeded: it writes the row's last token whatever that is.  Two
+ * growth to have succeeded: it writes the row's last token whatever that is.  With
+ * index->ref_counts a token whose page other rows hold too is written nowhere and reported
+ * likewise (NULL: not checked; one more dependent load).  Two
  * tokens of one call must not name the same row and position (which one stays is not
  * defined).  One kernel launch; tokens = 0 succeeds and touches nothing.
  */

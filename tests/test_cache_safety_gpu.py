@@ -93,3 +93,37 @@ def test_new_lengths_that_lie_in_the_lengths(hsp, rows, pages):  # noqa: F811
         assert st.tolist() == c.model.resize(list(who[:n]), list(c.model.lens[:n]))
         c.check()
     hsp.check_device_error()
+
+
+@pytest.mark.parametrize("with_positions", [False, True])
+def test_append_to_a_page_that_others_hold(hsp, with_positions):  # noqa: F811
+    """Row 1 is a fork of row 0 whose growth found no free page; rows 2 and 3 have pages of their own.  With the holder
+    counts the shared page stays as it is, also where the call writes each row's last token."""
+    page = 16
+    k = torch.randn(1, 4, page, 2, 64, device="cuda").to(BF)
+    v = torch.randn_like(k)
+    table = torch.full((4, 2), -1, dtype=torch.int32, device="cuda")
+    lens, refs = torch.zeros(4, dtype=torch.int32, device="cuda"), torch.zeros(4, dtype=torch.int32, device="cuda")
+    a, pools = (table, lens, refs), [k, v]
+    assert not hsp.cache_resize(*a, ints([0, 2, 3]), ints([30, 10, 7]), page, pools).any()
+    assert not hsp.cache_fork(*a, ints([0]), ints([1]), page).any()
+    assert hsp.cache_resize(*a, ints([1, 2, 3]), ints([31, 11, 7]), page, pools).tolist() == [1, 0, 0]
+    rows, kn = ints([1, 2, 3]), torch.randn(3, 2, 64, device="cuda").to(BF)
+    pos = lens[rows.long()] - 1 if with_positions else None
+    args = dict(rows=rows, positions=pos)
+    before, old = [t.clone() for t in pools], lens.clone()
+    if pos is None:
+        lens_of = torch.zeros(3, dtype=torch.int32, device="cuda")      # (without rows and positions: rows 0 .. 2 of a table)
+        lens_of.copy_(lens[1:])
+        hsp.cache_append(kn, kn, k[0], v[0], table[1:], lens_of, ref_counts=refs)
+    else:
+        hsp.cache_append(kn, kn, k[0], v[0], table, lens, ref_counts=refs, **args)
+    expect_bad_index(hsp)
+    assert torch.equal(lens, old)
+    for t, b in zip(pools, before):
+        b[0, table[2, 0].long(), 10] = kn[1]
+        b[0, table[3, 0].long(), 6] = kn[2]
+        assert torch.equal(t, b)
+    # rows of their own alone: nothing to report
+    hsp.cache_append(kn[1:], kn[1:], k[0], v[0], table, lens, rows=rows[1:], ref_counts=refs)
+    hsp.check_device_error()
