@@ -37,6 +37,7 @@ EXPORTED = ("proj_fused_gemm", "proj_fused_gemm_prefetch", "proj_fused_gemm_host
             "proj_fused_gemm_rmsnorm_static",
             "proj_paged_attention", "proj_paged_attention_workspace_bytes", "proj_cache_append", "proj_cache_resize",
             "proj_cache_fork", "proj_cache_compact", "proj_cache_workspace_bytes", "proj_cache_copy_pages",
+            "proj_paged_attention_q8", "proj_paged_attention_q8_workspace_bytes", "proj_cache_append_q8", "proj_cache_read_q8",
             "proj_separate_gemm", "proj_pack_weights", "proj_pack_check",
             "proj_supported", "proj_describe_plan", "proj_set_options", "proj_get_options",
             "proj_check_device_error", "proj_launch_count", "proj_last_error_string", "proj_version")
@@ -117,6 +118,14 @@ def lib() -> ctypes.CDLL:
     L.proj_paged_attention_workspace_bytes.restype = ctypes.c_size_t
     L.proj_cache_append.argtypes = [vp, i64, vp, i64, cp, cp, vp, vp, i32, cp, vp, i64, i64, vp, i64, i64, i32, vp]
     L.proj_cache_append.restype = ctypes.c_int
+    L.proj_paged_attention_q8.argtypes = L.proj_paged_attention.argtypes
+    L.proj_paged_attention_q8.restype = ctypes.c_int
+    L.proj_paged_attention_q8_workspace_bytes.argtypes = [i32] * 5
+    L.proj_paged_attention_q8_workspace_bytes.restype = ctypes.c_size_t
+    L.proj_cache_append_q8.argtypes = L.proj_cache_append.argtypes
+    L.proj_cache_append_q8.restype = ctypes.c_int
+    L.proj_cache_read_q8.argtypes = [cp, cp, vp, vp, i32, vp, i64, vp, i64, vp]
+    L.proj_cache_read_q8.restype = ctypes.c_int
     L.proj_cache_resize.argtypes = [cp, vp, vp, i32, cp, i32, vp, vp, ctypes.c_size_t, vp]
     L.proj_cache_resize.restype = ctypes.c_int
     L.proj_cache_fork.argtypes = [cp, vp, vp, i32, vp, vp]
@@ -584,6 +593,80 @@ def cache_copy_pages(pools: Sequence[torch.Tensor], src, dst, stream=None) -> No
     if not isinstance(dst, torch.Tensor):
         dst = torch.tensor(dst, dtype=torch.int32)
     (_cache or _cache_py()).cache_copy_pages(pools, src, dst, None if stream is None else _stream_ptr(stream))
+
+
+# ---- the paged cache in 8 bits ----------------------------------------------------
+#
+# k_pages and v_pages are torch.float8_e4m3fn tensors of the shapes above (strides in multiples of 16), k_scales and
+# v_scales float32 [num_pages, page_size / block, kv_heads], any strides: a value is code * scale.  Page calls
+# (cache_resize, ...) move codes and scales alike, as pools (a uint8 pool that holds both will do: its views as
+# float8_e4m3fn and float32 are the tensors here).
+
+def paged_attention_q8_workspace_bytes(heads: int, kv_heads: int, k_dim: int, v_dim: int, latent: bool) -> int:
+    """Workspace bytes of proj_paged_attention_q8 (raises if the heads and columns are not supported)."""
+    n = int(lib().proj_paged_attention_q8_workspace_bytes(_i32(heads), _i32(kv_heads), _i32(k_dim), _i32(v_dim), int(latent)))
+    if n == 0:  # the same heads and columns are refused of a bf16 cache, with the status that goes with the text
+        paged_attention_workspace_bytes(heads, kv_heads, k_dim, v_dim, latent)
+        raise ProjError(2, "unsupported heads and columns")
+    return n
+
+
+def paged_attention_q8(q: torch.Tensor, k_pages: torch.Tensor, v_pages: Optional[torch.Tensor], k_scales: torch.Tensor,
+                       v_scales: Optional[torch.Tensor], block_table: torch.Tensor, seq_lens: torch.Tensor, scale: float,
+                       v_dim: Optional[int] = None, rows: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+                       lse: Optional[torch.Tensor] = None, return_lse: bool = False,
+                       workspace: Optional[torch.Tensor] = None, stream=None):
+    """paged_attention over a cache in 8 bits: q and the result are bf16, keys and values code * scale (v_pages and
+    v_scales None: a latent cache)."""
+    if stream is not None:
+        if _ranks((q, 3), (k_pages, 4)) and (v_pages is None or _ranks((v_pages, 4))):
+            batch, heads, k_dim = q.shape
+            dv = v_pages.shape[3] if v_pages is not None else 512 if v_dim is None else v_dim
+            if workspace is None:
+                workspace = _new(q, paged_attention_q8_workspace_bytes(heads, k_pages.shape[2], k_dim, dv, v_pages is None),
+                                 torch.uint8, stream)
+            if out is None:
+                out = _new(q, (batch, heads, dv), torch.bfloat16, stream)
+            if lse is None and return_lse:
+                lse = _new(q, (batch, heads), torch.float32, stream)
+        stream = _stream_ptr(stream)
+    return (_cache or _cache_py()).paged_attention_q8(q, k_pages, v_pages, k_scales, v_scales, block_table, seq_lens, scale,
+                                                      v_dim, rows, out, lse, return_lse, workspace, stream)
+
+
+def cache_append_q8(k_new: torch.Tensor, v_new: Optional[torch.Tensor], k_pages: torch.Tensor, v_pages: Optional[torch.Tensor],
+                    k_scales: torch.Tensor, v_scales: Optional[torch.Tensor], block_table: torch.Tensor, seq_lens: torch.Tensor,
+                    rows: Optional[torch.Tensor] = None, positions: Optional[torch.Tensor] = None,
+                    cos_sin: Optional[torch.Tensor] = None, interleaved: bool = True, q: Optional[torch.Tensor] = None,
+                    q_out: Optional[torch.Tensor] = None, stream=None, ref_counts: Optional[torch.Tensor] = None):
+    """cache_append into a cache in 8 bits: the bf16 keys and values are turned, then quantised, one scale for each block
+    of tokens and head (the smallest power of two under which the block's new tokens fit, never below the scale of the
+    tokens in front of them, whose codes follow where it grows).  New tokens of a row that share a block stand next to
+    each other in the call."""
+    if stream is not None:
+        if q is not None and q_out is None and _ranks((q, 3)):
+            q_out = _new(q, q.shape, torch.bfloat16, stream)
+        stream = _stream_ptr(stream)
+    return (_cache or _cache_py()).cache_append_q8(k_new, v_new, k_pages, v_pages, k_scales, v_scales, block_table, seq_lens, rows,
+                                                   positions, cos_sin, interleaved, q, q_out, stream, ref_counts)
+
+
+def cache_read_q8(k_pages: torch.Tensor, v_pages: Optional[torch.Tensor], k_scales: torch.Tensor,
+                  v_scales: Optional[torch.Tensor], block_table: torch.Tensor, seq_lens: torch.Tensor,
+                  rows: Optional[torch.Tensor] = None, positions: Optional[torch.Tensor] = None,
+                  k_out: Optional[torch.Tensor] = None, v_out: Optional[torch.Tensor] = None, stream=None):
+    """Tokens of a cache in 8 bits, in bf16: token i is the one at positions[i] of row rows[i] (default: the last of row
+    i).  Returns (k [tokens, kv_heads, k_dim], v or None); a token outside the cache gives zeros and is reported."""
+    if stream is not None:
+        n = rows if rows is not None else positions if positions is not None else seq_lens
+        if _ranks((k_pages, 4), (n, 1)) and (v_pages is None or _ranks((v_pages, 4))):
+            if k_out is None:
+                k_out = _new(k_pages, (n.shape[0], *k_pages.shape[2:]), torch.bfloat16, stream)
+            if v_out is None and v_pages is not None:
+                v_out = _new(k_pages, (n.shape[0], *v_pages.shape[2:]), torch.bfloat16, stream)
+        stream = _stream_ptr(stream)
+    return (_cache or _cache_py()).cache_read_q8(k_pages, v_pages, k_scales, v_scales, block_table, seq_lens, rows, positions,
+                                                 k_out, v_out, stream)
 
 
 def supported(M: int, K: int, n_total: int, dtype: int) -> bool:

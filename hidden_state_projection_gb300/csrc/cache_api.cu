@@ -144,6 +144,26 @@ proj_status check_apart(const proj_kv_pages *kv, const proj_page_index *ix) {
     return PROJ_OK;
 }
 
+// The rotary turn of an append, and the queries that go with it.
+proj_status check_turn(const proj_rotary *rotary, int k_dim, const void *q) {
+    if (q && !rotary) return api_fail(PROJ_ERR_INVALID_ARG, "queries are only turned: q needs rotary");
+    if (rotary) {
+        if (!rotary->cos_sin || rotary->max_pos < 1) return api_fail(PROJ_ERR_INVALID_ARG, "rotary without a table");
+        if (rotary->dim < 16 || rotary->dim % 16 || rotary->dim > k_dim)
+            return api_fail(PROJ_ERR_UNSUPPORTED_SHAPE, "rotary dim=%d is not a multiple of 16 up to k_dim=%d", rotary->dim, k_dim);
+        if (!aligned(rotary->cos_sin, 16)) return api_fail(PROJ_ERR_MISALIGNED, "cos_sin must be 16-byte aligned");
+    }
+    return PROJ_OK;
+}
+proj_status check_q_out(const void *q, int64_t q_row, int64_t q_head, const void *q_out, int64_t qo_row, int64_t qo_head,
+                        int tokens, int heads, int k_dim) {
+    Dim dims[2] = {{tokens, qo_row}, {heads, qo_head}};
+    if (!nested(dims, k_dim)) return api_fail(PROJ_ERR_UNSUPPORTED_SHAPE, "tokens and heads of q_out must not overlap");
+    if (q == q_out && ((tokens > 1 && q_row != qo_row) || (heads > 1 && q_head != qo_head)))
+        return api_fail(PROJ_ERR_INVALID_ARG, "q_out may be q, with the same strides");
+    return PROJ_OK;
+}
+
 // [pages][heads][64-column boxes][tokens][64]: token lines of 128 bytes as the products read them.
 proj_status encode_pages(const void *p, const proj_page_index *ix, int heads, int dim, int64_t page, int64_t token,
                          int64_t head, int box_count, CUtensorMap *out) {
@@ -194,6 +214,72 @@ proj_status check_layers(const proj_page_pool *pools, int num_pools, int num_pag
         if (!nested(dims, pools[i].page_bytes)) return api_fail(PROJ_ERR_INVALID_ARG, "pools[%d]: layers overlap", i);
     }
     return PROJ_OK;
+}
+
+// ---- the cache in 8 bits ----
+
+// Pointers, strides and block size; `heads` and columns are the callers' to check.
+proj_status check_kv_q8(const proj_kv_pages_q8 *kv, const proj_page_index *ix) {
+    if (!kv || !kv->k || !kv->k_scale) return api_fail(PROJ_ERR_INVALID_ARG, "kv, kv->k and kv->k_scale must not be NULL");
+    if ((kv->v != nullptr) != (kv->v_scale != nullptr)) return api_fail(PROJ_ERR_INVALID_ARG, "v_scale goes with v");
+    if (!aligned(kv->k, 16) || !aligned(kv->v, 16)) return api_fail(PROJ_ERR_MISALIGNED, "k and v must be 16-byte aligned");
+    if (!aligned(kv->k_scale, 4) || !aligned(kv->v_scale, 4)) return api_fail(PROJ_ERR_MISALIGNED, "scales must be 4-byte aligned");
+    if (kv->block < 1 || kv->block > ix->page_size || (kv->block & (kv->block - 1)) != 0)
+        return api_fail(PROJ_ERR_UNSUPPORTED_SHAPE, "block=%d is not a power of two up to the page size %d", kv->block, ix->page_size);
+    const int64_t st[6] = {kv->k_page_stride, kv->k_token_stride, kv->k_head_stride,
+                           kv->v ? kv->v_page_stride : 16, kv->v ? kv->v_token_stride : 16, kv->v ? kv->v_head_stride : 16};
+    for (int64_t x : st) {
+        if (x < 0 || x >= (int64_t(1) << 39)) return api_fail(PROJ_ERR_UNSUPPORTED_SHAPE, "cache stride %lld out of range", (long long)x);
+        if (x % 16 != 0) return api_fail(PROJ_ERR_MISALIGNED, "cache stride %lld is not a multiple of 16 bytes", (long long)x);
+    }
+    const int64_t ss[6] = {kv->k_scale_page_stride, kv->k_scale_block_stride, kv->k_scale_head_stride,
+                           kv->v ? kv->v_scale_page_stride : 0, kv->v ? kv->v_scale_block_stride : 0, kv->v ? kv->v_scale_head_stride : 0};
+    for (int64_t x : ss)
+        if (x < 0 || x >= (int64_t(1) << 38)) return api_fail(PROJ_ERR_UNSUPPORTED_SHAPE, "scale stride %lld out of range", (long long)x);
+    return PROJ_OK;
+}
+
+// Tokens, heads and pages that steps can reach lie apart (the smallest step of a tensor copy is 16 bytes).
+proj_status check_apart_q8(const proj_kv_pages_q8 *kv, const proj_page_index *ix) {
+    if (kv->k_token_stride < 16 || (kv->v && kv->v_token_stride < 16))
+        return api_fail(PROJ_ERR_UNSUPPORTED_SHAPE, "tokens of the cache must lie apart (token stride 0)");
+    if ((kv->kv_heads > 1 && (kv->k_head_stride < 16 || (kv->v && kv->v_head_stride < 16))) ||
+        (ix->num_pages > 1 && (kv->k_page_stride < 16 || (kv->v && kv->v_page_stride < 16))))
+        return api_fail(PROJ_ERR_UNSUPPORTED_SHAPE, "heads and pages of the cache must lie apart (stride 0)");
+    return PROJ_OK;
+}
+
+// Heads and columns that tokens are written to or read from by pieces of 16 codes.
+proj_status check_columns_q8(const proj_kv_pages_q8 *kv, int64_t more) {
+    if (kv->kv_heads < 1 || kv->kv_heads > 65536 || kv->k_dim < 16 || kv->k_dim % 16 || kv->k_dim > 65536 ||
+        (kv->v && (kv->v_dim < 16 || kv->v_dim % 16 || kv->v_dim > 65536)))
+        return api_fail(PROJ_ERR_UNSUPPORTED_SHAPE, "kv_heads=%d, k_dim=%d, v_dim=%d: columns in multiples of 16, heads at least 1",
+                        kv->kv_heads, kv->k_dim, kv->v_dim);
+    const int64_t columns = static_cast<int64_t>(kv->kv_heads) * (kv->k_dim + (kv->v ? kv->v_dim : 0)) + more;
+    if (columns > (1 << 24)) return api_fail(PROJ_ERR_UNSUPPORTED_SHAPE, "%lld columns of a token exceed 2^24", (long long)columns);
+    return PROJ_OK;
+}
+
+// Places of codes and scales that are written lie apart.
+proj_status check_writable_q8(const proj_kv_pages_q8 *kv, const proj_page_index *ix) {
+    const int blocks = ix->page_size / kv->block;
+    Dim k[3] = {{ix->num_pages, kv->k_page_stride}, {ix->page_size, kv->k_token_stride}, {kv->kv_heads, kv->k_head_stride}};
+    Dim v[3] = {{ix->num_pages, kv->v_page_stride}, {ix->page_size, kv->v_token_stride}, {kv->kv_heads, kv->v_head_stride}};
+    Dim ks[3] = {{ix->num_pages, kv->k_scale_page_stride}, {blocks, kv->k_scale_block_stride}, {kv->kv_heads, kv->k_scale_head_stride}};
+    Dim vs[3] = {{ix->num_pages, kv->v_scale_page_stride}, {blocks, kv->v_scale_block_stride}, {kv->kv_heads, kv->v_scale_head_stride}};
+    if (!nested(k, kv->k_dim) || !nested(ks, 1) || (kv->v && (!nested(v, kv->v_dim) || !nested(vs, 1))))
+        return api_fail(PROJ_ERR_UNSUPPORTED_SHAPE, "pages, tokens (blocks) and heads of a cache that is written must not overlap");
+    return PROJ_OK;
+}
+
+hsp::Q8Side k_side(const proj_kv_pages_q8 *kv) {
+    return {static_cast<uint8_t *>(kv->k), kv->k_scale, kv->k_page_stride, kv->k_token_stride, kv->k_head_stride,
+            kv->k_scale_page_stride, kv->k_scale_block_stride, kv->k_scale_head_stride, kv->k_dim};
+}
+hsp::Q8Side v_side(const proj_kv_pages_q8 *kv) {
+    if (!kv->v) return {nullptr, nullptr, 0, 0, 0, 0, 0, 0, 0};
+    return {static_cast<uint8_t *>(kv->v), kv->v_scale, kv->v_page_stride, kv->v_token_stride, kv->v_head_stride,
+            kv->v_scale_page_stride, kv->v_scale_block_stride, kv->v_scale_head_stride, kv->v_dim};
 }
 
 hsp::IndexArgs index_args(const proj_page_index *ix, int *err_word) {
@@ -360,13 +446,7 @@ proj_status proj_cache_append(const void *k_new, int64_t k_row_stride, const voi
                             (q ? static_cast<int64_t>(heads) * kv->k_dim : 0);
     if (columns > (1 << 24)) return api_fail(PROJ_ERR_UNSUPPORTED_SHAPE, "%lld columns of a token exceed 2^24", (long long)columns);
     if ((st = check_writable(kv, index)) != PROJ_OK) return st;
-    if (q && !rotary) return api_fail(PROJ_ERR_INVALID_ARG, "queries are only turned: q needs rotary");
-    if (rotary) {
-        if (!rotary->cos_sin || rotary->max_pos < 1) return api_fail(PROJ_ERR_INVALID_ARG, "rotary without a table");
-        if (rotary->dim < 16 || rotary->dim % 16 || rotary->dim > kv->k_dim)
-            return api_fail(PROJ_ERR_UNSUPPORTED_SHAPE, "rotary dim=%d is not a multiple of 16 up to k_dim=%d", rotary->dim, kv->k_dim);
-        if (!aligned(rotary->cos_sin, 16)) return api_fail(PROJ_ERR_MISALIGNED, "cos_sin must be 16-byte aligned");
-    }
+    if ((st = check_turn(rotary, kv->k_dim, q)) != PROJ_OK) return st;
     if (tokens == 0) return hsp::api_ok();
     if (!rows && tokens > index->num_rows)
         return api_fail(PROJ_ERR_INVALID_ARG, "tokens=%d exceeds the table's %d rows", tokens, index->num_rows);
@@ -376,12 +456,8 @@ proj_status proj_cache_append(const void *k_new, int64_t k_row_stride, const voi
         return api_fail(PROJ_ERR_MISALIGNED, "k_new, v_new, q and q_out: 16-byte aligned, strides multiples of 8 elements");
     if (!aligned(rows, 4) || !aligned(positions, 4))
         return api_fail(PROJ_ERR_MISALIGNED, "rows and positions must be 4-byte aligned");
-    if (q) {
-        Dim dims[2] = {{tokens, q_out_row_stride}, {heads, q_out_head_stride}};
-        if (!nested(dims, kv->k_dim)) return api_fail(PROJ_ERR_UNSUPPORTED_SHAPE, "tokens and heads of q_out must not overlap");
-        if (q == q_out && ((tokens > 1 && q_row_stride != q_out_row_stride) || (heads > 1 && q_head_stride != q_out_head_stride)))
-            return api_fail(PROJ_ERR_INVALID_ARG, "q_out may be q, with the same strides");
-    }
+    if (q && (st = check_q_out(q, q_row_stride, q_head_stride, q_out, q_out_row_stride, q_out_head_stride, tokens, heads, kv->k_dim)) != PROJ_OK)
+        return st;
     hsp::ApiDevice dev;
     if ((st = hsp::api_device(&dev)) != PROJ_OK) return st;
     hsp::AppendArgs a;
@@ -426,6 +502,192 @@ proj_status proj_cache_append(const void *k_new, int64_t k_row_stride, const voi
     a.err_word = dev.err_word;
     const cudaError_t e = hsp::launch_append(a, dev.sms, hsp::api_options().pdl, reinterpret_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return hsp::api_cuda_fail(e, "kernel launch (cache append)");
+    hsp::api_count_launches(1);
+    return hsp::api_ok();
+}
+
+proj_status proj_cache_append_q8(const void *k_new, int64_t k_row_stride, const void *v_new, int64_t v_row_stride,
+                                 const proj_kv_pages_q8 *kv, const proj_page_index *index, const int32_t *rows,
+                                 const int32_t *positions, int32_t tokens, const proj_rotary *rotary, const void *q,
+                                 int64_t q_row_stride, int64_t q_head_stride, void *q_out, int64_t q_out_row_stride,
+                                 int64_t q_out_head_stride, int32_t heads, proj_stream_t stream) {
+    proj_status st = check_index(index, false);
+    if (st != PROJ_OK) return st;
+    if ((st = check_kv_q8(kv, index)) != PROJ_OK) return st;
+    if (tokens < 0) return api_fail(PROJ_ERR_INVALID_ARG, "tokens=%d is negative", tokens);
+    if ((kv->v != nullptr) != (v_new != nullptr) && tokens > 0)
+        return api_fail(PROJ_ERR_INVALID_ARG, "v_new goes with a cache that has values of its own");
+    if (q && (heads < 1 || heads > 65536)) return api_fail(PROJ_ERR_INVALID_ARG, "heads=%d (1..65536)", heads);
+    if ((st = check_columns_q8(kv, q ? static_cast<int64_t>(heads) * kv->k_dim : 0)) != PROJ_OK) return st;
+    if ((st = check_writable_q8(kv, index)) != PROJ_OK) return st;
+    if ((st = check_turn(rotary, kv->k_dim, q)) != PROJ_OK) return st;
+    if (tokens == 0) return hsp::api_ok();
+    if (!rows && tokens > index->num_rows)
+        return api_fail(PROJ_ERR_INVALID_ARG, "tokens=%d exceeds the table's %d rows", tokens, index->num_rows);
+    if (!k_new || (q && !q_out)) return api_fail(PROJ_ERR_INVALID_ARG, "k_new (and q_out beside q) must not be NULL");
+    if (!aligned(k_new, 16) || !aligned(v_new, 16) || !aligned(q, 16) || !aligned(q_out, 16) || k_row_stride % 8 ||
+        v_row_stride % 8 || q_row_stride % 8 || q_head_stride % 8 || q_out_row_stride % 8 || q_out_head_stride % 8)
+        return api_fail(PROJ_ERR_MISALIGNED, "k_new, v_new, q and q_out: 16-byte aligned, strides multiples of 8 elements");
+    if (!aligned(rows, 4) || !aligned(positions, 4))
+        return api_fail(PROJ_ERR_MISALIGNED, "rows and positions must be 4-byte aligned");
+    if (q && (st = check_q_out(q, q_row_stride, q_head_stride, q_out, q_out_row_stride, q_out_head_stride, tokens, heads, kv->k_dim)) != PROJ_OK)
+        return st;
+    hsp::ApiDevice dev;
+    if ((st = hsp::api_device(&dev)) != PROJ_OK) return st;
+    hsp::AppendQ8Args a;
+    memset(&a, 0, sizeof a);
+    a.k_new = k_new;
+    a.v_new = v_new;
+    a.k_row = k_row_stride;
+    a.v_row = v_row_stride;
+    a.k = k_side(kv);
+    a.v = v_side(kv);
+    a.table = index->block_table;
+    a.table_stride = index->table_stride;
+    a.lens = index->seq_lens;
+    a.refs = index->ref_counts;
+    a.rows = rows;
+    a.positions = positions;
+    a.cos_sin = rotary ? rotary->cos_sin : nullptr;
+    a.rot = rotary ? rotary->dim : 0;
+    a.max_pos = rotary ? rotary->max_pos : 0;
+    a.interleaved = rotary ? (rotary->interleaved != 0) : 1;
+    a.q = q;
+    a.q_out = q_out;
+    a.q_row = q_row_stride;
+    a.q_head = q_head_stride;
+    a.qo_row = q_out_row_stride;
+    a.qo_head = q_out_head_stride;
+    a.num_rows = index->num_rows;
+    a.max_pages = index->max_pages;
+    a.num_pages = index->num_pages;
+    a.page_shift = log2_of(index->page_size);
+    a.block_shift = log2_of(kv->block);
+    a.tokens = tokens;
+    a.kv_heads = kv->kv_heads;
+    a.heads = q ? heads : 0;
+    a.err_word = dev.err_word;
+    const cudaError_t e = hsp::launch_append_q8(a, dev.sms, hsp::api_options().pdl, reinterpret_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return hsp::api_cuda_fail(e, "kernel launch (cache append, 8 bits)");
+    hsp::api_count_launches(1);
+    return hsp::api_ok();
+}
+
+proj_status proj_cache_read_q8(const proj_kv_pages_q8 *kv, const proj_page_index *index, const int32_t *rows,
+                               const int32_t *positions, int32_t tokens, void *k_out, int64_t k_row_stride, void *v_out,
+                               int64_t v_row_stride, proj_stream_t stream) {
+    proj_status st = check_index(index, false);
+    if (st != PROJ_OK) return st;
+    if ((st = check_kv_q8(kv, index)) != PROJ_OK) return st;
+    if (tokens < 0) return api_fail(PROJ_ERR_INVALID_ARG, "tokens=%d is negative", tokens);
+    if ((kv->v != nullptr) != (v_out != nullptr) && tokens > 0)
+        return api_fail(PROJ_ERR_INVALID_ARG, "v_out goes with a cache that has values of its own");
+    if ((st = check_columns_q8(kv, 0)) != PROJ_OK) return st;
+    if (tokens == 0) return hsp::api_ok();
+    if (!rows && tokens > index->num_rows)
+        return api_fail(PROJ_ERR_INVALID_ARG, "tokens=%d exceeds the table's %d rows", tokens, index->num_rows);
+    if (!k_out) return api_fail(PROJ_ERR_INVALID_ARG, "k_out must not be NULL");
+    if (!aligned(k_out, 16) || !aligned(v_out, 16) || k_row_stride % 8 || v_row_stride % 8)
+        return api_fail(PROJ_ERR_MISALIGNED, "k_out and v_out: 16-byte aligned, strides multiples of 8 elements");
+    if (!aligned(rows, 4) || !aligned(positions, 4))
+        return api_fail(PROJ_ERR_MISALIGNED, "rows and positions must be 4-byte aligned");
+    Dim dk[1] = {{tokens, k_row_stride}}, dv[1] = {{tokens, v_row_stride}};
+    if (!nested(dk, static_cast<int64_t>(kv->kv_heads) * kv->k_dim) || (v_out && !nested(dv, static_cast<int64_t>(kv->kv_heads) * kv->v_dim)))
+        return api_fail(PROJ_ERR_UNSUPPORTED_SHAPE, "tokens of k_out and v_out must not overlap");
+    hsp::ApiDevice dev;
+    if ((st = hsp::api_device(&dev)) != PROJ_OK) return st;
+    hsp::ReadQ8Args a;
+    memset(&a, 0, sizeof a);
+    a.k = k_side(kv);
+    a.v = v_side(kv);
+    a.k_out = k_out;
+    a.v_out = v_out;
+    a.k_row = k_row_stride;
+    a.v_row = v_row_stride;
+    a.table = index->block_table;
+    a.table_stride = index->table_stride;
+    a.lens = index->seq_lens;
+    a.rows = rows;
+    a.positions = positions;
+    a.num_rows = index->num_rows;
+    a.max_pages = index->max_pages;
+    a.num_pages = index->num_pages;
+    a.page_shift = log2_of(index->page_size);
+    a.block_shift = log2_of(kv->block);
+    a.tokens = tokens;
+    a.kv_heads = kv->kv_heads;
+    a.err_word = dev.err_word;
+    const cudaError_t e = hsp::launch_read_q8(a, dev.sms, hsp::api_options().pdl, reinterpret_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return hsp::api_cuda_fail(e, "kernel launch (cache read, 8 bits)");
+    hsp::api_count_launches(1);
+    return hsp::api_ok();
+}
+
+size_t proj_paged_attention_q8_workspace_bytes(int32_t heads, int32_t kv_heads, int32_t k_dim, int32_t v_dim, int32_t latent) {
+    AttnShape s;
+    if (attn_shape(heads, kv_heads, k_dim, v_dim, latent != 0, &s) != PROJ_OK) return 0;
+    return attn_workspace(s, attn_ctas(s, hsp::api_plan_sms()));
+}
+
+proj_status proj_paged_attention_q8(const void *q, int64_t q_row_stride, int64_t q_head_stride, const proj_kv_pages_q8 *kv,
+                                    const proj_page_index *index, const int32_t *rows, int32_t batch, int32_t heads,
+                                    float scale, void *out, float *lse, void *workspace, size_t workspace_bytes,
+                                    proj_stream_t stream) {
+    proj_status st = check_index(index, false);
+    if (st != PROJ_OK) return st;
+    if ((st = check_kv_q8(kv, index)) != PROJ_OK) return st;
+    AttnShape s;
+    if ((st = attn_shape(heads, kv->kv_heads, kv->k_dim, kv->v_dim, kv->v == nullptr, &s)) != PROJ_OK) return st;
+    if (batch < 0) return api_fail(PROJ_ERR_INVALID_ARG, "batch=%d is negative", batch);
+    const float scale_log2 = scale * 1.4426950408889634f;  // log2(e)
+    if (!std::isfinite(scale_log2)) return api_fail(PROJ_ERR_INVALID_ARG, "scale (times log2 e) must be finite");
+    // (units of the line fit 30 bits)
+    const int64_t most_tiles = (static_cast<int64_t>(index->max_pages) * index->page_size + hsp::kAttnTile - 1) / hsp::kAttnTile;
+    if (static_cast<int64_t>(batch) * kv->kv_heads * (most_tiles + s.weight) >= (int64_t(1) << 30))
+        return api_fail(PROJ_ERR_UNSUPPORTED_SHAPE, "batch=%d of up to %d pages is too large", batch, index->max_pages);
+    if ((st = check_apart_q8(kv, index)) != PROJ_OK) return st;
+    if (batch == 0) return hsp::api_ok();
+    if (!rows && batch > index->num_rows)
+        return api_fail(PROJ_ERR_INVALID_ARG, "batch=%d exceeds the table's %d rows", batch, index->num_rows);
+    if (!q || !out) return api_fail(PROJ_ERR_INVALID_ARG, "q and out must not be NULL");
+    if (!aligned(q, 16) || !aligned(out, 16) || q_row_stride % 8 || q_head_stride % 8)
+        return api_fail(PROJ_ERR_MISALIGNED, "q and out must be 16-byte aligned, q's strides multiples of 8 elements");
+    if ((heads > 1 && (q_head_stride < 8 || q_head_stride >= (int64_t(1) << 38))) ||
+        (batch > 1 && (q_row_stride < 8 || q_row_stride >= (int64_t(1) << 38))))
+        return api_fail(PROJ_ERR_UNSUPPORTED_SHAPE, "queries must lie apart (strides %lld, %lld)", (long long)q_row_stride,
+                        (long long)q_head_stride);
+    if (!aligned(lse, 4) || !aligned(rows, 4)) return api_fail(PROJ_ERR_MISALIGNED, "lse and rows must be 4-byte aligned");
+    hsp::ApiDevice dev;
+    if ((st = hsp::api_device(&dev)) != PROJ_OK) return st;
+    const int ctas = attn_ctas(s, dev.sms);
+    const bool split = most_tiles > kAttnWholeTiles;
+    if (split && (st = check_workspace(workspace, workspace_bytes, attn_workspace(s, ctas))) != PROJ_OK) return st;
+    const hsp::ApiOptions opt = hsp::api_options();
+    hsp::AttnQ8Args a;
+    memset(&a, 0, sizeof a);
+    a.q = q;
+    a.q_row = batch > 1 ? q_row_stride : 0;
+    a.q_head = q_head_stride;
+    a.k = k_side(kv);
+    a.v = v_side(kv);
+    a.table = index->block_table;
+    a.table_stride = index->table_stride;
+    a.lens = index->seq_lens;
+    a.rows = rows;
+    a.num_rows = index->num_rows;
+    a.max_pages = index->max_pages;
+    a.num_pages = index->num_pages;
+    a.page_shift = log2_of(index->page_size);
+    a.block_shift = log2_of(kv->block);
+    a.batch = batch;
+    a.kv_heads = kv->kv_heads;
+    a.group = heads / kv->kv_heads;
+    a.scale_log2 = scale_log2;
+    a.out = out;
+    a.lse = lse;
+    a.err_word = dev.err_word;
+    const cudaError_t e = hsp::launch_attn_q8_simple(a, opt.pdl, reinterpret_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return hsp::api_cuda_fail(e, "kernel launch (paged attention, 8 bits)");
     hsp::api_count_launches(1);
     return hsp::api_ok();
 }

@@ -93,6 +93,65 @@ struct AppendArgs {
 };
 cudaError_t launch_append(const AppendArgs &a, int sms, int pdl, cudaStream_t stream);
 
+// ---- the cache in 8 bits ------------------------------------------------------------------
+
+// Where the codes and scales of one side (keys or values) lie: codes in bytes, scales in elements.
+struct Q8Side {
+    uint8_t *codes;                  // null: none (the values of a latent cache)
+    float *scales;
+    int64_t page, token, head;       // code strides
+    int64_t s_page, s_block, s_head; // scale strides
+    int32_t dim;
+};
+
+struct AppendQ8Args {
+    const void *k_new, *v_new;       // as in AppendArgs
+    int64_t k_row, v_row;
+    Q8Side k, v;
+    const int32_t *table;
+    int64_t table_stride;
+    const int32_t *lens, *rows, *positions;  // rows, positions may be null
+    const int32_t *refs;
+    const float *cos_sin;
+    const void *q;
+    void *q_out;
+    int64_t q_row, q_head, qo_row, qo_head;
+    int32_t num_rows, max_pages, num_pages, page_shift;
+    int32_t block_shift;             // log2(tokens per scale)
+    int32_t tokens, kv_heads, heads, rot, max_pos, interleaved;
+    int *err_word;
+};
+cudaError_t launch_append_q8(const AppendQ8Args &a, int sms, int pdl, cudaStream_t stream);
+
+struct ReadQ8Args {
+    Q8Side k, v;
+    void *k_out, *v_out;             // [tokens, kv_heads, dim] bf16, tokens at *_row (elements)
+    int64_t k_row, v_row;
+    const int32_t *table;
+    int64_t table_stride;
+    const int32_t *lens, *rows, *positions;
+    int32_t num_rows, max_pages, num_pages, page_shift, block_shift;
+    int32_t tokens, kv_heads;
+    int *err_word;
+};
+cudaError_t launch_read_q8(const ReadQ8Args &a, int sms, int pdl, cudaStream_t stream);
+
+struct AttnQ8Args {
+    const void *q;                   // [batch, heads, k_dim] bf16
+    int64_t q_row, q_head;
+    Q8Side k, v;                     // (latent: v is k's first columns)
+    const int32_t *table;
+    int64_t table_stride;
+    const int32_t *lens, *rows;
+    int32_t num_rows, max_pages, num_pages, page_shift, block_shift;
+    int32_t batch, kv_heads, group;
+    float scale_log2;
+    void *out;
+    float *lse;
+    int *err_word;
+};
+cudaError_t launch_attn_q8_simple(const AttnQ8Args &a, int pdl, cudaStream_t stream);
+
 // ---- pages ------------------------------------------------------------------------------
 
 constexpr int kMaxPools = 4;

@@ -153,13 +153,13 @@ proj_page_index page_index(const at::Tensor &table, const at::Tensor &lens, cons
 }
 
 // v_dim None: the values' columns, or 512 of a latent cache.
-proj_kv_pages kv_pages(const at::Tensor &k, const at::Tensor &v, PyObject *v_dim_or_none) {
+proj_kv_pages kv_pages(const at::Tensor &k, const at::Tensor &v, PyObject *v_dim_or_none, at::ScalarType type = at::kBFloat16) {
     const bool given = v_dim_or_none != Py_None;
     const int64_t v_dim = given ? integer(v_dim_or_none) : 512;
     if (k.dim() != 4 || k.stride(3) != 1)
         refuse(PROJ_ERR_INVALID_ARG, "k_pages must be a [num_pages, page_size, kv_heads, k_dim] tensor with dense columns");
-    if (k.scalar_type() != at::kBFloat16 || (v.defined() && v.scalar_type() != at::kBFloat16))
-        refuse(PROJ_ERR_UNSUPPORTED_DTYPE, "the cache holds bf16");
+    if (k.scalar_type() != type || (v.defined() && v.scalar_type() != type))
+        refuse(PROJ_ERR_UNSUPPORTED_DTYPE, "the cache holds %s", type == at::kBFloat16 ? "bf16" : "float8_e4m3fn");
     proj_kv_pages p = {};
     p.k = k.data_ptr();
     p.kv_heads = narrow(k.size(2));
@@ -262,53 +262,117 @@ void arguments(Py_ssize_t have, Py_ssize_t want) {
     }
 }
 
+// A cache in 8 bits: its bf16 counterpart's checks (sizes, columns, v_dim), with codes for elements, and the scales.
+proj_kv_pages_q8 kv_pages_q8(const at::Tensor &k, const at::Tensor &v, const at::Tensor &ks, const at::Tensor &vs, PyObject *v_dim_or_none) {
+    const proj_kv_pages e = kv_pages(k, v, v_dim_or_none, at::kFloat8_e4m3fn);
+    proj_kv_pages_q8 p = {};
+    p.k = e.k;
+    p.v = e.v;
+    p.kv_heads = e.kv_heads;
+    p.k_dim = e.k_dim;
+    p.v_dim = e.v_dim;
+    p.k_page_stride = e.k_page_stride;
+    p.k_token_stride = e.k_token_stride;
+    p.k_head_stride = e.k_head_stride;
+    p.v_page_stride = e.v_page_stride;
+    p.v_token_stride = e.v_token_stride;
+    p.v_head_stride = e.v_head_stride;
+    if (vs.defined() != v.defined()) refuse(PROJ_ERR_INVALID_ARG, "v_scales goes with v_pages");
+    auto scales = [&](const char *name, const at::Tensor &t) {
+        if (t.scalar_type() != at::kFloat) refuse(PROJ_ERR_UNSUPPORTED_DTYPE, "%s must be float32", name);
+        if (t.dim() != 3 || t.size(0) != k.size(0) || t.size(1) < 1 || k.size(1) % t.size(1) != 0 || t.size(2) != k.size(2) ||
+            (name[0] == 'v' && t.size(1) != ks.size(1)))
+            refuse(PROJ_ERR_INVALID_ARG, "%s must be [num_pages, page_size / block, kv_heads]", name);
+        return static_cast<float *>(t.data_ptr());
+    };
+    p.k_scale = scales("k_scales", ks);
+    p.block = narrow(k.size(1) / ks.size(1));
+    p.k_scale_page_stride = ks.stride(0);
+    p.k_scale_block_stride = ks.stride(1);
+    p.k_scale_head_stride = ks.stride(2);
+    if (vs.defined()) {
+        p.v_scale = scales("v_scales", vs);
+        p.v_scale_page_stride = vs.stride(0);
+        p.v_scale_block_stride = vs.stride(1);
+        p.v_scale_head_stride = vs.stride(2);
+    }
+    return p;
+}
+
+// What is the same for both kinds of cache: queries, outputs, workspace, and the call with all of them.
+struct AttentionCall {
+    const at::Tensor &q;
+    const at::Tensor &table, &lens;
+    float scale;
+    at::Tensor rows, out, lse;
+    bool return_lse;
+    at::Tensor workspace;
+    PyObject *stream;
+};
+template <typename Kv, typename Bytes, typename Call>
+PyObject *attend(AttentionCall &c, const Kv &kv, int64_t num_pages, int64_t page_size, int dev, Bytes workspace_bytes, Call call) {
+    const at::Tensor &q = c.q;
+    at::Tensor &out = c.out, &lse = c.lse;
+    if (q.dim() != 3 || q.size(2) != kv.k_dim || q.stride(2) != 1)
+        refuse(PROJ_ERR_INVALID_ARG, "q must be a [batch, heads, k_dim] tensor with dense columns");
+    if (q.scalar_type() != at::kBFloat16) refuse(PROJ_ERR_UNSUPPORTED_DTYPE, "unsupported tensor dtype %s", c10::toString(q.scalar_type()));
+    const int64_t batch = q.size(0), heads = q.size(1), dv = kv.v_dim;
+    if (dv < 1 || dv > kv.k_dim)  // (before out is made)
+        refuse(PROJ_ERR_UNSUPPORTED_SHAPE, "k_dim=%d, v_dim=%d: the values are at most as wide as the keys", kv.k_dim, kv.v_dim);
+    const proj_page_index ix = page_index(c.table, c.lens, at::Tensor(), num_pages, page_size);
+    if (!out.defined()) out = make({batch, heads, dv}, at::kBFloat16, dev);
+    else if (out.sizes() != at::IntArrayRef({batch, heads, dv}) || out.scalar_type() != at::kBFloat16 || !out.is_contiguous())
+        refuse(PROJ_ERR_INVALID_ARG, "out must be a dense [%lld, %lld, %lld] bf16 tensor", (long long)batch, (long long)heads, (long long)dv);
+    if (!lse.defined()) {
+        if (c.return_lse) lse = make({batch, heads}, at::kFloat, dev);
+    } else if (lse.sizes() != at::IntArrayRef({batch, heads}) || lse.scalar_type() != at::kFloat || !lse.is_contiguous()) {
+        refuse(PROJ_ERR_INVALID_ARG, "lse must be a dense [%lld, %lld] float32 tensor", (long long)batch, (long long)heads);
+    }
+    const int32_t *rp = c.rows.defined() ? ints("rows", c.rows, batch) : nullptr;
+    Workspace ws;
+    if (c.workspace.defined() || static_cast<int64_t>(ix.max_pages) * ix.page_size > PROJ_UNCUT_TOKENS)
+        use(&ws, c.workspace, c.workspace.defined() ? 0 : workspace_bytes(narrow(heads), kv.kv_heads, kv.k_dim, kv.v_dim, kv.v == nullptr));
+    const proj_stream_t stream = stream_of(c.stream, dev);
+    const void *qp = q.data_ptr();
+    void *op = out.data_ptr();
+    float *lp = lse.defined() ? static_cast<float *>(lse.data_ptr()) : nullptr;
+    const int64_t qs = q.stride(0), qh = q.stride(1);
+    run([&] { return call(qp, qs, qh, &kv, &ix, rp, narrow(batch), narrow(heads), c.scale, op, lp, ws.ptr, ws.bytes, stream); });
+    if (!c.return_lse) return THPVariable_Wrap(out);
+    PyObject *a = THPVariable_Wrap(out), *b = THPVariable_Wrap(lse);
+    PyObject *both = a && b ? PyTuple_Pack(2, a, b) : nullptr;
+    Py_XDECREF(a);
+    Py_XDECREF(b);
+    return both;
+}
+
 // (q, k_pages, v_pages, block_table, seq_lens, scale, v_dim, rows, out, lse, return_lse, workspace, stream)
 PyObject *paged_attention(PyObject *, PyObject *const *args, Py_ssize_t nargs) {
     return guarded([&]() -> PyObject * {
         arguments(nargs, 13);
-        const at::Tensor &q = tensor(args[0], "q"), &k = tensor(args[1], "k_pages");
+        const at::Tensor &k = tensor(args[1], "k_pages");
         const at::Tensor v = optional(args[2], "v_pages");
-        const at::Tensor &table = tensor(args[3], "block_table"), &lens = tensor(args[4], "seq_lens");
-        const float scale = static_cast<float>(number(args[5]));
-        const at::Tensor rows = optional(args[7], "rows");
-        at::Tensor out = optional(args[8], "out"), lse = optional(args[9], "lse");
-        const bool return_lse = truth(args[10]);
-        const at::Tensor given = optional(args[11], "workspace");
-        const int dev = device_of({&q, &k, &v, &table, &lens, &rows, &out, &lse, &given});
+        AttentionCall c{tensor(args[0], "q"), tensor(args[3], "block_table"), tensor(args[4], "seq_lens"), static_cast<float>(number(args[5])),
+                        optional(args[7], "rows"), optional(args[8], "out"), optional(args[9], "lse"), truth(args[10]),
+                        optional(args[11], "workspace"), args[12]};
+        const int dev = device_of({&c.q, &k, &v, &c.table, &c.lens, &c.rows, &c.out, &c.lse, &c.workspace});
         const proj_kv_pages kv = kv_pages(k, v, args[6]);
-        if (q.dim() != 3 || q.size(2) != kv.k_dim || q.stride(2) != 1)
-            refuse(PROJ_ERR_INVALID_ARG, "q must be a [batch, heads, k_dim] tensor with dense columns");
-        if (q.scalar_type() != at::kBFloat16) refuse(PROJ_ERR_UNSUPPORTED_DTYPE, "unsupported tensor dtype %s", c10::toString(q.scalar_type()));
-        const int64_t batch = q.size(0), heads = q.size(1), dv = kv.v_dim;
-        if (dv < 1 || dv > kv.k_dim)  // (before out is made)
-            refuse(PROJ_ERR_UNSUPPORTED_SHAPE, "k_dim=%d, v_dim=%d: the values are at most as wide as the keys", kv.k_dim, kv.v_dim);
-        const proj_page_index ix = page_index(table, lens, at::Tensor(), k.size(0), k.size(1));
-        if (!out.defined()) out = make({batch, heads, dv}, at::kBFloat16, dev);
-        else if (out.sizes() != at::IntArrayRef({batch, heads, dv}) || out.scalar_type() != at::kBFloat16 || !out.is_contiguous())
-            refuse(PROJ_ERR_INVALID_ARG, "out must be a dense [%lld, %lld, %lld] bf16 tensor", (long long)batch, (long long)heads, (long long)dv);
-        if (!lse.defined()) {
-            if (return_lse) lse = make({batch, heads}, at::kFloat, dev);
-        } else if (lse.sizes() != at::IntArrayRef({batch, heads}) || lse.scalar_type() != at::kFloat || !lse.is_contiguous()) {
-            refuse(PROJ_ERR_INVALID_ARG, "lse must be a dense [%lld, %lld] float32 tensor", (long long)batch, (long long)heads);
-        }
-        const int32_t *rp = rows.defined() ? ints("rows", rows, batch) : nullptr;
-        Workspace ws;
-        if (given.defined() || static_cast<int64_t>(ix.max_pages) * ix.page_size > PROJ_UNCUT_TOKENS)
-            use(&ws, given, given.defined() ? 0 : proj_paged_attention_workspace_bytes(narrow(heads), kv.kv_heads, kv.k_dim, kv.v_dim, !v.defined()));
-        const proj_stream_t stream = stream_of(args[12], dev);
-        const void *qp = q.data_ptr();
-        void *op = out.data_ptr();
-        float *lp = lse.defined() ? static_cast<float *>(lse.data_ptr()) : nullptr;
-        const int64_t qs = q.stride(0), qh = q.stride(1);
-        run([&] {
-            return proj_paged_attention(qp, qs, qh, &kv, &ix, rp, narrow(batch), narrow(heads), scale, op, lp, ws.ptr, ws.bytes, stream);
-        });
-        if (!return_lse) return THPVariable_Wrap(out);
-        PyObject *a = THPVariable_Wrap(out), *b = THPVariable_Wrap(lse);
-        PyObject *both = a && b ? PyTuple_Pack(2, a, b) : nullptr;
-        Py_XDECREF(a);
-        Py_XDECREF(b);
-        return both;
+        return attend(c, kv, k.size(0), k.size(1), dev, proj_paged_attention_workspace_bytes, proj_paged_attention);
+    });
+}
+
+// (q, k_pages, v_pages, k_scales, v_scales, block_table, seq_lens, scale, v_dim, rows, out, lse, return_lse, workspace, stream)
+PyObject *paged_attention_q8(PyObject *, PyObject *const *args, Py_ssize_t nargs) {
+    return guarded([&]() -> PyObject * {
+        arguments(nargs, 15);
+        const at::Tensor &k = tensor(args[1], "k_pages"), &ks = tensor(args[3], "k_scales");
+        const at::Tensor v = optional(args[2], "v_pages"), vs = optional(args[4], "v_scales");
+        AttentionCall c{tensor(args[0], "q"), tensor(args[5], "block_table"), tensor(args[6], "seq_lens"), static_cast<float>(number(args[7])),
+                        optional(args[9], "rows"), optional(args[10], "out"), optional(args[11], "lse"), truth(args[12]),
+                        optional(args[13], "workspace"), args[14]};
+        const int dev = device_of({&c.q, &k, &v, &ks, &vs, &c.table, &c.lens, &c.rows, &c.out, &c.lse, &c.workspace});
+        const proj_kv_pages_q8 kv = kv_pages_q8(k, v, ks, vs, args[8]);
+        return attend(c, kv, k.size(0), k.size(1), dev, proj_paged_attention_q8_workspace_bytes, proj_paged_attention_q8);
     });
 }
 
@@ -324,61 +388,126 @@ const void *new_rows(const char *name, const at::Tensor &t, int64_t tokens, int6
     return t.data_ptr();
 }
 
+// What is the same for both kinds of cache: the new rows, the turn, the queries, and the call with all of them.
+struct AppendCall {
+    const at::Tensor &kn;
+    at::Tensor vn;
+    const at::Tensor &table, &lens;
+    at::Tensor rows, pos, cs;
+    PyObject *interleaved;
+    at::Tensor q, q_out;
+    PyObject *q_out_given, *stream;
+    at::Tensor refs;
+};
+template <typename Kv, typename Call>
+PyObject *append(AppendCall &c, const Kv &kv, int64_t num_pages, int64_t page_size, int dev, Call call) {
+    const at::Tensor &kn = c.kn, &q = c.q;
+    at::Tensor &q_out = c.q_out;
+    if (kn.dim() < 1) refuse(PROJ_ERR_INVALID_ARG, "k_new must be [tokens, ...]");
+    const int64_t tokens = kn.size(0), dim = kv.k_dim;
+    if (c.vn.defined() != (kv.v != nullptr)) refuse(PROJ_ERR_INVALID_ARG, "v_new goes with a cache that has values of its own");
+    int64_t ks = 0, vs = 0;
+    const void *kp = new_rows("k_new", kn, tokens, kv.kv_heads, dim, &ks);
+    const void *vp = c.vn.defined() ? new_rows("v_new", c.vn, tokens, kv.kv_heads, kv.v_dim, &vs) : nullptr;
+    const proj_page_index ix = page_index(c.table, c.lens, c.refs, num_pages, page_size);
+    proj_rotary rot = {};
+    if (c.cs.defined()) {
+        if (c.cs.scalar_type() != at::kFloat || c.cs.dim() != 2 || !c.cs.is_contiguous())
+            refuse(PROJ_ERR_INVALID_ARG, "cos_sin must be a dense [max_pos, rot] float32 tensor");
+        rot.cos_sin = static_cast<const float *>(c.cs.data_ptr());
+        rot.max_pos = narrow(c.cs.size(0));
+        rot.dim = narrow(c.cs.size(1));
+        rot.interleaved = truth(c.interleaved);
+    }
+    int64_t heads = 0, qs = 0, qh = 0, os = 0, oh = 0;
+    if (q.defined()) {
+        if (!q_out.defined()) q_out = make(q.sizes(), at::kBFloat16, dev);
+        if (q.dim() != 3 || q.size(0) != tokens || q.size(2) != dim || q_out.sizes() != q.sizes() || q.stride(2) != 1 ||
+            q_out.stride(2) != 1)
+            refuse(PROJ_ERR_INVALID_ARG, "q and q_out must be [tokens, heads, %lld] with dense columns", (long long)dim);
+        if (q.scalar_type() != at::kBFloat16 || q_out.scalar_type() != at::kBFloat16)
+            refuse(PROJ_ERR_UNSUPPORTED_DTYPE, "unsupported tensor dtype %s", c10::toString(q.scalar_type()));
+        heads = q.size(1);
+        qs = q.stride(0);
+        qh = q.stride(1);
+        os = q_out.stride(0);
+        oh = q_out.stride(1);
+    }
+    const int32_t *rp = c.rows.defined() ? ints("rows", c.rows, tokens) : nullptr;
+    const int32_t *pp = c.pos.defined() ? ints("positions", c.pos, tokens) : nullptr;
+    const proj_stream_t stream = stream_of(c.stream, dev);
+    const void *qp = q.defined() ? q.data_ptr() : nullptr;
+    void *op = q.defined() ? q_out.data_ptr() : nullptr;
+    run([&] {
+        return call(kp, ks, vp, vs, &kv, &ix, rp, pp, narrow(tokens), c.cs.defined() ? &rot : nullptr, qp, qs, qh, op, os, oh,
+                    narrow(heads), stream);
+    });
+    if (!q.defined()) Py_RETURN_NONE;
+    if (c.q_out_given != Py_None) return Py_NewRef(c.q_out_given);
+    return THPVariable_Wrap(q_out);
+}
+
 // (k_new, v_new, k_pages, v_pages, block_table, seq_lens, rows, positions, cos_sin, interleaved, q, q_out, stream, ref_counts)
 PyObject *cache_append(PyObject *, PyObject *const *args, Py_ssize_t nargs) {
     return guarded([&]() -> PyObject * {
         arguments(nargs, 14);
-        const at::Tensor &kn = tensor(args[0], "k_new"), &k = tensor(args[2], "k_pages");
-        const at::Tensor vn = optional(args[1], "v_new"), v = optional(args[3], "v_pages");
-        const at::Tensor &table = tensor(args[4], "block_table"), &lens = tensor(args[5], "seq_lens");
-        const at::Tensor rows = optional(args[6], "rows"), pos = optional(args[7], "positions"), cs = optional(args[8], "cos_sin");
-        const at::Tensor q = optional(args[10], "q");
-        at::Tensor q_out = optional(args[11], "q_out");
-        const at::Tensor refs = optional(args[13], "ref_counts");
-        const int dev = device_of({&kn, &vn, &k, &v, &table, &lens, &rows, &pos, &cs, &q, &q_out, &refs});
+        const at::Tensor &k = tensor(args[2], "k_pages");
+        const at::Tensor v = optional(args[3], "v_pages");
+        AppendCall c{tensor(args[0], "k_new"), optional(args[1], "v_new"), tensor(args[4], "block_table"), tensor(args[5], "seq_lens"),
+                     optional(args[6], "rows"), optional(args[7], "positions"), optional(args[8], "cos_sin"), args[9],
+                     optional(args[10], "q"), optional(args[11], "q_out"), args[11], args[12], optional(args[13], "ref_counts")};
+        const int dev = device_of({&c.kn, &c.vn, &k, &v, &c.table, &c.lens, &c.rows, &c.pos, &c.cs, &c.q, &c.q_out, &c.refs});
         const proj_kv_pages kv = kv_pages(k, v, Py_None);
-        if (kn.dim() < 1) refuse(PROJ_ERR_INVALID_ARG, "k_new must be [tokens, ...]");
-        const int64_t tokens = kn.size(0), dim = kv.k_dim;
-        if (vn.defined() != v.defined()) refuse(PROJ_ERR_INVALID_ARG, "v_new goes with a cache that has values of its own");
-        int64_t ks = 0, vs = 0;
-        const void *kp = new_rows("k_new", kn, tokens, kv.kv_heads, dim, &ks);
-        const void *vp = vn.defined() ? new_rows("v_new", vn, tokens, kv.kv_heads, kv.v_dim, &vs) : nullptr;
-        const proj_page_index ix = page_index(table, lens, refs, k.size(0), k.size(1));
-        proj_rotary rot = {};
-        if (cs.defined()) {
-            if (cs.scalar_type() != at::kFloat || cs.dim() != 2 || !cs.is_contiguous())
-                refuse(PROJ_ERR_INVALID_ARG, "cos_sin must be a dense [max_pos, rot] float32 tensor");
-            rot.cos_sin = static_cast<const float *>(cs.data_ptr());
-            rot.max_pos = narrow(cs.size(0));
-            rot.dim = narrow(cs.size(1));
-            rot.interleaved = truth(args[9]);
-        }
-        int64_t heads = 0, qs = 0, qh = 0, os = 0, oh = 0;
-        if (q.defined()) {
-            if (!q_out.defined()) q_out = make(q.sizes(), at::kBFloat16, dev);
-            if (q.dim() != 3 || q.size(0) != tokens || q.size(2) != dim || q_out.sizes() != q.sizes() || q.stride(2) != 1 ||
-                q_out.stride(2) != 1)
-                refuse(PROJ_ERR_INVALID_ARG, "q and q_out must be [tokens, heads, %lld] with dense columns", (long long)dim);
-            if (q.scalar_type() != at::kBFloat16 || q_out.scalar_type() != at::kBFloat16)
-                refuse(PROJ_ERR_UNSUPPORTED_DTYPE, "unsupported tensor dtype %s", c10::toString(q.scalar_type()));
-            heads = q.size(1);
-            qs = q.stride(0);
-            qh = q.stride(1);
-            os = q_out.stride(0);
-            oh = q_out.stride(1);
-        }
+        return append(c, kv, k.size(0), k.size(1), dev, proj_cache_append);
+    });
+}
+
+// (k_new, v_new, k_pages, v_pages, k_scales, v_scales, block_table, seq_lens, rows, positions, cos_sin, interleaved, q, q_out,
+// stream, ref_counts)
+PyObject *cache_append_q8(PyObject *, PyObject *const *args, Py_ssize_t nargs) {
+    return guarded([&]() -> PyObject * {
+        arguments(nargs, 16);
+        const at::Tensor &k = tensor(args[2], "k_pages"), &ks = tensor(args[4], "k_scales");
+        const at::Tensor v = optional(args[3], "v_pages"), vs = optional(args[5], "v_scales");
+        AppendCall c{tensor(args[0], "k_new"), optional(args[1], "v_new"), tensor(args[6], "block_table"), tensor(args[7], "seq_lens"),
+                     optional(args[8], "rows"), optional(args[9], "positions"), optional(args[10], "cos_sin"), args[11],
+                     optional(args[12], "q"), optional(args[13], "q_out"), args[13], args[14], optional(args[15], "ref_counts")};
+        const int dev = device_of({&c.kn, &c.vn, &k, &v, &ks, &vs, &c.table, &c.lens, &c.rows, &c.pos, &c.cs, &c.q, &c.q_out, &c.refs});
+        const proj_kv_pages_q8 kv = kv_pages_q8(k, v, ks, vs, Py_None);
+        return append(c, kv, k.size(0), k.size(1), dev, proj_cache_append_q8);
+    });
+}
+
+// (k_pages, v_pages, k_scales, v_scales, block_table, seq_lens, rows, positions, k_out, v_out, stream)
+PyObject *cache_read_q8(PyObject *, PyObject *const *args, Py_ssize_t nargs) {
+    return guarded([&]() -> PyObject * {
+        arguments(nargs, 11);
+        const at::Tensor &k = tensor(args[0], "k_pages"), &ks = tensor(args[2], "k_scales");
+        const at::Tensor v = optional(args[1], "v_pages"), vs = optional(args[3], "v_scales");
+        const at::Tensor &table = tensor(args[4], "block_table"), &lens = tensor(args[5], "seq_lens");
+        const at::Tensor rows = optional(args[6], "rows"), pos = optional(args[7], "positions");
+        at::Tensor ko = optional(args[8], "k_out"), vo = optional(args[9], "v_out");
+        const int dev = device_of({&k, &v, &ks, &vs, &table, &lens, &rows, &pos, &ko, &vo});
+        const proj_kv_pages_q8 kv = kv_pages_q8(k, v, ks, vs, Py_None);
+        const proj_page_index ix = page_index(table, lens, at::Tensor(), k.size(0), k.size(1));
+        if (vo.defined() && !v.defined()) refuse(PROJ_ERR_INVALID_ARG, "v_out goes with a cache that has values of its own");
+        // as many tokens as rows or positions name, else one of every row
+        const int64_t tokens = rows.defined() ? rows.numel() : pos.defined() ? pos.numel() : lens.numel();
         const int32_t *rp = rows.defined() ? ints("rows", rows, tokens) : nullptr;
         const int32_t *pp = pos.defined() ? ints("positions", pos, tokens) : nullptr;
-        const proj_stream_t stream = stream_of(args[12], dev);
-        const void *qp = q.defined() ? q.data_ptr() : nullptr;
-        void *op = q.defined() ? q_out.data_ptr() : nullptr;
-        run([&] {
-            return proj_cache_append(kp, ks, vp, vs, &kv, &ix, rp, pp, narrow(tokens), cs.defined() ? &rot : nullptr, qp, qs, qh, op,
-                                     os, oh, narrow(heads), stream);
-        });
-        if (!q.defined()) Py_RETURN_NONE;
-        if (args[11] != Py_None) return Py_NewRef(args[11]);
-        return THPVariable_Wrap(q_out);
+        int64_t ks_row = 0, vs_row = 0;
+        if (!ko.defined()) ko = make({tokens, k.size(2), k.size(3)}, at::kBFloat16, dev);
+        if (v.defined() && !vo.defined()) vo = make({tokens, v.size(2), v.size(3)}, at::kBFloat16, dev);
+        void *kp = const_cast<void *>(new_rows("k_out", ko, tokens, kv.kv_heads, kv.k_dim, &ks_row));
+        void *vp = vo.defined() ? const_cast<void *>(new_rows("v_out", vo, tokens, kv.kv_heads, kv.v_dim, &vs_row)) : nullptr;
+        const proj_stream_t stream = stream_of(args[10], dev);
+        run([&] { return proj_cache_read_q8(&kv, &ix, rp, pp, narrow(tokens), kp, ks_row, vp, vs_row, stream); });
+        PyObject *a = args[8] != Py_None ? Py_NewRef(args[8]) : THPVariable_Wrap(ko);
+        PyObject *b = !vo.defined() ? Py_NewRef(Py_None) : args[9] != Py_None ? Py_NewRef(args[9]) : THPVariable_Wrap(vo);
+        PyObject *both = a && b ? PyTuple_Pack(2, a, b) : nullptr;
+        Py_XDECREF(a);
+        Py_XDECREF(b);
+        return both;
     });
 }
 
@@ -487,6 +616,9 @@ PyObject *set_error(PyObject *, PyObject *cls) {
 PyMethodDef kMethods[] = {
     {"paged_attention", reinterpret_cast<PyCFunction>(reinterpret_cast<void *>(paged_attention)), METH_FASTCALL, nullptr},
     {"cache_append", reinterpret_cast<PyCFunction>(reinterpret_cast<void *>(cache_append)), METH_FASTCALL, nullptr},
+    {"paged_attention_q8", reinterpret_cast<PyCFunction>(reinterpret_cast<void *>(paged_attention_q8)), METH_FASTCALL, nullptr},
+    {"cache_append_q8", reinterpret_cast<PyCFunction>(reinterpret_cast<void *>(cache_append_q8)), METH_FASTCALL, nullptr},
+    {"cache_read_q8", reinterpret_cast<PyCFunction>(reinterpret_cast<void *>(cache_read_q8)), METH_FASTCALL, nullptr},
     {"cache_resize", reinterpret_cast<PyCFunction>(reinterpret_cast<void *>(cache_resize)), METH_FASTCALL, nullptr},
     {"cache_fork", reinterpret_cast<PyCFunction>(reinterpret_cast<void *>(cache_fork)), METH_FASTCALL, nullptr},
     {"cache_compact", reinterpret_cast<PyCFunction>(reinterpret_cast<void *>(cache_compact)), METH_FASTCALL, nullptr},

@@ -558,6 +558,87 @@ proj_status proj_cache_copy_pages(const proj_page_pool *pools, int32_t num_pools
                                   int32_t n, proj_stream_t stream);
 
 /*
+ * The cache in 8 bits: the same pages, tables, lengths and page calls, half the bytes.
+ *
+ * A value is code * scale: the code is e4m3 (1 sign, 4 exponent, 3 mantissa bits; largest 448; no infinities, NaN
+ * 0x7f and 0xff), the scale one fp32 number for each `block` tokens of a page (from a multiple of `block` on) and
+ * each kv head, positive and finite.  The scales that proj_cache_append_q8 writes are powers of two from 2^-60 to
+ * 2^60; the calls that read take any from 2^-60 to 2^60.
+ *   k, v       codes, 16-byte aligned: k_dim consecutive bytes at k + p * k_page_stride + t * k_token_stride +
+ *              h * k_head_stride (bytes; multiples of 16), v likewise
+ *   k_scale    fp32, at k_scale + p * k_scale_page_stride + (t / block) * k_scale_block_stride +
+ *              h * k_scale_head_stride (elements)
+ *   block      a power of two from 1 to the page size
+ * Latent and grouped caches as proj_kv_pages has them (a latent cache's values have its keys' scales).  Where the cache
+ * is written, steps do not overlap.  Pages that proj_cache_resize, _compact and _copy_pages move must carry their
+ * scales along: pools of their own, or codes and scales side by side in one pool's pages (a page of a pool is a multiple
+ * of 16 bytes).
+ */
+typedef struct {
+    void *k;
+    void *v;                /* NULL: a latent cache */
+    float *k_scale;
+    float *v_scale;         /* NULL with v */
+    int32_t kv_heads, k_dim, v_dim;
+    int32_t block;
+    int64_t k_page_stride, k_token_stride, k_head_stride;
+    int64_t v_page_stride, v_token_stride, v_head_stride;
+    int64_t k_scale_page_stride, k_scale_block_stride, k_scale_head_stride;
+    int64_t v_scale_page_stride, v_scale_block_stride, v_scale_head_stride;
+} proj_kv_pages_q8;
+
+/*
+ * proj_cache_append_q8 -- proj_cache_append into a cache in 8 bits: bf16 keys and values of `tokens` new tokens are
+ * turned, quantised and written, the queries turned.  Arguments, limits and errors as proj_cache_append has them
+ * (columns in multiples of 16).  For each block and head that the call writes, with x the turned keys
+ * (or the values) of its new tokens there:
+ *     s    = the smallest power of two from 2^-60 to 2^60 with max |x| <= 448 s
+ *     s    = the block's scale so far, if that is larger and the block has tokens in front of the first new one
+ *     code = x / s rounded to the nearest e4m3 value, ties to the even code
+ * Where s grew, the codes in front are rounded to the new scale alike (exact for codes that stay normal).  The turn is
+ * rounded only here: x is the exact sum of its two fp32 products.  Values that are NaN, infinite or beyond 448 * 2^60 do
+ * not count for s and become NaN.
+ * New tokens of a row that share a block stand next to each other in the call (in any order): two groups of them
+ * in one call would each make the block's scale, and which one stays is not defined.  What a block holds behind its
+ * first new token, written by earlier calls, loses its meaning unless this call writes it anew.
+ * One kernel launch; tokens = 0 succeeds and touches nothing.
+ */
+proj_status proj_cache_append_q8(const void *k_new, int64_t k_row_stride, const void *v_new, int64_t v_row_stride,
+                                 const proj_kv_pages_q8 *kv, const proj_page_index *index, const int32_t *rows,
+                                 const int32_t *positions, int32_t tokens, const proj_rotary *rotary, const void *q,
+                                 int64_t q_row_stride, int64_t q_head_stride, void *q_out, int64_t q_out_row_stride,
+                                 int64_t q_out_head_stride, int32_t heads, proj_stream_t stream);
+
+/*
+ * proj_cache_read_q8 -- tokens of a cache in 8 bits, in bf16: k_out[i] (and v_out[i]) = code * scale, rounded once
+ * (exact for scales that are powers of two).
+ *   rows       device [tokens] table rows, or NULL for token i = row i
+ *   positions  device [tokens], each below its row's seq_lens, or NULL for the last place of the row
+ *   k_out      device [tokens, kv_heads, k_dim] bf16, 16-byte aligned, tokens at k_row_stride (elements, a multiple
+ *              of 8), heads dense
+ *   v_out      device [tokens, kv_heads, v_dim] (NULL for a latent cache)
+ * A token outside the cache gives zeros and is reported (PROJ_ERR_BAD_INDEX).  One kernel launch; tokens = 0 succeeds
+ * and touches nothing.
+ */
+proj_status proj_cache_read_q8(const proj_kv_pages_q8 *kv, const proj_page_index *index, const int32_t *rows,
+                               const int32_t *positions, int32_t tokens, void *k_out, int64_t k_row_stride, void *v_out,
+                               int64_t v_row_stride, proj_stream_t stream);
+
+/*
+ * proj_paged_attention_q8 -- proj_paged_attention over a cache in 8 bits: q and out are bf16, keys and values
+ * code * scale.  Arguments, shapes, limits and errors as proj_paged_attention has them.
+ */
+proj_status proj_paged_attention_q8(const void *q, int64_t q_row_stride, int64_t q_head_stride,
+                                    const proj_kv_pages_q8 *kv, const proj_page_index *index,
+                                    const int32_t *rows, int32_t batch, int32_t heads, float scale,
+                                    void *out, float *lse, void *workspace, size_t workspace_bytes,
+                                    proj_stream_t stream);
+
+/* Workspace bytes of proj_paged_attention_q8 (as for proj_paged_attention). */
+size_t proj_paged_attention_q8_workspace_bytes(int32_t heads, int32_t kv_heads, int32_t k_dim,
+                                               int32_t v_dim, int32_t latent);
+
+/*
  * proj_supported -- host-side query: 1 if (M, K, n_total, dtype) is served,
  * 0 otherwise (the shape gate; TensorRT-LLM PR #20502, dense-MLP and fused-A
  * commit messages: a host query answers whether the kernels serve a shape).
