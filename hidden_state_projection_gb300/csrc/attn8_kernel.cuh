@@ -1,0 +1,825 @@
+// attn8_kernel.cuh -- attention of one new token per sequence over a paged cache held in 8 bits.
+//
+//   o[b, h] = sum_t p_t vs_t vc_t,  p = softmax_t(scale ks_t q[b, h] . kc_t),  t < len_b
+//
+// kc, vc: e4m3 codes, ks, vs: the scales of their blocks.  The shape of the bf16 kernel (attn_kernel.cuh: tokens or
+// value columns on the instruction's rows, query heads its columns, tiles in a ring, a line of tiles cut over the
+// CTAs), with 8-bit instructions that read the codes as they lie in the cache, so that nothing is converted on the
+// way and a byte of the cache passes shared memory three times (copy, scores, values):
+//   S^T[128 tokens x 2N] = KC[128 x dk] . [Qh; Ql]^T       (both operands K-major)
+//   O^T[dv x N]         += VC^T[dv x 128] . (Wh + Wl)^T    (both MN-major)
+//
+// Queries.  A bf16 number has 8 significant bits, e4m3 has 4: q 2^-e = Qh + Ql / 16, e the head's own exponent (the
+// largest |q| of the head falls to 224 .. 448), is exact down to 2^-14, 2^-21.8 of the head's largest.  The two products
+// lie side by side in tensor memory and are added in the softmax.
+//
+// Weights.  The scale of a token's values goes into its weight: w_t = p_t vs_t, in the softmax's own units
+// 2^(s_t + log2 vs_t - m).  w = Wh + Wl, Wh rounded to e4m3, the rest to e5m2: at most 2^-7 of w while w is at least
+// 2^-6 (the rest of a smaller one is half of 2^-9 or less, and e5m2 keeps an eighth of that), largest 448.  Two 8-bit
+// pieces have not the range of a bf16 number, so the reference point m follows the tiles in both directions: a tile whose
+// largest weight in some column is beyond 2^8.75, or below 2^0.5, moves that column's m (largest weight to 2^4.5)
+// and rescales O^T; what a tile's rounding leaves out is small beside the tile's own largest weight, whatever weights
+// other tiles have (a first token with nearly all the weight before a long tail).  Downwards m stops 30 below
+// its highest point.  O^T is divided by l = sum (Wh + Wl)_t / vs_t, so the rounding that all of a row's weight has in
+// common cancels; lse takes the sum u of the unrounded weights.  Sums and statistics are fp32.
+//
+// Warps: four for the softmax (they also carry O^T out), a copy producer, an issuer of the scores, an issuer of the
+// products with the values, one that fetches the tiles' scales ahead; over a latent cache four more that split the next
+// part's queries while the last one is under way (of a grouped cache, few and short, the softmax warps do).  All
+// waits are at mbarriers and bounded.
+#pragma once
+
+#include <cuda_fp16.h>
+
+#include "attn_common.cuh"
+#include "q8.cuh"
+
+namespace hsp {
+
+// K-major operand in 64-byte lines (64-byte swizzle): eight rows in 512 bytes.
+__device__ __forceinline__ uint64_t umma_desc_sw64(uint32_t smem_addr) {
+    uint64_t d = 0;
+    d |= static_cast<uint64_t>((smem_addr & 0x3FFFFu) >> 4);
+    d |= static_cast<uint64_t>(16u >> 4) << 16;
+    d |= static_cast<uint64_t>(512u >> 4) << 32;
+    d |= static_cast<uint64_t>(1u) << 46;
+    d |= static_cast<uint64_t>(4u) << 61;
+    return d;
+}
+// MN-major operand whose M (or N) extent lies in one line of LINE bytes, swizzled over that width; eight lines of K
+// follow each other, groups of eight 8 * LINE bytes apart.  (K-major with LINE = 128 or 64: the same numbers.)
+template <int LINE>
+__device__ __forceinline__ uint64_t umma_desc_lines(uint32_t smem_addr) {
+    static_assert(LINE == 128 || LINE == 64 || LINE == 32, "a swizzle width");
+    uint64_t d = 0;
+    d |= static_cast<uint64_t>((smem_addr & 0x3FFFFu) >> 4);
+    d |= static_cast<uint64_t>((8u * LINE) >> 4) << 16;
+    d |= static_cast<uint64_t>((8u * LINE) >> 4) << 32;
+    d |= static_cast<uint64_t>(1u) << 46;
+    d |= static_cast<uint64_t>(LINE == 128 ? 2u : LINE == 64 ? 4u : 6u) << 61;
+    return d;
+}
+// Where 16-byte piece `chunk` of line `row` lies in its line.
+template <int LINE>
+__device__ __forceinline__ int swizzled(int row, int chunk) {
+    return LINE == 128 ? (chunk ^ (row & 7)) << 4 : LINE == 64 ? (chunk ^ ((row >> 1) & 3)) << 4 : (chunk ^ ((row >> 2) & 1)) << 4;
+}
+
+// Two fp16 numbers to e4m3 or e5m2 codes and e5m2 codes back (`lo` in bits 0-7).
+__device__ __forceinline__ uint32_t half2_to_e4m3x2(__half2 v) {
+    uint32_t r;
+    asm("{\n\t.reg .b16 c;\n\tcvt.rn.satfinite.e4m3x2.f16x2 c, %1;\n\tcvt.u32.u16 %0, c;\n\t}" : "=r"(r) : "r"(*reinterpret_cast<const uint32_t *>(&v)));
+    return r;
+}
+__device__ __forceinline__ uint32_t half2_to_e5m2x2(__half2 v) {
+    uint32_t r;
+    asm("{\n\t.reg .b16 c;\n\tcvt.rn.satfinite.e5m2x2.f16x2 c, %1;\n\tcvt.u32.u16 %0, c;\n\t}" : "=r"(r) : "r"(*reinterpret_cast<const uint32_t *>(&v)));
+    return r;
+}
+__device__ __forceinline__ __half2 e5m2x2_to_half2(uint32_t codes) {
+    uint32_t r;
+    asm("{\n\t.reg .b16 c;\n\tcvt.u16.u32 c, %1;\n\tcvt.rn.f16x2.e5m2x2 %0, c;\n\t}" : "=r"(r) : "r"(codes));
+    return *reinterpret_cast<const __half2 *>(&r);
+}
+
+// Barrier 2 of four warps that split queries.
+__device__ __forceinline__ void query_sync() { asm volatile("barrier.cta.sync.aligned 2, 128;" ::: "memory"); }
+
+template <int DK, int DV, bool SHARED, int N>
+struct Attn8Cfg {
+    static constexpr int kW = DV >= 128 ? 128 : 64;           // columns of a box: its line in bytes
+    static constexpr int kMV = kW;                            // rows of one O^T instruction
+    static constexpr int kOT = DV / kMV;                      // O^T tiles
+    static constexpr int kVG = DV / kW;                       // value groups of a tile
+    static constexpr int kKG = SHARED ? 0 : 1;                // key groups of its own
+    static constexpr int kGroups = kVG + kKG;
+    static constexpr bool kRope = SHARED && DK > DV;          // 64 rotary columns
+    static constexpr int kGroupBytes = kAttn8Tile * kW;
+    static constexpr int kQRows = 2 * N;
+    static constexpr int kQBytes = kQRows * DK;
+    static constexpr int kPLine = 2 * N;                      // bytes of a token's weights: Wh, then Wl
+    static constexpr int kPBytes = kAttn8Tile * kPLine;
+    static constexpr int kCols = kOT * N + 4 * N;             // O^T, then two S^T
+    static constexpr uint32_t kTmemCols = kCols <= 128 ? 128 : kCols <= 256 ? 256 : 512;
+    static_assert(kCols <= 512, "tensor memory");
+    static constexpr int kThreads = attn8_threads(SHARED);
+    static constexpr int kC = N / 4;                          // heads of a softmax thread
+};
+
+// The window of a column's largest weight in a tile, log2, and where it is put.
+constexpr float kAttn8Up = 8.75f, kAttn8Low = 0.5f, kAttn8Aim = 4.5f, kAttn8Down = 30.f;
+
+template <int DK, int DV, bool SHARED, int N>
+__global__ void __launch_bounds__(attn8_threads(SHARED), attn8_ctas_per_sm(DK, SHARED, N))
+    hsp_attn8_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v, const __grid_constant__ Attn8Args g) {
+    using C = Attn8Cfg<DK, DV, SHARED, N>;
+    constexpr int T = kAttn8Tile, kC = C::kC;
+    const AttnArgs &a = g.line;
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw = smem_u32(smem_raw);
+    uint8_t *smem = smem_raw + ((1024u - (raw & 1023u)) & 1023u);
+    const uint32_t ring = smem_u32(smem);
+    uint8_t *const x_smem = smem + a.slots * C::kGroupBytes;            // the rotary boxes' two places
+    uint8_t *const q_smem = x_smem + (C::kRope ? 2 * kAttn8RopeBytes : 0);
+    uint8_t *const p_smem = q_smem + C::kQBytes;
+    float *const scales = reinterpret_cast<float *>(p_smem + C::kPBytes);  // [slots][3][T]: ks (times the scale), log2 vs, 1 / vs
+    float *const red = scales + kAttn8ScaleSlots * 3 * T;               // [4 warps][N]
+    float *const fac = red + 4 * N;                                     // [N]
+    float *const top = fac + N;                                         // [4 warps][N] highest reference point so far
+    float *const q_unit = top + 4 * N;                                  // [4][N] the unit of a part's queries, 2^e of the head
+    uint32_t *const seen = reinterpret_cast<uint32_t *>(q_unit + 4 * N);   // [2][2][4 warps], 16-byte aligned
+    uint64_t *const full = reinterpret_cast<uint64_t *>(seen + 16);
+    uint64_t *const empty = full + a.slots;
+    uint64_t *const x_full = empty + a.slots;                           // [2]
+    uint64_t *const x_empty = x_full + 2;                               // [2]
+    uint64_t *const s_full = x_empty + 2;                               // [2]
+    uint64_t *const s_free = s_full + 2;                                // [2]
+    uint64_t *const q_full = s_free + 2;
+    uint64_t *const q_free = q_full + 1;
+    uint64_t *const p_full = q_free + 1;
+    uint64_t *const pv_done = p_full + 1;
+    uint64_t *const drained = pv_done + 1;
+    uint64_t *const unit_full = drained + 1;                            // [4] q_unit
+    uint64_t *const sc_full = unit_full + 4;                            // [kAttn8ScaleSlots]
+    uint64_t *const sc_empty = sc_full + kAttn8ScaleSlots;
+    int *const ints = reinterpret_cast<int *>(sc_empty + kAttn8ScaleSlots);
+    uint32_t *const tmem_slot = reinterpret_cast<uint32_t *>(ints);
+    volatile int *const abort_flag = ints + 1;
+    int *const issued = ints + 2;                                       // groups and rotary boxes whose copies were issued
+    int *const place = ints + 4;
+    int *const warp_sum = ints + 7;                                     // [12]
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int ht = blockIdx.x, cta = blockIdx.y;
+
+    if (tid == 0) {
+        for (int s = 0; s < a.slots; ++s) {
+            mbar_init(smem_u32(&full[s]), 1);
+            mbar_init(smem_u32(&empty[s]), 1);
+        }
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(smem_u32(&x_full[s]), 1);
+            mbar_init(smem_u32(&x_empty[s]), 1);
+            mbar_init(smem_u32(&s_full[s]), 1);
+            mbar_init(smem_u32(&s_free[s]), 128);
+        }
+        for (int s = 0; s < 4; ++s) mbar_init(smem_u32(&unit_full[s]), 1);
+        for (int s = 0; s < kAttn8ScaleSlots; ++s) {
+            mbar_init(smem_u32(&sc_full[s]), 32);
+            mbar_init(smem_u32(&sc_empty[s]), 128);
+        }
+        mbar_init(smem_u32(q_full), 1);
+        mbar_init(smem_u32(q_free), 1);
+        mbar_init(smem_u32(p_full), 128);
+        mbar_init(smem_u32(pv_done), 1);
+        mbar_init(smem_u32(drained), 2);
+        *abort_flag = 0;
+        issued[0] = issued[1] = 0;
+        mbar_fence_init();
+        tma_prefetch_map(&tmap_k);
+        if (!SHARED || C::kRope) tma_prefetch_map(&tmap_v);
+    }
+    if (warp == 5) {
+        tmem_alloc(smem_u32(tmem_slot), C::kTmemCols);
+        tmem_relinquish();
+    }
+    tc_fence_before_sync();
+    __syncthreads();
+    tc_fence_after_sync();
+    griddep_wait();  // everything read below may come from the previous kernel
+
+    const AttnLine ln = attn_find_line<T, C::kThreads>(a, cta, place, warp_sum);
+    const uint32_t tmem = *tmem_slot;
+    const uint32_t tmem_s = tmem + C::kOT * N;
+    auto await = [&](uint64_t *bar, uint32_t phase) { return attn_wait(smem_u32(bar), phase & 1u, a.wait_limit_ns, abort_flag); };
+
+    // The queries of part `seg` in two pieces, by four warps (w: 0 .. 3).  A head to a group of lanes, eight columns to a
+    // lane and round; the head's largest number decides its unit.
+    auto split_queries = [&](const AttnSegment &sg, uint32_t seg, int w4) {
+        constexpr int kLanes = DK / 8 < 32 ? DK / 8 : 32, kPer = 32 / kLanes, kRounds = (DK / 8 + kLanes - 1) / kLanes;
+        const int sub = lane / kLanes, at = lane % kLanes;
+        const int nheads = min(N, a.group - ht * N);
+        const __nv_bfloat16 *q = static_cast<const __nv_bfloat16 *>(g.q) + sg.b * g.q_row + (sg.kv * a.group + ht * N) * g.q_head;
+        auto fetch = [&](int h, uint4 (&v)[kRounds]) {
+#pragma unroll
+            for (int r = 0; r < kRounds; ++r) {
+                const int c = (r * kLanes + at) * 8;
+                v[r] = make_uint4(0, 0, 0, 0);
+                if (h < nheads && c < DK) v[r] = *reinterpret_cast<const uint4 *>(q + h * g.q_head + c);
+            }
+        };
+        uint4 ahead[kRounds];
+        int h = w4 * kPer + sub;
+        fetch(h, ahead);
+        await(q_free, seg ^ 1u);  // the last part's are done with (given up: the warps still meet at their barrier)
+        for (; h - sub < N; h += 4 * kPer) {
+            uint4 v[kRounds];
+#pragma unroll
+            for (int r = 0; r < kRounds; ++r) v[r] = ahead[r];
+            fetch(h + 4 * kPer, ahead);
+            float amax = 0.f;
+#pragma unroll
+            for (int r = 0; r < kRounds; ++r) {
+                const uint32_t w[4] = {v[r].x, v[r].y, v[r].z, v[r].w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float lo = fabsf(__uint_as_float(w[e] << 16)), hi = fabsf(__uint_as_float(w[e] & 0xffff0000u));
+                    if (lo <= 3.0e38f) amax = fmaxf(amax, lo);  // (NaN and infinities make the head's scores NaN)
+                    if (hi <= 3.0e38f) amax = fmaxf(amax, hi);
+                }
+            }
+#pragma unroll
+            for (int d = kLanes / 2; d > 0; d >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, d));
+            // 2^-e amax in 224 .. 448: a normal amax, so e is above -135; the unit of a smaller one is 2^-126
+            const uint32_t u = __float_as_uint(amax);
+            const int e2 = max(-126, min(126, static_cast<int>(u >> 23) - 127 - 8 + ((u & 0x7fffffu) > 0x600000u ? 1 : 0)));
+            const float inv = two_to(-e2);
+            // row of the head among the instruction's columns: a softmax thread has columns 8 j + 2 c + e, c its
+            // place in four, of every step j: those are its heads c N / 4 + 2 j + e
+            const int c4 = h / kC, in4 = h % kC;
+            const int row = 8 * (in4 >> 1) + 2 * c4 + (in4 & 1);
+#pragma unroll
+            for (int r = 0; r < kRounds; ++r) {
+                const int c = (r * kLanes + at) * 8;
+                if (c >= DK) continue;
+                const uint32_t w[4] = {v[r].x, v[r].y, v[r].z, v[r].w};
+                uint32_t hi[4], lo[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float x0 = __uint_as_float(w[e] << 16) * inv, x1 = __uint_as_float(w[e] & 0xffff0000u) * inv;
+                    const float y0 = fabsf(x0) <= kQ8Top ? x0 : __uint_as_float(0x7fc00000u), y1 = fabsf(x1) <= kQ8Top ? x1 : __uint_as_float(0x7fc00000u);
+                    const __half2 x = __floats2half2_rn(y0, y1);
+                    hi[e] = half2_to_e4m3x2(x);
+                    lo[e] = half2_to_e4m3x2(__hmul2(__hsub2(x, e4m3x2_to_half2(hi[e])), __float2half2_rn(16.f)));
+                }
+                const uint2 h8 = make_uint2(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16), l8 = make_uint2(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16);
+                uint8_t *to;
+                int line;
+                if (C::kRope && c >= DV) {
+                    to = q_smem + C::kQRows * DV + row * 64 + swizzled<64>(row, (c - DV) >> 4) + (c & 8);
+                    line = 64;
+                } else {
+                    to = q_smem + c / C::kW * (C::kQRows * C::kW) + row * C::kW + swizzled<C::kW>(row, c % C::kW >> 4) + (c & 8);
+                    line = C::kW;
+                }
+                *reinterpret_cast<uint2 *>(to) = h8;
+                *reinterpret_cast<uint2 *>(to + N * line) = l8;  // (N rows on, a multiple of 8: the same swizzle)
+            }
+            if (at == 0) q_unit[(seg & 3u) * N + h] = two_to(e2);
+        }
+        fence_proxy_async_smem();
+        if (SHARED) query_sync();
+        else softmax_sync();
+        if (w4 == 0 && lane == 0) {
+            mbar_arrive(smem_u32(&unit_full[seg & 3u]));
+            mbar_arrive(smem_u32(q_full));
+        }
+    };
+
+    if (warp == 4) {
+        // ---------------- copy producer: one thread reads the table a tile ahead and issues ----------------
+        if (elect_one()) {
+            AttnWalk walk(ln);
+            int i = 0;
+            AttnSegment sg;
+            RingPos rp, xp;
+            int ng = 0;
+            const int pbox = min(T, 1 << a.page_shift);  // tokens per box
+            const int boxes = T / pbox;                  // pages that meet a tile (1 to 8)
+            bool alive = true;
+            while (alive && attn_next_segment<T>(a, ln, walk, sg)) {
+                const int row = a.rows ? a.rows[sg.b] : sg.b;
+                const int32_t *tbl = a.table + row * a.table_stride;
+                const int pages = static_cast<int>((static_cast<int64_t>(sg.len) + (1 << a.page_shift) - 1) >> a.page_shift);
+                auto ids_of = [&](int tile, int (&id)[8]) {
+                    const int p0 = static_cast<int>((static_cast<int64_t>(tile) * T) >> a.page_shift);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) id[e] = (e < boxes && p0 + e < pages) ? tbl[p0 + e] : 0;
+                };
+                int next[8];
+                ids_of(sg.t0, next);
+                for (int k = 0; k < sg.n && alive; ++k, ++i) {
+                    int id[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        id[e] = next[e];
+                        if (id[e] < 0 || id[e] >= a.num_pages) {
+                            atomicCAS(a.err_word, 0, kDeviceErrIndex);
+                            id[e] = 0;  // stays inside the pool; the call is reported
+                        }
+                    }
+                    if (k + 1 < sg.n) ids_of(sg.t0 + k + 1, next);
+                    const int64_t tok = static_cast<int64_t>(sg.t0 + k) * T;
+                    const int np = min(boxes, pages - static_cast<int>(tok >> a.page_shift));
+                    const int off = static_cast<int>(tok & ((1 << a.page_shift) - 1));
+                    auto load = [&](const CUtensorMap *map, int box, int line, uint32_t dst, uint32_t fb) {
+                        const uint32_t bytes = static_cast<uint32_t>(pbox) * line;
+                        mbar_arrive_expect_tx(fb, static_cast<uint32_t>(np) * bytes);
+#pragma unroll
+                        for (int e = 0; e < 8; ++e)
+                            if (e < np) tma_load_5d(dst + e * bytes, map, 0, boxes == 1 ? off : 0, box, sg.kv, id[e], fb);
+                    };
+                    const bool skip = i == a.skip_tile;
+#pragma unroll 1
+                    for (int gr = 0; gr < C::kGroups; ++gr) {
+                        // (a fresh barrier's phase before the first counts as complete)
+                        alive = await(&empty[rp.slot], rp.phase ^ 1u);
+                        if (!alive) break;
+                        ++ng;
+                        if (!skip) {
+                            load(SHARED || gr < C::kKG ? &tmap_k : &tmap_v, SHARED ? gr : 0, C::kW, ring + rp.slot * C::kGroupBytes, smem_u32(&full[rp.slot]));
+                            issued[0] = ng;
+                        }
+                        rp.next(a.slots);
+                    }
+                    if (C::kRope && alive) {
+                        alive = await(&x_empty[xp.slot], xp.phase ^ 1u);
+                        if (!alive) break;
+                        if (!skip) {
+                            load(&tmap_v, 0, 64, smem_u32(x_smem) + xp.slot * kAttn8RopeBytes, smem_u32(&x_full[xp.slot]));
+                            issued[1] = i + 1;
+                        }
+                        xp.next(2);
+                    }
+                }
+            }
+        }
+        __syncwarp();
+    } else if (warp == 5) {
+        // ---------------- issuer of the scores ----------------
+        if (elect_one()) {
+            constexpr uint32_t kDesc = (1u << 4) | (static_cast<uint32_t>(C::kQRows >> 3) << 17) | (static_cast<uint32_t>(T >> 4) << 24);
+            AttnWalk walk(ln);
+            uint32_t seg = 0;
+            AttnSegment sg;
+            bool alive = true;
+            const uint64_t qd = umma_desc_lines<C::kW>(smem_u32(q_smem));
+            RingPos rp, xp, sp;
+            while (alive && attn_next_segment<T>(a, ln, walk, sg)) {
+                if (!await(q_full, seg)) break;
+                ++seg;
+                for (int k = 0; k < sg.n; ++k) {
+                    // the scores of the tile before last have been read out of this accumulator
+                    if (!(alive = await(&s_free[sp.slot], sp.phase ^ 1u))) break;
+                    const uint32_t d = tmem_s + sp.slot * C::kQRows;
+                    constexpr int kGroupsK = SHARED ? C::kVG : C::kKG;
+#pragma unroll
+                    for (int gr = 0; gr < kGroupsK; ++gr) {
+                        if (alive) alive = await(&full[rp.slot], rp.phase);
+                        if (!alive) break;
+                        tc_fence_after_sync();
+                        const uint64_t kd = umma_desc_lines<C::kW>(ring + rp.slot * C::kGroupBytes);
+#pragma unroll
+                        for (int e = 0; e < C::kW / 32; ++e)  // (descriptors count 16 bytes)
+                            umma_f8(d, kd + e * 2, qd + gr * (C::kQRows * C::kW / 16) + e * 2, kDesc, (gr | e) != 0 ? 1u : 0u);
+                        if (!SHARED) umma_commit(smem_u32(&empty[rp.slot]));
+                        rp.next(a.slots);
+                    }
+                    if (!alive) break;
+                    if (!SHARED) rp.next(a.slots);  // the value group
+                    if (C::kRope) {
+                        if (!(alive = await(&x_full[xp.slot], xp.phase))) break;
+                        tc_fence_after_sync();
+                        const uint64_t kd = umma_desc_lines<64>(smem_u32(x_smem) + xp.slot * kAttn8RopeBytes);
+                        const uint64_t xd = umma_desc_lines<64>(smem_u32(q_smem) + C::kQRows * DV);
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) umma_f8(d, kd + e * 2, xd + e * 2, kDesc, 1u);
+                        umma_commit(smem_u32(&x_empty[xp.slot]));
+                        xp.next(2);
+                    }
+                    umma_commit(smem_u32(&s_full[sp.slot]));
+                    sp.next(2);
+                }
+                umma_commit(smem_u32(q_free));
+            }
+            umma_commit(smem_u32(drained));
+        }
+        __syncwarp();
+    } else if (warp == 6) {
+        // ---------------- issuer of the products with the values ----------------
+        if (elect_one()) {
+            constexpr uint32_t kDescH = (1u << 4) | (1u << 15) | (1u << 16) | (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(C::kMV >> 4) << 24);
+            constexpr uint32_t kDescL = kDescH | (1u << 10);  // e5m2 weights
+            AttnWalk walk(ln);
+            int i = 0;
+            AttnSegment sg;
+            bool alive = true;
+            const uint64_t pd = umma_desc_lines<C::kPLine>(smem_u32(p_smem));
+            RingPos rp;
+            while (alive && attn_next_segment<T>(a, ln, walk, sg)) {
+                for (int k = 0; k < sg.n; ++k, ++i) {
+                    const int valid = min(T, sg.len - (sg.t0 + k) * T);  // tokens of this tile
+                    alive = await(p_full, static_cast<uint32_t>(i));
+                    if (!alive) break;
+                    tc_fence_after_sync();
+                    if (!SHARED) {
+                        rp.next(a.slots);  // the key group
+                        alive = await(&full[rp.slot], rp.phase);
+                        if (!alive) break;
+                        tc_fence_after_sync();
+                    }
+#pragma unroll
+                    for (int jt = 0; jt < C::kOT; ++jt) {
+                        const uint64_t vd = umma_desc_lines<C::kW>(ring + rp.slot * C::kGroupBytes);
+#pragma unroll
+                        for (int e = 0; e < T / 32; ++e)
+                            if (e * 32 < valid) {
+                                umma_f8(tmem + jt * N, vd + e * (2 * C::kW), pd + e * (2 * C::kPLine), kDescH, (k | e) != 0 ? 1u : 0u);
+                                umma_f8(tmem + jt * N, vd + e * (2 * C::kW), pd + e * (2 * C::kPLine) + N / 16, kDescL, 1u);
+                            }
+                        umma_commit(smem_u32(&empty[rp.slot]));
+                        rp.next(a.slots);
+                    }
+                    umma_commit(smem_u32(pv_done));
+                }
+            }
+            // always committed and awaited (both issuers'), so that no product is in flight when the memory goes
+            umma_commit(smem_u32(drained));
+            const uint64_t t0 = global_timer_ns();
+            while (!mbar_try_wait(smem_u32(drained), 0u) && global_timer_ns() - t0 < a.wait_limit_ns) {
+            }
+        }
+        __syncwarp();
+    } else if (warp == 7) {
+        // ---------------- the tiles' scales, up to kAttn8ScaleSlots tiles ahead ----------------
+        AttnWalk walk(ln);
+        int i = 0;
+        AttnSegment sg;
+        bool alive = true;
+        while (alive && attn_next_segment<T>(a, ln, walk, sg)) {
+            const int row = a.rows ? a.rows[sg.b] : sg.b;
+            const int32_t *tbl = a.table + row * a.table_stride;
+            const float *ks = g.k_scales + sg.kv * g.ks_head, *vs = g.v_scales + sg.kv * g.vs_head;
+            for (int k = 0; k < sg.n; ++k, ++i) {
+                float kk[4], vv[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int t = (sg.t0 + k) * T + e * 32 + lane;
+                    kk[e] = 0.f;
+                    vv[e] = 1.f;
+                    if (t < sg.len) {
+                        int page = tbl[t >> a.page_shift];
+                        if (page < 0 || page >= a.num_pages) page = 0;  // (reported by the copy producer)
+                        const int blk = (t & ((1 << a.page_shift) - 1)) >> g.block_shift;
+                        kk[e] = ks[page * g.ks_page + blk * g.ks_block];
+                        vv[e] = SHARED ? kk[e] : vs[page * g.vs_page + blk * g.vs_block];
+                    }
+                }
+                const int slot = i % kAttn8ScaleSlots;
+                alive = await(&sc_empty[slot], static_cast<uint32_t>(i / kAttn8ScaleSlots) ^ 1u);
+                alive = __all_sync(0xffffffffu, alive);
+                if (!alive) break;
+                float *to = scales + slot * 3 * T;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float v = fminf(fmaxf(vv[e], two_to(kQ8MinExp)), two_to(kQ8MaxExp));
+                    to[e * 32 + lane] = kk[e] * a.scale_log2;
+                    to[T + e * 32 + lane] = log2f(v);
+                    to[2 * T + e * 32 + lane] = 1.f / v;
+                }
+                mbar_arrive(smem_u32(&sc_full[slot]));
+            }
+        }
+    } else if (SHARED && warp >= 8) {
+        // ---------------- the queries of the next part, while the last one is under way ----------------
+        AttnWalk walk(ln);
+        AttnSegment sg;
+        for (uint32_t seg = 0; attn_next_segment<T>(a, ln, walk, sg); ++seg) split_queries(sg, seg, warp - 8);
+    } else {
+        // ---------------- softmax warps ----------------
+        AttnWalk walk(ln);
+        int i = 0;
+        AttnSegment sg;
+        uint32_t seg = 0;
+        const int head0 = ht * N;                              // of the group
+        const int nheads = min(N, a.group - head0);            // real heads of this tile
+        const int all_heads = a.kv_heads * a.group;
+        __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(a.out);
+        const int r0 = warp * 32 + (lane >> 2);                // this thread's token rows: r0 + 0, 8, 16, 24
+        const int c4 = lane & 3;                               // its heads: c4 * kC + 0 .. kC - 1
+        const uint32_t lane_base = static_cast<uint32_t>(warp * 32) << 16;
+        if (a.split && ht == 0 && tid == 96) {
+            AttnEntry e;
+            e.batch = -1;
+            e.kv_head = e.last = e.slot = 0;
+            a.entries[cta] = e;
+        }
+        // heads behind the last one: columns that nothing reads, which move nothing
+        uint32_t unused = 0;
+#pragma unroll
+        for (int c = 0; c < kC; ++c)
+            if (c4 * kC + c >= nheads) unused |= 1u << c;
+        bool more = attn_next_segment<T>(a, ln, walk, sg);
+        if (!SHARED && more) split_queries(sg, 0, warp);
+        while (more) {
+            const bool begins = sg.t0 == 0, ends = sg.t0 + sg.n == sg.tiles;
+            float m[kC];             // reference points
+            float2 l[kC / 2], u[kC / 2];  // sums of the rounded and the unrounded weights
+            uint32_t lowest = unused;  // columns whose reference point goes no further down
+#pragma unroll
+            for (int e = 0; e < kC; ++e) m[e] = 0.f;
+#pragma unroll
+            for (int j = 0; j < kC / 2; ++j) l[j] = u[j] = make_float2(0.f, 0.f);
+            await(&unit_full[seg & 3u], seg >> 2);
+            const float *unit = q_unit + (seg & 3u) * N + c4 * kC;
+            ++seg;
+            for (int k = 0; k < sg.n; ++k, ++i) {
+                const int64_t tok0 = static_cast<int64_t>(sg.t0 + k) * T;
+                const int valid = static_cast<int>(min(static_cast<int64_t>(T), sg.len - tok0));
+                const int slot = i % kAttn8ScaleSlots;
+                float ksc[4], vlog[4], vinv[4];
+                await(&sc_full[slot], static_cast<uint32_t>(i / kAttn8ScaleSlots));
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    ksc[r] = scales[slot * 3 * T + r0 + 8 * r];
+                    vlog[r] = scales[slot * 3 * T + T + r0 + 8 * r];
+                    vinv[r] = scales[slot * 3 * T + 2 * T + r0 + 8 * r];
+                }
+                mbar_arrive(smem_u32(&sc_empty[slot]));
+                await(&s_full[i & 1], static_cast<uint32_t>(i >> 1));
+                tc_fence_after_sync();
+                // s[r][c]: row r0 + 8 r, head c4 kC + c, in log2 units with the values' scale
+                float s[4][kC];
+#pragma unroll
+                for (int hf = 0; hf < 2; ++hf) {
+                    float hi[N / 2], lo[N / 2];
+                    const uint32_t from = tmem_s + (i & 1) * C::kQRows + lane_base + (static_cast<uint32_t>(hf * 16) << 16);
+                    tmem_ld_frag<N / 8>(from, hi);
+                    tmem_ld_frag<N / 8>(from + N, lo);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int j = 0; j < N / 8; ++j)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const int r = 2 * hf + (e >> 1), c = 2 * j + (e & 1);
+                            s[r][c] = fmaf(lo[4 * j + e], 0.0625f, hi[4 * j + e]);
+                        }
+                }
+                tc_fence_before_sync();
+                mbar_arrive(smem_u32(&s_free[i & 1]));
+#pragma unroll
+                for (int c = 0; c < kC; ++c) {
+                    const float q1 = unit[c];
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) s[r][c] = fmaf(s[r][c] * q1, ksc[r], vlog[r]);
+                }
+                if (valid < T) {
+#pragma unroll
+                    for (int r = 0; r < 4; ++r)
+                        if (r0 + 8 * r >= valid) {
+#pragma unroll
+                            for (int c = 0; c < kC; ++c) s[r][c] = -INFINITY;
+                        }
+                }
+                // columns that exceed the window, and those that some token reaches from below
+                bool over = k == 0;
+                uint32_t reached = lowest;
+#pragma unroll
+                for (int c = 0; c < kC; ++c) {
+                    const float most = fmaxf(fmaxf(s[0][c], s[1][c]), fmaxf(s[2][c], s[3][c])) - m[c];
+                    over |= most > kAttn8Up && !((unused >> c) & 1u);
+                    if (most >= kAttn8Low) reached |= 1u << c;
+                }
+                {
+                    // kC bits for each of the four places: one word, or two for 64 heads
+                    constexpr int kWords = kC * 4 > 32 ? 2 : 1, kPlaces = 4 / kWords;
+#pragma unroll
+                    for (int w = 0; w < kWords; ++w) {
+                        const uint32_t mine = c4 / kPlaces == w ? reached << (c4 % kPlaces * kC) : 0u;
+                        const uint32_t all = __reduce_or_sync(0xffffffffu, mine);
+                        if (lane == 0) seen[((i & 1) * 2 + w) * 4 + warp] = all;
+                    }
+                }
+                bool move = softmax_any(over);
+                {
+                    constexpr int kWords = kC * 4 > 32 ? 2 : 1;
+                    constexpr uint32_t kAll = kC * 4 >= 32 ? 0xffffffffu : (1u << (kC * 4 & 31)) - 1u;
+#pragma unroll
+                    for (int w = 0; w < kWords; ++w) {
+                        const uint4 x = *reinterpret_cast<const uint4 *>(seen + ((i & 1) * 2 + w) * 4);
+                        move |= (x.x | x.y | x.z | x.w) != kAll;
+                    }
+                }
+                if (move) {
+                    // column maxima over the tile's tokens, new reference points, O^T rescaled
+                    float mx[kC];
+#pragma unroll
+                    for (int c = 0; c < kC; ++c) {
+                        float t = fmaxf(fmaxf(s[0][c], s[1][c]), fmaxf(s[2][c], s[3][c]));
+                        t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 4));
+                        t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 8));
+                        t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 16));
+                        mx[c] = t;
+                    }
+                    if (lane < 4) {
+#pragma unroll
+                        for (int c = 0; c < kC; c += 4)
+                            *reinterpret_cast<float4 *>(red + warp * N + c4 * kC + c) = make_float4(mx[c], mx[c + 1], mx[c + 2], mx[c + 3]);
+                    }
+                    softmax_sync();
+                    lowest = unused;
+#pragma unroll
+                    for (int c = 0; c < kC; ++c) {
+                        const int at = c4 * kC + c;
+                        const float t = fmaxf(fmaxf(red[at], red[N + at]), fmaxf(red[2 * N + at], red[3 * N + at]));
+                        const float most = t - m[c];
+                        float peak = k == 0 ? -INFINITY : top[warp * N + at];
+                        float n = m[c];
+                        if (k == 0 || most > kAttn8Up || most < kAttn8Low) n = t - kAttn8Aim;
+                        if (k == 0 && !(n > -INFINITY)) n = 0.f;  // (nothing but NaN or minus infinity in the first tile)
+                        if (n <= peak - kAttn8Down) n = peak - kAttn8Down;
+                        if (n == peak - kAttn8Down) lowest |= 1u << c;
+                        peak = fmaxf(peak, n);
+                        const float f = k == 0 ? 0.f : fast_exp2(m[c] - n);
+                        m[c] = n;
+                        float2 &lc = l[c >> 1], &uc = u[c >> 1];
+                        if ((c & 1) == 0) {
+                            lc.x *= f;
+                            uc.x *= f;
+                        } else {
+                            lc.y *= f;
+                            uc.y *= f;
+                        }
+                        __syncwarp();  // every lane has read its columns' peaks
+                        if (lane < 4) {
+                            top[warp * N + at] = peak;
+                            if (warp == 0) fac[at] = f;
+                        }
+                    }
+                    __syncwarp();
+                    if (k > 0) {
+                        await(pv_done, static_cast<uint32_t>(i - 1));
+                        tc_fence_after_sync();
+                        softmax_sync();
+#pragma unroll 1
+                        for (int c0 = 0; c0 < C::kOT * N; c0 += 16) {
+                            float o[16];
+                            tmem_ld16(tmem + c0 + lane_base, o);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) o[e] *= fac[(c0 & (N - 1)) + e];
+                            tmem_st16(tmem + c0 + lane_base, o);
+                        }
+                        tmem_wait_st();
+                    }
+                }
+                if (valid < T) {
+                    // the last tile: what lies behind the sequence must not reach the product (0 x NaN).  Its last
+                    // step of 32 tokens is filled up with zeros; the steps behind that are not taken.
+                    const int first = i * C::kGroups + C::kKG;  // its first value group in the ring
+                    if (!SHARED)                                // (a latent tile's scores have waited for it)
+                        await(&full[first % a.slots], static_cast<uint32_t>(first / a.slots));
+                    constexpr int kPieces = C::kW / 16;
+                    int at = first % a.slots;
+#pragma unroll
+                    for (int gr = 0; gr < C::kVG; ++gr) {
+                        for (int e = tid; e < (-valid & 31) * kPieces; e += 128)
+                            *reinterpret_cast<uint4 *>(smem + at * C::kGroupBytes + valid * C::kW + e * 16) = make_uint4(0, 0, 0, 0);
+                        at = at + 1 == a.slots ? 0 : at + 1;
+                    }
+                }
+                // the weights in two pieces, and their sums
+                uint32_t wh[4][kC / 4], wl[4][kC / 4];
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+#pragma unroll
+                    for (int c = 0; c < kC; c += 2) {
+                        const float p0 = fast_exp2(s[r][c] - m[c]), p1 = fast_exp2(s[r][c + 1] - m[c + 1]);
+                        const __half2 p = __floats2half2_rn(p0, p1);
+                        const uint32_t h8 = half2_to_e4m3x2(p);
+                        const __half2 h16 = e4m3x2_to_half2(h8);
+                        const uint32_t l8 = half2_to_e5m2x2(__hsub2(p, h16));
+                        const float2 w = __half22float2(__hadd2(h16, e5m2x2_to_half2(l8)));
+                        if ((c & 2) == 0) {
+                            wh[r][c >> 2] = h8;
+                            wl[r][c >> 2] = l8;
+                        } else {
+                            wh[r][c >> 2] |= h8 << 16;
+                            wl[r][c >> 2] |= l8 << 16;
+                        }
+                        u[c >> 1].x = fmaf(p0, vinv[r], u[c >> 1].x);
+                        u[c >> 1].y = fmaf(p1, vinv[r], u[c >> 1].y);
+                        l[c >> 1].x = fmaf(w.x, vinv[r], l[c >> 1].x);
+                        l[c >> 1].y = fmaf(w.y, vinv[r], l[c >> 1].y);
+                    }
+                // the weights of tile i - 1 have been read before these replace them
+                if (i > 0) await(pv_done, static_cast<uint32_t>(i - 1));
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const int row = r0 + 8 * r;
+                    uint8_t *line = p_smem + row * C::kPLine;
+                    if (N == 64) {
+                        *reinterpret_cast<uint4 *>(line + swizzled<C::kPLine>(row, c4)) = make_uint4(wh[r][0], wh[r][1 % (kC / 4)], wh[r][2 % (kC / 4)], wh[r][3 % (kC / 4)]);
+                        *reinterpret_cast<uint4 *>(line + swizzled<C::kPLine>(row, 4 + c4)) = make_uint4(wl[r][0], wl[r][1 % (kC / 4)], wl[r][2 % (kC / 4)], wl[r][3 % (kC / 4)]);
+                    } else if (N == 32) {
+                        *reinterpret_cast<uint2 *>(line + swizzled<C::kPLine>(row, c4 >> 1) + (c4 & 1) * 8) = make_uint2(wh[r][0], wh[r][1 % (kC / 4)]);
+                        *reinterpret_cast<uint2 *>(line + swizzled<C::kPLine>(row, 2 + (c4 >> 1)) + (c4 & 1) * 8) = make_uint2(wl[r][0], wl[r][1 % (kC / 4)]);
+                    } else {
+                        *reinterpret_cast<uint32_t *>(line + swizzled<C::kPLine>(row, 0) + c4 * 4) = wh[r][0];
+                        *reinterpret_cast<uint32_t *>(line + swizzled<C::kPLine>(row, 1) + c4 * 4) = wl[r][0];
+                    }
+                }
+                fence_proxy_async_smem();
+                tc_fence_before_sync();
+                mbar_arrive(smem_u32(p_full));
+            }
+            // (the next part's scores are under way while this one leaves)
+            AttnSegment after;
+            more = attn_next_segment<T>(a, ln, walk, after);
+            if (!SHARED && more) split_queries(after, seg, warp);
+            // ---- the part is done: l (and u) over the tokens, then O^T out of tensor memory ----
+            auto over_tokens = [&](float2 (&v)[kC / 2]) {  // a warp's sums to `red`
+#pragma unroll
+                for (int j = 0; j < kC / 2; ++j)
+#pragma unroll
+                    for (int d = 4; d < 32; d <<= 1) {
+                        v[j].x += __shfl_xor_sync(0xffffffffu, v[j].x, d);
+                        v[j].y += __shfl_xor_sync(0xffffffffu, v[j].y, d);
+                    }
+                softmax_sync();  // the last tile's maxima and factors (l), the sums l (u) have been read
+                if (lane < 4) {
+#pragma unroll
+                    for (int j = 0; j < kC / 2; ++j) *reinterpret_cast<float2 *>(red + warp * N + c4 * kC + 2 * j) = v[j];
+                }
+            };
+            over_tokens(l);
+            if (warp == 0 && lane < 4) {
+#pragma unroll
+                for (int j = 0; j < kC / 2; ++j) *reinterpret_cast<float2 *>(fac + c4 * kC + 2 * j) = make_float2(m[2 * j], m[2 * j + 1]);
+            }
+            softmax_sync();
+            const bool whole = begins && ends;
+            const int slot = sg.x0 == ln.x0 ? 0 : 1;
+            float *part = a.parts + (static_cast<int64_t>(ht) * a.ctas + cta) * 2 * attn_part(DV, N) + slot * attn_part(DV, N);
+            float ref = 0.f;
+            if (tid < N) {  // a column per thread
+                const float t = red[tid] + red[N + tid] + red[2 * N + tid] + red[3 * N + tid];
+                ref = fac[tid];
+                if (whole) {
+                    fac[tid] = t == 0.f ? 0.f : 1.f / t;
+                } else {
+                    part[N * DV + tid] = ref;
+                    part[N * DV + N + tid] = t;
+                }
+            }
+            if (a.lse) {
+                over_tokens(u);
+                softmax_sync();
+                if (tid < N) {
+                    const float t = red[tid] + red[N + tid] + red[2 * N + tid] + red[3 * N + tid];
+                    if (!whole)
+                        part[N * DV + 2 * N + tid] = t;
+                    else if (tid < nheads && *abort_flag == 0)
+                        a.lse[static_cast<int64_t>(sg.b) * all_heads + sg.kv * a.group + head0 + tid] =
+                            t == 0.f ? -INFINITY : (ref + log2f(t)) * 0.6931471805599453f;
+                }
+            }
+            if (ht == 0 && tid == 96 && begins && !ends) {
+                AttnEntry e;
+                e.batch = sg.b;
+                e.kv_head = sg.kv;
+                e.last = line_owner(ln.total, sg.end - 1, ln.ctas);
+                e.slot = slot;
+                a.entries[cta] = e;
+            }
+            await(pv_done, static_cast<uint32_t>(i - 1));
+            tc_fence_after_sync();
+            softmax_sync();
+            const bool good = *abort_flag == 0;
+            const int64_t obase = (static_cast<int64_t>(sg.b) * all_heads + sg.kv * a.group + head0) * DV;
+            attn_store_part<N, DV, C::kMV, C::kOT>(tmem, warp, lane, good, whole, nheads, fac, out + obase, part);
+            tc_fence_before_sync();
+            softmax_sync();  // red and fac are free again
+            sg = after;
+        }
+        attn_store_empty<DV>(a, cta, head0, nheads);
+    }
+    tc_fence_before_sync();
+    if (a.split) {  // the join waits for the end of this grid: no fence
+        __syncthreads();
+        griddep_launch_dependents();
+    } else {
+        cta_release_and_trigger();
+    }
+    if (*abort_flag != 0 && tid == 0) {
+        atomicCAS(a.err_word, 0, kDeviceErrTimeout);
+        // copies still in flight land before the shared memory goes
+        const int n = issued[0], nx = issued[1];
+        auto land = [&](uint64_t *bar, int phase) {
+            const uint64_t t0 = global_timer_ns();
+            while (!mbar_try_wait(smem_u32(bar), static_cast<uint32_t>(phase) & 1u) && global_timer_ns() - t0 < a.wait_limit_ns / 16 + 1) {
+            }
+        };
+        for (int j = max(0, n - a.slots); j < n; ++j)
+            if (j / C::kGroups != a.skip_tile) land(&full[j % a.slots], j / a.slots);
+        for (int j = max(0, nx - 2); j < nx; ++j)
+            if (j != a.skip_tile) land(&x_full[j & 1], j >> 1);
+    }
+    if (warp == 5) {
+        tc_fence_after_sync();
+        tmem_dealloc(tmem, C::kTmemCols);
+    }
+    __syncthreads();
+}
+
+}  // namespace hsp

@@ -43,9 +43,6 @@ proj_status check_index(const proj_page_index *ix, bool counts) {
     return PROJ_OK;
 }
 
-// Tables of at most so many tiles per row: no sequence is cut, no workspace is used.
-constexpr int kAttnWholeTiles = PROJ_UNCUT_TOKENS / hsp::kAttnTile;
-
 // Heads and columns the attention kernel serves.
 struct AttnShape {
     int KB, VB, shared, N, head_tiles, slots, per_sm, smem, weight;
@@ -79,6 +76,22 @@ proj_status attn_shape(int heads, int kv_heads, int k_dim, int v_dim, bool laten
     // 49.3 (1), 47.0 (2), 48.0 (5); 64 x 4 with 64 each 40.3 (2), 37.4 (3), 39.6 (8); latent heads: 100 x 16
     // 23.7 (0), 22.9 (1), 24.5 (4); 64 x 128 72.2 (2), 70.4 (3), 75.0 (8).
     s->weight = 1 + s->N / 32;
+    return PROJ_OK;
+}
+
+// The same of a cache in 8 bits: the same heads and columns, other tiles and places.
+proj_status attn8_shape(int heads, int kv_heads, int k_dim, int v_dim, bool latent, AttnShape *s) {
+    const proj_status st = attn_shape(heads, kv_heads, k_dim, v_dim, latent, s);
+    if (st != PROJ_OK) return st;
+    const int group_bytes = hsp::kAttn8Tile * (v_dim >= 128 ? 128 : 64);
+    const int fixed = hsp::attn8_fixed_smem(k_dim, latent && k_dim > v_dim, s->N);
+    s->per_sm = hsp::attn8_ctas_per_sm(k_dim, latent, s->N);
+    const int room = s->per_sm == 1 ? kSmemLimit : kSmemPerSm / s->per_sm - kSmemReserved;
+    s->slots = (room - fixed) / group_bytes;
+    if (s->slots > hsp::kAttnMaxSlots) s->slots = hsp::kAttnMaxSlots;
+    if (!latent) s->slots &= ~1;  // (as above)
+    s->smem = fixed + s->slots * group_bytes;
+    s->weight = 1;
     return PROJ_OK;
 }
 
@@ -177,6 +190,19 @@ proj_status encode_pages(const void *p, const proj_page_index *ix, int heads, in
                                  ix->num_pages > 1 ? static_cast<uint64_t>(page) * 2 : 128};
     const uint32_t box[5] = {64, static_cast<uint32_t>(tok), static_cast<uint32_t>(tok == tile ? box_count : 1), 1, 1};
     return hsp::api_encode_5d(p, dims, strides, box, out);
+}
+
+// [pages][heads][boxes of `width` columns][tokens][width]: the codes of `dim` columns, token lines of `width` bytes.
+proj_status encode_codes(const void *p, const proj_page_index *ix, int heads, int dim, int width, int64_t page, int64_t token, int64_t head,
+                         CUtensorMap *out) {
+    const int tok = ix->page_size < hsp::kAttn8Tile ? ix->page_size : hsp::kAttn8Tile;
+    const uint64_t w = static_cast<uint64_t>(width);
+    const uint64_t dims[5] = {w, static_cast<uint64_t>(ix->page_size), static_cast<uint64_t>(dim / width), static_cast<uint64_t>(heads),
+                              static_cast<uint64_t>(ix->num_pages)};
+    const uint64_t strides[4] = {static_cast<uint64_t>(token), w, heads > 1 ? static_cast<uint64_t>(head) : w,
+                                 ix->num_pages > 1 ? static_cast<uint64_t>(page) : w};
+    const uint32_t box[5] = {static_cast<uint32_t>(width), static_cast<uint32_t>(tok), 1, 1, 1};
+    return hsp::api_encode_codes_5d(p, dims, strides, box, out);
 }
 
 proj_status check_pools(const proj_page_pool *pools, int num_pools, hsp::PoolList *out) {
@@ -311,6 +337,64 @@ CacheWorkspace cache_workspace(const proj_page_index *ix, int n) {
     return w;
 }
 
+// What both attention calls ask of their batch, scale and queries.
+proj_status check_attention(const proj_page_index *index, const AttnShape &s, int batch, int kv_heads, int tile, float scale, float *scale_log2) {
+    if (batch < 0) return api_fail(PROJ_ERR_INVALID_ARG, "batch=%d is negative", batch);
+    *scale_log2 = scale * 1.4426950408889634f;  // log2(e)
+    if (!std::isfinite(*scale_log2)) return api_fail(PROJ_ERR_INVALID_ARG, "scale (times log2 e) must be finite");
+    // (units of the line fit 30 bits)
+    const int64_t most_tiles = (static_cast<int64_t>(index->max_pages) * index->page_size + tile - 1) / tile;
+    if (static_cast<int64_t>(batch) * kv_heads * (most_tiles + s.weight) >= (int64_t(1) << 30))
+        return api_fail(PROJ_ERR_UNSUPPORTED_SHAPE, "batch=%d of up to %d pages is too large", batch, index->max_pages);
+    return PROJ_OK;
+}
+proj_status check_queries(const void *q, int64_t q_row_stride, int64_t q_head_stride, const proj_page_index *index, const int32_t *rows,
+                          int batch, int heads, const void *out, const float *lse) {
+    if (!rows && batch > index->num_rows)
+        return api_fail(PROJ_ERR_INVALID_ARG, "batch=%d exceeds the table's %d rows", batch, index->num_rows);
+    if (!q || !out) return api_fail(PROJ_ERR_INVALID_ARG, "q and out must not be NULL");
+    if (!aligned(q, 16) || !aligned(out, 16) || q_row_stride % 8 || q_head_stride % 8)
+        return api_fail(PROJ_ERR_MISALIGNED, "q and out must be 16-byte aligned, q's strides multiples of 8 elements");
+    if ((heads > 1 && (q_head_stride < 8 || q_head_stride >= (int64_t(1) << 38))) ||
+        (batch > 1 && (q_row_stride < 8 || q_row_stride >= (int64_t(1) << 38))))
+        return api_fail(PROJ_ERR_UNSUPPORTED_SHAPE, "queries must lie apart (strides %lld, %lld)", (long long)q_row_stride,
+                        (long long)q_head_stride);
+    if (!aligned(lse, 4) || !aligned(rows, 4)) return api_fail(PROJ_ERR_MISALIGNED, "lse and rows must be 4-byte aligned");
+    return PROJ_OK;
+}
+
+// The launch arguments that both attention kernels walk their line of tiles by.
+void attention_line(const proj_page_index *index, const int32_t *rows, int batch, int heads, int kv_heads, const AttnShape &s, int ctas,
+                    bool split, float scale_log2, void *out, float *lse, void *workspace, const hsp::ApiOptions &opt,
+                    const hsp::ApiDevice &dev, hsp::AttnArgs *args) {
+    hsp::AttnArgs &a = *args;
+    a.table = index->block_table;
+    a.table_stride = index->table_stride;
+    a.lens = index->seq_lens;
+    a.rows = rows;
+    a.num_rows = index->num_rows;
+    a.max_pages = index->max_pages;
+    a.num_pages = index->num_pages;
+    a.page_shift = log2_of(index->page_size);
+    a.batch = batch;
+    a.kv_heads = kv_heads;
+    a.group = heads / kv_heads;
+    a.ctas = ctas;
+    a.split = split ? 1 : 0;
+    a.weight = s.weight;
+    a.slots = s.slots;
+    a.scale_log2 = scale_log2;
+    a.out = out;
+    a.lse = lse;
+    if (split) {
+        a.entries = static_cast<hsp::AttnEntry *>(workspace);
+        a.parts = reinterpret_cast<float *>(static_cast<char *>(workspace) + up256(static_cast<size_t>(ctas) * sizeof(hsp::AttnEntry)));
+    }
+    a.skip_tile = opt.skip_stage;
+    a.wait_limit_ns = opt.wait_limit_ns;
+    a.err_word = dev.err_word;
+}
+
 proj_status check_workspace(const void *ws, size_t have, size_t need) {
     if (!ws) return api_fail(PROJ_ERR_INVALID_ARG, "workspace must not be NULL");
     if (!aligned(ws, 16)) return api_fail(PROJ_ERR_MISALIGNED, "workspace must be 16-byte aligned");
@@ -337,29 +421,15 @@ proj_status proj_paged_attention(const void *q, int64_t q_row_stride, int64_t q_
     if ((st = check_kv(kv)) != PROJ_OK) return st;
     AttnShape s;
     if ((st = attn_shape(heads, kv->kv_heads, kv->k_dim, kv->v_dim, kv->v == nullptr, &s)) != PROJ_OK) return st;
-    if (batch < 0) return api_fail(PROJ_ERR_INVALID_ARG, "batch=%d is negative", batch);
-    const float scale_log2 = scale * 1.4426950408889634f;  // log2(e)
-    if (!std::isfinite(scale_log2)) return api_fail(PROJ_ERR_INVALID_ARG, "scale (times log2 e) must be finite");
-    // (units of the line fit 30 bits)
-    const int64_t most_tiles = (static_cast<int64_t>(index->max_pages) * index->page_size + hsp::kAttnTile - 1) / hsp::kAttnTile;
-    if (static_cast<int64_t>(batch) * kv->kv_heads * (most_tiles + s.weight) >= (int64_t(1) << 30))
-        return api_fail(PROJ_ERR_UNSUPPORTED_SHAPE, "batch=%d of up to %d pages is too large", batch, index->max_pages);
+    float scale_log2;
+    if ((st = check_attention(index, s, batch, kv->kv_heads, hsp::kAttnTile, scale, &scale_log2)) != PROJ_OK) return st;
     if ((st = check_apart(kv, index)) != PROJ_OK) return st;
     if (batch == 0) return hsp::api_ok();
-    if (!rows && batch > index->num_rows)
-        return api_fail(PROJ_ERR_INVALID_ARG, "batch=%d exceeds the table's %d rows", batch, index->num_rows);
-    if (!q || !out) return api_fail(PROJ_ERR_INVALID_ARG, "q and out must not be NULL");
-    if (!aligned(q, 16) || !aligned(out, 16) || q_row_stride % 8 || q_head_stride % 8)
-        return api_fail(PROJ_ERR_MISALIGNED, "q and out must be 16-byte aligned, q's strides multiples of 8 elements");
-    if ((heads > 1 && (q_head_stride < 8 || q_head_stride >= (int64_t(1) << 38))) ||
-        (batch > 1 && (q_row_stride < 8 || q_row_stride >= (int64_t(1) << 38))))
-        return api_fail(PROJ_ERR_UNSUPPORTED_SHAPE, "queries must lie apart (strides %lld, %lld)", (long long)q_row_stride,
-                        (long long)q_head_stride);
-    if (!aligned(lse, 4) || !aligned(rows, 4)) return api_fail(PROJ_ERR_MISALIGNED, "lse and rows must be 4-byte aligned");
+    if ((st = check_queries(q, q_row_stride, q_head_stride, index, rows, batch, heads, out, lse)) != PROJ_OK) return st;
     hsp::ApiDevice dev;
     if ((st = hsp::api_device(&dev)) != PROJ_OK) return st;
     const int ctas = attn_ctas(s, dev.sms);
-    const bool split = most_tiles > kAttnWholeTiles;
+    const bool split = static_cast<int64_t>(index->max_pages) * index->page_size > PROJ_UNCUT_TOKENS;
     if (split && (st = check_workspace(workspace, workspace_bytes, attn_workspace(s, ctas))) != PROJ_OK) return st;
     hsp::AttnLaunchReq r{};
     const int boxes = hsp::attn_group_boxes(s.VB);
@@ -394,35 +464,10 @@ proj_status proj_paged_attention(const void *q, int64_t q_row_stride, int64_t q_
     r.pdl = opt.pdl;
     r.sms = dev.sms;
     r.stream = reinterpret_cast<cudaStream_t>(stream);
-    hsp::AttnArgs &a = r.args;
-    a.table = index->block_table;
-    a.table_stride = index->table_stride;
-    a.lens = index->seq_lens;
-    a.rows = rows;
-    a.num_rows = index->num_rows;
-    a.max_pages = index->max_pages;
-    a.num_pages = index->num_pages;
-    a.page_shift = log2_of(index->page_size);
-    a.batch = batch;
-    a.kv_heads = kv->kv_heads;
-    a.group = heads / kv->kv_heads;
-    a.ctas = ctas;
-    a.split = split ? 1 : 0;
-    a.weight = s.weight;
-    a.slots = s.slots;
-    a.scale_log2 = scale_log2;
-    a.out = out;
-    a.lse = lse;
-    if (split) {
-        a.entries = static_cast<hsp::AttnEntry *>(workspace);
-        a.parts = reinterpret_cast<float *>(static_cast<char *>(workspace) + up256(static_cast<size_t>(ctas) * sizeof(hsp::AttnEntry)));
-    }
-    a.skip_tile = opt.skip_stage;
-    a.wait_limit_ns = opt.wait_limit_ns;
-    a.err_word = dev.err_word;
+    attention_line(index, rows, batch, heads, kv->kv_heads, s, ctas, split, scale_log2, out, lse, workspace, opt, dev, &r.args);
     const cudaError_t e = s.shared ? hsp::launch_attn_latent(r) : hsp::launch_attn_grouped(r);
     if (e != cudaSuccess) return hsp::api_cuda_fail(e, "kernel launch (paged attention)");
-    hsp::api_count_launches(a.split ? 2 : 1);
+    hsp::api_count_launches(split ? 2 : 1);
     return hsp::api_ok();
 }
 
@@ -625,7 +670,7 @@ proj_status proj_cache_read_q8(const proj_kv_pages_q8 *kv, const proj_page_index
 
 size_t proj_paged_attention_q8_workspace_bytes(int32_t heads, int32_t kv_heads, int32_t k_dim, int32_t v_dim, int32_t latent) {
     AttnShape s;
-    if (attn_shape(heads, kv_heads, k_dim, v_dim, latent != 0, &s) != PROJ_OK) return 0;
+    if (attn8_shape(heads, kv_heads, k_dim, v_dim, latent != 0, &s) != PROJ_OK) return 0;
     return attn_workspace(s, attn_ctas(s, hsp::api_plan_sms()));
 }
 
@@ -637,58 +682,58 @@ proj_status proj_paged_attention_q8(const void *q, int64_t q_row_stride, int64_t
     if (st != PROJ_OK) return st;
     if ((st = check_kv_q8(kv, index)) != PROJ_OK) return st;
     AttnShape s;
-    if ((st = attn_shape(heads, kv->kv_heads, kv->k_dim, kv->v_dim, kv->v == nullptr, &s)) != PROJ_OK) return st;
-    if (batch < 0) return api_fail(PROJ_ERR_INVALID_ARG, "batch=%d is negative", batch);
-    const float scale_log2 = scale * 1.4426950408889634f;  // log2(e)
-    if (!std::isfinite(scale_log2)) return api_fail(PROJ_ERR_INVALID_ARG, "scale (times log2 e) must be finite");
-    // (units of the line fit 30 bits)
-    const int64_t most_tiles = (static_cast<int64_t>(index->max_pages) * index->page_size + hsp::kAttnTile - 1) / hsp::kAttnTile;
-    if (static_cast<int64_t>(batch) * kv->kv_heads * (most_tiles + s.weight) >= (int64_t(1) << 30))
-        return api_fail(PROJ_ERR_UNSUPPORTED_SHAPE, "batch=%d of up to %d pages is too large", batch, index->max_pages);
+    if ((st = attn8_shape(heads, kv->kv_heads, kv->k_dim, kv->v_dim, kv->v == nullptr, &s)) != PROJ_OK) return st;
+    float scale_log2;
+    if ((st = check_attention(index, s, batch, kv->kv_heads, hsp::kAttn8Tile, scale, &scale_log2)) != PROJ_OK) return st;
     if ((st = check_apart_q8(kv, index)) != PROJ_OK) return st;
     if (batch == 0) return hsp::api_ok();
-    if (!rows && batch > index->num_rows)
-        return api_fail(PROJ_ERR_INVALID_ARG, "batch=%d exceeds the table's %d rows", batch, index->num_rows);
-    if (!q || !out) return api_fail(PROJ_ERR_INVALID_ARG, "q and out must not be NULL");
-    if (!aligned(q, 16) || !aligned(out, 16) || q_row_stride % 8 || q_head_stride % 8)
-        return api_fail(PROJ_ERR_MISALIGNED, "q and out must be 16-byte aligned, q's strides multiples of 8 elements");
-    if ((heads > 1 && (q_head_stride < 8 || q_head_stride >= (int64_t(1) << 38))) ||
-        (batch > 1 && (q_row_stride < 8 || q_row_stride >= (int64_t(1) << 38))))
-        return api_fail(PROJ_ERR_UNSUPPORTED_SHAPE, "queries must lie apart (strides %lld, %lld)", (long long)q_row_stride,
-                        (long long)q_head_stride);
-    if (!aligned(lse, 4) || !aligned(rows, 4)) return api_fail(PROJ_ERR_MISALIGNED, "lse and rows must be 4-byte aligned");
+    if ((st = check_queries(q, q_row_stride, q_head_stride, index, rows, batch, heads, out, lse)) != PROJ_OK) return st;
     hsp::ApiDevice dev;
     if ((st = hsp::api_device(&dev)) != PROJ_OK) return st;
     const int ctas = attn_ctas(s, dev.sms);
-    const bool split = most_tiles > kAttnWholeTiles;
+    const bool split = static_cast<int64_t>(index->max_pages) * index->page_size > PROJ_UNCUT_TOKENS;
     if (split && (st = check_workspace(workspace, workspace_bytes, attn_workspace(s, ctas))) != PROJ_OK) return st;
+    hsp::Attn8LaunchReq r{};
+    const int width = kv->v_dim >= 128 ? 128 : 64;
+    if ((st = encode_codes(kv->k, index, kv->kv_heads, kv->v ? kv->k_dim : kv->v_dim, width, kv->k_page_stride, kv->k_token_stride,
+                           kv->k_head_stride, &r.tmap_k)) != PROJ_OK)
+        return st;
+    // the values' map; of a latent cache, the rotary columns of the same pages
+    st = PROJ_OK;
+    if (kv->v)
+        st = encode_codes(kv->v, index, kv->kv_heads, kv->v_dim, width, kv->v_page_stride, kv->v_token_stride, kv->v_head_stride, &r.tmap_v);
+    else if (kv->k_dim > kv->v_dim)
+        st = encode_codes(static_cast<const char *>(kv->k) + kv->v_dim, index, kv->kv_heads, 64, 64, kv->k_page_stride, kv->k_token_stride,
+                          kv->k_head_stride, &r.tmap_v);
+    else
+        r.tmap_v = r.tmap_k;
+    if (st != PROJ_OK) return st;
     const hsp::ApiOptions opt = hsp::api_options();
-    hsp::AttnQ8Args a;
-    memset(&a, 0, sizeof a);
-    a.q = q;
-    a.q_row = batch > 1 ? q_row_stride : 0;
-    a.q_head = q_head_stride;
-    a.k = k_side(kv);
-    a.v = v_side(kv);
-    a.table = index->block_table;
-    a.table_stride = index->table_stride;
-    a.lens = index->seq_lens;
-    a.rows = rows;
-    a.num_rows = index->num_rows;
-    a.max_pages = index->max_pages;
-    a.num_pages = index->num_pages;
-    a.page_shift = log2_of(index->page_size);
-    a.block_shift = log2_of(kv->block);
-    a.batch = batch;
-    a.kv_heads = kv->kv_heads;
-    a.group = heads / kv->kv_heads;
-    a.scale_log2 = scale_log2;
-    a.out = out;
-    a.lse = lse;
-    a.err_word = dev.err_word;
-    const cudaError_t e = hsp::launch_attn_q8_simple(a, opt.pdl, reinterpret_cast<cudaStream_t>(stream));
+    r.DK = kv->k_dim;
+    r.DV = kv->v_dim;
+    r.shared = s.shared;
+    r.N = s.N;
+    r.head_tiles = s.head_tiles;
+    r.smem_bytes = s.smem;
+    r.pdl = opt.pdl;
+    r.sms = dev.sms;
+    r.stream = reinterpret_cast<cudaStream_t>(stream);
+    attention_line(index, rows, batch, heads, kv->kv_heads, s, ctas, split, scale_log2, out, lse, workspace, opt, dev, &r.args.line);
+    r.args.q = q;
+    r.args.q_row = batch > 1 ? q_row_stride : 0;
+    r.args.q_head = heads > 1 ? q_head_stride : 0;
+    r.args.k_scales = kv->k_scale;
+    r.args.v_scales = kv->v ? kv->v_scale : kv->k_scale;
+    r.args.ks_page = kv->k_scale_page_stride;
+    r.args.ks_block = kv->k_scale_block_stride;
+    r.args.ks_head = kv->k_scale_head_stride;
+    r.args.vs_page = kv->v_scale_page_stride;
+    r.args.vs_block = kv->v_scale_block_stride;
+    r.args.vs_head = kv->v_scale_head_stride;
+    r.args.block_shift = log2_of(kv->block);
+    const cudaError_t e = s.shared ? hsp::launch_attn8_latent(r) : hsp::launch_attn8_grouped(r);
     if (e != cudaSuccess) return hsp::api_cuda_fail(e, "kernel launch (paged attention, 8 bits)");
-    hsp::api_count_launches(1);
+    hsp::api_count_launches(split ? 2 : 1);
     return hsp::api_ok();
 }
 

@@ -136,21 +136,38 @@ struct ReadQ8Args {
 };
 cudaError_t launch_read_q8(const ReadQ8Args &a, int sms, int pdl, cudaStream_t stream);
 
-struct AttnQ8Args {
+constexpr int kAttn8Tile = 128;      // tokens per tile
+constexpr int kAttn8ScaleSlots = 4;  // tiles whose scales lie ready
+struct Attn8Args {
+    AttnArgs line;                   // (no host tables of its own: sizes, table, lengths, outputs, workspace)
     const void *q;                   // [batch, heads, k_dim] bf16
     int64_t q_row, q_head;
-    Q8Side k, v;                     // (latent: v is k's first columns)
-    const int32_t *table;
-    int64_t table_stride;
-    const int32_t *lens, *rows;
-    int32_t num_rows, max_pages, num_pages, page_shift, block_shift;
-    int32_t batch, kv_heads, group;
-    float scale_log2;
-    void *out;
-    float *lse;
-    int *err_word;
+    const float *k_scales, *v_scales;
+    int64_t ks_page, ks_block, ks_head, vs_page, vs_block, vs_head;
+    int32_t block_shift;
 };
-cudaError_t launch_attn_q8_simple(const AttnQ8Args &a, int pdl, cudaStream_t stream);
+struct Attn8LaunchReq {
+    int DK, DV, shared, N;           // columns, v = columns of k, head tile
+    int head_tiles;                  // grid.x
+    int smem_bytes;
+    int pdl;
+    int sms;
+    cudaStream_t stream;
+    CUtensorMap tmap_k, tmap_v;      // boxes of 128 (64) columns; latent: tmap_v has the 64 rotary columns
+    Attn8Args args;
+};
+cudaError_t launch_attn8_latent(const Attn8LaunchReq &r);
+cudaError_t launch_attn8_grouped(const Attn8LaunchReq &r);
+// A latent cache's queries are split by four warps of their own, a grouped one's (few and short) by the softmax warps.
+constexpr int attn8_threads(bool shared) { return shared ? 384 : 256; }
+// CTAs per SM (see attn_ctas_per_sm; 64 heads fill tensor memory or the registers).
+constexpr int attn8_ctas_per_sm(int DK, bool shared, int N) { return shared || N == 64 ? 1 : DK == 64 && N == 16 ? 3 : 2; }
+constexpr int kAttn8RopeBytes = kAttn8Tile * 64;
+// Shared memory besides the ring of groups: queries (two pieces), probabilities, rotary boxes, scales, reduction
+// buffers, barriers and the alignment slack.
+inline int attn8_fixed_smem(int DK, bool rope, int N) {
+    return 2 * N * DK + kAttn8Tile * 2 * N + (rope ? 2 * kAttn8RopeBytes : 0) + kAttn8ScaleSlots * kAttn8Tile * 12 + 13 * N * 4 + 640 + 1024;
+}
 
 // ---- pages ------------------------------------------------------------------------------
 

@@ -1156,8 +1156,9 @@ ApiOptions api_options() {
 }
 void api_count_launches(int n) { g_launches.fetch_add(static_cast<uint64_t>(n), std::memory_order_relaxed); }
 
-proj_status api_encode_5d(const void *ptr, const uint64_t (&dims)[5], const uint64_t (&strides)[4],
-                          const uint32_t (&box)[5], CUtensorMap *out) {
+namespace {
+proj_status encode_5d(CUtensorMapDataType type, CUtensorMapSwizzle swizzle, const void *ptr, const uint64_t (&dims)[5],
+                      const uint64_t (&strides)[4], const uint32_t (&box)[5], CUtensorMap *out) {
     proj_status st = load_encode();
     if (st != PROJ_OK) return st;
     cuuint64_t d[5], sd[4];
@@ -1167,14 +1168,26 @@ proj_status api_encode_5d(const void *ptr, const uint64_t (&dims)[5], const uint
         b[i] = box[i];
         if (i < 4) sd[i] = strides[i];
     }
-    const CUresult r = g_encode(out, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, const_cast<void *>(ptr), d, sd, b, estr,
-                                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+    const CUresult r = g_encode(out, type, 5, const_cast<void *>(ptr), d, sd, b, estr,
+                                CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
                                 CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     if (r != CUDA_SUCCESS)
         return fail(PROJ_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d): dims [%llu %llu %llu %llu %llu], box [%u %u %u]",
                     static_cast<int>(r), (unsigned long long)d[0], (unsigned long long)d[1], (unsigned long long)d[2],
                     (unsigned long long)d[3], (unsigned long long)d[4], b[0], b[1], b[2]);
     return PROJ_OK;
+}
+}  // namespace
+
+proj_status api_encode_5d(const void *ptr, const uint64_t (&dims)[5], const uint64_t (&strides)[4],
+                          const uint32_t (&box)[5], CUtensorMap *out) {
+    return encode_5d(CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, CU_TENSOR_MAP_SWIZZLE_128B, ptr, dims, strides, box, out);
+}
+
+proj_status api_encode_codes_5d(const void *ptr, const uint64_t (&dims)[5], const uint64_t (&strides)[4],
+                                const uint32_t (&box)[5], CUtensorMap *out) {
+    return encode_5d(CU_TENSOR_MAP_DATA_TYPE_UINT8, box[0] == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, ptr, dims,
+                     strides, box, out);
 }
 
 }  // namespace hsp
