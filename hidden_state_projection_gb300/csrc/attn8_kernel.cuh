@@ -17,10 +17,11 @@
 // 2^(s_t + log2 vs_t - m).  w = Wh + Wl, Wh rounded to e4m3, the rest to e5m2: at most 2^-7 of w while w is at least
 // 2^-6 (the rest of a smaller one is half of 2^-9 or less, and e5m2 keeps an eighth of that), largest 448.  Two 8-bit
 // pieces have not the range of a bf16 number, so the reference point m follows the tiles in both directions: a tile whose
-// largest weight in some column is beyond 2^8.75, or below 2^0.5, moves that column's m (largest weight to 2^4.5)
-// and rescales O^T; what a tile's rounding leaves out is small beside the tile's own largest weight, whatever weights
-// other tiles have (a first token with nearly all the weight before a long tail).  Downwards m stops 30 below
-// its highest point.  O^T is divided by l = sum (Wh + Wl)_t / vs_t, so the rounding that all of a row's weight has in
+// largest weight in some column is beyond 2^8.75, or below 2^-4, moves that column's m (largest weight to 2^3) and
+// rescales O^T; what a tile's rounding leaves out is small beside the largest weight of the tile and of the row,
+// whatever weights other tiles have (a first token with nearly all the weight before a long tail).  Normal scores of
+// variance 3 in 64 columns move a point in 2 tiles of 133 (in 54 with a window of 2^0.5 to 2^8.75).  Downwards m stops 30
+// below its highest point.  O^T is divided by l = sum (Wh + Wl)_t / vs_t, so the rounding that all of a row's weight has in
 // common cancels; lse takes the sum u of the unrounded weights.  Sums and statistics are fp32.
 //
 // Warps: four for the softmax (they also carry O^T out), a copy producer, an issuer of the scores, an issuer of the
@@ -82,6 +83,12 @@ __device__ __forceinline__ __half2 e5m2x2_to_half2(uint32_t codes) {
     return *reinterpret_cast<const __half2 *>(&r);
 }
 
+// Column c of pairs of columns.
+template <int P>
+__device__ __forceinline__ float col(const float2 (&v)[P], int c) {
+    return (c & 1) ? v[c >> 1].y : v[c >> 1].x;
+}
+
 // Barrier 2 of four warps that split queries.
 __device__ __forceinline__ void query_sync() { asm volatile("barrier.cta.sync.aligned 2, 128;" ::: "memory"); }
 
@@ -102,15 +109,19 @@ struct Attn8Cfg {
     static constexpr int kCols = kOT * N + 4 * N;             // O^T, then two S^T
     static constexpr uint32_t kTmemCols = kCols <= 128 ? 128 : kCols <= 256 ? 256 : 512;
     static_assert(kCols <= 512, "tensor memory");
-    static constexpr int kThreads = attn8_threads(SHARED);
-    static constexpr int kC = N / 4;                          // heads of a softmax thread
+    static constexpr int kThreads = attn8_threads(SHARED, N);
+    static constexpr int kSets = attn8_sets(N);               // sets of four softmax warps
+    static constexpr int kSoft = 128 * kSets;                 // softmax threads
+    static constexpr int kHeads = N / kSets;                  // heads of a set
+    static constexpr int kC = kHeads / 4;                     // heads of a softmax thread
+    static constexpr int kRoles = 4 * kSets;                  // the first warp behind the softmax
 };
 
 // The window of a column's largest weight in a tile, log2, and where it is put.
-constexpr float kAttn8Up = 8.75f, kAttn8Low = 0.5f, kAttn8Aim = 4.5f, kAttn8Down = 30.f;
+constexpr float kAttn8Up = 8.75f, kAttn8Low = -4.f, kAttn8Aim = 3.f, kAttn8Down = 30.f;
 
 template <int DK, int DV, bool SHARED, int N>
-__global__ void __launch_bounds__(attn8_threads(SHARED), attn8_ctas_per_sm(DK, SHARED, N))
+__global__ void __launch_bounds__(attn8_threads(SHARED, N), attn8_ctas_per_sm(DK, SHARED, N))
     hsp_attn8_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v, const __grid_constant__ Attn8Args g) {
     using C = Attn8Cfg<DK, DV, SHARED, N>;
     constexpr int T = kAttn8Tile, kC = C::kC;
@@ -127,7 +138,7 @@ __global__ void __launch_bounds__(attn8_threads(SHARED), attn8_ctas_per_sm(DK, S
     float *const fac = red + 4 * N;                                     // [N]
     float *const top = fac + N;                                         // [4 warps][N] highest reference point so far
     float *const q_unit = top + 4 * N;                                  // [4][N] the unit of a part's queries, 2^e of the head
-    uint32_t *const seen = reinterpret_cast<uint32_t *>(q_unit + 4 * N);   // [2][2][4 warps], 16-byte aligned
+    uint32_t *const seen = reinterpret_cast<uint32_t *>(q_unit + 4 * N);   // [2][8 warps], 16-byte aligned
     uint64_t *const full = reinterpret_cast<uint64_t *>(seen + 16);
     uint64_t *const empty = full + a.slots;
     uint64_t *const x_full = empty + a.slots;                           // [2]
@@ -147,7 +158,7 @@ __global__ void __launch_bounds__(attn8_threads(SHARED), attn8_ctas_per_sm(DK, S
     volatile int *const abort_flag = ints + 1;
     int *const issued = ints + 2;                                       // groups and rotary boxes whose copies were issued
     int *const place = ints + 4;
-    int *const warp_sum = ints + 7;                                     // [12]
+    int *const warp_sum = ints + 7;                                     // [16]
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int ht = blockIdx.x, cta = blockIdx.y;
@@ -161,16 +172,16 @@ __global__ void __launch_bounds__(attn8_threads(SHARED), attn8_ctas_per_sm(DK, S
             mbar_init(smem_u32(&x_full[s]), 1);
             mbar_init(smem_u32(&x_empty[s]), 1);
             mbar_init(smem_u32(&s_full[s]), 1);
-            mbar_init(smem_u32(&s_free[s]), 128);
+            mbar_init(smem_u32(&s_free[s]), C::kSoft);
         }
         for (int s = 0; s < 4; ++s) mbar_init(smem_u32(&unit_full[s]), 1);
         for (int s = 0; s < kAttn8ScaleSlots; ++s) {
             mbar_init(smem_u32(&sc_full[s]), 32);
-            mbar_init(smem_u32(&sc_empty[s]), 128);
+            mbar_init(smem_u32(&sc_empty[s]), C::kSoft);
         }
         mbar_init(smem_u32(q_full), 1);
         mbar_init(smem_u32(q_free), 1);
-        mbar_init(smem_u32(p_full), 128);
+        mbar_init(smem_u32(p_full), C::kSoft);
         mbar_init(smem_u32(pv_done), 1);
         mbar_init(smem_u32(drained), 2);
         *abort_flag = 0;
@@ -179,7 +190,7 @@ __global__ void __launch_bounds__(attn8_threads(SHARED), attn8_ctas_per_sm(DK, S
         tma_prefetch_map(&tmap_k);
         if (!SHARED || C::kRope) tma_prefetch_map(&tmap_v);
     }
-    if (warp == 5) {
+    if (warp == C::kRoles + 1) {
         tmem_alloc(smem_u32(tmem_slot), C::kTmemCols);
         tmem_relinquish();
     }
@@ -193,9 +204,10 @@ __global__ void __launch_bounds__(attn8_threads(SHARED), attn8_ctas_per_sm(DK, S
     const uint32_t tmem_s = tmem + C::kOT * N;
     auto await = [&](uint64_t *bar, uint32_t phase) { return attn_wait(smem_u32(bar), phase & 1u, a.wait_limit_ns, abort_flag); };
 
-    // The queries of part `seg` in two pieces, by four warps (w: 0 .. 3).  A head to a group of lanes, eight columns to a
+    // The queries of part `seg` in two pieces, by kQW warps (w4: which).  A head to a group of lanes, eight columns to a
     // lane and round; the head's largest number decides its unit.
     auto split_queries = [&](const AttnSegment &sg, uint32_t seg, int w4) {
+        constexpr int kQW = SHARED ? 4 : 4 * C::kSets;
         constexpr int kLanes = DK / 8 < 32 ? DK / 8 : 32, kPer = 32 / kLanes, kRounds = (DK / 8 + kLanes - 1) / kLanes;
         const int sub = lane / kLanes, at = lane % kLanes;
         const int nheads = min(N, a.group - ht * N);
@@ -212,11 +224,11 @@ __global__ void __launch_bounds__(attn8_threads(SHARED), attn8_ctas_per_sm(DK, S
         int h = w4 * kPer + sub;
         fetch(h, ahead);
         await(q_free, seg ^ 1u);  // the last part's are done with (given up: the warps still meet at their barrier)
-        for (; h - sub < N; h += 4 * kPer) {
+        for (; h - sub < N; h += kQW * kPer) {
             uint4 v[kRounds];
 #pragma unroll
             for (int r = 0; r < kRounds; ++r) v[r] = ahead[r];
-            fetch(h + 4 * kPer, ahead);
+            fetch(h + kQW * kPer, ahead);
             float amax = 0.f;
 #pragma unroll
             for (int r = 0; r < kRounds; ++r) {
@@ -234,10 +246,10 @@ __global__ void __launch_bounds__(attn8_threads(SHARED), attn8_ctas_per_sm(DK, S
             const uint32_t u = __float_as_uint(amax);
             const int e2 = max(-126, min(126, static_cast<int>(u >> 23) - 127 - 8 + ((u & 0x7fffffu) > 0x600000u ? 1 : 0)));
             const float inv = two_to(-e2);
-            // row of the head among the instruction's columns: a softmax thread has columns 8 j + 2 c + e, c its
-            // place in four, of every step j: those are its heads c N / 4 + 2 j + e
-            const int c4 = h / kC, in4 = h % kC;
-            const int row = 8 * (in4 >> 1) + 2 * c4 + (in4 & 1);
+            // row of the head among the instruction's columns: a softmax thread has columns 8 j + 2 c + e of its set, c
+            // its place in four, of every step j: those are the set's heads c kC + 2 j + e
+            const int in = h % C::kHeads, c4 = in / kC, in4 = in % kC;
+            const int row = h - in + 8 * (in4 >> 1) + 2 * c4 + (in4 & 1);
 #pragma unroll
             for (int r = 0; r < kRounds; ++r) {
                 const int c = (r * kLanes + at) * 8;
@@ -269,14 +281,14 @@ __global__ void __launch_bounds__(attn8_threads(SHARED), attn8_ctas_per_sm(DK, S
         }
         fence_proxy_async_smem();
         if (SHARED) query_sync();
-        else softmax_sync();
+        else softmax_sync<C::kSoft>();
         if (w4 == 0 && lane == 0) {
             mbar_arrive(smem_u32(&unit_full[seg & 3u]));
             mbar_arrive(smem_u32(q_full));
         }
     };
 
-    if (warp == 4) {
+    if (warp == C::kRoles) {
         // ---------------- copy producer: one thread reads the table a tile ahead and issues ----------------
         if (elect_one()) {
             AttnWalk walk(ln);
@@ -345,7 +357,7 @@ __global__ void __launch_bounds__(attn8_threads(SHARED), attn8_ctas_per_sm(DK, S
             }
         }
         __syncwarp();
-    } else if (warp == 5) {
+    } else if (warp == C::kRoles + 1) {
         // ---------------- issuer of the scores ----------------
         if (elect_one()) {
             constexpr uint32_t kDesc = (1u << 4) | (static_cast<uint32_t>(C::kQRows >> 3) << 17) | (static_cast<uint32_t>(T >> 4) << 24);
@@ -395,7 +407,7 @@ __global__ void __launch_bounds__(attn8_threads(SHARED), attn8_ctas_per_sm(DK, S
             umma_commit(smem_u32(drained));
         }
         __syncwarp();
-    } else if (warp == 6) {
+    } else if (warp == C::kRoles + 2) {
         // ---------------- issuer of the products with the values ----------------
         if (elect_one()) {
             constexpr uint32_t kDescH = (1u << 4) | (1u << 15) | (1u << 16) | (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(C::kMV >> 4) << 24);
@@ -440,7 +452,7 @@ __global__ void __launch_bounds__(attn8_threads(SHARED), attn8_ctas_per_sm(DK, S
             }
         }
         __syncwarp();
-    } else if (warp == 7) {
+    } else if (warp == C::kRoles + 3) {
         // ---------------- the tiles' scales, up to kAttn8ScaleSlots tiles ahead ----------------
         AttnWalk walk(ln);
         int i = 0;
@@ -450,11 +462,11 @@ __global__ void __launch_bounds__(attn8_threads(SHARED), attn8_ctas_per_sm(DK, S
             const int row = a.rows ? a.rows[sg.b] : sg.b;
             const int32_t *tbl = a.table + row * a.table_stride;
             const float *ks = g.k_scales + sg.kv * g.ks_head, *vs = g.v_scales + sg.kv * g.vs_head;
-            for (int k = 0; k < sg.n; ++k, ++i) {
-                float kk[4], vv[4];
+            // a tile's scales are requested while the ones before wait for their place
+            auto fetch = [&](int tile, float (&kk)[4], float (&vv)[4]) {
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    const int t = (sg.t0 + k) * T + e * 32 + lane;
+                    const int t = tile * T + e * 32 + lane;
                     kk[e] = 0.f;
                     vv[e] = 1.f;
                     if (t < sg.len) {
@@ -465,6 +477,12 @@ __global__ void __launch_bounds__(attn8_threads(SHARED), attn8_ctas_per_sm(DK, S
                         vv[e] = SHARED ? kk[e] : vs[page * g.vs_page + blk * g.vs_block];
                     }
                 }
+            };
+            float kk[2][4], vv[2][4];
+            fetch(sg.t0, kk[0], vv[0]);
+            if (sg.n > 1) fetch(sg.t0 + 1, kk[1], vv[1]);
+#pragma unroll 1
+            for (int k = 0; k < sg.n; ++k, ++i) {
                 const int slot = i % kAttn8ScaleSlots;
                 alive = await(&sc_empty[slot], static_cast<uint32_t>(i / kAttn8ScaleSlots) ^ 1u);
                 alive = __all_sync(0xffffffffu, alive);
@@ -472,19 +490,22 @@ __global__ void __launch_bounds__(attn8_threads(SHARED), attn8_ctas_per_sm(DK, S
                 float *to = scales + slot * 3 * T;
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    const float v = fminf(fmaxf(vv[e], two_to(kQ8MinExp)), two_to(kQ8MaxExp));
-                    to[e * 32 + lane] = kk[e] * a.scale_log2;
+                    const float v = fminf(fmaxf(vv[0][e], two_to(kQ8MinExp)), two_to(kQ8MaxExp));
+                    to[e * 32 + lane] = kk[0][e] * a.scale_log2;
                     to[T + e * 32 + lane] = log2f(v);
                     to[2 * T + e * 32 + lane] = 1.f / v;
+                    kk[0][e] = kk[1][e];
+                    vv[0][e] = vv[1][e];
                 }
                 mbar_arrive(smem_u32(&sc_full[slot]));
+                if (k + 2 < sg.n) fetch(sg.t0 + k + 2, kk[1], vv[1]);
             }
         }
-    } else if (SHARED && warp >= 8) {
+    } else if (SHARED && warp >= C::kRoles + 4) {
         // ---------------- the queries of the next part, while the last one is under way ----------------
         AttnWalk walk(ln);
         AttnSegment sg;
-        for (uint32_t seg = 0; attn_next_segment<T>(a, ln, walk, sg); ++seg) split_queries(sg, seg, warp - 8);
+        for (uint32_t seg = 0; attn_next_segment<T>(a, ln, walk, sg); ++seg) split_queries(sg, seg, warp - C::kRoles - 4);
     } else {
         // ---------------- softmax warps ----------------
         AttnWalk walk(ln);
@@ -495,9 +516,11 @@ __global__ void __launch_bounds__(attn8_threads(SHARED), attn8_ctas_per_sm(DK, S
         const int nheads = min(N, a.group - head0);            // real heads of this tile
         const int all_heads = a.kv_heads * a.group;
         __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(a.out);
-        const int r0 = warp * 32 + (lane >> 2);                // this thread's token rows: r0 + 0, 8, 16, 24
-        const int c4 = lane & 3;                               // its heads: c4 * kC + 0 .. kC - 1
-        const uint32_t lane_base = static_cast<uint32_t>(warp * 32) << 16;
+        const int wq = warp & 3, set = warp >> 2;
+        const int r0 = wq * 32 + (lane >> 2);                  // this thread's token rows: r0 + 0, 8, 16, 24
+        const int c4 = lane & 3;
+        const int h0 = set * C::kHeads + c4 * kC;              // its heads: h0 + 0 .. kC - 1
+        const uint32_t lane_base = static_cast<uint32_t>(wq * 32) << 16;
         if (a.split && ht == 0 && tid == 96) {
             AttnEntry e;
             e.batch = -1;
@@ -508,7 +531,7 @@ __global__ void __launch_bounds__(attn8_threads(SHARED), attn8_ctas_per_sm(DK, S
         uint32_t unused = 0;
 #pragma unroll
         for (int c = 0; c < kC; ++c)
-            if (c4 * kC + c >= nheads) unused |= 1u << c;
+            if (h0 + c >= nheads) unused |= 1u << c;
         bool more = attn_next_segment<T>(a, ln, walk, sg);
         if (!SHARED && more) split_queries(sg, 0, warp);
         while (more) {
@@ -521,7 +544,7 @@ __global__ void __launch_bounds__(attn8_threads(SHARED), attn8_ctas_per_sm(DK, S
 #pragma unroll
             for (int j = 0; j < kC / 2; ++j) l[j] = u[j] = make_float2(0.f, 0.f);
             await(&unit_full[seg & 3u], seg >> 2);
-            const float *unit = q_unit + (seg & 3u) * N + c4 * kC;
+            const float *unit = q_unit + (seg & 3u) * N + h0;
             ++seg;
             for (int k = 0; k < sg.n; ++k, ++i) {
                 const int64_t tok0 = static_cast<int64_t>(sg.t0 + k) * T;
@@ -538,37 +561,37 @@ __global__ void __launch_bounds__(attn8_threads(SHARED), attn8_ctas_per_sm(DK, S
                 mbar_arrive(smem_u32(&sc_empty[slot]));
                 await(&s_full[i & 1], static_cast<uint32_t>(i >> 1));
                 tc_fence_after_sync();
-                // s[r][c]: row r0 + 8 r, head c4 kC + c, in log2 units with the values' scale
-                float s[4][kC];
+                // s[r][j]: row r0 + 8 r, heads h0 + 2 j and + 1, in log2 units with the values' scale
+                float2 s[4][kC / 2];
 #pragma unroll
                 for (int hf = 0; hf < 2; ++hf) {
-                    float hi[N / 2], lo[N / 2];
-                    const uint32_t from = tmem_s + (i & 1) * C::kQRows + lane_base + (static_cast<uint32_t>(hf * 16) << 16);
-                    tmem_ld_frag<N / 8>(from, hi);
-                    tmem_ld_frag<N / 8>(from + N, lo);
+                    float hi[kC * 2], lo[kC * 2];
+                    const uint32_t from = tmem_s + (i & 1) * C::kQRows + set * C::kHeads + lane_base + (static_cast<uint32_t>(hf * 16) << 16);
+                    tmem_ld_frag<kC / 2>(from, hi);
+                    tmem_ld_frag<kC / 2>(from + N, lo);
                     tmem_wait_ld();
 #pragma unroll
-                    for (int j = 0; j < N / 8; ++j)
+                    for (int j = 0; j < kC / 2; ++j)
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const int r = 2 * hf + (e >> 1), c = 2 * j + (e & 1);
-                            s[r][c] = fmaf(lo[4 * j + e], 0.0625f, hi[4 * j + e]);
-                        }
+                        for (int e = 0; e < 2; ++e)
+                            s[2 * hf + e][j] = fma2(make_float2(lo[4 * j + 2 * e], lo[4 * j + 2 * e + 1]), make_float2(0.0625f, 0.0625f),
+                                                    make_float2(hi[4 * j + 2 * e], hi[4 * j + 2 * e + 1]));
                 }
                 tc_fence_before_sync();
                 mbar_arrive(smem_u32(&s_free[i & 1]));
 #pragma unroll
-                for (int c = 0; c < kC; ++c) {
-                    const float q1 = unit[c];
+                for (int j = 0; j < kC / 2; ++j) {
+                    const float2 q2 = *reinterpret_cast<const float2 *>(unit + 2 * j);
 #pragma unroll
-                    for (int r = 0; r < 4; ++r) s[r][c] = fmaf(s[r][c] * q1, ksc[r], vlog[r]);
+                    for (int r = 0; r < 4; ++r)
+                        s[r][j] = fma2(mul2(s[r][j], q2), make_float2(ksc[r], ksc[r]), make_float2(vlog[r], vlog[r]));
                 }
                 if (valid < T) {
 #pragma unroll
                     for (int r = 0; r < 4; ++r)
                         if (r0 + 8 * r >= valid) {
 #pragma unroll
-                            for (int c = 0; c < kC; ++c) s[r][c] = -INFINITY;
+                            for (int j = 0; j < kC / 2; ++j) s[r][j] = make_float2(-INFINITY, -INFINITY);
                         }
                 }
                 // columns that exceed the window, and those that some token reaches from below
@@ -576,36 +599,28 @@ __global__ void __launch_bounds__(attn8_threads(SHARED), attn8_ctas_per_sm(DK, S
                 uint32_t reached = lowest;
 #pragma unroll
                 for (int c = 0; c < kC; ++c) {
-                    const float most = fmaxf(fmaxf(s[0][c], s[1][c]), fmaxf(s[2][c], s[3][c])) - m[c];
+                    const float most = fmaxf(fmaxf(col(s[0], c), col(s[1], c)), fmaxf(col(s[2], c), col(s[3], c))) - m[c];
                     over |= most > kAttn8Up && !((unused >> c) & 1u);
                     if (most >= kAttn8Low) reached |= 1u << c;
                 }
                 {
-                    // kC bits for each of the four places: one word, or two for 64 heads
-                    constexpr int kWords = kC * 4 > 32 ? 2 : 1, kPlaces = 4 / kWords;
-#pragma unroll
-                    for (int w = 0; w < kWords; ++w) {
-                        const uint32_t mine = c4 / kPlaces == w ? reached << (c4 % kPlaces * kC) : 0u;
-                        const uint32_t all = __reduce_or_sync(0xffffffffu, mine);
-                        if (lane == 0) seen[((i & 1) * 2 + w) * 4 + warp] = all;
-                    }
+                    // kC bits for each of the four places, the warps of a set together
+                    const uint32_t all = __reduce_or_sync(0xffffffffu, reached << (c4 * kC));
+                    if (lane == 0) seen[(i & 1) * 8 + warp] = all;
                 }
-                bool move = softmax_any(over);
-                {
-                    constexpr int kWords = kC * 4 > 32 ? 2 : 1;
-                    constexpr uint32_t kAll = kC * 4 >= 32 ? 0xffffffffu : (1u << (kC * 4 & 31)) - 1u;
+                bool move = softmax_any<C::kSoft>(over);
 #pragma unroll
-                    for (int w = 0; w < kWords; ++w) {
-                        const uint4 x = *reinterpret_cast<const uint4 *>(seen + ((i & 1) * 2 + w) * 4);
-                        move |= (x.x | x.y | x.z | x.w) != kAll;
-                    }
+                for (int w = 0; w < C::kSets; ++w) {
+                    constexpr uint32_t kAll = kC * 4 >= 32 ? 0xffffffffu : (1u << (kC * 4 & 31)) - 1u;
+                    const uint4 x = *reinterpret_cast<const uint4 *>(seen + (i & 1) * 8 + w * 4);
+                    move |= (x.x | x.y | x.z | x.w) != kAll;
                 }
                 if (move) {
                     // column maxima over the tile's tokens, new reference points, O^T rescaled
                     float mx[kC];
 #pragma unroll
                     for (int c = 0; c < kC; ++c) {
-                        float t = fmaxf(fmaxf(s[0][c], s[1][c]), fmaxf(s[2][c], s[3][c]));
+                        float t = fmaxf(fmaxf(col(s[0], c), col(s[1], c)), fmaxf(col(s[2], c), col(s[3], c)));
                         t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 4));
                         t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 8));
                         t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 16));
@@ -614,16 +629,16 @@ __global__ void __launch_bounds__(attn8_threads(SHARED), attn8_ctas_per_sm(DK, S
                     if (lane < 4) {
 #pragma unroll
                         for (int c = 0; c < kC; c += 4)
-                            *reinterpret_cast<float4 *>(red + warp * N + c4 * kC + c) = make_float4(mx[c], mx[c + 1], mx[c + 2], mx[c + 3]);
+                            *reinterpret_cast<float4 *>(red + wq * N + h0 + c) = make_float4(mx[c], mx[c + 1], mx[c + 2], mx[c + 3]);
                     }
-                    softmax_sync();
+                    softmax_sync<C::kSoft>();
                     lowest = unused;
 #pragma unroll
                     for (int c = 0; c < kC; ++c) {
-                        const int at = c4 * kC + c;
+                        const int at = h0 + c;
                         const float t = fmaxf(fmaxf(red[at], red[N + at]), fmaxf(red[2 * N + at], red[3 * N + at]));
                         const float most = t - m[c];
-                        float peak = k == 0 ? -INFINITY : top[warp * N + at];
+                        float peak = k == 0 ? -INFINITY : top[wq * N + at];
                         float n = m[c];
                         if (k == 0 || most > kAttn8Up || most < kAttn8Low) n = t - kAttn8Aim;
                         if (k == 0 && !(n > -INFINITY)) n = 0.f;  // (nothing but NaN or minus infinity in the first tile)
@@ -642,17 +657,17 @@ __global__ void __launch_bounds__(attn8_threads(SHARED), attn8_ctas_per_sm(DK, S
                         }
                         __syncwarp();  // every lane has read its columns' peaks
                         if (lane < 4) {
-                            top[warp * N + at] = peak;
-                            if (warp == 0) fac[at] = f;
+                            top[wq * N + at] = peak;
+                            if (wq == 0) fac[at] = f;
                         }
                     }
                     __syncwarp();
                     if (k > 0) {
                         await(pv_done, static_cast<uint32_t>(i - 1));
                         tc_fence_after_sync();
-                        softmax_sync();
+                        softmax_sync<C::kSoft>();
 #pragma unroll 1
-                        for (int c0 = 0; c0 < C::kOT * N; c0 += 16) {
+                        for (int c0 = set * 16; c0 < C::kOT * N; c0 += C::kSets * 16) {
                             float o[16];
                             tmem_ld16(tmem + c0 + lane_base, o);
                             tmem_wait_ld();
@@ -673,7 +688,7 @@ __global__ void __launch_bounds__(attn8_threads(SHARED), attn8_ctas_per_sm(DK, S
                     int at = first % a.slots;
 #pragma unroll
                     for (int gr = 0; gr < C::kVG; ++gr) {
-                        for (int e = tid; e < (-valid & 31) * kPieces; e += 128)
+                        for (int e = tid; e < (-valid & 31) * kPieces; e += C::kSoft)
                             *reinterpret_cast<uint4 *>(smem + at * C::kGroupBytes + valid * C::kW + e * 16) = make_uint4(0, 0, 0, 0);
                         at = at + 1 == a.slots ? 0 : at + 1;
                     }
@@ -681,42 +696,42 @@ __global__ void __launch_bounds__(attn8_threads(SHARED), attn8_ctas_per_sm(DK, S
                 // the weights in two pieces, and their sums
                 uint32_t wh[4][kC / 4], wl[4][kC / 4];
 #pragma unroll
-                for (int r = 0; r < 4; ++r)
+                for (int r = 0; r < 4; ++r) {
+                    const float2 inv = make_float2(vinv[r], vinv[r]);
 #pragma unroll
-                    for (int c = 0; c < kC; c += 2) {
-                        const float p0 = fast_exp2(s[r][c] - m[c]), p1 = fast_exp2(s[r][c + 1] - m[c + 1]);
-                        const __half2 p = __floats2half2_rn(p0, p1);
-                        const uint32_t h8 = half2_to_e4m3x2(p);
+                    for (int j = 0; j < kC / 2; ++j) {
+                        float2 p = s[r][j];
+                        add2(p, make_float2(-m[2 * j], -m[2 * j + 1]));
+                        p = make_float2(fast_exp2(p.x), fast_exp2(p.y));
+                        const __half2 p16 = __floats2half2_rn(p.x, p.y);
+                        const uint32_t h8 = half2_to_e4m3x2(p16);
                         const __half2 h16 = e4m3x2_to_half2(h8);
-                        const uint32_t l8 = half2_to_e5m2x2(__hsub2(p, h16));
+                        const uint32_t l8 = half2_to_e5m2x2(__hsub2(p16, h16));
                         const float2 w = __half22float2(__hadd2(h16, e5m2x2_to_half2(l8)));
-                        if ((c & 2) == 0) {
-                            wh[r][c >> 2] = h8;
-                            wl[r][c >> 2] = l8;
+                        if ((j & 1) == 0) {
+                            wh[r][j >> 1] = h8;
+                            wl[r][j >> 1] = l8;
                         } else {
-                            wh[r][c >> 2] |= h8 << 16;
-                            wl[r][c >> 2] |= l8 << 16;
+                            wh[r][j >> 1] |= h8 << 16;
+                            wl[r][j >> 1] |= l8 << 16;
                         }
-                        u[c >> 1].x = fmaf(p0, vinv[r], u[c >> 1].x);
-                        u[c >> 1].y = fmaf(p1, vinv[r], u[c >> 1].y);
-                        l[c >> 1].x = fmaf(w.x, vinv[r], l[c >> 1].x);
-                        l[c >> 1].y = fmaf(w.y, vinv[r], l[c >> 1].y);
+                        u[j] = fma2(p, inv, u[j]);
+                        l[j] = fma2(w, inv, l[j]);
                     }
+                }
                 // the weights of tile i - 1 have been read before these replace them
                 if (i > 0) await(pv_done, static_cast<uint32_t>(i - 1));
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
                     const int row = r0 + 8 * r;
                     uint8_t *line = p_smem + row * C::kPLine;
-                    if (N == 64) {
-                        *reinterpret_cast<uint4 *>(line + swizzled<C::kPLine>(row, c4)) = make_uint4(wh[r][0], wh[r][1 % (kC / 4)], wh[r][2 % (kC / 4)], wh[r][3 % (kC / 4)]);
-                        *reinterpret_cast<uint4 *>(line + swizzled<C::kPLine>(row, 4 + c4)) = make_uint4(wl[r][0], wl[r][1 % (kC / 4)], wl[r][2 % (kC / 4)], wl[r][3 % (kC / 4)]);
-                    } else if (N == 32) {
-                        *reinterpret_cast<uint2 *>(line + swizzled<C::kPLine>(row, c4 >> 1) + (c4 & 1) * 8) = make_uint2(wh[r][0], wh[r][1 % (kC / 4)]);
-                        *reinterpret_cast<uint2 *>(line + swizzled<C::kPLine>(row, 2 + (c4 >> 1)) + (c4 & 1) * 8) = make_uint2(wl[r][0], wl[r][1 % (kC / 4)]);
+                    uint8_t *hi = line + swizzled<C::kPLine>(row, h0 >> 4) + (h0 & 15), *lo = line + swizzled<C::kPLine>(row, (N + h0) >> 4) + (h0 & 15);
+                    if (kC == 8) {
+                        *reinterpret_cast<uint2 *>(hi) = make_uint2(wh[r][0], wh[r][1 % (kC / 4)]);
+                        *reinterpret_cast<uint2 *>(lo) = make_uint2(wl[r][0], wl[r][1 % (kC / 4)]);
                     } else {
-                        *reinterpret_cast<uint32_t *>(line + swizzled<C::kPLine>(row, 0) + c4 * 4) = wh[r][0];
-                        *reinterpret_cast<uint32_t *>(line + swizzled<C::kPLine>(row, 1) + c4 * 4) = wl[r][0];
+                        *reinterpret_cast<uint32_t *>(hi) = wh[r][0];
+                        *reinterpret_cast<uint32_t *>(lo) = wl[r][0];
                     }
                 }
                 fence_proxy_async_smem();
@@ -736,18 +751,18 @@ __global__ void __launch_bounds__(attn8_threads(SHARED), attn8_ctas_per_sm(DK, S
                         v[j].x += __shfl_xor_sync(0xffffffffu, v[j].x, d);
                         v[j].y += __shfl_xor_sync(0xffffffffu, v[j].y, d);
                     }
-                softmax_sync();  // the last tile's maxima and factors (l), the sums l (u) have been read
+                softmax_sync<C::kSoft>();  // the last tile's maxima and factors (l), the sums l (u) have been read
                 if (lane < 4) {
 #pragma unroll
-                    for (int j = 0; j < kC / 2; ++j) *reinterpret_cast<float2 *>(red + warp * N + c4 * kC + 2 * j) = v[j];
+                    for (int j = 0; j < kC / 2; ++j) *reinterpret_cast<float2 *>(red + wq * N + h0 + 2 * j) = v[j];
                 }
             };
             over_tokens(l);
-            if (warp == 0 && lane < 4) {
+            if (wq == 0 && lane < 4) {
 #pragma unroll
-                for (int j = 0; j < kC / 2; ++j) *reinterpret_cast<float2 *>(fac + c4 * kC + 2 * j) = make_float2(m[2 * j], m[2 * j + 1]);
+                for (int j = 0; j < kC / 2; ++j) *reinterpret_cast<float2 *>(fac + h0 + 2 * j) = make_float2(m[2 * j], m[2 * j + 1]);
             }
-            softmax_sync();
+            softmax_sync<C::kSoft>();
             const bool whole = begins && ends;
             const int slot = sg.x0 == ln.x0 ? 0 : 1;
             float *part = a.parts + (static_cast<int64_t>(ht) * a.ctas + cta) * 2 * attn_part(DV, N) + slot * attn_part(DV, N);
@@ -764,7 +779,7 @@ __global__ void __launch_bounds__(attn8_threads(SHARED), attn8_ctas_per_sm(DK, S
             }
             if (a.lse) {
                 over_tokens(u);
-                softmax_sync();
+                softmax_sync<C::kSoft>();
                 if (tid < N) {
                     const float t = red[tid] + red[N + tid] + red[2 * N + tid] + red[3 * N + tid];
                     if (!whole)
@@ -784,15 +799,15 @@ __global__ void __launch_bounds__(attn8_threads(SHARED), attn8_ctas_per_sm(DK, S
             }
             await(pv_done, static_cast<uint32_t>(i - 1));
             tc_fence_after_sync();
-            softmax_sync();
+            softmax_sync<C::kSoft>();
             const bool good = *abort_flag == 0;
             const int64_t obase = (static_cast<int64_t>(sg.b) * all_heads + sg.kv * a.group + head0) * DV;
-            attn_store_part<N, DV, C::kMV, C::kOT>(tmem, warp, lane, good, whole, nheads, fac, out + obase, part);
+            attn_store_part<N, DV, C::kMV, C::kOT, C::kSets>(tmem, wq, lane, good, whole, nheads, fac, out + obase, part, set);
             tc_fence_before_sync();
-            softmax_sync();  // red and fac are free again
+            softmax_sync<C::kSoft>();  // red and fac are free again
             sg = after;
         }
-        attn_store_empty<DV>(a, cta, head0, nheads);
+        if (tid < 128) attn_store_empty<DV>(a, cta, head0, nheads);
     }
     tc_fence_before_sync();
     if (a.split) {  // the join waits for the end of this grid: no fence
@@ -815,7 +830,7 @@ __global__ void __launch_bounds__(attn8_threads(SHARED), attn8_ctas_per_sm(DK, S
         for (int j = max(0, nx - 2); j < nx; ++j)
             if (j != a.skip_tile) land(&x_full[j & 1], j >> 1);
     }
-    if (warp == 5) {
+    if (warp == C::kRoles + 1) {
         tc_fence_after_sync();
         tmem_dealloc(tmem, C::kTmemCols);
     }

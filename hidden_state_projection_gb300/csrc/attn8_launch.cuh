@@ -32,7 +32,7 @@ cudaError_t launch_attn8_variant(const Attn8LaunchReq &r) {
     }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(r.head_tiles), static_cast<unsigned>(r.args.line.ctas), 1);
-    cfg.blockDim = dim3(attn8_threads(SHARED), 1, 1);
+    cfg.blockDim = dim3(attn8_threads(SHARED, N), 1, 1);
     cfg.dynamicSmemBytes = static_cast<size_t>(r.smem_bytes);
     cfg.stream = r.stream;
     cfg.attrs = attrs;

@@ -102,15 +102,19 @@ __device__ __forceinline__ bool elect_one() {
     return r != 0;
 }
 
-// Barrier 1 of the 128 softmax threads, and the same with an OR over their predicates.
-__device__ __forceinline__ void softmax_sync() { asm volatile("barrier.cta.sync.aligned 1, 128;" ::: "memory"); }
+// Barrier 1 of the softmax threads, and the same with an OR over their predicates.
+template <int THREADS = 128>
+__device__ __forceinline__ void softmax_sync() {
+    asm volatile("barrier.cta.sync.aligned 1, %0;" ::"n"(THREADS) : "memory");
+}
+template <int THREADS = 128>
 __device__ __forceinline__ bool softmax_any(bool p) {
     uint32_t r;
     asm volatile(
         "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
-        "barrier.cta.red.or.pred.aligned q, 1, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+        "barrier.cta.red.or.pred.aligned q, 1, %2, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
         : "=r"(r)
-        : "r"(static_cast<uint32_t>(p))
+        : "r"(static_cast<uint32_t>(p)), "n"(THREADS)
         : "memory");
     return r != 0;
 }
@@ -126,6 +130,21 @@ __device__ __forceinline__ void add2(float2 &a, float2 b) {
     asm("{\n\t.reg .b64 x, y;\n\tmov.b64 x, {%0, %1};\n\tmov.b64 y, {%2, %3};\n\tadd.rn.f32x2 x, x, y;\n\tmov.b64 {%0, %1}, x;\n\t}"
         : "+f"(a.x), "+f"(a.y)
         : "f"(b.x), "f"(b.y));
+}
+
+// Two columns at a time.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 z, {%6, %7};\n\t"
+        "fma.rn.f32x2 x, x, y, z;\n\tmov.b64 {%0, %1}, x;\n\t}"
+        : "=f"(c.x), "=f"(c.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return c;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    asm("{\n\t.reg .b64 x, y;\n\tmov.b64 x, {%0, %1};\n\tmov.b64 y, {%2, %3};\n\tmul.rn.f32x2 x, x, y;\n\tmov.b64 {%0, %1}, x;\n\t}"
+        : "+f"(a.x), "+f"(a.y)
+        : "f"(b.x), "f"(b.y));
+    return a;
 }
 
 // A box of a tensor on its way to L2.
@@ -344,15 +363,16 @@ __device__ __forceinline__ AttnLine attn_find_line(const AttnArgs &a, int cta, i
 
 // ---- the end of a part -----------------------------------------------------------------
 //
-// O^T (OT tiles of MV value columns, N heads each) out of tensor memory by four warps: a whole sequence's rows times
-// fac[head] to `out`, of a cut one to its partial, as they are.  Heads from `nheads` on go nowhere.
-template <int N, int DV, int MV, int OT>
+// O^T (OT tiles of MV value columns, N heads each) out of tensor memory by SETS times four warps (warp: of the four, set:
+// which steps of 16 columns): a whole sequence's rows times fac[head] to `out`, of a cut one to its partial, as they
+// are.  Heads from `nheads` on go nowhere.
+template <int N, int DV, int MV, int OT, int SETS = 1>
 __device__ __forceinline__ void attn_store_part(uint32_t tmem, int warp, int lane, bool good, bool whole, int nheads, const float *fac,
-                                                __nv_bfloat16 *out, float *part) {
+                                                __nv_bfloat16 *out, float *part, int set = 0) {
     constexpr int rpw = MV / 4;
     const uint32_t lane_base = static_cast<uint32_t>(warp * 32) << 16;
 #pragma unroll 1
-    for (int c0 = 0; c0 < OT * N; c0 += 16) {
+    for (int c0 = set * 16; c0 < OT * N; c0 += SETS * 16) {
         const int h0 = c0 & (N - 1);
         if (h0 >= nheads) continue;
         float o[16];

@@ -158,8 +158,10 @@ struct Attn8LaunchReq {
 };
 cudaError_t launch_attn8_latent(const Attn8LaunchReq &r);
 cudaError_t launch_attn8_grouped(const Attn8LaunchReq &r);
-// A latent cache's queries are split by four warps of their own, a grouped one's (few and short) by the softmax warps.
-constexpr int attn8_threads(bool shared) { return shared ? 384 : 256; }
+// Softmax warps: four for each set of at most 32 heads.  A latent cache's queries are split by four warps of their own, a
+// grouped one's (few and short) by the softmax warps.
+constexpr int attn8_sets(int N) { return N > 16 ? 2 : 1; }
+constexpr int attn8_threads(bool shared, int N) { return 128 * attn8_sets(N) + 128 + (shared ? 128 : 0); }
 // CTAs per SM (see attn_ctas_per_sm; 64 heads fill tensor memory or the registers).
 constexpr int attn8_ctas_per_sm(int DK, bool shared, int N) { return shared || N == 64 ? 1 : DK == 64 && N == 16 ? 3 : 2; }
 constexpr int kAttn8RopeBytes = kAttn8Tile * 64;

@@ -6,9 +6,10 @@ s = scale * sum_i |q_i k_i| (the largest over t):
     2^-14 * 2^e, so 2^-21.8 max |q| each: a score is off by that times scale * sum_i |k_i|;
   * a score is an fp32 sum of dk products: dk * 2^-24 * s, and 2^-22 of its size for the scaling, the logarithm of the
     values' scale and the exponential; a weight and the sum l are off by that (relative) each, l by len * 2^-24 more;
-  * a weight in two pieces, e4m3 (half a step 2^-4) and e5m2 (2^-3): 2^-7 of it while it is at least 2^-6 in units in
-    which the tile's largest is at least 2^0.5; of a smaller one an eighth of 2^-10: 2^-13, that is 2^-13.5 of the largest
-    w of the column's 128-token tile.  fp16 in between: 2^-11.  The same in l, which the sum is divided by;
+  * a weight in two pieces, e4m3 (half a step 2^-4) and e5m2 (2^-3): 2^-7 of it while it is at least 2^-6; of a smaller
+    one an eighth of 2^-10: 2^-13.  In these units the largest w of every 128-token tile is at least 2^-4, and that of the
+    tile that set them 2^3, which the row's is not below: so 2^-9 of the tile's largest and 2^-16 of the row's, the smaller
+    of the two.  fp16 in between: 2^-11.  The same in l, which the sum is divided by;
   * the fp32 sum over the tokens: len * 2^-24 * A; joining parts: a few 2^-24 * A more;
   * the result is rounded to bf16 once: 2^-8 |o|.
 Rounding errors of many weights are as good as independent, and the bound above then far too wide.  So the 2-norm of all
@@ -109,13 +110,14 @@ def reference(q, k, v, ks, vs, table, lens, scale, dv, rows=None):
             a = p @ vv.abs()
             pad = -n % 128
             w = torch.nn.functional.pad(p * vscale[:, h], (0, pad)).unflatten(-1, (-1, 128)).amax(-1)          # [G, tiles]
+            w = torch.minimum(w * 2.0 ** -9, w.amax(-1, keepdim=True) * 2.0 ** -16)
             codes = torch.nn.functional.pad(vc[:, h].abs(), (0, 0, 0, pad)).unflatten(0, (-1, 128)).sum(1)     # [tiles, dv]
             inv = torch.nn.functional.pad(1 / vscale[:, h], (0, pad)).view(-1, 128).sum(-1)                    # [tiles]
             o = out[b, at].abs()
-            tol[b, at] = (a + o) * (2.0 ** -7 + 2.0 ** -11) + 2.0 ** -13.5 * (w @ codes + o * (w @ inv)[:, None])
+            tol[b, at] = (a + o) * (2.0 ** -7 + 2.0 ** -11) + w @ codes + o * (w @ inv)[:, None]
             tol[b, at] += a * (2 * rel + (2 * n + 64) * 2.0 ** -24) + o * 2.0 ** -8
             vs1 = vscale[:, h]
-            d2 = ((p * vs1) * (2.0 ** -7 + 2.0 ** -11) + 2.0 ** -13.5 * w.repeat_interleave(128, -1)[:, :n]) ** 2
+            d2 = ((p * vs1) * (2.0 ** -7 + 2.0 ** -11) + w.repeat_interleave(128, -1)[:, :n]) ** 2
             square[b, at] = d2 @ vc[:, h] ** 2 + 2 * o * ((d2 / vs1) @ vc[:, h].abs()) + o ** 2 * (d2 / vs1 ** 2).sum(-1, keepdim=True)
             square[b, at] += (2.0 ** -8 * o + a * 2 * rel) ** 2
             ltol[b, at] = rel + (n + 64) * 2.0 ** -24 + lse[b, at].abs() * 2.0 ** -22
