@@ -120,7 +120,7 @@ def lib() -> ctypes.CDLL:
     L.proj_cache_append.restype = ctypes.c_int
     L.proj_paged_attention_q8.argtypes = L.proj_paged_attention.argtypes
     L.proj_paged_attention_q8.restype = ctypes.c_int
-    L.proj_paged_attention_q8_workspace_bytes.argtypes = [i32] * 5
+    L.proj_paged_attention_q8_workspace_bytes.argtypes = [i32] * 6
     L.proj_paged_attention_q8_workspace_bytes.restype = ctypes.c_size_t
     L.proj_cache_append_q8.argtypes = L.proj_cache_append.argtypes
     L.proj_cache_append_q8.restype = ctypes.c_int
@@ -602,9 +602,11 @@ def cache_copy_pages(pools: Sequence[torch.Tensor], src, dst, stream=None) -> No
 # (cache_resize, ...) move codes and scales alike, as pools (a uint8 pool that holds both will do: its views as
 # float8_e4m3fn and float32 are the tensors here).
 
-def paged_attention_q8_workspace_bytes(heads: int, kv_heads: int, k_dim: int, v_dim: int, latent: bool) -> int:
-    """Workspace bytes of proj_paged_attention_q8 (raises if the heads and columns are not supported)."""
-    n = int(lib().proj_paged_attention_q8_workspace_bytes(_i32(heads), _i32(kv_heads), _i32(k_dim), _i32(v_dim), int(latent)))
+def paged_attention_q8_workspace_bytes(batch: int, heads: int, kv_heads: int, k_dim: int, v_dim: int, latent: bool) -> int:
+    """Workspace bytes of proj_paged_attention_q8 (raises if the sizes are not supported)."""
+    n = int(lib().proj_paged_attention_q8_workspace_bytes(_i32(batch), _i32(heads), _i32(kv_heads), _i32(k_dim), _i32(v_dim), int(latent)))
+    if n == 0 and batch < 0:
+        raise ProjError(1, lib().proj_last_error_string().decode())
     if n == 0:  # the same heads and columns are refused of a bf16 cache, with the status that goes with the text
         paged_attention_workspace_bytes(heads, kv_heads, k_dim, v_dim, latent)
         raise ProjError(2, "unsupported heads and columns")
@@ -623,7 +625,7 @@ def paged_attention_q8(q: torch.Tensor, k_pages: torch.Tensor, v_pages: Optional
             batch, heads, k_dim = q.shape
             dv = v_pages.shape[3] if v_pages is not None else 512 if v_dim is None else v_dim
             if workspace is None:
-                workspace = _new(q, paged_attention_q8_workspace_bytes(heads, k_pages.shape[2], k_dim, dv, v_pages is None),
+                workspace = _new(q, paged_attention_q8_workspace_bytes(batch, heads, k_pages.shape[2], k_dim, dv, v_pages is None),
                                  torch.uint8, stream)
             if out is None:
                 out = _new(q, (batch, heads, dv), torch.bfloat16, stream)

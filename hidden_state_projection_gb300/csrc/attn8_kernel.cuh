@@ -16,18 +16,18 @@
 // Weights.  The scale of a token's values goes into its weight: w_t = p_t vs_t, in the softmax's own units
 // 2^(s_t + log2 vs_t - m).  w = Wh + Wl, Wh rounded to e4m3, the rest to e5m2: at most 2^-7 of w while w is at least
 // 2^-6 (the rest of a smaller one is half of 2^-9 or less, and e5m2 keeps an eighth of that), largest 448.  Two 8-bit
-// pieces have not the range of a bf16 number, so the reference point m follows the tiles in both directions: a tile whose
-// largest weight in some column is beyond 2^8.75, or below 2^-4, moves that column's m (largest weight to 2^3) and
+// pieces have not the range of a bf16 number, so the reference point m (a whole number) follows the tiles in both directions: a tile whose
+// largest weight in some column is beyond 2^8.75, or below 2^-4, moves that column's m (largest weight to 2^3 .. 2^4) and
 // rescales O^T; what a tile's rounding leaves out is small beside the largest weight of the tile and of the row,
 // whatever weights other tiles have (a first token with nearly all the weight before a long tail).  Normal scores of
 // variance 3 in 64 columns move a point in 2 tiles of 133 (in 54 with a window of 2^0.5 to 2^8.75).  Downwards m stops 30
 // below its highest point.  O^T is divided by l = sum (Wh + Wl)_t / vs_t, so the rounding that all of a row's weight has in
 // common cancels; lse takes the sum u of the unrounded weights.  Sums and statistics are fp32.
 //
-// Warps: four for the softmax (they also carry O^T out), a copy producer, an issuer of the scores, an issuer of the
-// products with the values, one that fetches the tiles' scales ahead; over a latent cache four more that split the next
-// part's queries while the last one is under way (of a grouped cache, few and short, the softmax warps do).  All
-// waits are at mbarriers and bounded.
+// Warps: four for the softmax of every 16 heads (they also carry O^T out), a copy producer, an issuer of the scores, an
+// issuer of the products with the values, one that fetches the tiles' scales ahead.  All waits are at mbarriers and
+// bounded.  The queries are split by a small kernel in front, into the images that the instructions read (split by every
+// CTA for itself they took 4 to 10 us: all wait for it, and code that runs once comes from L2 at 100 cycles per 128 bytes).
 #pragma once
 
 #include <cuda_fp16.h>
@@ -89,9 +89,6 @@ __device__ __forceinline__ float col(const float2 (&v)[P], int c) {
     return (c & 1) ? v[c >> 1].y : v[c >> 1].x;
 }
 
-// Barrier 2 of four warps that split queries.
-__device__ __forceinline__ void query_sync() { asm volatile("barrier.cta.sync.aligned 2, 128;" ::: "memory"); }
-
 template <int DK, int DV, bool SHARED, int N>
 struct Attn8Cfg {
     static constexpr int kW = DV >= 128 ? 128 : 64;           // columns of a box: its line in bytes
@@ -101,6 +98,7 @@ struct Attn8Cfg {
     static constexpr int kKG = SHARED ? 0 : 1;                // key groups of its own
     static constexpr int kGroups = kVG + kKG;
     static constexpr bool kRope = SHARED && DK > DV;          // 64 rotary columns
+    static constexpr int kX = kRope ? attn8_rope_slots(N) : 0;  // places of the rotary boxes
     static constexpr int kGroupBytes = kAttn8Tile * kW;
     static constexpr int kQRows = 2 * N;
     static constexpr int kQBytes = kQRows * DK;
@@ -109,11 +107,9 @@ struct Attn8Cfg {
     static constexpr int kCols = kOT * N + 4 * N;             // O^T, then two S^T
     static constexpr uint32_t kTmemCols = kCols <= 128 ? 128 : kCols <= 256 ? 256 : 512;
     static_assert(kCols <= 512, "tensor memory");
-    static constexpr int kThreads = attn8_threads(SHARED, N);
-    static constexpr int kSets = attn8_sets(N);               // sets of four softmax warps
+    static constexpr int kThreads = attn8_threads(N);
+    static constexpr int kSets = N / 16;                      // sets of four softmax warps, 16 heads each
     static constexpr int kSoft = 128 * kSets;                 // softmax threads
-    static constexpr int kHeads = N / kSets;                  // heads of a set
-    static constexpr int kC = kHeads / 4;                     // heads of a softmax thread
     static constexpr int kRoles = 4 * kSets;                  // the first warp behind the softmax
 };
 
@@ -121,25 +117,23 @@ struct Attn8Cfg {
 constexpr float kAttn8Up = 8.75f, kAttn8Low = -4.f, kAttn8Aim = 3.f, kAttn8Down = 30.f;
 
 template <int DK, int DV, bool SHARED, int N>
-__global__ void __launch_bounds__(attn8_threads(SHARED, N), attn8_ctas_per_sm(DK, SHARED, N))
+__global__ void __launch_bounds__(attn8_threads(N), attn8_ctas_per_sm(DK, SHARED, N))
     hsp_attn8_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v, const __grid_constant__ Attn8Args g) {
     using C = Attn8Cfg<DK, DV, SHARED, N>;
-    constexpr int T = kAttn8Tile, kC = C::kC;
+    constexpr int T = kAttn8Tile, kC = 4;  // (heads of a softmax thread)
     const AttnArgs &a = g.line;
-    extern __shared__ uint8_t smem_raw[];
-    const uint32_t raw = smem_u32(smem_raw);
-    uint8_t *smem = smem_raw + ((1024u - (raw & 1023u)) & 1023u);
+    extern __shared__ __align__(1024) uint8_t smem[];
     const uint32_t ring = smem_u32(smem);
-    uint8_t *const x_smem = smem + a.slots * C::kGroupBytes;            // the rotary boxes' two places
-    uint8_t *const q_smem = x_smem + (C::kRope ? 2 * kAttn8RopeBytes : 0);
+    uint8_t *const x_smem = smem + a.slots * C::kGroupBytes;            // the rotary boxes' places
+    uint8_t *const q_smem = x_smem + C::kX * kAttn8RopeBytes;
     uint8_t *const p_smem = q_smem + C::kQBytes;
-    float *const scales = reinterpret_cast<float *>(p_smem + C::kPBytes);  // [slots][3][T]: ks (times the scale), log2 vs, 1 / vs
-    float *const red = scales + kAttn8ScaleSlots * 3 * T;               // [4 warps][N]
-    float *const fac = red + 4 * N;                                     // [N]
-    float *const top = fac + N;                                         // [4 warps][N] highest reference point so far
-    float *const q_unit = top + 4 * N;                                  // [4][N] the unit of a part's queries, 2^e of the head
-    uint32_t *const seen = reinterpret_cast<uint32_t *>(q_unit + 4 * N);   // [2][8 warps], 16-byte aligned
-    uint64_t *const full = reinterpret_cast<uint64_t *>(seen + 16);
+    float *const red = reinterpret_cast<float *>(p_smem);               // [4 warps][N], where the weights are not under way
+    float *const fac = red + 4 * N;                                     // [N], likewise
+    float *const points = fac + N, *const bottom = points + N;          // [N], likewise
+    float *const scales = reinterpret_cast<float *>(p_smem + C::kPBytes);  // [slots][2][T]: ks (times the scale), log2 vs
+    uint32_t *const seen = reinterpret_cast<uint32_t *>(scales + kAttn8ScaleSlots * 2 * T);  // [2][16 warps], 16-byte aligned
+    uint8_t *const q_unit = reinterpret_cast<uint8_t *>(seen + 32);     // [4][N] the unit of a part's queries, 2^(e - 127) of the head
+    uint64_t *const full = reinterpret_cast<uint64_t *>(q_unit + 4 * N);
     uint64_t *const empty = full + a.slots;
     uint64_t *const x_full = empty + a.slots;                           // [2]
     uint64_t *const x_empty = x_full + 2;                               // [2]
@@ -156,9 +150,9 @@ __global__ void __launch_bounds__(attn8_threads(SHARED, N), attn8_ctas_per_sm(DK
     int *const ints = reinterpret_cast<int *>(sc_empty + kAttn8ScaleSlots);
     uint32_t *const tmem_slot = reinterpret_cast<uint32_t *>(ints);
     volatile int *const abort_flag = ints + 1;
-    int *const issued = ints + 2;                                       // groups and rotary boxes whose copies were issued
-    int *const place = ints + 4;
-    int *const warp_sum = ints + 7;                                     // [16]
+    int *const issued = ints + 2;                                       // groups, rotary boxes, queries whose copies were issued
+    int *const place = ints + 5;
+    int *const warp_sum = ints + 8;                                     // [20]
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int ht = blockIdx.x, cta = blockIdx.y;
@@ -185,7 +179,7 @@ __global__ void __launch_bounds__(attn8_threads(SHARED, N), attn8_ctas_per_sm(DK
         mbar_init(smem_u32(pv_done), 1);
         mbar_init(smem_u32(drained), 2);
         *abort_flag = 0;
-        issued[0] = issued[1] = 0;
+        issued[0] = issued[1] = issued[2] = 0;
         mbar_fence_init();
         tma_prefetch_map(&tmap_k);
         if (!SHARED || C::kRope) tma_prefetch_map(&tmap_v);
@@ -197,96 +191,13 @@ __global__ void __launch_bounds__(attn8_threads(SHARED, N), attn8_ctas_per_sm(DK
     tc_fence_before_sync();
     __syncthreads();
     tc_fence_after_sync();
-    griddep_wait();  // everything read below may come from the previous kernel
+    // What is read below comes from before the kernel that splits the queries, which has let this one start when all of
+    // that was complete; only its own images are still to come, and the copy producer waits for those.
 
     const AttnLine ln = attn_find_line<T, C::kThreads>(a, cta, place, warp_sum);
     const uint32_t tmem = *tmem_slot;
     const uint32_t tmem_s = tmem + C::kOT * N;
     auto await = [&](uint64_t *bar, uint32_t phase) { return attn_wait(smem_u32(bar), phase & 1u, a.wait_limit_ns, abort_flag); };
-
-    // The queries of part `seg` in two pieces, by kQW warps (w4: which).  A head to a group of lanes, eight columns to a
-    // lane and round; the head's largest number decides its unit.
-    auto split_queries = [&](const AttnSegment &sg, uint32_t seg, int w4) {
-        constexpr int kQW = SHARED ? 4 : 4 * C::kSets;
-        constexpr int kLanes = DK / 8 < 32 ? DK / 8 : 32, kPer = 32 / kLanes, kRounds = (DK / 8 + kLanes - 1) / kLanes;
-        const int sub = lane / kLanes, at = lane % kLanes;
-        const int nheads = min(N, a.group - ht * N);
-        const __nv_bfloat16 *q = static_cast<const __nv_bfloat16 *>(g.q) + sg.b * g.q_row + (sg.kv * a.group + ht * N) * g.q_head;
-        auto fetch = [&](int h, uint4 (&v)[kRounds]) {
-#pragma unroll
-            for (int r = 0; r < kRounds; ++r) {
-                const int c = (r * kLanes + at) * 8;
-                v[r] = make_uint4(0, 0, 0, 0);
-                if (h < nheads && c < DK) v[r] = *reinterpret_cast<const uint4 *>(q + h * g.q_head + c);
-            }
-        };
-        uint4 ahead[kRounds];
-        int h = w4 * kPer + sub;
-        fetch(h, ahead);
-        await(q_free, seg ^ 1u);  // the last part's are done with (given up: the warps still meet at their barrier)
-        for (; h - sub < N; h += kQW * kPer) {
-            uint4 v[kRounds];
-#pragma unroll
-            for (int r = 0; r < kRounds; ++r) v[r] = ahead[r];
-            fetch(h + kQW * kPer, ahead);
-            float amax = 0.f;
-#pragma unroll
-            for (int r = 0; r < kRounds; ++r) {
-                const uint32_t w[4] = {v[r].x, v[r].y, v[r].z, v[r].w};
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float lo = fabsf(__uint_as_float(w[e] << 16)), hi = fabsf(__uint_as_float(w[e] & 0xffff0000u));
-                    if (lo <= 3.0e38f) amax = fmaxf(amax, lo);  // (NaN and infinities make the head's scores NaN)
-                    if (hi <= 3.0e38f) amax = fmaxf(amax, hi);
-                }
-            }
-#pragma unroll
-            for (int d = kLanes / 2; d > 0; d >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, d));
-            // 2^-e amax in 224 .. 448: a normal amax, so e is above -135; the unit of a smaller one is 2^-126
-            const uint32_t u = __float_as_uint(amax);
-            const int e2 = max(-126, min(126, static_cast<int>(u >> 23) - 127 - 8 + ((u & 0x7fffffu) > 0x600000u ? 1 : 0)));
-            const float inv = two_to(-e2);
-            // row of the head among the instruction's columns: a softmax thread has columns 8 j + 2 c + e of its set, c
-            // its place in four, of every step j: those are the set's heads c kC + 2 j + e
-            const int in = h % C::kHeads, c4 = in / kC, in4 = in % kC;
-            const int row = h - in + 8 * (in4 >> 1) + 2 * c4 + (in4 & 1);
-#pragma unroll
-            for (int r = 0; r < kRounds; ++r) {
-                const int c = (r * kLanes + at) * 8;
-                if (c >= DK) continue;
-                const uint32_t w[4] = {v[r].x, v[r].y, v[r].z, v[r].w};
-                uint32_t hi[4], lo[4];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float x0 = __uint_as_float(w[e] << 16) * inv, x1 = __uint_as_float(w[e] & 0xffff0000u) * inv;
-                    const float y0 = fabsf(x0) <= kQ8Top ? x0 : __uint_as_float(0x7fc00000u), y1 = fabsf(x1) <= kQ8Top ? x1 : __uint_as_float(0x7fc00000u);
-                    const __half2 x = __floats2half2_rn(y0, y1);
-                    hi[e] = half2_to_e4m3x2(x);
-                    lo[e] = half2_to_e4m3x2(__hmul2(__hsub2(x, e4m3x2_to_half2(hi[e])), __float2half2_rn(16.f)));
-                }
-                const uint2 h8 = make_uint2(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16), l8 = make_uint2(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16);
-                uint8_t *to;
-                int line;
-                if (C::kRope && c >= DV) {
-                    to = q_smem + C::kQRows * DV + row * 64 + swizzled<64>(row, (c - DV) >> 4) + (c & 8);
-                    line = 64;
-                } else {
-                    to = q_smem + c / C::kW * (C::kQRows * C::kW) + row * C::kW + swizzled<C::kW>(row, c % C::kW >> 4) + (c & 8);
-                    line = C::kW;
-                }
-                *reinterpret_cast<uint2 *>(to) = h8;
-                *reinterpret_cast<uint2 *>(to + N * line) = l8;  // (N rows on, a multiple of 8: the same swizzle)
-            }
-            if (at == 0) q_unit[(seg & 3u) * N + h] = two_to(e2);
-        }
-        fence_proxy_async_smem();
-        if (SHARED) query_sync();
-        else softmax_sync<C::kSoft>();
-        if (w4 == 0 && lane == 0) {
-            mbar_arrive(smem_u32(&unit_full[seg & 3u]));
-            mbar_arrive(smem_u32(q_full));
-        }
-    };
 
     if (warp == C::kRoles) {
         // ---------------- copy producer: one thread reads the table a tile ahead and issues ----------------
@@ -296,6 +207,7 @@ __global__ void __launch_bounds__(attn8_threads(SHARED, N), attn8_ctas_per_sm(DK
             AttnSegment sg;
             RingPos rp, xp;
             int ng = 0;
+            uint32_t seg = 0;
             const int pbox = min(T, 1 << a.page_shift);  // tokens per box
             const int boxes = T / pbox;                  // pages that meet a tile (1 to 8)
             bool alive = true;
@@ -307,6 +219,19 @@ __global__ void __launch_bounds__(attn8_threads(SHARED, N), attn8_ctas_per_sm(DK
                     const int p0 = static_cast<int>((static_cast<int64_t>(tile) * T) >> a.page_shift);
 #pragma unroll
                     for (int e = 0; e < 8; ++e) id[e] = (e < boxes && p0 + e < pages) ? tbl[p0 + e] : 0;
+                };
+                // the part's queries, behind its first tile, which does not have to wait for the last part's (nor the first
+                // one for the kernel that makes the images)
+                auto queries = [&]() {
+                    alive = await(q_free, seg ^ 1u);
+                    if (!alive) return;
+                    if (seg == 0) griddep_wait();
+                    const uint8_t *from = g.images + ((static_cast<int64_t>(sg.b) * a.kv_heads + sg.kv) * gridDim.x + ht) * attn8_image_bytes(DK, N);
+                    mbar_arrive_expect_tx(smem_u32(q_full), C::kQBytes);
+                    bulk_load(smem_u32(q_smem), from, C::kQBytes, smem_u32(q_full));
+                    mbar_arrive_expect_tx(smem_u32(&unit_full[seg & 3u]), N);
+                    bulk_load(smem_u32(q_unit) + (seg & 3u) * N, from + C::kQBytes, N, smem_u32(&unit_full[seg & 3u]));
+                    issued[2] = static_cast<int>(++seg);
                 };
                 int next[8];
                 ids_of(sg.t0, next);
@@ -351,10 +276,12 @@ __global__ void __launch_bounds__(attn8_threads(SHARED, N), attn8_ctas_per_sm(DK
                             load(&tmap_v, 0, 64, smem_u32(x_smem) + xp.slot * kAttn8RopeBytes, smem_u32(&x_full[xp.slot]));
                             issued[1] = i + 1;
                         }
-                        xp.next(2);
+                        xp.next(C::kX);
                     }
+                    if (k == 0 && alive) queries();
                 }
             }
+            if (seg == 0) griddep_wait();  // (every CTA: the next kernel but one may write the images anew)
         }
         __syncwarp();
     } else if (warp == C::kRoles + 1) {
@@ -375,7 +302,7 @@ __global__ void __launch_bounds__(attn8_threads(SHARED, N), attn8_ctas_per_sm(DK
                     if (!(alive = await(&s_free[sp.slot], sp.phase ^ 1u))) break;
                     const uint32_t d = tmem_s + sp.slot * C::kQRows;
                     constexpr int kGroupsK = SHARED ? C::kVG : C::kKG;
-#pragma unroll
+#pragma unroll 1
                     for (int gr = 0; gr < kGroupsK; ++gr) {
                         if (alive) alive = await(&full[rp.slot], rp.phase);
                         if (!alive) break;
@@ -397,7 +324,7 @@ __global__ void __launch_bounds__(attn8_threads(SHARED, N), attn8_ctas_per_sm(DK
 #pragma unroll
                         for (int e = 0; e < 2; ++e) umma_f8(d, kd + e * 2, xd + e * 2, kDesc, 1u);
                         umma_commit(smem_u32(&x_empty[xp.slot]));
-                        xp.next(2);
+                        xp.next(C::kX);
                     }
                     umma_commit(smem_u32(&s_full[sp.slot]));
                     sp.next(2);
@@ -430,7 +357,7 @@ __global__ void __launch_bounds__(attn8_threads(SHARED, N), attn8_ctas_per_sm(DK
                         if (!alive) break;
                         tc_fence_after_sync();
                     }
-#pragma unroll
+#pragma unroll 1
                     for (int jt = 0; jt < C::kOT; ++jt) {
                         const uint64_t vd = umma_desc_lines<C::kW>(ring + rp.slot * C::kGroupBytes);
 #pragma unroll
@@ -487,13 +414,12 @@ __global__ void __launch_bounds__(attn8_threads(SHARED, N), attn8_ctas_per_sm(DK
                 alive = await(&sc_empty[slot], static_cast<uint32_t>(i / kAttn8ScaleSlots) ^ 1u);
                 alive = __all_sync(0xffffffffu, alive);
                 if (!alive) break;
-                float *to = scales + slot * 3 * T;
+                float *to = scales + slot * 2 * T;
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     const float v = fminf(fmaxf(vv[0][e], two_to(kQ8MinExp)), two_to(kQ8MaxExp));
                     to[e * 32 + lane] = kk[0][e] * a.scale_log2;
-                    to[T + e * 32 + lane] = log2f(v);
-                    to[2 * T + e * 32 + lane] = 1.f / v;
+                    to[T + e * 32 + lane] = __log2f(v);
                     kk[0][e] = kk[1][e];
                     vv[0][e] = vv[1][e];
                 }
@@ -501,11 +427,6 @@ __global__ void __launch_bounds__(attn8_threads(SHARED, N), attn8_ctas_per_sm(DK
                 if (k + 2 < sg.n) fetch(sg.t0 + k + 2, kk[1], vv[1]);
             }
         }
-    } else if (SHARED && warp >= C::kRoles + 4) {
-        // ---------------- the queries of the next part, while the last one is under way ----------------
-        AttnWalk walk(ln);
-        AttnSegment sg;
-        for (uint32_t seg = 0; attn_next_segment<T>(a, ln, walk, sg); ++seg) split_queries(sg, seg, warp - C::kRoles - 4);
     } else {
         // ---------------- softmax warps ----------------
         AttnWalk walk(ln);
@@ -519,7 +440,7 @@ __global__ void __launch_bounds__(attn8_threads(SHARED, N), attn8_ctas_per_sm(DK
         const int wq = warp & 3, set = warp >> 2;
         const int r0 = wq * 32 + (lane >> 2);                  // this thread's token rows: r0 + 0, 8, 16, 24
         const int c4 = lane & 3;
-        const int h0 = set * C::kHeads + c4 * kC;              // its heads: h0 + 0 .. kC - 1
+        const int h0 = set * 16 + c4 * kC;                     // its heads: h0 + 0 .. kC - 1
         const uint32_t lane_base = static_cast<uint32_t>(wq * 32) << 16;
         if (a.split && ht == 0 && tid == 96) {
             AttnEntry e;
@@ -532,59 +453,60 @@ __global__ void __launch_bounds__(attn8_threads(SHARED, N), attn8_ctas_per_sm(DK
 #pragma unroll
         for (int c = 0; c < kC; ++c)
             if (h0 + c >= nheads) unused |= 1u << c;
-        bool more = attn_next_segment<T>(a, ln, walk, sg);
-        if (!SHARED && more) split_queries(sg, 0, warp);
-        while (more) {
+        while (attn_next_segment<T>(a, ln, walk, sg)) {
             const bool begins = sg.t0 == 0, ends = sg.t0 + sg.n == sg.tiles;
             float m[kC];             // reference points
             float2 l[kC / 2], u[kC / 2];  // sums of the rounded and the unrounded weights
-            uint32_t lowest = unused;  // columns whose reference point goes no further down
+            uint32_t lowest = unused;     // columns whose reference point goes no further down
+            float mine = 0.f, peak = 0.f;  // column tid's point, and its highest
 #pragma unroll
             for (int e = 0; e < kC; ++e) m[e] = 0.f;
 #pragma unroll
             for (int j = 0; j < kC / 2; ++j) l[j] = u[j] = make_float2(0.f, 0.f);
             await(&unit_full[seg & 3u], seg >> 2);
-            const float *unit = q_unit + (seg & 3u) * N + h0;
+            float2 unit[kC / 2];     // of the heads' queries
+#pragma unroll
+            for (int j = 0; j < kC / 2; ++j) {
+                const uint32_t e = *reinterpret_cast<const uint16_t *>(q_unit + (seg & 3u) * N + h0 + 2 * j);
+                unit[j] = make_float2(__uint_as_float((e & 0xffu) << 23), __uint_as_float(e >> 8 << 23));
+            }
             ++seg;
             for (int k = 0; k < sg.n; ++k, ++i) {
                 const int64_t tok0 = static_cast<int64_t>(sg.t0 + k) * T;
                 const int valid = static_cast<int>(min(static_cast<int64_t>(T), sg.len - tok0));
-                const int slot = i % kAttn8ScaleSlots;
-                float ksc[4], vlog[4], vinv[4];
-                await(&sc_full[slot], static_cast<uint32_t>(i / kAttn8ScaleSlots));
+                const float *const sc = scales + i % kAttn8ScaleSlots * 2 * T + r0;
+                float ksc[4], vlog[4];
+                await(&sc_full[i % kAttn8ScaleSlots], static_cast<uint32_t>(i / kAttn8ScaleSlots));
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
-                    ksc[r] = scales[slot * 3 * T + r0 + 8 * r];
-                    vlog[r] = scales[slot * 3 * T + T + r0 + 8 * r];
-                    vinv[r] = scales[slot * 3 * T + 2 * T + r0 + 8 * r];
+                    ksc[r] = sc[8 * r];
+                    vlog[r] = sc[T + 8 * r];
                 }
-                mbar_arrive(smem_u32(&sc_empty[slot]));
+                mbar_arrive(smem_u32(&sc_empty[i % kAttn8ScaleSlots]));
                 await(&s_full[i & 1], static_cast<uint32_t>(i >> 1));
                 tc_fence_after_sync();
                 // s[r][j]: row r0 + 8 r, heads h0 + 2 j and + 1, in log2 units with the values' scale
                 float2 s[4][kC / 2];
+                {
+                    float hi[2][8], lo[2][8];
 #pragma unroll
-                for (int hf = 0; hf < 2; ++hf) {
-                    float hi[kC * 2], lo[kC * 2];
-                    const uint32_t from = tmem_s + (i & 1) * C::kQRows + set * C::kHeads + lane_base + (static_cast<uint32_t>(hf * 16) << 16);
-                    tmem_ld_frag<kC / 2>(from, hi);
-                    tmem_ld_frag<kC / 2>(from + N, lo);
+                    for (int hf = 0; hf < 2; ++hf) {
+                        const uint32_t from = tmem_s + (i & 1) * C::kQRows + set * 16 + lane_base + (static_cast<uint32_t>(hf * 16) << 16);
+                        tmem_ld_frag<2>(from, hi[hf]);
+                        tmem_ld_frag<2>(from + N, lo[hf]);
+                    }
                     tmem_wait_ld();
-#pragma unroll
-                    for (int j = 0; j < kC / 2; ++j)
-#pragma unroll
-                        for (int e = 0; e < 2; ++e)
-                            s[2 * hf + e][j] = fma2(make_float2(lo[4 * j + 2 * e], lo[4 * j + 2 * e + 1]), make_float2(0.0625f, 0.0625f),
-                                                    make_float2(hi[4 * j + 2 * e], hi[4 * j + 2 * e + 1]));
-                }
-                tc_fence_before_sync();
-                mbar_arrive(smem_u32(&s_free[i & 1]));
-#pragma unroll
-                for (int j = 0; j < kC / 2; ++j) {
-                    const float2 q2 = *reinterpret_cast<const float2 *>(unit + 2 * j);
+                    tc_fence_before_sync();
+                    mbar_arrive(smem_u32(&s_free[i & 1]));
 #pragma unroll
                     for (int r = 0; r < 4; ++r)
-                        s[r][j] = fma2(mul2(s[r][j], q2), make_float2(ksc[r], ksc[r]), make_float2(vlog[r], vlog[r]));
+#pragma unroll
+                        for (int j = 0; j < kC / 2; ++j) {
+                            const int at = 4 * j + 2 * (r & 1);
+                            const float2 x = fma2(make_float2(lo[r >> 1][at], lo[r >> 1][at + 1]), make_float2(0.0625f, 0.0625f),
+                                                  make_float2(hi[r >> 1][at], hi[r >> 1][at + 1]));
+                            s[r][j] = fma2(mul2(x, unit[j]), make_float2(ksc[r], ksc[r]), make_float2(vlog[r], vlog[r]));
+                        }
                 }
                 if (valid < T) {
 #pragma unroll
@@ -594,78 +516,69 @@ __global__ void __launch_bounds__(attn8_threads(SHARED, N), attn8_ctas_per_sm(DK
                             for (int j = 0; j < kC / 2; ++j) s[r][j] = make_float2(-INFINITY, -INFINITY);
                         }
                 }
+                float mx[kC];
+#pragma unroll
+                for (int c = 0; c < kC; ++c) mx[c] = fmaxf(fmaxf(col(s[0], c), col(s[1], c)), fmaxf(col(s[2], c), col(s[3], c)));
                 // columns that exceed the window, and those that some token reaches from below
                 bool over = k == 0;
                 uint32_t reached = lowest;
 #pragma unroll
                 for (int c = 0; c < kC; ++c) {
-                    const float most = fmaxf(fmaxf(col(s[0], c), col(s[1], c)), fmaxf(col(s[2], c), col(s[3], c))) - m[c];
+                    const float most = mx[c] - m[c];
                     over |= most > kAttn8Up && !((unused >> c) & 1u);
                     if (most >= kAttn8Low) reached |= 1u << c;
                 }
                 {
                     // kC bits for each of the four places, the warps of a set together
                     const uint32_t all = __reduce_or_sync(0xffffffffu, reached << (c4 * kC));
-                    if (lane == 0) seen[(i & 1) * 8 + warp] = all;
+                    if (lane == 0) seen[(i & 1) * 16 + warp] = all;
                 }
                 bool move = softmax_any<C::kSoft>(over);
 #pragma unroll
                 for (int w = 0; w < C::kSets; ++w) {
-                    constexpr uint32_t kAll = kC * 4 >= 32 ? 0xffffffffu : (1u << (kC * 4 & 31)) - 1u;
-                    const uint4 x = *reinterpret_cast<const uint4 *>(seen + (i & 1) * 8 + w * 4);
-                    move |= (x.x | x.y | x.z | x.w) != kAll;
+                    const uint4 x = *reinterpret_cast<const uint4 *>(seen + (i & 1) * 16 + w * 4);
+                    move |= (x.x | x.y | x.z | x.w) != 0xffffu;
                 }
                 if (move) {
-                    // column maxima over the tile's tokens, new reference points, O^T rescaled
-                    float mx[kC];
+                    // column maxima over the tile's tokens, new reference points (a column per thread), O^T rescaled
+                    if (i > 0) await(pv_done, static_cast<uint32_t>(i - 1));  // (red, fac and points lie where the weights did)
+                    tc_fence_after_sync();
 #pragma unroll
-                    for (int c = 0; c < kC; ++c) {
-                        float t = fmaxf(fmaxf(col(s[0], c), col(s[1], c)), fmaxf(col(s[2], c), col(s[3], c)));
-                        t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 4));
-                        t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 8));
-                        t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 16));
-                        mx[c] = t;
-                    }
+                    for (int c = 0; c < kC; ++c)
+#pragma unroll
+                        for (int d = 4; d < 32; d <<= 1) mx[c] = fmaxf(mx[c], __shfl_xor_sync(0xffffffffu, mx[c], d));
                     if (lane < 4) {
 #pragma unroll
                         for (int c = 0; c < kC; c += 4)
                             *reinterpret_cast<float4 *>(red + wq * N + h0 + c) = make_float4(mx[c], mx[c + 1], mx[c + 2], mx[c + 3]);
                     }
                     softmax_sync<C::kSoft>();
+                    if (tid < N) {
+                        const float t = fmaxf(fmaxf(red[tid], red[N + tid]), fmaxf(red[2 * N + tid], red[3 * N + tid]));
+                        const float most = t - mine;
+                        float n = mine;
+                        if (k == 0) n = t > -INFINITY ? floorf(t - kAttn8Aim) : 0.f;  // (0: nothing but NaN or minus infinity)
+                        else if (most > kAttn8Up || !(most >= kAttn8Low)) n = fmaxf(floorf(t - kAttn8Aim), peak - kAttn8Down);
+                        peak = k == 0 ? n : fmaxf(peak, n);
+                        fac[tid] = k == 0 ? 0.f : fast_exp2(mine - n);
+                        points[tid] = n;
+                        bottom[tid] = n == peak - kAttn8Down ? 1.f : 0.f;
+                        mine = n;
+                    }
+                    softmax_sync<C::kSoft>();
                     lowest = unused;
 #pragma unroll
-                    for (int c = 0; c < kC; ++c) {
-                        const int at = h0 + c;
-                        const float t = fmaxf(fmaxf(red[at], red[N + at]), fmaxf(red[2 * N + at], red[3 * N + at]));
-                        const float most = t - m[c];
-                        float peak = k == 0 ? -INFINITY : top[wq * N + at];
-                        float n = m[c];
-                        if (k == 0 || most > kAttn8Up || most < kAttn8Low) n = t - kAttn8Aim;
-                        if (k == 0 && !(n > -INFINITY)) n = 0.f;  // (nothing but NaN or minus infinity in the first tile)
-                        if (n <= peak - kAttn8Down) n = peak - kAttn8Down;
-                        if (n == peak - kAttn8Down) lowest |= 1u << c;
-                        peak = fmaxf(peak, n);
-                        const float f = k == 0 ? 0.f : fast_exp2(m[c] - n);
-                        m[c] = n;
-                        float2 &lc = l[c >> 1], &uc = u[c >> 1];
-                        if ((c & 1) == 0) {
-                            lc.x *= f;
-                            uc.x *= f;
-                        } else {
-                            lc.y *= f;
-                            uc.y *= f;
-                        }
-                        __syncwarp();  // every lane has read its columns' peaks
-                        if (lane < 4) {
-                            top[wq * N + at] = peak;
-                            if (wq == 0) fac[at] = f;
-                        }
+                    for (int j = 0; j < kC / 2; ++j) {
+                        const float2 f = *reinterpret_cast<const float2 *>(fac + h0 + 2 * j), n = *reinterpret_cast<const float2 *>(points + h0 + 2 * j);
+                        const float2 d = *reinterpret_cast<const float2 *>(bottom + h0 + 2 * j);
+                        l[j] = mul2(l[j], f);
+                        u[j] = mul2(u[j], f);
+                        m[2 * j] = n.x;
+                        m[2 * j + 1] = n.y;
+                        if (d.x != 0.f) lowest |= 1u << 2 * j;
+                        if (d.y != 0.f) lowest |= 2u << 2 * j;
                     }
-                    __syncwarp();
                     if (k > 0) {
-                        await(pv_done, static_cast<uint32_t>(i - 1));
-                        tc_fence_after_sync();
-                        softmax_sync<C::kSoft>();
 #pragma unroll 1
                         for (int c0 = set * 16; c0 < C::kOT * N; c0 += C::kSets * 16) {
                             float o[16];
@@ -677,6 +590,7 @@ __global__ void __launch_bounds__(attn8_threads(SHARED, N), attn8_ctas_per_sm(DK
                         }
                         tmem_wait_st();
                     }
+                    softmax_sync<C::kSoft>();  // (before weights take their place)
                 }
                 if (valid < T) {
                     // the last tile: what lies behind the sequence must not reach the product (0 x NaN).  Its last
@@ -694,55 +608,43 @@ __global__ void __launch_bounds__(attn8_threads(SHARED, N), attn8_ctas_per_sm(DK
                     }
                 }
                 // the weights in two pieces, and their sums
-                uint32_t wh[4][kC / 4], wl[4][kC / 4];
+                uint32_t wh[4], wl[4];
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
-                    const float2 inv = make_float2(vinv[r], vinv[r]);
+                    const float v = fast_exp2(-vlog[r]);  // 1 / vs
+                    uint32_t h8[2], l8[2];
 #pragma unroll
                     for (int j = 0; j < kC / 2; ++j) {
                         float2 p = s[r][j];
                         add2(p, make_float2(-m[2 * j], -m[2 * j + 1]));
                         p = make_float2(fast_exp2(p.x), fast_exp2(p.y));
                         const __half2 p16 = __floats2half2_rn(p.x, p.y);
-                        const uint32_t h8 = half2_to_e4m3x2(p16);
-                        const __half2 h16 = e4m3x2_to_half2(h8);
-                        const uint32_t l8 = half2_to_e5m2x2(__hsub2(p16, h16));
-                        const float2 w = __half22float2(__hadd2(h16, e5m2x2_to_half2(l8)));
-                        if ((j & 1) == 0) {
-                            wh[r][j >> 1] = h8;
-                            wl[r][j >> 1] = l8;
-                        } else {
-                            wh[r][j >> 1] |= h8 << 16;
-                            wl[r][j >> 1] |= l8 << 16;
-                        }
-                        u[j] = fma2(p, inv, u[j]);
-                        l[j] = fma2(w, inv, l[j]);
+                        h8[j] = half2_to_e4m3x2(p16);
+                        const __half2 h16 = e4m3x2_to_half2(h8[j]);
+                        l8[j] = half2_to_e5m2x2(__hsub2(p16, h16));
+                        const float2 w = __half22float2(__hadd2(h16, e5m2x2_to_half2(l8[j])));
+                        u[j] = fma2(p, make_float2(v, v), u[j]);
+                        l[j] = fma2(w, make_float2(v, v), l[j]);
                     }
+                    wh[r] = __byte_perm(h8[0], h8[1], 0x5410);
+                    wl[r] = __byte_perm(l8[0], l8[1], 0x5410);
                 }
                 // the weights of tile i - 1 have been read before these replace them
                 if (i > 0) await(pv_done, static_cast<uint32_t>(i - 1));
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
                     const int row = r0 + 8 * r;
-                    uint8_t *line = p_smem + row * C::kPLine;
-                    uint8_t *hi = line + swizzled<C::kPLine>(row, h0 >> 4) + (h0 & 15), *lo = line + swizzled<C::kPLine>(row, (N + h0) >> 4) + (h0 & 15);
-                    if (kC == 8) {
-                        *reinterpret_cast<uint2 *>(hi) = make_uint2(wh[r][0], wh[r][1 % (kC / 4)]);
-                        *reinterpret_cast<uint2 *>(lo) = make_uint2(wl[r][0], wl[r][1 % (kC / 4)]);
-                    } else {
-                        *reinterpret_cast<uint32_t *>(hi) = wh[r][0];
-                        *reinterpret_cast<uint32_t *>(lo) = wl[r][0];
-                    }
+                    uint8_t *line = p_smem + row * C::kPLine + c4 * 4;
+                    *reinterpret_cast<uint32_t *>(line + swizzled<C::kPLine>(row, set)) = wh[r];
+                    *reinterpret_cast<uint32_t *>(line + swizzled<C::kPLine>(row, C::kSets + set)) = wl[r];
                 }
                 fence_proxy_async_smem();
                 tc_fence_before_sync();
                 mbar_arrive(smem_u32(p_full));
             }
-            // (the next part's scores are under way while this one leaves)
-            AttnSegment after;
-            more = attn_next_segment<T>(a, ln, walk, after);
-            if (!SHARED && more) split_queries(after, seg, warp);
             // ---- the part is done: l (and u) over the tokens, then O^T out of tensor memory ----
+            await(pv_done, static_cast<uint32_t>(i - 1));  // (red and fac lie where the weights did)
+            tc_fence_after_sync();
             auto over_tokens = [&](float2 (&v)[kC / 2]) {  // a warp's sums to `red`
 #pragma unroll
                 for (int j = 0; j < kC / 2; ++j)
@@ -797,15 +699,12 @@ __global__ void __launch_bounds__(attn8_threads(SHARED, N), attn8_ctas_per_sm(DK
                 e.slot = slot;
                 a.entries[cta] = e;
             }
-            await(pv_done, static_cast<uint32_t>(i - 1));
-            tc_fence_after_sync();
             softmax_sync<C::kSoft>();
             const bool good = *abort_flag == 0;
             const int64_t obase = (static_cast<int64_t>(sg.b) * all_heads + sg.kv * a.group + head0) * DV;
             attn_store_part<N, DV, C::kMV, C::kOT, C::kSets>(tmem, wq, lane, good, whole, nheads, fac, out + obase, part, set);
             tc_fence_before_sync();
             softmax_sync<C::kSoft>();  // red and fac are free again
-            sg = after;
         }
         if (tid < 128) attn_store_empty<DV>(a, cta, head0, nheads);
     }
@@ -827,8 +726,13 @@ __global__ void __launch_bounds__(attn8_threads(SHARED, N), attn8_ctas_per_sm(DK
         };
         for (int j = max(0, n - a.slots); j < n; ++j)
             if (j / C::kGroups != a.skip_tile) land(&full[j % a.slots], j / a.slots);
-        for (int j = max(0, nx - 2); j < nx; ++j)
-            if (j != a.skip_tile) land(&x_full[j & 1], j >> 1);
+        if (issued[2] > 0) {
+            land(q_full, issued[2] - 1);
+            land(&unit_full[(issued[2] - 1) & 3], (issued[2] - 1) >> 2);
+        }
+        if (C::kRope)
+            for (int j = max(0, nx - C::kX); j < nx; ++j)
+                if (j != a.skip_tile) land(&x_full[j % max(C::kX, 1)], j / max(C::kX, 1));
     }
     if (warp == C::kRoles + 1) {
         tc_fence_after_sync();

@@ -1,4 +1,5 @@
-// attn8_launch.cuh -- launch of one instance of the attention kernel over a cache in 8 bits, and its join.
+// attn8_launch.cuh -- launch of one instance of the attention kernel over a cache in 8 bits, the kernel that splits its
+// queries in front and its join behind it.
 #pragma once
 
 #include <atomic>
@@ -23,6 +24,8 @@ cudaError_t launch_attn8_variant(const Attn8LaunchReq &r) {
         if (e != cudaSuccess) return e;
         configured[dev].store(current_context_id(), std::memory_order_release);
     }
+    e = launch_attn8_queries(r);
+    if (e != cudaSuccess) return e;
     cudaLaunchAttribute attrs[1];
     unsigned n = 0;
     if (r.pdl) {
@@ -32,7 +35,7 @@ cudaError_t launch_attn8_variant(const Attn8LaunchReq &r) {
     }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(r.head_tiles), static_cast<unsigned>(r.args.line.ctas), 1);
-    cfg.blockDim = dim3(attn8_threads(SHARED, N), 1, 1);
+    cfg.blockDim = dim3(attn8_threads(N), 1, 1);
     cfg.dynamicSmemBytes = static_cast<size_t>(r.smem_bytes);
     cfg.stream = r.stream;
     cfg.attrs = attrs;

@@ -108,6 +108,11 @@ size_t attn_workspace(const AttnShape &s, int ctas) {
            static_cast<size_t>(s.head_tiles) * ctas * 2 * hsp::attn_part(s.VB * 64, s.N) * 4;
 }
 
+// Of a cache in 8 bits, in front: the queries' images.
+size_t attn8_images(const AttnShape &s, int batch, int kv_heads, int k_dim) {
+    return up256(static_cast<size_t>(batch) * kv_heads * s.head_tiles * hsp::attn8_image_bytes(k_dim, s.N));
+}
+
 proj_status check_kv(const proj_kv_pages *kv) {
     if (!kv || !kv->k) return api_fail(PROJ_ERR_INVALID_ARG, "kv and kv->k must not be NULL");
     if (!aligned(kv->k, 16) || !aligned(kv->v, 16)) return api_fail(PROJ_ERR_MISALIGNED, "k and v must be 16-byte aligned");
@@ -668,10 +673,15 @@ proj_status proj_cache_read_q8(const proj_kv_pages_q8 *kv, const proj_page_index
     return hsp::api_ok();
 }
 
-size_t proj_paged_attention_q8_workspace_bytes(int32_t heads, int32_t kv_heads, int32_t k_dim, int32_t v_dim, int32_t latent) {
+size_t proj_paged_attention_q8_workspace_bytes(int32_t batch, int32_t heads, int32_t kv_heads, int32_t k_dim, int32_t v_dim,
+                                               int32_t latent) {
     AttnShape s;
     if (attn8_shape(heads, kv_heads, k_dim, v_dim, latent != 0, &s) != PROJ_OK) return 0;
-    return attn_workspace(s, attn_ctas(s, hsp::api_plan_sms()));
+    if (batch < 0) {
+        api_fail(PROJ_ERR_INVALID_ARG, "batch=%d is negative", batch);
+        return 0;
+    }
+    return attn8_images(s, batch, kv_heads, k_dim) + attn_workspace(s, attn_ctas(s, hsp::api_plan_sms()));
 }
 
 proj_status proj_paged_attention_q8(const void *q, int64_t q_row_stride, int64_t q_head_stride, const proj_kv_pages_q8 *kv,
@@ -692,7 +702,9 @@ proj_status proj_paged_attention_q8(const void *q, int64_t q_row_stride, int64_t
     if ((st = hsp::api_device(&dev)) != PROJ_OK) return st;
     const int ctas = attn_ctas(s, dev.sms);
     const bool split = static_cast<int64_t>(index->max_pages) * index->page_size > PROJ_UNCUT_TOKENS;
-    if (split && (st = check_workspace(workspace, workspace_bytes, attn_workspace(s, ctas))) != PROJ_OK) return st;
+    const size_t images = attn8_images(s, batch, kv->kv_heads, kv->k_dim);
+    if (images >= (size_t(1) << 40)) return api_fail(PROJ_ERR_UNSUPPORTED_SHAPE, "batch=%d of %d heads is too large", batch, heads);
+    if ((st = check_workspace(workspace, workspace_bytes, images + (split ? attn_workspace(s, ctas) : 0))) != PROJ_OK) return st;
     hsp::Attn8LaunchReq r{};
     const int width = kv->v_dim >= 128 ? 128 : 64;
     if ((st = encode_codes(kv->k, index, kv->kv_heads, kv->v ? kv->k_dim : kv->v_dim, width, kv->k_page_stride, kv->k_token_stride,
@@ -718,10 +730,11 @@ proj_status proj_paged_attention_q8(const void *q, int64_t q_row_stride, int64_t
     r.pdl = opt.pdl;
     r.sms = dev.sms;
     r.stream = reinterpret_cast<cudaStream_t>(stream);
-    attention_line(index, rows, batch, heads, kv->kv_heads, s, ctas, split, scale_log2, out, lse, workspace, opt, dev, &r.args.line);
-    r.args.q = q;
-    r.args.q_row = batch > 1 ? q_row_stride : 0;
-    r.args.q_head = heads > 1 ? q_head_stride : 0;
+    attention_line(index, rows, batch, heads, kv->kv_heads, s, ctas, split, scale_log2, out, lse, static_cast<char *>(workspace) + images, opt,
+                   dev, &r.args.line);
+    r.queries = {q, batch > 1 ? q_row_stride : 0, heads > 1 ? q_head_stride : 0, static_cast<uint8_t *>(workspace), batch, kv->kv_heads,
+                 heads / kv->kv_heads, s.head_tiles, s.N};
+    r.args.images = static_cast<const uint8_t *>(workspace);
     r.args.k_scales = kv->k_scale;
     r.args.v_scales = kv->v ? kv->v_scale : kv->k_scale;
     r.args.ks_page = kv->k_scale_page_stride;
@@ -733,7 +746,7 @@ proj_status proj_paged_attention_q8(const void *q, int64_t q_row_stride, int64_t
     r.args.block_shift = log2_of(kv->block);
     const cudaError_t e = s.shared ? hsp::launch_attn8_latent(r) : hsp::launch_attn8_grouped(r);
     if (e != cudaSuccess) return hsp::api_cuda_fail(e, "kernel launch (paged attention, 8 bits)");
-    hsp::api_count_launches(split ? 2 : 1);
+    hsp::api_count_launches(split ? 3 : 2);
     return hsp::api_ok();
 }
 

@@ -137,11 +137,19 @@ struct ReadQ8Args {
 cudaError_t launch_read_q8(const ReadQ8Args &a, int sms, int pdl, cudaStream_t stream);
 
 constexpr int kAttn8Tile = 128;      // tokens per tile
-constexpr int kAttn8ScaleSlots = 4;  // tiles whose scales lie ready
-struct Attn8Args {
-    AttnArgs line;                   // (no host tables of its own: sizes, table, lengths, outputs, workspace)
+constexpr int kAttn8ScaleSlots = 2;  // tiles whose scales lie ready
+// The queries in two 8-bit pieces, as a kernel of its own writes them: for each sequence, kv head and head tile of N the
+// image of shared memory that the attention's instructions read (2 N rows of DK bytes, swizzled), then N bytes of units.
+struct Attn8QueryArgs {
     const void *q;                   // [batch, heads, k_dim] bf16
     int64_t q_row, q_head;
+    uint8_t *images;
+    int32_t batch, kv_heads, group, head_tiles, N;
+};
+__host__ __device__ constexpr int attn8_image_bytes(int DK, int N) { return 2 * N * DK + N; }
+struct Attn8Args {
+    AttnArgs line;
+    const uint8_t *images;
     const float *k_scales, *v_scales;
     int64_t ks_page, ks_block, ks_head, vs_page, vs_block, vs_head;
     int32_t block_shift;
@@ -154,21 +162,23 @@ struct Attn8LaunchReq {
     int sms;
     cudaStream_t stream;
     CUtensorMap tmap_k, tmap_v;      // boxes of 128 (64) columns; latent: tmap_v has the 64 rotary columns
+    Attn8QueryArgs queries;
     Attn8Args args;
 };
+cudaError_t launch_attn8_queries(const Attn8LaunchReq &r);
 cudaError_t launch_attn8_latent(const Attn8LaunchReq &r);
 cudaError_t launch_attn8_grouped(const Attn8LaunchReq &r);
-// Softmax warps: four for each set of at most 32 heads.  A latent cache's queries are split by four warps of their own, a
-// grouped one's (few and short) by the softmax warps.
-constexpr int attn8_sets(int N) { return N > 16 ? 2 : 1; }
-constexpr int attn8_threads(bool shared, int N) { return 128 * attn8_sets(N) + 128 + (shared ? 128 : 0); }
-// CTAs per SM (see attn_ctas_per_sm; 64 heads fill tensor memory or the registers).
+// Four softmax warps for every 16 heads, then the copies, the two issuers, the scales.
+constexpr int attn8_threads(int N) { return 8 * N + 128; }
+// CTAs per SM (see attn_ctas_per_sm; 64 heads fill tensor memory).
 constexpr int attn8_ctas_per_sm(int DK, bool shared, int N) { return shared || N == 64 ? 1 : DK == 64 && N == 16 ? 3 : 2; }
 constexpr int kAttn8RopeBytes = kAttn8Tile * 64;
-// Shared memory besides the ring of groups: queries (two pieces), probabilities, rotary boxes, scales, reduction
-// buffers, barriers and the alignment slack.
+// Places of the rotary boxes: one where the queries of 64 heads leave no more beside two whole tiles.
+constexpr int attn8_rope_slots(int N) { return N == 64 ? 1 : 2; }
+// Shared memory besides the ring of groups: queries (two pieces), probabilities, rotary boxes, scales, the queries' units,
+// barriers.  (Together with two tiles of 576 columns and 64 heads nearly all that a CTA can have.)
 inline int attn8_fixed_smem(int DK, bool rope, int N) {
-    return 2 * N * DK + kAttn8Tile * 2 * N + (rope ? 2 * kAttn8RopeBytes : 0) + kAttn8ScaleSlots * kAttn8Tile * 12 + 13 * N * 4 + 640 + 1024;
+    return 2 * N * DK + kAttn8Tile * 2 * N + (rope ? attn8_rope_slots(N) * kAttn8RopeBytes : 0) + kAttn8ScaleSlots * kAttn8Tile * 8 + 4 * N + 768;
 }
 
 // ---- pages ------------------------------------------------------------------------------

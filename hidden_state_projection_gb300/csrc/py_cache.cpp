@@ -310,7 +310,7 @@ struct AttentionCall {
     PyObject *stream;
 };
 template <typename Kv, typename Bytes, typename Call>
-PyObject *attend(AttentionCall &c, const Kv &kv, int64_t num_pages, int64_t page_size, int dev, Bytes workspace_bytes, Call call) {
+PyObject *attend(AttentionCall &c, const Kv &kv, int64_t num_pages, int64_t page_size, int dev, bool always, Bytes workspace_bytes, Call call) {
     const at::Tensor &q = c.q;
     at::Tensor &out = c.out, &lse = c.lse;
     if (q.dim() != 3 || q.size(2) != kv.k_dim || q.stride(2) != 1)
@@ -330,8 +330,8 @@ PyObject *attend(AttentionCall &c, const Kv &kv, int64_t num_pages, int64_t page
     }
     const int32_t *rp = c.rows.defined() ? ints("rows", c.rows, batch) : nullptr;
     Workspace ws;
-    if (c.workspace.defined() || static_cast<int64_t>(ix.max_pages) * ix.page_size > PROJ_UNCUT_TOKENS)
-        use(&ws, c.workspace, c.workspace.defined() ? 0 : workspace_bytes(narrow(heads), kv.kv_heads, kv.k_dim, kv.v_dim, kv.v == nullptr));
+    if (c.workspace.defined() || always || static_cast<int64_t>(ix.max_pages) * ix.page_size > PROJ_UNCUT_TOKENS)
+        use(&ws, c.workspace, c.workspace.defined() ? 0 : workspace_bytes(narrow(batch), narrow(heads), kv.kv_heads, kv.k_dim, kv.v_dim, kv.v == nullptr));
     const proj_stream_t stream = stream_of(c.stream, dev);
     const void *qp = q.data_ptr();
     void *op = out.data_ptr();
@@ -357,7 +357,10 @@ PyObject *paged_attention(PyObject *, PyObject *const *args, Py_ssize_t nargs) {
                         optional(args[11], "workspace"), args[12]};
         const int dev = device_of({&c.q, &k, &v, &c.table, &c.lens, &c.rows, &c.out, &c.lse, &c.workspace});
         const proj_kv_pages kv = kv_pages(k, v, args[6]);
-        return attend(c, kv, k.size(0), k.size(1), dev, proj_paged_attention_workspace_bytes, proj_paged_attention);
+        auto bytes = [](int32_t, int32_t heads, int32_t kv_heads, int32_t k_dim, int32_t v_dim, bool latent) {
+            return proj_paged_attention_workspace_bytes(heads, kv_heads, k_dim, v_dim, latent);
+        };
+        return attend(c, kv, k.size(0), k.size(1), dev, false, bytes, proj_paged_attention);
     });
 }
 
@@ -372,7 +375,7 @@ PyObject *paged_attention_q8(PyObject *, PyObject *const *args, Py_ssize_t nargs
                         optional(args[13], "workspace"), args[14]};
         const int dev = device_of({&c.q, &k, &v, &ks, &vs, &c.table, &c.lens, &c.rows, &c.out, &c.lse, &c.workspace});
         const proj_kv_pages_q8 kv = kv_pages_q8(k, v, ks, vs, args[8]);
-        return attend(c, kv, k.size(0), k.size(1), dev, proj_paged_attention_q8_workspace_bytes, proj_paged_attention_q8);
+        return attend(c, kv, k.size(0), k.size(1), dev, true, proj_paged_attention_q8_workspace_bytes, proj_paged_attention_q8);
     });
 }
 

@@ -626,7 +626,13 @@ proj_status proj_cache_read_q8(const proj_kv_pages_q8 *kv, const proj_page_index
 
 /*
  * proj_paged_attention_q8 -- proj_paged_attention over a cache in 8 bits: q and out are bf16, keys and values
- * code * scale.  Arguments, shapes, limits and errors as proj_paged_attention has them.
+ * code * scale.  Arguments, shapes, limits and errors as proj_paged_attention has them, but for
+ *   workspace  device, 16-byte aligned, at least proj_paged_attention_q8_workspace_bytes bytes: always needed (the
+ *              queries are laid out there), needs no initialisation and keeps nothing
+ * Scores are exact products summed in fp32, of queries in two 8-bit pieces (exact but for numbers below 2^-21 of the
+ * head's largest); the weights are rounded to two 8-bit pieces (2^-7 at most, of weights below a hundredth or so of
+ * their tile's largest more) and the result, once, to bf16.  Two kernel launches, three where a table row holds more
+ * than PROJ_UNCUT_TOKENS tokens.
  */
 proj_status proj_paged_attention_q8(const void *q, int64_t q_row_stride, int64_t q_head_stride,
                                     const proj_kv_pages_q8 *kv, const proj_page_index *index,
@@ -634,8 +640,9 @@ proj_status proj_paged_attention_q8(const void *q, int64_t q_row_stride, int64_t
                                     void *out, float *lse, void *workspace, size_t workspace_bytes,
                                     proj_stream_t stream);
 
-/* Workspace bytes of proj_paged_attention_q8 (as for proj_paged_attention). */
-size_t proj_paged_attention_q8_workspace_bytes(int32_t heads, int32_t kv_heads, int32_t k_dim,
+/* Workspace bytes of proj_paged_attention_q8 (host only; 0 when the sizes are not supported, with
+ * proj_last_error_string saying why). */
+size_t proj_paged_attention_q8_workspace_bytes(int32_t batch, int32_t heads, int32_t kv_heads, int32_t k_dim,
                                                int32_t v_dim, int32_t latent);
 
 /*

@@ -211,14 +211,14 @@ def test_many_sequences(hsp, latent):
 
 @pytest.mark.parametrize("latent", [True, False])
 def test_many_short_sequences_are_not_cut(hsp, latent):
-    """Tables of at most 256 tokens per row: one launch, no workspace."""
+    """Tables of at most 256 tokens per row: no join."""
     lens = [(37 * i) % 241 for i in range(700)]
     dk, dv, heads, kv = (512, 512, 70, 1) if latent else (64, 64, 6, 3)
     args = make(lens, heads, kv, dk, latent, 16, 13)
     assert args[5].shape[1] * 16 == 256
     n = hsp.launch_count()
     check(hsp, args, dk ** -0.5, dv)
-    assert hsp.launch_count() == n + 1
+    assert hsp.launch_count() == n + 2
 
 
 @pytest.mark.parametrize("latent", [True, False])
@@ -446,7 +446,7 @@ def test_outputs_and_workspace_lie_between_untouched_bytes(hsp):
         out = buf[4096:4096 + 2 * heads * dv].view(2, heads, dv)
         check(hsp, args, 0.07, dv, out=out)
         assert (buf[:4096] == 7).all() and (buf[-4096:] == 7).all()
-        need = hsp.paged_attention_q8_workspace_bytes(heads, kv, dk, dv, dv == 512)
+        need = hsp.paged_attention_q8_workspace_bytes(2, heads, kv, dk, dv, dv == 512)
         ws = torch.full((need + 512,), 0x5A, dtype=torch.uint8, device="cuda")
         assert torch.equal(hsp.paged_attention_q8(*args, 0.07, workspace=ws[:need]), out)
         assert (ws[need:] == 0x5A).all()

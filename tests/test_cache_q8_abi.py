@@ -53,7 +53,7 @@ def test_attention_refusals(hsp):
         (dict(kvp=kv(kst=(36864, 0, 576))), 1), (dict(kvp=kv(kst=(0, 576, 576))), 1), (dict(ix=index(width=1 << 25, stride=1 << 25)), 1),
         (dict(qs=(0, 576)), 1), (dict(q=A + 8), 2), (dict(out=A + 8), 2), (dict(qs=(9216, 577)), 2), (dict(lse=A + 2), 2)])
     assert call(batch=0) == 0 and call(batch=0, kvp=kv(**GROUPED)) == 0
-    for ws in (dict(ws=None), dict(n=1000), dict(ws=A + 8)):   # a table row of 512 tokens: sequences may be cut
+    for ws in (dict(ws=None), dict(n=1000), dict(ws=A + 8)):
         assert call(**ws) != 0
 
 
@@ -89,8 +89,10 @@ def test_read_refusals(hsp):
 
 def test_workspace_bytes(hsp):
     for heads, kvh, dk, dv, latent in ((16, 1, 576, 512, True), (128, 1, 512, 512, True), (32, 8, 128, 128, False), (28, 4, 64, 64, False)):
-        assert hsp.paged_attention_q8_workspace_bytes(heads, kvh, dk, dv, latent) > 0
-    for args in ((16, 1, 640, 512, True), (0, 1, 576, 512, True), (7, 2, 64, 64, False), (8, 2, 96, 96, False), (1 << 40, 1, 576, 512, True)):
+        a, b = (hsp.paged_attention_q8_workspace_bytes(n, heads, kvh, dk, dv, latent) for n in (1, 9))
+        assert b >= a + 8 * heads * 2 * dk and hsp.paged_attention_q8_workspace_bytes(0, heads, kvh, dk, dv, latent) <= a
+    for args in ((1, 16, 1, 640, 512, True), (1, 0, 1, 576, 512, True), (1, 7, 2, 64, 64, False), (1, 8, 2, 96, 96, False),
+                 (1, 1 << 40, 1, 576, 512, True), (-1, 16, 1, 576, 512, True)):
         with pytest.raises(hsp.ProjError):
             hsp.paged_attention_q8_workspace_bytes(*args)
 
