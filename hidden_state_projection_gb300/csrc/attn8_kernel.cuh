@@ -192,7 +192,7 @@ __global__ void __launch_bounds__(attn8_threads(N), attn8_ctas_per_sm(DK, SHARED
     __syncthreads();
     tc_fence_after_sync();
     // What is read below comes from before the kernel that splits the queries, which has let this one start when all of
-    // that was complete; only its own images are still to come, and the copy producer waits for those.
+    // that was complete; only its own images are still to come, and the issuer of the scores waits for those.
 
     const AttnLine ln = attn_find_line<T, C::kThreads>(a, cta, place, warp_sum);
     const uint32_t tmem = *tmem_slot;
@@ -207,7 +207,6 @@ __global__ void __launch_bounds__(attn8_threads(N), attn8_ctas_per_sm(DK, SHARED
             AttnSegment sg;
             RingPos rp, xp;
             int ng = 0;
-            uint32_t seg = 0;
             const int pbox = min(T, 1 << a.page_shift);  // tokens per box
             const int boxes = T / pbox;                  // pages that meet a tile (1 to 8)
             bool alive = true;
@@ -219,19 +218,6 @@ __global__ void __launch_bounds__(attn8_threads(N), attn8_ctas_per_sm(DK, SHARED
                     const int p0 = static_cast<int>((static_cast<int64_t>(tile) * T) >> a.page_shift);
 #pragma unroll
                     for (int e = 0; e < 8; ++e) id[e] = (e < boxes && p0 + e < pages) ? tbl[p0 + e] : 0;
-                };
-                // the part's queries, behind its first tile, which does not have to wait for the last part's (nor the first
-                // one for the kernel that makes the images)
-                auto queries = [&]() {
-                    alive = await(q_free, seg ^ 1u);
-                    if (!alive) return;
-                    if (seg == 0) griddep_wait();
-                    const uint8_t *from = g.images + ((static_cast<int64_t>(sg.b) * a.kv_heads + sg.kv) * gridDim.x + ht) * attn8_image_bytes(DK, N);
-                    mbar_arrive_expect_tx(smem_u32(q_full), C::kQBytes);
-                    bulk_load(smem_u32(q_smem), from, C::kQBytes, smem_u32(q_full));
-                    mbar_arrive_expect_tx(smem_u32(&unit_full[seg & 3u]), N);
-                    bulk_load(smem_u32(q_unit) + (seg & 3u) * N, from + C::kQBytes, N, smem_u32(&unit_full[seg & 3u]));
-                    issued[2] = static_cast<int>(++seg);
                 };
                 int next[8];
                 ids_of(sg.t0, next);
@@ -256,6 +242,22 @@ __global__ void __launch_bounds__(attn8_threads(N), attn8_ctas_per_sm(DK, SHARED
                         for (int e = 0; e < 8; ++e)
                             if (e < np) tma_load_5d(dst + e * bytes, map, 0, boxes == 1 ? off : 0, box, sg.kv, id[e], fb);
                     };
+                    // A ring of two tiles is too short for DRAM's latency behind the products: with several head tiles one
+                    // of them sends the next tile to L2 while this one waits for its places (the first: when it has them).
+                    auto ahead = [&]() {
+                        if (N != 64 || !SHARED || boxes > 2 || gridDim.x == 1 || k + 1 >= sg.n || (k + 1) % static_cast<int>(gridDim.x) != ht) return;
+                        const int64_t then = tok + T;
+                        const int to = static_cast<int>(then & ((1 << a.page_shift) - 1));
+#pragma unroll 1
+                        for (int e = 0; e < boxes; ++e) {
+                            const int page = e == 0 ? next[0] : next[1];
+                            if (page < 0 || page >= a.num_pages || (then >> a.page_shift) + e >= pages) continue;
+#pragma unroll 1
+                            for (int gr = 0; gr < C::kGroups; ++gr) tma_prefetch_5d(&tmap_k, 0, boxes == 1 ? to : 0, gr, sg.kv, page);
+                            if (C::kRope) tma_prefetch_5d(&tmap_v, 0, boxes == 1 ? to : 0, 0, sg.kv, page);
+                        }
+                    };
+                    if (k > 0) ahead();
                     const bool skip = i == a.skip_tile;
 #pragma unroll 1
                     for (int gr = 0; gr < C::kGroups; ++gr) {
@@ -278,10 +280,9 @@ __global__ void __launch_bounds__(attn8_threads(N), attn8_ctas_per_sm(DK, SHARED
                         }
                         xp.next(C::kX);
                     }
-                    if (k == 0 && alive) queries();
+                    if (k == 0) ahead();
                 }
             }
-            if (seg == 0) griddep_wait();  // (every CTA: the next kernel but one may write the images anew)
         }
         __syncwarp();
     } else if (warp == C::kRoles + 1) {
@@ -294,7 +295,16 @@ __global__ void __launch_bounds__(attn8_threads(N), attn8_ctas_per_sm(DK, SHARED
             bool alive = true;
             const uint64_t qd = umma_desc_lines<C::kW>(smem_u32(q_smem));
             RingPos rp, xp, sp;
+            griddep_wait();  // the images (in every CTA: the next kernel but one may write them anew)
             while (alive && attn_next_segment<T>(a, ln, walk, sg)) {
+                // the part's queries, when the scores of the last part are done with theirs
+                if (!await(q_free, seg ^ 1u)) break;
+                const uint8_t *from = g.images + ((static_cast<int64_t>(sg.b) * a.kv_heads + sg.kv) * gridDim.x + ht) * attn8_image_bytes(DK, N);
+                mbar_arrive_expect_tx(smem_u32(q_full), C::kQBytes);
+                bulk_load(smem_u32(q_smem), from, C::kQBytes, smem_u32(q_full));
+                mbar_arrive_expect_tx(smem_u32(&unit_full[seg & 3u]), N);
+                bulk_load(smem_u32(q_unit) + (seg & 3u) * N, from + C::kQBytes, N, smem_u32(&unit_full[seg & 3u]));
+                issued[2] = static_cast<int>(seg + 1);
                 if (!await(q_full, seg)) break;
                 ++seg;
                 for (int k = 0; k < sg.n; ++k) {

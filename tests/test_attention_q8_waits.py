@@ -1,7 +1,7 @@
 """The model of waits (test_attention_waits.py) for the attention over a cache in 8 bits (csrc/attn8_kernel.cuh).
 
-Beside the agents in bf16 a warp fetches the scales of up to two tiles ahead; a part's queries are copied behind its first
-tile, their units into a ring of four that the softmax reads.
+Beside the agents in bf16 a warp fetches the scales of up to two tiles ahead; the issuer of the scores has a part's queries
+copied, their units into a ring of four that the softmax reads.
 """
 import pytest
 
@@ -22,14 +22,13 @@ class Model8(Model):
                 if self.rotary:
                     yield from self.wait(("x_empty", tile % self.ropes), tile // self.ropes - 1)
                     self.copies.append(("x_full", tile % self.ropes))
-                if k == 0:
-                    yield from self.wait(("q_free",), part - 1)
-                    self.copies += [("q_full",), ("unit_full", part & 3)]
                 tile += 1
 
     def scores(self):
         tile = 0
         for part, tiles in enumerate(PARTS):
+            yield from self.wait(("q_free",), part - 1)
+            self.copies += [("q_full",), ("unit_full", part & 3)]
             yield from self.wait(("q_full",), part)
             for _ in range(tiles):
                 yield from self.wait(("s_free", tile & 1), (tile >> 1) - 1)
