@@ -7,6 +7,7 @@
 #include <stdint.h>
 
 #include "cache_args.h"
+#include "packed.cuh"
 #include "ptx.cuh"
 #include "stream_args.h"
 
@@ -123,28 +124,6 @@ __device__ __forceinline__ float fast_exp2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
-}
-
-// a += b, both columns in one instruction.
-__device__ __forceinline__ void add2(float2 &a, float2 b) {
-    asm("{\n\t.reg .b64 x, y;\n\tmov.b64 x, {%0, %1};\n\tmov.b64 y, {%2, %3};\n\tadd.rn.f32x2 x, x, y;\n\tmov.b64 {%0, %1}, x;\n\t}"
-        : "+f"(a.x), "+f"(a.y)
-        : "f"(b.x), "f"(b.y));
-}
-
-// Two columns at a time.
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
-    asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 z, {%6, %7};\n\t"
-        "fma.rn.f32x2 x, x, y, z;\n\tmov.b64 {%0, %1}, x;\n\t}"
-        : "=f"(c.x), "=f"(c.y)
-        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
-    return c;
-}
-__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
-    asm("{\n\t.reg .b64 x, y;\n\tmov.b64 x, {%0, %1};\n\tmov.b64 y, {%2, %3};\n\tmul.rn.f32x2 x, x, y;\n\tmov.b64 {%0, %1}, x;\n\t}"
-        : "+f"(a.x), "+f"(a.y)
-        : "f"(b.x), "f"(b.y));
-    return a;
 }
 
 // A box of a tensor on its way to L2.

@@ -9,6 +9,8 @@
 #include <cuda_fp16.h>
 #include <stdint.h>
 
+#include "packed.cuh"
+
 namespace hsp {
 
 constexpr int kQ8MinExp = -60, kQ8MaxExp = 60;
@@ -41,21 +43,24 @@ __device__ __forceinline__ int q8_exponent(float amax) {
     return max(kQ8MinExp, min(kQ8MaxExp, e));
 }
 
-// a c + b d rounded to odd: a float whose last bit says whether something was cut off, so that the rounding to a
-// code (which is shorter by far) is that of the exact sum.  The products' errors and the sum's are found with fused
+// a c + b d rounded to odd, two at a time: floats whose last bits say whether something was cut off, so that the rounding to
+// a code (which is shorter by far) is that of the exact sum.  The products' errors and the sum's are found with fused
 // multiply-adds and the two-sum of Knuth (a few bits beyond 2^-70 of the larger product aside).
-__device__ __forceinline__ float dot2_odd(float a, float c, float b, float d) {
-    const float p = a * c, q = b * d;
-    const float ep = fmaf(a, c, -p), eq = fmaf(b, d, -q);
-    const float s = __fadd_rn(p, q);
-    const float bb = __fadd_rn(s, -p);
-    const float es = __fadd_rn(__fadd_rn(p, -__fadd_rn(s, -bb)), __fadd_rn(q, -bb));
-    const float rest = __fadd_rn(es, __fadd_rn(ep, eq));
-    const float h = __fadd_rn(s, rest);
-    const float l = __fadd_rn(rest, -__fadd_rn(h, -s));
+__device__ __forceinline__ float odd(float h, float l) {
     uint32_t u = __float_as_uint(h);
     if ((l > 0.f || l < 0.f) && (u & 1u) == 0) u = (l > 0.f) == (h > 0.f) ? u + 1 : u - 1;
     return __uint_as_float(u);
+}
+__device__ __forceinline__ float2 dot2_odd(float2 a, float2 c, float2 b, float2 d) {
+    const float2 p = mul2(a, c), q = mul2(b, d);
+    const float2 ep = fma2(a, c, make_float2(-p.x, -p.y)), eq = fma2(b, d, make_float2(-q.x, -q.y));
+    const float2 s = sum2(p, q);
+    const float2 bb = sub2(s, p);
+    const float2 es = sum2(sub2(p, sub2(s, bb)), sub2(q, bb));
+    const float2 rest = sum2(es, sum2(ep, eq));
+    const float2 h = sum2(s, rest);
+    const float2 l = sub2(rest, sub2(h, s));
+    return make_float2(odd(h.x, l.x), odd(h.y, l.y));
 }
 
 }  // namespace hsp
