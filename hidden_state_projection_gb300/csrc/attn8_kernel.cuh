@@ -117,7 +117,7 @@ struct Attn8Cfg {
 constexpr float kAttn8Up = 8.75f, kAttn8Low = -4.f, kAttn8Aim = 3.f, kAttn8Down = 30.f;
 
 template <int DK, int DV, bool SHARED, int N>
-__global__ void __launch_bounds__(attn8_threads(N), attn8_ctas_per_sm(DK, SHARED, N))
+__global__ void __launch_bounds__(attn8_threads(N), attn8_ctas_per_sm(SHARED, N))
     hsp_attn8_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v, const __grid_constant__ Attn8Args g) {
     using C = Attn8Cfg<DK, DV, SHARED, N>;
     constexpr int T = kAttn8Tile, kC = 4;  // (heads of a softmax thread)
@@ -518,7 +518,7 @@ __global__ void __launch_bounds__(attn8_threads(N), attn8_ctas_per_sm(DK, SHARED
                             s[r][j] = fma2(mul2(x, unit[j]), make_float2(ksc[r], ksc[r]), make_float2(vlog[r], vlog[r]));
                         }
                 }
-                if (valid < T) {
+                if (__builtin_expect(valid < T, false)) {
 #pragma unroll
                     for (int r = 0; r < 4; ++r)
                         if (r0 + 8 * r >= valid) {
@@ -549,7 +549,7 @@ __global__ void __launch_bounds__(attn8_threads(N), attn8_ctas_per_sm(DK, SHARED
                     const uint4 x = *reinterpret_cast<const uint4 *>(seen + (i & 1) * 16 + w * 4);
                     move |= (x.x | x.y | x.z | x.w) != 0xffffu;
                 }
-                if (move) {
+                if (__builtin_expect(move, false)) {
                     // column maxima over the tile's tokens, new reference points (a column per thread), O^T rescaled
                     if (i > 0) await(pv_done, static_cast<uint32_t>(i - 1));  // (red, fac and points lie where the weights did)
                     tc_fence_after_sync();
@@ -602,7 +602,7 @@ __global__ void __launch_bounds__(attn8_threads(N), attn8_ctas_per_sm(DK, SHARED
                     }
                     softmax_sync<C::kSoft>();  // (before weights take their place)
                 }
-                if (valid < T) {
+                if (__builtin_expect(valid < T, false)) {
                     // the last tile: what lies behind the sequence must not reach the product (0 x NaN).  Its last
                     // step of 32 tokens is filled up with zeros; the steps behind that are not taken.
                     const int first = i * C::kGroups + C::kKG;  // its first value group in the ring
