@@ -736,10 +736,8 @@ __global__ void __launch_bounds__(attn8_threads(N), attn8_ctas_per_sm(SHARED, N)
         };
         for (int j = max(0, n - a.slots); j < n; ++j)
             if (j / C::kGroups != a.skip_tile) land(&full[j % a.slots], j / a.slots);
-        if (issued[2] > 0) {
-            land(q_full, issued[2] - 1);
-            land(&unit_full[(issued[2] - 1) & 3], (issued[2] - 1) >> 2);
-        }
+        if (issued[2] > 0) land(q_full, issued[2] - 1);
+        for (int j = max(0, issued[2] - 4); j < issued[2]; ++j) land(&unit_full[j & 3], j >> 2);
         if (C::kRope)
             for (int j = max(0, nx - C::kX); j < nx; ++j)
                 if (j != a.skip_tile) land(&x_full[j % max(C::kX, 1)], j / max(C::kX, 1));

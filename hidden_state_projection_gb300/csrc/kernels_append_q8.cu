@@ -342,7 +342,7 @@ __global__ void __launch_bounds__(kAppend8Threads, 3) hsp_append_q8_kernel(const
             const bool lok = __shfl_sync(0xffffffffu, static_cast<int>(row_ok), last) != 0;
             for (int from = first + here; lok; from += 32) {
                 const int k = from + lane;
-                bool on = k < a.tokens && row_of(k) == lrow;
+                bool on = static_cast<uint32_t>(k) < static_cast<uint32_t>(a.tokens) && row_of(k) == lrow;  // (k may have passed 2^31)
                 if (on) {
                     const int p = append8_pos(a, k, llen);
                     on = (p >> a.block_shift) == lblk;
@@ -410,7 +410,7 @@ cudaError_t launch_append_q8(const AppendQ8Args &a, int sms, int pdl, cudaStream
         // (2047 tokens of 8 heads of 128 columns and values, blocks of 16: 25.3 us in chunks of 16, 21.5 of 32; latent rows, one
         // unit to a run: 1501 tokens in blocks of 16 9.9 and 12.6)
         per_cta = units >= 4 || block > kAppend8Chunk ? kAppend8Tokens : kAppend8Chunk;
-        const int chunks = (a.tokens + per_cta - 1) / per_cta;
+        const int chunks = static_cast<int>((static_cast<int64_t>(a.tokens) + per_cta - 1) / per_cta);
         parts = fit / chunks > 1 ? fit / chunks : 1;
         const int64_t runs = static_cast<int64_t>(units) * (block < per_cta ? per_cta / block : 1);  // units of a chunk, at least
         const int64_t batches = (static_cast<int64_t>(block) * krow + kAppend8Items * 256 - 1) / (kAppend8Items * 256);
@@ -423,7 +423,7 @@ cudaError_t launch_append_q8(const AppendQ8Args &a, int sms, int pdl, cudaStream
     const Append8Shape g{per_cta, static_cast<int>(parts), (a.k.dim - a.rot) / 8, krow, vrow, subs, FastDiv(krow), FastDiv(vrow), FastDiv(units),
                          FastDiv(a.kv_heads)};
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>((a.tokens + per_cta - 1) / per_cta * parts), 1, 1);
+    cfg.gridDim = dim3(static_cast<unsigned>((static_cast<int64_t>(a.tokens) + per_cta - 1) / per_cta * parts), 1, 1);
     cfg.blockDim = dim3(kAppend8Threads, 1, 1);
     cfg.stream = stream;
     cudaLaunchAttribute attrs[2];

@@ -115,13 +115,13 @@ cudaError_t launch_read_q8(const ReadQ8Args &a, int sms, int pdl, cudaStream_t s
     const int fit = sms * 4;
     int y = (total + kRead8Threads - 1) / kRead8Threads, per_cta = 1;
     if (static_cast<int64_t>(a.tokens) * y > fit) y = fit / a.tokens > 1 ? fit / a.tokens : 1;
-    if (a.tokens > fit) per_cta = (a.tokens + fit - 1) / fit;
+    if (a.tokens > fit) per_cta = static_cast<int>((static_cast<int64_t>(a.tokens) + fit - 1) / fit);
     if (per_cta > kRead8Tokens) per_cta = kRead8Tokens;
     if (y > 65535) y = 65535;
     auto wide = [&](const void *p, int64_t row) { return reinterpret_cast<uintptr_t>(p) % 32 == 0 && row % 16 == 0; };
     const Read8Shape g{per_cta, krow, vrow, wide(a.k_out, a.k_row) && wide(a.v_out, a.v_row) ? 1 : 0, FastDiv(kper), FastDiv(vper), FastDiv(krow), FastDiv(vrow)};
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>((a.tokens + per_cta - 1) / per_cta), static_cast<unsigned>(y), 1);
+    cfg.gridDim = dim3(static_cast<unsigned>((static_cast<int64_t>(a.tokens) + per_cta - 1) / per_cta), static_cast<unsigned>(y), 1);
     cfg.blockDim = dim3(kRead8Threads, 1, 1);
     cfg.stream = stream;
     cudaLaunchAttribute attrs[1];
