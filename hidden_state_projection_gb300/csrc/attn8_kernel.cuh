@@ -166,16 +166,16 @@ __global__ void __launch_bounds__(attn8_threads(N), attn8_ctas_per_sm(SHARED, N)
             mbar_init(smem_u32(&x_full[s]), 1);
             mbar_init(smem_u32(&x_empty[s]), 1);
             mbar_init(smem_u32(&s_full[s]), 1);
-            mbar_init(smem_u32(&s_free[s]), C::kSoft);
+            mbar_init(smem_u32(&s_free[s]), C::kSoft / 32);
         }
         for (int s = 0; s < 4; ++s) mbar_init(smem_u32(&unit_full[s]), 1);
         for (int s = 0; s < kAttn8ScaleSlots; ++s) {
-            mbar_init(smem_u32(&sc_full[s]), 32);
-            mbar_init(smem_u32(&sc_empty[s]), C::kSoft);
+            mbar_init(smem_u32(&sc_full[s]), 1);
+            mbar_init(smem_u32(&sc_empty[s]), C::kSoft / 32);
         }
         mbar_init(smem_u32(q_full), 1);
         mbar_init(smem_u32(q_free), 1);
-        mbar_init(smem_u32(p_full), C::kSoft);
+        mbar_init(smem_u32(p_full), C::kSoft / 32);
         mbar_init(smem_u32(pv_done), 1);
         mbar_init(smem_u32(drained), 2);
         *abort_flag = 0;
@@ -198,6 +198,11 @@ __global__ void __launch_bounds__(attn8_threads(N), attn8_ctas_per_sm(SHARED, N)
     const uint32_t tmem = *tmem_slot;
     const uint32_t tmem_s = tmem + C::kOT * N;
     auto await = [&](uint64_t *bar, uint32_t phase) { return attn_wait(smem_u32(bar), phase & 1u, a.wait_limit_ns, abort_flag); };
+
+    auto warp_arrive = [&](uint64_t *bar) {  // once for the warp, when all of its lanes are there
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(bar));
+    };
 
     if (warp == C::kRoles) {
         // ---------------- copy producer: one thread reads the table a tile ahead and issues ----------------
@@ -433,7 +438,7 @@ __global__ void __launch_bounds__(attn8_threads(N), attn8_ctas_per_sm(SHARED, N)
                     kk[0][e] = kk[1][e];
                     vv[0][e] = vv[1][e];
                 }
-                mbar_arrive(smem_u32(&sc_full[slot]));
+                warp_arrive(&sc_full[slot]);
                 if (k + 2 < sg.n) fetch(sg.t0 + k + 2, kk[1], vv[1]);
             }
         }
@@ -492,7 +497,7 @@ __global__ void __launch_bounds__(attn8_threads(N), attn8_ctas_per_sm(SHARED, N)
                     ksc[r] = sc[8 * r];
                     vlog[r] = sc[T + 8 * r];
                 }
-                mbar_arrive(smem_u32(&sc_empty[i % kAttn8ScaleSlots]));
+                warp_arrive(&sc_empty[i % kAttn8ScaleSlots]);
                 await(&s_full[i & 1], static_cast<uint32_t>(i >> 1));
                 tc_fence_after_sync();
                 // s[r][j]: row r0 + 8 r, heads h0 + 2 j and + 1, in log2 units with the values' scale
@@ -507,7 +512,7 @@ __global__ void __launch_bounds__(attn8_threads(N), attn8_ctas_per_sm(SHARED, N)
                     }
                     tmem_wait_ld();
                     tc_fence_before_sync();
-                    mbar_arrive(smem_u32(&s_free[i & 1]));
+                    warp_arrive(&s_free[i & 1]);
 #pragma unroll
                     for (int r = 0; r < 4; ++r)
 #pragma unroll
@@ -650,7 +655,7 @@ __global__ void __launch_bounds__(attn8_threads(N), attn8_ctas_per_sm(SHARED, N)
                 }
                 fence_proxy_async_smem();
                 tc_fence_before_sync();
-                mbar_arrive(smem_u32(p_full));
+                warp_arrive(p_full);
             }
             // ---- the part is done: l (and u) over the tokens, then O^T out of tensor memory ----
             await(pv_done, static_cast<uint32_t>(i - 1));  // (red and fac lie where the weights did)
