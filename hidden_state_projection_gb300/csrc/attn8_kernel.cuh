@@ -32,6 +32,8 @@
 
 #include <cuda_fp16.h>
 
+#include <type_traits>
+
 #include "attn_common.cuh"
 #include "q8.cuh"
 
@@ -205,89 +207,110 @@ __global__ void __launch_bounds__(attn8_threads(N), attn8_ctas_per_sm(SHARED, N)
     };
 
     if (warp == C::kRoles) {
-        // ---------------- copy producer: one thread reads the table a tile ahead and issues ----------------
+        // ---------------- copy producer: one thread reads the table two tiles ahead and issues ----------------
+        // A group's turn (a wait, the bytes, a copy for each page) is a chain of instructions on one thread beside busy softmax
+        // warps: what can be is done once for a tile, and pages of 64 tokens or more have code of their own (two pages to a
+        // tile, not eight).
         if (elect_one()) {
-            AttnWalk walk(ln);
-            int i = 0;
-            AttnSegment sg;
-            RingPos rp, xp;
-            int ng = 0;
-            const int pbox = min(T, 1 << a.page_shift);  // tokens per box
-            const int boxes = T / pbox;                  // pages that meet a tile (1 to 8)
-            bool alive = true;
-            while (alive && attn_next_segment<T>(a, ln, walk, sg)) {
-                const int row = a.rows ? a.rows[sg.b] : sg.b;
-                const int32_t *tbl = a.table + row * a.table_stride;
-                const int pages = static_cast<int>((static_cast<int64_t>(sg.len) + (1 << a.page_shift) - 1) >> a.page_shift);
-                auto ids_of = [&](int tile, int (&id)[8]) {
-                    const int p0 = static_cast<int>((static_cast<int64_t>(tile) * T) >> a.page_shift);
+            auto copies = [&](auto pages_of_a_tile) {
+                constexpr int E = decltype(pages_of_a_tile)::value;
+                constexpr bool kAhead = SHARED && N == 64 && E == 2;  // (see `ahead`; the table is read two tiles ahead, else one)
+                AttnWalk walk(ln);
+                int i = 0;
+                AttnSegment sg;
+                RingPos rp, xp;
+                int ng = 0, nx = 0;                          // groups and rotary boxes so far
+                const int pbox = min(T, 1 << a.page_shift);  // tokens per box
+                const int boxes = T / pbox;                  // pages that meet a tile (1 to E)
+                const uint32_t line_bytes = static_cast<uint32_t>(pbox) * C::kW;
+                const uint32_t full_at = smem_u32(full), empty_at = smem_u32(empty);
+                bool alive = true;
+                while (alive && attn_next_segment<T>(a, ln, walk, sg)) {
+                    const int row = a.rows ? a.rows[sg.b] : sg.b;
+                    const int32_t *tbl = a.table + row * a.table_stride;
+                    const int pages = static_cast<int>((static_cast<int64_t>(sg.len) + (1 << a.page_shift) - 1) >> a.page_shift);
+                    auto ids_of = [&](int k, int (&id)[E]) {  // (0: none)
+                        const int p0 = static_cast<int>((static_cast<int64_t>(sg.t0 + k) * T) >> a.page_shift);
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) id[e] = (e < boxes && p0 + e < pages) ? tbl[p0 + e] : 0;
-                };
-                int next[8];
-                ids_of(sg.t0, next);
-                for (int k = 0; k < sg.n && alive; ++k, ++i) {
-                    int id[8];
+                        for (int e = 0; e < E; ++e) id[e] = (e < boxes && p0 + e < pages) ? tbl[p0 + e] : 0;
+                    };
+                    int next[E], then[E];
+                    ids_of(0, next);
+                    if (kAhead) ids_of(1, then);
+                    for (int k = 0; k < sg.n && alive; ++k, ++i) {
+                        int id[E];
+                        bool out = false;
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        id[e] = next[e];
-                        if (id[e] < 0 || id[e] >= a.num_pages) {
+                        for (int e = 0; e < E; ++e) {
+                            id[e] = next[e];
+                            if (kAhead) next[e] = then[e];
+                            out |= static_cast<uint32_t>(id[e]) >= static_cast<uint32_t>(a.num_pages);
+                        }
+                        if (__builtin_expect(out, false)) {
                             atomicCAS(a.err_word, 0, kDeviceErrIndex);
-                            id[e] = 0;  // stays inside the pool; the call is reported
-                        }
-                    }
-                    if (k + 1 < sg.n) ids_of(sg.t0 + k + 1, next);
-                    const int64_t tok = static_cast<int64_t>(sg.t0 + k) * T;
-                    const int np = min(boxes, pages - static_cast<int>(tok >> a.page_shift));
-                    const int off = static_cast<int>(tok & ((1 << a.page_shift) - 1));
-                    auto load = [&](const CUtensorMap *map, int box, int line, uint32_t dst, uint32_t fb) {
-                        const uint32_t bytes = static_cast<uint32_t>(pbox) * line;
-                        mbar_arrive_expect_tx(fb, static_cast<uint32_t>(np) * bytes);
 #pragma unroll
-                        for (int e = 0; e < 8; ++e)
-                            if (e < np) tma_load_5d(dst + e * bytes, map, 0, boxes == 1 ? off : 0, box, sg.kv, id[e], fb);
-                    };
-                    // A ring of two tiles is too short for DRAM's latency behind the products: with several head tiles one
-                    // of them sends the next tile to L2 while this one waits for its places (the first: when it has them).
-                    auto ahead = [&]() {
-                        if (N != 64 || !SHARED || boxes > 2 || gridDim.x == 1 || k + 1 >= sg.n || (k + 1) % static_cast<int>(gridDim.x) != ht) return;
-                        const int64_t then = tok + T;
-                        const int to = static_cast<int>(then & ((1 << a.page_shift) - 1));
-#pragma unroll 1
-                        for (int e = 0; e < boxes; ++e) {
-                            const int page = e == 0 ? next[0] : next[1];
-                            if (page < 0 || page >= a.num_pages || (then >> a.page_shift) + e >= pages) continue;
-#pragma unroll 1
-                            for (int gr = 0; gr < C::kGroups; ++gr) tma_prefetch_5d(&tmap_k, 0, boxes == 1 ? to : 0, gr, sg.kv, page);
-                            if (C::kRope) tma_prefetch_5d(&tmap_v, 0, boxes == 1 ? to : 0, 0, sg.kv, page);
+                            for (int e = 0; e < E; ++e)
+                                if (static_cast<uint32_t>(id[e]) >= static_cast<uint32_t>(a.num_pages)) id[e] = 0;  // stays inside the pool; the call is reported
                         }
-                    };
-                    if (k > 0) ahead();
-                    const bool skip = i == a.skip_tile;
+                        if (k + 1 + kAhead < sg.n) ids_of(k + 1 + kAhead, kAhead ? then : next);
+                        const int64_t tok = static_cast<int64_t>(sg.t0 + k) * T;
+                        const int np = min(boxes, pages - static_cast<int>(tok >> a.page_shift));
+                        const int off = boxes == 1 ? static_cast<int>(tok & ((1 << a.page_shift) - 1)) : 0;
+                        const uint32_t bytes = static_cast<uint32_t>(np) * line_bytes;
+                        // A ring of two tiles is too short for DRAM's latency behind the products: with several head tiles one
+                        // of them sends the next tile to L2 while this one waits for its places (the first: when it has them).
+                        auto ahead = [&]() {
+                            if (!kAhead || gridDim.x == 1 || k + 1 >= sg.n || (k + 1) % static_cast<int>(gridDim.x) != ht) return;
+                            const int64_t after = tok + T;
+                            const int to = boxes == 1 ? static_cast<int>(after & ((1 << a.page_shift) - 1)) : 0;
 #pragma unroll 1
-                    for (int gr = 0; gr < C::kGroups; ++gr) {
-                        // (a fresh barrier's phase before the first counts as complete)
-                        alive = await(&empty[rp.slot], rp.phase ^ 1u);
-                        if (!alive) break;
-                        ++ng;
-                        if (!skip) {
-                            load(SHARED || gr < C::kKG ? &tmap_k : &tmap_v, SHARED ? gr : 0, C::kW, ring + rp.slot * C::kGroupBytes, smem_u32(&full[rp.slot]));
-                            issued[0] = ng;
+                            for (int e = 0; e < boxes; ++e) {
+                                const int page = e == 0 ? next[0] : next[E > 1 ? 1 : 0];
+                                if (static_cast<uint32_t>(page) >= static_cast<uint32_t>(a.num_pages) || (after >> a.page_shift) + e >= pages) continue;
+#pragma unroll 1
+                                for (int gr = 0; gr < C::kGroups; ++gr) tma_prefetch_5d(&tmap_k, 0, to, gr, sg.kv, page);
+                                if (C::kRope) tma_prefetch_5d(&tmap_v, 0, to, 0, sg.kv, page);
+                            }
+                        };
+                        if (k > 0) ahead();
+                        const bool skip = i == a.skip_tile;
+#pragma unroll 1
+                        for (int gr = 0; gr < C::kGroups; ++gr) {
+                            // (a fresh barrier's phase before the first counts as complete)
+                            alive = attn_wait(empty_at + rp.slot * 8, rp.phase ^ 1u, a.wait_limit_ns, abort_flag);
+                            if (!alive) break;
+                            ++ng;
+                            if (!skip) {
+                                const CUtensorMap *map = SHARED || gr < C::kKG ? &tmap_k : &tmap_v;
+                                const uint32_t fb = full_at + rp.slot * 8, dst = ring + rp.slot * C::kGroupBytes;
+                                mbar_arrive_expect_tx(fb, bytes);
+#pragma unroll
+                                for (int e = 0; e < E; ++e)
+                                    if (e < np) tma_load_5d(dst + e * line_bytes, map, 0, off, SHARED ? gr : 0, sg.kv, id[e], fb);
+                            }
+                            rp.next(a.slots);
                         }
-                        rp.next(a.slots);
+                        if (C::kRope && alive) {
+                            alive = await(&x_empty[xp.slot], xp.phase ^ 1u);
+                            if (!alive) break;
+                            ++nx;
+                            if (!skip) {
+                                const uint32_t fb = smem_u32(&x_full[xp.slot]), dst = smem_u32(x_smem) + xp.slot * kAttn8RopeBytes;
+                                mbar_arrive_expect_tx(fb, static_cast<uint32_t>(np * pbox) * 64);
+#pragma unroll
+                                for (int e = 0; e < E; ++e)
+                                    if (e < np) tma_load_5d(dst + e * (pbox * 64), &tmap_v, 0, off, 0, sg.kv, id[e], fb);
+                            }
+                            xp.next(C::kX);
+                        }
+                        if (k == 0) ahead();
                     }
-                    if (C::kRope && alive) {
-                        alive = await(&x_empty[xp.slot], xp.phase ^ 1u);
-                        if (!alive) break;
-                        if (!skip) {
-                            load(&tmap_v, 0, 64, smem_u32(x_smem) + xp.slot * kAttn8RopeBytes, smem_u32(&x_full[xp.slot]));
-                            issued[1] = i + 1;
-                        }
-                        xp.next(C::kX);
-                    }
-                    if (k == 0) ahead();
                 }
-            }
+                issued[0] = ng;
+                issued[1] = nx;
+            };
+            if (SHARED && a.page_shift >= 6) copies(std::integral_constant<int, 2>());
+            else copies(std::integral_constant<int, 8>());
         }
         __syncwarp();
     } else if (warp == C::kRoles + 1) {
