@@ -39,6 +39,15 @@
 
 namespace hsp {
 
+// A product of 8-bit operands (32 elements of K per instruction), fp32 accumulator.
+__device__ __forceinline__ void umma_f8(uint32_t tmem_d, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(tmem_d),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
 // K-major operand in 64-byte lines (64-byte swizzle): eight rows in 512 bytes.
 __device__ __forceinline__ uint64_t umma_desc_sw64(uint32_t smem_addr) {
     uint64_t d = 0;
