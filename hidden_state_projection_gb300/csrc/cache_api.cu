@@ -621,7 +621,7 @@ proj_status proj_cache_append_q8(const void *k_new, int64_t k_row_stride, const 
     a.err_word = dev.err_word;
     const cudaError_t e = hsp::launch_append_q8(a, dev.sms, hsp::api_options().pdl, reinterpret_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return hsp::api_cuda_fail(e, "kernel launch (cache append, 8 bits)");
-    hsp::api_count_launches(q ? 2 : 1);
+    hsp::api_count_launches(1);
     return hsp::api_ok();
 }
 

@@ -76,8 +76,7 @@ inline int attn_group_boxes(int VB) { return VB >= 2 ? 2 : 1; }
 struct AppendArgs {
     const void *k_new, *v_new;       // [tokens, kv_heads, k_dim / v_dim] bf16, tokens at *_row (elements)
     int64_t k_row, v_row;
-    void *k, *v;                     // the cache (v null: latent); k null: queries alone, beside the kernel in front that
-                                     // writes a cache in 8 bits
+    void *k, *v;                     // the cache (v null: latent)
     int64_t k_page, k_token, k_head; // strides in elements
     int64_t v_page, v_token, v_head;
     const int32_t *table;

@@ -40,7 +40,7 @@ struct AppendPlace {
 __global__ void __launch_bounds__(kAppendThreads, 4) hsp_append_kernel(const __grid_constant__ AppendArgs a, const __grid_constant__ AppendShape g,
                                                                      int per_cta) {
     __shared__ AppendPlace places[kAppendTokens];
-    if (a.k) griddep_wait();  // (queries alone: what is read comes from before the kernel in front)
+    griddep_wait();
     const int first = blockIdx.x * per_cta, here = min(per_cta, a.tokens - first);
     if (threadIdx.x < here) {
         const int i = first + threadIdx.x;
@@ -49,7 +49,7 @@ __global__ void __launch_bounds__(kAppendThreads, 4) hsp_append_kernel(const __g
         const int len = row_ok ? a.lens[row] : 0;
         const int pos = a.positions ? a.positions[i] : len - 1;
         int page = -1;
-        if (a.k && row_ok && pos >= 0 && (pos >> a.page_shift) < a.max_pages)
+        if (row_ok && pos >= 0 && (pos >> a.page_shift) < a.max_pages)
             page = a.table[row * a.table_stride + (pos >> a.page_shift)];
         if (pos >= len) page = -1;  // behind the row's end, as where its growth found no free page (on the way with the table's entry)
         if (a.refs && page >= 0 && page < a.num_pages && a.refs[page] > 1) page = -1;  // others hold it too
@@ -61,7 +61,7 @@ __global__ void __launch_bounds__(kAppendThreads, 4) hsp_append_kernel(const __g
         if (page >= 0 && page < a.num_pages && (angle || a.rot == 0)) {
             p.k = page * a.k_page + line * a.k_token;
             p.v = page * a.v_page + line * a.v_token;
-        } else if (blockIdx.y == 0 && (a.k || !angle)) {
+        } else if (blockIdx.y == 0) {
             atomicCAS(a.err_word, 0, kDeviceErrIndex);
         }
         places[threadIdx.x] = p;
@@ -123,14 +123,13 @@ __global__ void __launch_bounds__(kAppendThreads, 4) hsp_append_kernel(const __g
             *reinterpret_cast<uint4 *>(to[u]) = v[u];
         }
     }
-    if (!a.k) griddep_wait();
     cta_release_and_trigger();
 }
 
 cudaError_t launch_append(const AppendArgs &a, int sms, int pdl, cudaStream_t stream) {
     // pieces of a k or q row: copied ones, then turned ones (a pair of pieces each where the pairs lie apart)
     const int plain = (a.k_dim - a.rot) / 8, per_row = plain + a.rot / (a.interleaved ? 8 : 16);
-    const int per_v = a.v_new ? a.v_dim / 8 : 0, nk = a.k ? a.kv_heads * per_row : 0, nv = a.kv_heads * per_v;
+    const int per_v = a.v_new ? a.v_dim / 8 : 0, nk = a.kv_heads * per_row, nv = a.kv_heads * per_v;
     const int total = nk + nv + (a.q ? a.heads * per_row : 0);
     const AppendShape g{plain, per_row, per_v, nk, nv, total, FastDiv(total), FastDiv(per_row), FastDiv(per_v > 0 ? per_v : 1)};
     // as many CTAs as fit the GPU at once (four per SM): few tokens are spread over several CTAs each,

@@ -13,9 +13,15 @@
 // A CTA looks at `per_cta` tokens of the call, finds the runs of neighbouring tokens that share a row and block (a run
 // belongs to the CTA that holds its first token), and takes (run, side, head) units, each by 8, 32, 128 or 256 lanes, by
 // the longest of its runs: a lane has two 16-byte pieces, requested at once, and keeps their numbers from the search for
-// the largest to the codes (of larger units it reads them twice; where units are few, a cluster of CTAs shares one).  Latency bounds it, so what counts are short code and many lanes: with a warp for 256
-// pieces, eight each, 2047 tokens of 8 heads of 128 columns took 29 us.  The queries are turned by the kernel that does it
-// for a bf16 cache, beside this one.
+// the largest to the codes (of larger units it reads them twice; where units are few, a cluster of CTAs shares one).  Further
+// CTAs of the launch turn the queries.
+//
+// Bytes: two read and one written per number of the cache, two and two per query's.  What bounds it is latency (row,
+// position, length and page before the first new row, a scale between the two looks at the numbers), so what counts are short
+// code and many lanes: with a warp for 256 pieces, eight each, 2047 tokens of 8 heads of 128 columns took 29 us.  One GB300,
+// us: 8 latent tokens with 16 query heads 4.3; 2047 tokens of 8 kv and 32 query heads of 128 columns 20.0 (14.3 without
+// queries, 7.1 at the copy rate); 1501 latent tokens with 16 query heads 19.0 (11.3; 8.7).  With the queries in a second launch
+// beside this one 5.1, 21.4 and 21.7.
 #include <cuda_bf16.h>
 #include <stdint.h>
 
@@ -38,6 +44,10 @@ struct Append8Shape {
     int krow, vrow;                  // pieces of a key and a value row
     int subs;                        // CTAs that share a unit (a cluster), 1: none
     FastDiv by_krow, by_vrow, by_units, by_kv_heads;
+    // CTAs from cache_ctas on turn queries: q_slices of them q_per_cta tokens
+    int cache_ctas, q_per_cta, q_slices;
+    int q_row, q_total;              // pieces (pairs of pieces where the turn's pairs lie apart) of a head and of a token
+    FastDiv by_q_row, by_q_total;
 };
 
 struct Append8Run {
@@ -302,6 +312,63 @@ __device__ __forceinline__ void append8_units(const AppendQ8Args &a, const Appen
     }
 }
 
+// Queries: copied columns, turned columns.  Pieces are requested before their token's position is known, several by a
+// lane at once.  (A token without angles is reported with its keys; its queries stay as they are.)
+template <bool INTERLEAVED>
+__device__ __forceinline__ void append8_queries(const AppendQ8Args &a, const Append8Shape &g, int cta) {
+    constexpr int kMany = INTERLEAVED ? 8 : 4;
+    const int group = cta / g.q_slices, slice = cta - group * g.q_slices;
+    const int64_t first = static_cast<int64_t>(group) * g.q_per_cta;
+    const int here = static_cast<int>(min(static_cast<int64_t>(g.q_per_cta), a.tokens - first));  // (0 or less: none)
+    const int all = here * g.q_total, step = g.q_slices * kAppend8Threads, half = a.rot / 2;
+    const __nv_bfloat16 *const q = static_cast<const __nv_bfloat16 *>(a.q) + first * a.q_row;
+    __nv_bfloat16 *const out = static_cast<__nv_bfloat16 *>(a.q_out) + first * a.qo_row;
+#pragma unroll 1
+    for (int e0 = slice * kAppend8Threads + threadIdx.x; e0 < all; e0 += kMany * step) {
+        uint4 v[kMany], w[INTERLEAVED ? 1 : kMany];
+        int pos[kMany];
+#pragma unroll
+        for (int u = 0; u < kMany; ++u) {
+            const int e = e0 + u * step;
+            pos[u] = -1;
+            if (e >= all) continue;
+            const int tok = g.by_q_total(e), x = e - tok * g.q_total, h = g.by_q_row(x), t = x - h * g.q_row;
+            const __nv_bfloat16 *from = q + tok * a.q_row + h * a.q_head + t * 8;
+            v[u] = *reinterpret_cast<const uint4 *>(from);
+            if (!INTERLEAVED && t >= g.plain) w[INTERLEAVED ? 0 : u] = *reinterpret_cast<const uint4 *>(from + half);
+            const int i = static_cast<int>(first) + tok;
+            if (a.positions) {
+                pos[u] = a.positions[i];
+            } else {
+                const int row = a.rows ? a.rows[i] : i;
+                if (row >= 0 && row < a.num_rows) pos[u] = a.lens[row] - 1;
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < kMany; ++u) {
+            const int e = e0 + u * step;
+            if (e >= all || pos[u] < 0 || pos[u] >= a.max_pos) continue;
+            const int tok = g.by_q_total(e), x = e - tok * g.q_total, h = g.by_q_row(x), t = x - h * g.q_row;
+            __nv_bfloat16 *to = out + tok * a.qo_row + h * a.qo_head + t * 8;
+            if (t >= g.plain) {
+                const float *cs = a.cos_sin + static_cast<int64_t>(pos[u]) * a.rot + (t - g.plain) * (INTERLEAVED ? 4 : 8);
+                const float4 c0 = *reinterpret_cast<const float4 *>(cs), s0 = *reinterpret_cast<const float4 *>(cs + half);
+                if (INTERLEAVED) {
+                    v[u] = turn_pairs(v[u], c0, s0);
+                } else {
+                    const float4 c1 = *reinterpret_cast<const float4 *>(cs + 4), s1 = *reinterpret_cast<const float4 *>(cs + half + 4);
+                    turn_halves(v[u].x, w[INTERLEAVED ? 0 : u].x, c0.x, c0.y, s0.x, s0.y);
+                    turn_halves(v[u].y, w[INTERLEAVED ? 0 : u].y, c0.z, c0.w, s0.z, s0.w);
+                    turn_halves(v[u].z, w[INTERLEAVED ? 0 : u].z, c1.x, c1.y, s1.x, s1.y);
+                    turn_halves(v[u].w, w[INTERLEAVED ? 0 : u].w, c1.z, c1.w, s1.z, s1.w);
+                    *reinterpret_cast<uint4 *>(to + half) = w[INTERLEAVED ? 0 : u];
+                }
+            }
+            *reinterpret_cast<uint4 *>(to) = v[u];
+        }
+    }
+}
+
 __global__ void __launch_bounds__(kAppend8Threads, 3) hsp_append_q8_kernel(const __grid_constant__ AppendQ8Args a, const __grid_constant__ Append8Shape g) {
     __shared__ Append8Run runs[kAppend8Tokens];
     __shared__ int num_runs, longest, first_pos[kAppend8Tokens];
@@ -310,9 +377,12 @@ __global__ void __launch_bounds__(kAppend8Threads, 3) hsp_append_q8_kernel(const
     __shared__ int redi[kAppend8Threads / 32];
     __shared__ float shared[2][3];
     griddep_wait();
-    // (queries are turned by a kernel behind this one, which does not read what this one writes: it may start at once, and
-    // waits for this one at its own end)
-    if (a.q) griddep_launch_dependents();
+    if (static_cast<int>(blockIdx.x) >= g.cache_ctas) {
+        if (a.interleaved) append8_queries<true>(a, g, static_cast<int>(blockIdx.x) - g.cache_ctas);
+        else append8_queries<false>(a, g, static_cast<int>(blockIdx.x) - g.cache_ctas);
+        cta_release_and_trigger();
+        return;
+    }
     const int tid = threadIdx.x, lane = tid & 31;
     const int chunk = blockIdx.x / g.parts, part = blockIdx.x - chunk * g.parts;
     const int first = chunk * g.per_cta, here = min(g.per_cta, a.tokens - first);
@@ -388,11 +458,7 @@ __global__ void __launch_bounds__(kAppend8Threads, 3) hsp_append_q8_kernel(const
     else if (pieces <= 128 * kAppend8Items) append8_units<128>(a, g, runs, num_runs, lines, first_pos, first, part, red, redi, shared);
     else append8_units<256>(a, g, runs, num_runs, lines, first_pos, first, part, red, redi, shared);
     if (g.subs > 1) cluster_sync_all();  // (nobody reads another CTA's memory any more)
-    __syncthreads();
-    if (threadIdx.x == 0) {
-        fence_release_gpu();
-        if (!a.q) griddep_launch_dependents();
-    }
+    cta_release_and_trigger();
 }
 
 cudaError_t launch_append_q8(const AppendQ8Args &a, int sms, int pdl, cudaStream_t stream) {
@@ -420,10 +486,23 @@ cudaError_t launch_append_q8(const AppendQ8Args &a, int sms, int pdl, cudaStream
             parts = subs > 1 ? subs : runs;
         }
     }
-    const Append8Shape g{per_cta, static_cast<int>(parts), (a.k.dim - a.rot) / 8, krow, vrow, subs, FastDiv(krow), FastDiv(vrow), FastDiv(units),
-                         FastDiv(a.kv_heads)};
+    const int64_t cache_ctas = (static_cast<int64_t>(a.tokens) + per_cta - 1) / per_cta * parts;
+    // Queries: a piece per lane where they are few, else twice the CTAs that fit the GPU (2047 tokens with 32 heads of 128 columns: as
+    // many as fit 20.9 us, twice 19.9, four times 20.5; 1501 with 16 of 576 21.4, 18.9, 20.0).
+    const int plain = (a.k.dim - a.rot) / 8, q_row = plain + a.rot / (a.interleaved ? 8 : 16), q_total = a.q ? a.heads * q_row : 1;
+    int64_t q_slices = (q_total + kAppend8Threads - 1) / kAppend8Threads, q_per_cta = 1, q_ctas = 0;
+    if (a.q) {
+        if (a.tokens * q_slices > 2 * fit) q_slices = 2 * fit / a.tokens > 1 ? 2 * fit / a.tokens : 1;
+        if (a.tokens > 2 * fit) q_per_cta = (static_cast<int64_t>(a.tokens) + 2 * fit - 1) / (2 * fit);
+        const int64_t most = (int64_t(1) << 30) / q_total;  // (pieces of a CTA are counted in 32 bits)
+        if (q_per_cta > most) q_per_cta = most;
+        q_ctas = (a.tokens + q_per_cta - 1) / q_per_cta * q_slices;
+        q_ctas = (q_ctas + subs - 1) / subs * subs;         // (whole clusters)
+    }
+    const Append8Shape g{per_cta, static_cast<int>(parts), plain, krow, vrow, subs, FastDiv(krow), FastDiv(vrow), FastDiv(units), FastDiv(a.kv_heads),
+                         static_cast<int>(cache_ctas), static_cast<int>(q_per_cta), static_cast<int>(q_slices), q_row, q_total, FastDiv(q_row), FastDiv(q_total)};
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>((static_cast<int64_t>(a.tokens) + per_cta - 1) / per_cta * parts), 1, 1);
+    cfg.gridDim = dim3(static_cast<unsigned>(cache_ctas + q_ctas), 1, 1);
     cfg.blockDim = dim3(kAppend8Threads, 1, 1);
     cfg.stream = stream;
     cudaLaunchAttribute attrs[2];
@@ -442,28 +521,7 @@ cudaError_t launch_append_q8(const AppendQ8Args &a, int sms, int pdl, cudaStream
     }
     cfg.attrs = attrs;
     cfg.numAttrs = n;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, hsp_append_q8_kernel, a, g);
-    if (e != cudaSuccess || !a.q) return e;
-    AppendArgs q = {};
-    q.k_dim = a.k.dim;
-    q.lens = a.lens;
-    q.rows = a.rows;
-    q.positions = a.positions;
-    q.num_rows = a.num_rows;
-    q.cos_sin = a.cos_sin;
-    q.rot = a.rot;
-    q.max_pos = a.max_pos;
-    q.interleaved = a.interleaved;
-    q.q = a.q;
-    q.q_out = a.q_out;
-    q.q_row = a.q_row;
-    q.q_head = a.q_head;
-    q.qo_row = a.qo_row;
-    q.qo_head = a.qo_head;
-    q.tokens = a.tokens;
-    q.heads = a.heads;
-    q.err_word = a.err_word;
-    return launch_append(q, sms, pdl, stream);
+    return cudaLaunchKernelEx(&cfg, hsp_append_q8_kernel, a, g);
 }
 
 }  // namespace hsp

@@ -601,7 +601,7 @@ typedef struct {
  * New tokens of a row that share a block stand next to each other in the call (in any order): two groups of them
  * in one call would each make the block's scale, and which one stays is not defined.  What a block holds behind its
  * first new token, written by earlier calls, loses its meaning unless this call writes it anew.
- * One kernel launch, two with queries; tokens = 0 succeeds and touches nothing.
+ * One kernel launch; tokens = 0 succeeds and touches nothing.
  */
 proj_status proj_cache_append_q8(const void *k_new, int64_t k_row_stride, const void *v_new, int64_t v_row_stride,
                                  const proj_kv_pages_q8 *kv, const proj_page_index *index, const int32_t *rows,

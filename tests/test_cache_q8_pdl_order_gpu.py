@@ -1,8 +1,7 @@
 """Programmatic-dependent-launch ordering of the kernels of the 8-bit cache, on both sides.  Behind them: a consumer
 that never waits on its grid dependency reads final values (as test_cache_pdl_order_gpu.py has it).  In front: the
-kernels of a call that start while the one before them runs (the attention beside the kernel that splits its queries,
-the turn of queries beside the keys') read inputs that were written right before the call, at addresses where they read
-other values the call before."""
+kernels read inputs that were written right before the call, at addresses where they read other values the call before;
+the attention among them, which starts while the kernel that splits its queries runs."""
 import pytest
 import torch
 
