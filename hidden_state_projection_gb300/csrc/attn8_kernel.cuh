@@ -28,6 +28,16 @@
 // issuer of the products with the values, one that fetches the tiles' scales ahead.  All waits are at mbarriers and
 // bounded.  The queries are split by a small kernel in front, into the images that the instructions read (split by every
 // CTA for itself they took 4 to 10 us: all wait for it, and code that runs once comes from L2 at 100 cycles per 128 bytes).
+//
+// What bounds it (one GB300, cycles at 1.9 GHz).  64 latent heads: operands from shared memory.  A tile of 576 columns is
+// 73 KB written by copies, 147 read for the scores (18 products of 128 x 128 x 32, 65 cycles each), 196 for the values (32 of
+// 128 x 64 x 32, 48 cycles each) and 16 of weights: 3400 cycles at 128 bytes each, 3800 to 4300 measured; the softmax (2500)
+// and the copies hide behind it.  Fewer heads: memory.  Beside the tiles stand 4.5 us from the launch to the first copy, 4 to
+// 5 from there to the first weights (DRAM, and code that runs for the first time), 5 us for each further part (its queries,
+// 128 KB of partial O^T at 28 bytes a cycle) and the join.  With the queries' kernel and the join: 48 sequences up to 6001
+// tokens, 128 heads of 576 columns 58.3 us (bf16 cache 61.9); one of 131071 tokens, 64 heads of 512 columns 34.9 (41.0);
+// 61 sequences up to 4099 tokens, 32 heads over 8 of 128 columns 69.8 (91.4; 325 MB, 65 % of the DRAM's rate); 13 sequences up to
+// 2333 tokens, 28 heads over 4 of 64 columns 16.8; 1 sequence of 77 tokens, 16 heads, not cut 8.0.
 #pragma once
 
 #include <cuda_fp16.h>

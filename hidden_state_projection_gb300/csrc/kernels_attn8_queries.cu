@@ -5,7 +5,8 @@
 // written as the attention's instructions read them from shared memory (attn8_kernel.cuh): rows in the order of the softmax
 // threads' columns, 128 (64) columns to a swizzled line.  A warp takes a head of 512 or 576 columns, two of 128, four of
 // 64; two bytes are read and two written per number.  The attention kernel starts as soon as every CTA here has seen the
-// kernel before complete, and waits for the images alone.
+// kernel before complete, and waits for the images alone: its own start (4.5 us) hides this kernel but for the launch (7 us by
+// itself, with cold caches, for 6144 heads of 576 columns, 4.6 for 64).
 #include <cuda_bf16.h>
 
 #include "attn8_kernel.cuh"

