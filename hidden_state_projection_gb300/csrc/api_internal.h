@@ -37,6 +37,6 @@ proj_status api_encode_5d(const void *ptr, const uint64_t (&dims)[5], const uint
                           const uint32_t (&box)[5], CUtensorMap *out);
 // The same of bytes, boxes 128 or 64 columns wide (128- or 64-byte swizzle).
 proj_status api_encode_codes_5d(const void *ptr, const uint64_t (&dims)[5], const uint64_t (&strides)[4],
-                                const uint32_t (&box)[5], CUtensorMap *out);
+                                const uint32_t (&box)[5], bool joined, CUtensorMap *out);
 
 }  // namespace hsp

@@ -199,9 +199,10 @@ proj_status encode_pages(const void *p, const proj_page_index *ix, int heads, in
     return hsp::api_encode_5d(p, dims, strides, box, out);
 }
 
-// [pages][heads][boxes of `width` columns][tokens][width]: the codes of `dim` columns, token lines of `width` bytes.
+// [pages][heads][boxes of `width` columns][tokens][width]: the codes of `dim` columns, token lines of `width` bytes (joined: next to
+// each other, or to the other boxes').
 proj_status encode_codes(const void *p, const proj_page_index *ix, int heads, int dim, int width, int64_t page, int64_t token, int64_t head,
-                         CUtensorMap *out) {
+                         bool joined, CUtensorMap *out) {
     const int tok = ix->page_size < hsp::kAttn8Tile ? ix->page_size : hsp::kAttn8Tile;
     const uint64_t w = static_cast<uint64_t>(width);
     const uint64_t dims[5] = {w, static_cast<uint64_t>(ix->page_size), static_cast<uint64_t>(dim / width), static_cast<uint64_t>(heads),
@@ -209,7 +210,7 @@ proj_status encode_codes(const void *p, const proj_page_index *ix, int heads, in
     const uint64_t strides[4] = {static_cast<uint64_t>(token), w, heads > 1 ? static_cast<uint64_t>(head) : w,
                                  ix->num_pages > 1 ? static_cast<uint64_t>(page) : w};
     const uint32_t box[5] = {static_cast<uint32_t>(width), static_cast<uint32_t>(tok), 1, 1, 1};
-    return hsp::api_encode_codes_5d(p, dims, strides, box, out);
+    return hsp::api_encode_codes_5d(p, dims, strides, box, joined, out);
 }
 
 proj_status check_pools(const proj_page_pool *pools, int num_pools, hsp::PoolList *out) {
@@ -710,15 +711,16 @@ proj_status proj_paged_attention_q8(const void *q, int64_t q_row_stride, int64_t
     hsp::Attn8LaunchReq r{};
     const int width = kv->v_dim >= 128 ? 128 : 64;
     if ((st = encode_codes(kv->k, index, kv->kv_heads, kv->v ? kv->k_dim : kv->v_dim, width, kv->k_page_stride, kv->k_token_stride,
-                           kv->k_head_stride, &r.tmap_k)) != PROJ_OK)
+                           kv->k_head_stride, !kv->v || kv->k_token_stride == kv->k_dim, &r.tmap_k)) != PROJ_OK)
         return st;
     // the values' map; of a latent cache, the rotary columns of the same pages
     st = PROJ_OK;
     if (kv->v)
-        st = encode_codes(kv->v, index, kv->kv_heads, kv->v_dim, width, kv->v_page_stride, kv->v_token_stride, kv->v_head_stride, &r.tmap_v);
+        st = encode_codes(kv->v, index, kv->kv_heads, kv->v_dim, width, kv->v_page_stride, kv->v_token_stride, kv->v_head_stride,
+                          kv->v_token_stride == kv->v_dim, &r.tmap_v);
     else if (kv->k_dim > kv->v_dim)
         st = encode_codes(static_cast<const char *>(kv->k) + kv->v_dim, index, kv->kv_heads, 64, 64, kv->k_page_stride, kv->k_token_stride,
-                          kv->k_head_stride, &r.tmap_v);
+                          kv->k_head_stride, true, &r.tmap_v);
     else
         r.tmap_v = r.tmap_k;
     if (st != PROJ_OK) return st;
