@@ -137,8 +137,8 @@ struct Attn8Cfg {
 // The window of a column's largest weight in a tile, log2, and where it is put.
 constexpr float kAttn8Up = 8.75f, kAttn8Low = -4.f, kAttn8Aim = 3.f, kAttn8Down = 30.f;
 
-template <int DK, int DV, bool SHARED, int N>
-__global__ void __launch_bounds__(attn8_threads(N), attn8_ctas_per_sm(SHARED, N))
+template <int DK, int DV, bool SHARED, int N, int PER_SM>
+__global__ void __launch_bounds__(attn8_threads(N), PER_SM)
     hsp_attn8_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v, const __grid_constant__ Attn8Args g) {
     using C = Attn8Cfg<DK, DV, SHARED, N>;
     constexpr int T = kAttn8Tile, kC = 4;  // (heads of a softmax thread)

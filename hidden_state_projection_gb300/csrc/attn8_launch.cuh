@@ -10,10 +10,10 @@
 
 namespace hsp {
 
-template <int DK, int DV, bool SHARED, int N>
+template <int DK, int DV, bool SHARED, int N, int PER_SM>
 cudaError_t launch_attn8_variant(const Attn8LaunchReq &r) {
     constexpr int kMaxDev = 64;
-    auto kern = hsp_attn8_kernel<DK, DV, SHARED, N>;
+    auto kern = hsp_attn8_kernel<DK, DV, SHARED, N, PER_SM>;
     static std::atomic<uint64_t> configured[kMaxDev];
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);

@@ -80,20 +80,20 @@ proj_status attn_shape(int heads, int kv_heads, int k_dim, int v_dim, bool laten
 }
 
 // The same of a cache in 8 bits: the same heads and columns, other tiles and places.
-proj_status attn8_shape(int heads, int kv_heads, int k_dim, int v_dim, bool latent, AttnShape *s) {
+proj_status attn8_shape(int batch, int heads, int kv_heads, int k_dim, int v_dim, bool latent, int sms, AttnShape *s) {
     const proj_status st = attn_shape(heads, kv_heads, k_dim, v_dim, latent, s);
     if (st != PROJ_OK) return st;
     const int group_bytes = hsp::kAttn8Tile * (v_dim >= 128 ? 128 : 64);
     const int fixed = hsp::attn8_fixed_smem(k_dim, latent && k_dim > v_dim, s->N);
-    s->per_sm = hsp::attn8_ctas_per_sm(latent, s->N);
+    s->per_sm = hsp::attn8_ctas_per_sm(latent, s->N, static_cast<int64_t>(batch) * kv_heads, sms);
     const int room = s->per_sm == 1 ? kSmemLimit : kSmemPerSm / s->per_sm - kSmemReserved;
     s->slots = (room - fixed) / group_bytes;
     if (s->slots > hsp::kAttnMaxSlots) s->slots = hsp::kAttnMaxSlots;
     if (!latent) s->slots &= ~1;  // (as above)
     s->smem = fixed + s->slots * group_bytes;
-    // (a part's start and end in tiles: 61 sequences up to 4099 tokens, 8 kv heads of 128 columns with 4 heads each, 74.2 us (1), 71.2
-    // (2), 71.1 (3); 48 latent sequences with 128 heads 59.3, 59.3, 60.2; 13 x 4 kv heads of 64 columns 16.7, 17.0, 17.1)
-    s->weight = v_dim == 64 ? 1 : 2;
+    // (a part's start and end in tiles: 61 sequences up to 4099 tokens, 8 kv heads of 128 columns with 4 heads each, 65.3 us (1), 60.3
+    // (2), 59.7 (3), 60.2 (4); 48 latent sequences with 128 heads 58.5, 58.8, 59.3, 59.3; 13 x 4 kv heads of 64 columns 16.7, 17.0, 17.1)
+    s->weight = v_dim == 64 ? 1 : latent ? 2 : 3;
     return PROJ_OK;
 }
 
@@ -679,7 +679,7 @@ proj_status proj_cache_read_q8(const proj_kv_pages_q8 *kv, const proj_page_index
 size_t proj_paged_attention_q8_workspace_bytes(int32_t batch, int32_t heads, int32_t kv_heads, int32_t k_dim, int32_t v_dim,
                                                int32_t latent) {
     AttnShape s;
-    if (attn8_shape(heads, kv_heads, k_dim, v_dim, latent != 0, &s) != PROJ_OK) return 0;
+    if (attn8_shape(batch, heads, kv_heads, k_dim, v_dim, latent != 0, hsp::api_plan_sms(), &s) != PROJ_OK) return 0;
     if (batch < 0) {
         api_fail(PROJ_ERR_INVALID_ARG, "batch=%d is negative", batch);
         return 0;
@@ -695,7 +695,7 @@ proj_status proj_paged_attention_q8(const void *q, int64_t q_row_stride, int64_t
     if (st != PROJ_OK) return st;
     if ((st = check_kv_q8(kv, index)) != PROJ_OK) return st;
     AttnShape s;
-    if ((st = attn8_shape(heads, kv->kv_heads, kv->k_dim, kv->v_dim, kv->v == nullptr, &s)) != PROJ_OK) return st;
+    if ((st = attn8_shape(batch, heads, kv->kv_heads, kv->k_dim, kv->v_dim, kv->v == nullptr, hsp::api_plan_sms(), &s)) != PROJ_OK) return st;
     float scale_log2;
     if ((st = check_attention(index, s, batch, kv->kv_heads, hsp::kAttn8Tile, scale, &scale_log2)) != PROJ_OK) return st;
     if ((st = check_apart_q8(kv, index)) != PROJ_OK) return st;
@@ -729,6 +729,7 @@ proj_status proj_paged_attention_q8(const void *q, int64_t q_row_stride, int64_t
     r.DV = kv->v_dim;
     r.shared = s.shared;
     r.N = s.N;
+    r.per_sm = s.per_sm;
     r.head_tiles = s.head_tiles;
     r.smem_bytes = s.smem;
     r.pdl = opt.pdl;

@@ -156,6 +156,7 @@ struct Attn8Args {
 };
 struct Attn8LaunchReq {
     int DK, DV, shared, N;           // columns, v = columns of k, head tile
+    int per_sm;                      // CTAs
     int head_tiles;                  // grid.x
     int smem_bytes;
     int pdl;
@@ -170,9 +171,13 @@ cudaError_t launch_attn8_latent(const Attn8LaunchReq &r);
 cudaError_t launch_attn8_grouped(const Attn8LaunchReq &r);
 // Four softmax warps for every 16 heads, then the copies, the two issuers, the scales.
 constexpr int attn8_threads(int N) { return 8 * N + 128; }
-// CTAs per SM (see attn_ctas_per_sm; 64 heads fill tensor memory; 61 sequences up to 4099 tokens, 8 kv heads of 128 columns: 71.2 us
-// with two, 69.5 with three).
-constexpr int attn8_ctas_per_sm(bool shared, int N) { return shared || N == 64 ? 1 : N == 16 ? 3 : 2; }
+// CTAs per SM (see attn_ctas_per_sm; 64 heads fill tensor memory).  16 grouped heads: three where there is a part for every SM
+// from the start, else two, with more registers and longer rings (sequences x kv heads x columns, up to so many tokens, us with
+// two and three: 61 x 8 x 128, 4099 64.0 and 60.0; 40 x 8 x 64, 1000 25.2 and 23.6; 24 x 8 x 128, 1000 18.5 and 18.2; 12 x 8 x 128, 4000
+// 23.5 and 24.6; 16 x 8 x 128, 2000 19.7 and 22.7; 13 x 4 x 64, 2333 15.4 and 16.7; 1 x 8 x 128, 60000 32.5 and 34.6).
+inline int attn8_ctas_per_sm(bool shared, int N, int64_t sequence_heads, int sms) {
+    return shared || N == 64 ? 1 : N == 16 && sequence_heads >= sms ? 3 : 2;
+}
 constexpr int kAttn8RopeBytes = kAttn8Tile * 64;
 // Places of the rotary boxes: one where the queries of 64 heads leave no more beside two whole tiles.
 constexpr int attn8_rope_slots(int N) { return N == 64 ? 1 : 2; }

@@ -209,6 +209,14 @@ def test_many_sequences(hsp, latent):
     check(hsp, make(lens, heads, kv, dk, latent, 16, 3), dk ** -0.5, dv)
 
 
+@pytest.mark.parametrize("page", [16, 128])
+@pytest.mark.parametrize("d", [64, 128])
+def test_a_part_for_every_sm(hsp, d, page):
+    """From 152 sequences and kv heads on three CTAs share an SM: cut and whole ones, with shorter rings."""
+    lens = [(331 * i) % 1500 for i in range(38)] + [4000, 0]
+    check(hsp, make(lens, 20, 4, d, False, page, 9), d ** -0.5, d)
+
+
 @pytest.mark.parametrize("latent", [True, False])
 def test_many_short_sequences_are_not_cut(hsp, latent):
     """Tables of at most 256 tokens per row: no join."""
