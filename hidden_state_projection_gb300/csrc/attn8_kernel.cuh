@@ -36,8 +36,8 @@
 // 5 from there to the first weights (DRAM, and code that runs for the first time), 5 us for each further part (its queries,
 // 128 KB of partial O^T at 28 bytes a cycle) and the join.  With the queries' kernel and the join: 48 sequences up to 6001
 // tokens, 128 heads of 576 columns 58.3 us (bf16 cache 61.9); one of 131071 tokens, 64 heads of 512 columns 34.9 (41.0);
-// 61 sequences up to 4099 tokens, 32 heads over 8 of 128 columns 69.8 (91.4; 325 MB, 65 % of the DRAM's rate); 13 sequences up to
-// 2333 tokens, 28 heads over 4 of 64 columns 16.8; 1 sequence of 77 tokens, 16 heads, not cut 8.0.
+// 61 sequences up to 4099 tokens, 32 heads over 8 of 128 columns 61.0 (91.4; 253 MB, 56 % of the DRAM's rate); 13 sequences up to
+// 2333 tokens, 28 heads over 4 of 64 columns 15.3; 1 sequence of 77 tokens, 16 heads, not cut 8.0.
 #pragma once
 
 #include <cuda_fp16.h>
