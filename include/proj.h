@@ -599,7 +599,8 @@ typedef struct {
  * rounded only here: x is the exact sum of its two fp32 products.  Values that are NaN, infinite or beyond 448 * 2^60 do
  * not count for s and become NaN.
  * New tokens of a row that share a block stand next to each other in the call (in any order): two groups of them
- * in one call would each make the block's scale, and which one stays is not defined.  What a block holds behind its
+ * in one call would each make the block's scale, and which one stays is not defined.  (A place named twice by neighbours
+ * holds numbers of either token, under a scale for both.)  What a block holds behind its
  * first new token, written by earlier calls, loses its meaning unless this call writes it anew.
  * One kernel launch; tokens = 0 succeeds and touches nothing.
  */

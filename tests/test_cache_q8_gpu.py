@@ -407,3 +407,62 @@ def test_no_tokens(hsp):
     k, _ = hsp.cache_read_q8(c.k, None, c.ks, None, c.table, c.lens, rows=ints([]), positions=ints([]))
     assert k.shape == (0, 1, 64)
     c.same(m)
+
+
+def test_a_place_named_twice(hsp):
+    """Neighbours in the call: the same row twice is that row; the scale is that of both."""
+    c = Cache8(2, 2, 16, 8, 2, 64, 64, 21)
+    c.lens.copy_(ints([20, 9]))
+    kn, vn = new_rows(c.g, 4, 2, 64), new_rows(c.g, 4, 2, 64)
+    kn[2], vn[2] = kn[1], vn[1]
+    append(hsp, c, [0, 0, 0, 1], [16, 18, 18, 3], 64, 2, 64, kn=kn, vn=vn)
+    kn[2] *= 64                                                        # (another row: the place holds numbers of either)
+    hsp.cache_append_q8(kn, vn, c.k, c.v, c.ks, c.vs, c.table, c.lens, rows=ints([0, 0, 0, 1]), positions=ints([16, 18, 18, 3]))
+    hsp.check_device_error()
+    got, _ = hsp.cache_read_q8(c.k, c.v, c.ks, c.vs, c.table, c.lens, rows=ints([0]), positions=ints([18]))
+    for h in range(2):
+        s = float(c.ks[int(c.table[0, 1]), 0, h])
+        either = [nearest(numbers(kn)[i, h] / s) * s for i in (1, 2)]
+        assert float(numbers(kn)[2, h].max()) <= 448 * s
+        x = numbers(got)[0, h]
+        assert ((x == either[0]) | (x == either[1])).all()
+
+
+def test_without_dependent_launches_and_from_threads(hsp):
+    """pdl off, then four threads at once, each with a cache and a stream of its own: the same bytes as alone."""
+    import threading
+
+    def work(seed, stream):
+        with torch.cuda.stream(stream):
+            c = Cache8(4, 4, 32, 16, 2, 128, 128, seed)
+            c.lens.copy_(ints([128] * 4))
+            rows, pos = ints([i // 60 for i in range(240)]), ints([i % 60 + 3 for i in range(240)])
+            kn, vn, q, cs = new_rows(c.g, 240, 2, 128), new_rows(c.g, 240, 2, 128), new_rows(c.g, 240, 8, 128), angles(128, 128)
+            out = []
+            for _ in range(5):
+                qt = hsp.cache_append_q8(kn, vn, c.k, c.v, c.ks, c.vs, c.table, c.lens, rows=rows, positions=pos, cos_sin=cs, q=q)
+                read = hsp.cache_read_q8(c.k, c.v, c.ks, c.vs, c.table, c.lens, rows=rows, positions=pos)
+                att = hsp.paged_attention_q8(qt[::60].contiguous(), c.k, c.v, c.ks, c.vs, c.table, c.lens, 0.09)
+                out += [qt, *read, att]
+            stream.synchronize()
+        return [t.cpu() for t in out]
+
+    hsp.set_options(pdl=False)
+    try:
+        want = [work(seed, torch.cuda.current_stream()) for seed in range(4)]
+    finally:
+        hsp.set_options(pdl=True)
+    got, streams = [None] * 4, [torch.cuda.Stream() for _ in range(4)]
+
+    def run(i):
+        got[i] = work(i, streams[i])
+
+    torch.cuda.synchronize()
+    threads = [threading.Thread(target=run, args=(i,)) for i in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    hsp.check_device_error()
+    for a, b in zip(want, got):
+        assert b is not None and all(torch.equal(x.view(torch.uint8), y.view(torch.uint8)) for x, y in zip(a, b))
