@@ -642,7 +642,7 @@ proj_status proj_paged_attention_q8(const void *q, int64_t q_row_stride, int64_t
                                     proj_stream_t stream);
 
 /* Workspace bytes of proj_paged_attention_q8 (host only; 0 when the sizes are not supported, with
- * proj_last_error_string saying why). */
+ * proj_last_error_string saying why).  They do not fall with the batch: a workspace for the largest serves all. */
 size_t proj_paged_attention_q8_workspace_bytes(int32_t batch, int32_t heads, int32_t kv_heads, int32_t k_dim,
                                                int32_t v_dim, int32_t latent);
 

@@ -97,6 +97,12 @@ def test_workspace_bytes(hsp):
             hsp.paged_attention_q8_workspace_bytes(*args)
 
 
+def test_workspace_of_a_larger_batch_serves_a_smaller_one(hsp):
+    for heads, kv, dk, dv, latent in ((16, 1, 576, 512, True), (128, 1, 512, 512, True), (32, 8, 128, 128, False), (28, 4, 64, 64, False), (80, 2, 64, 64, False)):
+        sizes = [hsp.paged_attention_q8_workspace_bytes(b, heads, kv, dk, dv, latent) for b in (0, 1, 2, 18, 19, 20, 37, 38, 39, 151, 152, 153, 4000)]
+        assert sizes == sorted(sizes) and sizes[-1] > sizes[0]
+
+
 def test_python_refusals(hsp):
     k, ks = torch.zeros(4, 16, 1, 576, dtype=torch.float8_e4m3fn), torch.ones(4, 1, 1)
     table, lens, q = torch.zeros(2, 2, dtype=torch.int32), torch.zeros(2, dtype=torch.int32), torch.zeros(2, 16, 576, dtype=torch.bfloat16)
