@@ -21,8 +21,17 @@
 // rescales O^T; what a tile's rounding leaves out is small beside the largest weight of the tile and of the row,
 // whatever weights other tiles have (a first token with nearly all the weight before a long tail).  Normal scores of
 // variance 3 in 64 columns move a point in 2 tiles of 133 (in 54 with a window of 2^0.5 to 2^8.75).  Downwards m stops 30
-// below its highest point.  O^T is divided by l = sum (Wh + Wl)_t / vs_t, so the rounding that all of a row's weight has in
-// common cancels; lse takes the sum u of the unrounded weights.  Sums and statistics are fp32.
+// below its highest point.
+//
+// Sums.  A token whose weight is nothing beside the others' because its values are (a block of zeros has the scale 2^-60)
+// still has its probability, and that counts in what O^T is divided by: l = u + sum over w_t >= 2^-6 of (Wh + Wl - w)_t / vs_t,
+// u = sum w_t / vs_t of the unrounded weights.  So a large weight counts as it is rounded, and the rounding that all of a row's
+// weight has in common cancels; a small one counts as it is, with the 2^-22 of fp32's exponential.  (Summed as rounded, small
+// weights took their probabilities with them: of two tokens with equal scores, one with values of zero, the other came out
+// whole.)  What is lost is what fp32 has no number for: weights below 2^-126 of the reference point, 2^-129 of the row's largest, which
+// takes values' scales more than 2^90 apart.  (With those summed apart, and sums moved from point to point in two steps, the
+// grouped batch below took 66.8 us.)  The mask of the large weights takes 0.5 of the 128 heads' 59.  lse takes u.  Sums
+// and statistics are fp32.
 //
 // Warps: four for the softmax of every 16 heads (they also carry O^T out), a copy producer, an issuer of the scores, an
 // issuer of the products with the values, one that fetches the tiles' scales ahead.  All waits are at mbarriers and
@@ -136,6 +145,8 @@ struct Attn8Cfg {
 
 // The window of a column's largest weight in a tile, log2, and where it is put.
 constexpr float kAttn8Up = 8.75f, kAttn8Low = -4.f, kAttn8Aim = 3.f, kAttn8Down = 30.f;
+// Weights from here on count in the sum as they are rounded.
+constexpr float kAttn8Large = 0x1p-6f;
 
 template <int DK, int DV, bool SHARED, int N, int PER_SM>
 __global__ void __launch_bounds__(attn8_threads(N), PER_SM)
@@ -513,13 +524,13 @@ __global__ void __launch_bounds__(attn8_threads(N), PER_SM)
         while (attn_next_segment<T>(a, ln, walk, sg)) {
             const bool begins = sg.t0 == 0, ends = sg.t0 + sg.n == sg.tiles;
             float m[kC];             // reference points
-            float2 l[kC / 2], u[kC / 2];  // sums of the rounded and the unrounded weights
+            float2 u[kC / 2], d[kC / 2];  // sums of the unrounded weights, and of what the rounding of the large ones adds
             uint32_t lowest = unused;     // columns whose reference point goes no further down
             float mine = 0.f, peak = 0.f;  // column tid's point, and its highest
 #pragma unroll
             for (int e = 0; e < kC; ++e) m[e] = 0.f;
 #pragma unroll
-            for (int j = 0; j < kC / 2; ++j) l[j] = u[j] = make_float2(0.f, 0.f);
+            for (int j = 0; j < kC / 2; ++j) u[j] = d[j] = make_float2(0.f, 0.f);
             await(&unit_full[seg & 3u], seg >> 2);
             float2 unit[kC / 2];     // of the heads' queries
 #pragma unroll
@@ -627,13 +638,13 @@ __global__ void __launch_bounds__(attn8_threads(N), PER_SM)
 #pragma unroll
                     for (int j = 0; j < kC / 2; ++j) {
                         const float2 f = *reinterpret_cast<const float2 *>(fac + h0 + 2 * j), n = *reinterpret_cast<const float2 *>(points + h0 + 2 * j);
-                        const float2 d = *reinterpret_cast<const float2 *>(bottom + h0 + 2 * j);
-                        l[j] = mul2(l[j], f);
+                        const float2 low = *reinterpret_cast<const float2 *>(bottom + h0 + 2 * j);
+                        d[j] = mul2(d[j], f);
                         u[j] = mul2(u[j], f);
                         m[2 * j] = n.x;
                         m[2 * j + 1] = n.y;
-                        if (d.x != 0.f) lowest |= 1u << 2 * j;
-                        if (d.y != 0.f) lowest |= 2u << 2 * j;
+                        if (low.x != 0.f) lowest |= 1u << 2 * j;
+                        if (low.y != 0.f) lowest |= 2u << 2 * j;
                     }
                     if (k > 0) {
 #pragma unroll 1
@@ -677,11 +688,13 @@ __global__ void __launch_bounds__(attn8_threads(N), PER_SM)
                         p = make_float2(fast_exp2(p.x), fast_exp2(p.y));
                         const __half2 p16 = __floats2half2_rn(p.x, p.y);
                         h8[j] = half2_to_e4m3x2(p16);
-                        const __half2 h16 = e4m3x2_to_half2(h8[j]);
-                        l8[j] = half2_to_e5m2x2(__hsub2(p16, h16));
-                        const float2 w = __half22float2(__hadd2(h16, e5m2x2_to_half2(l8[j])));
+                        const __half2 rest = __hsub2(p16, e4m3x2_to_half2(h8[j]));
+                        l8[j] = half2_to_e5m2x2(rest);
+                        // Wh + Wl - w (w as fp16: the 2^-11 between them does not cancel), exact
+                        const __half2 off = __hsub2(e5m2x2_to_half2(l8[j]), rest);
+                        const uint32_t large = __hge2_mask(p16, __float2half2_rn(kAttn8Large)) & *reinterpret_cast<const uint32_t *>(&off);
                         u[j] = fma2(p, make_float2(v, v), u[j]);
-                        l[j] = fma2(w, make_float2(v, v), l[j]);
+                        d[j] = fma2(__half22float2(*reinterpret_cast<const __half2 *>(&large)), make_float2(v, v), d[j]);
                     }
                     wh[r] = __byte_perm(h8[0], h8[1], 0x5410);
                     wl[r] = __byte_perm(l8[0], l8[1], 0x5410);
@@ -699,7 +712,7 @@ __global__ void __launch_bounds__(attn8_threads(N), PER_SM)
                 tc_fence_before_sync();
                 warp_arrive(p_full);
             }
-            // ---- the part is done: l (and u) over the tokens, then O^T out of tensor memory ----
+            // ---- the part is done: its sums over the tokens, then O^T out of tensor memory ----
             await(pv_done, static_cast<uint32_t>(i - 1));  // (red and fac lie where the weights did)
             tc_fence_after_sync();
             auto over_tokens = [&](float2 (&v)[kC / 2]) {  // a warp's sums to `red`
@@ -710,13 +723,15 @@ __global__ void __launch_bounds__(attn8_threads(N), PER_SM)
                         v[j].x += __shfl_xor_sync(0xffffffffu, v[j].x, d);
                         v[j].y += __shfl_xor_sync(0xffffffffu, v[j].y, d);
                     }
-                softmax_sync<C::kSoft>();  // the last tile's maxima and factors (l), the sums l (u) have been read
+                softmax_sync<C::kSoft>();  // the last tile's maxima and factors, the sums l (u) have been read
                 if (lane < 4) {
 #pragma unroll
                     for (int j = 0; j < kC / 2; ++j) *reinterpret_cast<float2 *>(red + wq * N + h0 + 2 * j) = v[j];
                 }
             };
-            over_tokens(l);
+#pragma unroll
+            for (int j = 0; j < kC / 2; ++j) add2(d[j], u[j]);
+            over_tokens(d);
             if (wq == 0 && lane < 4) {
 #pragma unroll
                 for (int j = 0; j < kC / 2; ++j) *reinterpret_cast<float2 *>(fac + h0 + 2 * j) = make_float2(m[2 * j], m[2 * j + 1]);

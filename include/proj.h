@@ -631,9 +631,13 @@ proj_status proj_cache_read_q8(const proj_kv_pages_q8 *kv, const proj_page_index
  *   workspace  device, 16-byte aligned, at least proj_paged_attention_q8_workspace_bytes bytes: always needed (the
  *              queries are laid out there), needs no initialisation and keeps nothing
  * Scores are exact products summed in fp32, of queries in two 8-bit pieces (exact but for numbers below 2^-21 of the
- * head's largest); the weights are rounded to two 8-bit pieces (2^-7 at most, of weights below a hundredth or so of
- * their tile's largest more) and the result, once, to bf16.  Two kernel launches, three where a table row holds more
- * than PROJ_UNCUT_TOKENS tokens.
+ * head's largest).  What multiplies token t's codes is its probability times the scale of its values, w_t = p_t vs_t, rounded to
+ * two 8-bit pieces: off by 2^-7 + 2^-11 of itself and, where it is below a quarter of the largest of its 128 tokens', by
+ * 2^-9 of that largest or 2^-16 of the row's, whichever is less (and 2^-43 of the row's).  The sum that the result is
+ * divided by is that of the p_t, each off by 2^-7 + 2^-11 of itself at most, whatever the scale of its values (a token of
+ * zeros counts too); only one whose w_t is below 2^-120 of the row's largest may be missing.  lse has the unrounded sum.
+ * The result is rounded, once, to bf16.
+ * Two kernel launches, three where a table row holds more than PROJ_UNCUT_TOKENS tokens.
  */
 proj_status proj_paged_attention_q8(const void *q, int64_t q_row_stride, int64_t q_head_stride,
                                     const proj_kv_pages_q8 *kv, const proj_page_index *index,
