@@ -428,6 +428,7 @@ __global__ void __launch_bounds__(kAppend8Threads, 3) hsp_append_q8_kernel(const
         }
         bool bad = page < 0 || page >= a.num_pages || line_of(pos, len) < 0;
         if (page < 0 || page >= a.num_pages) page = -1;
+        if (a.rot > 0 && (pos & ~page_mask) >= a.max_pos) page = -1;  // no token of this page is written: no angle may be read either
         if (a.refs && page >= 0 && a.refs[page] > 1) page = -1, bad = true;  // others hold it too
         if (part == 0 && lane < here && bad) atomicCAS(a.err_word, 0, kDeviceErrIndex);
         if (lane < here) lines[lane] = line_of(pos, len);
