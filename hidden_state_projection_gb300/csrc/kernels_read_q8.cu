@@ -33,6 +33,16 @@ __device__ __forceinline__ void store32(void *p, const uint32_t (&o)[8]) {
                  : "memory");
 }
 
+// Two codes times s, in bf16: a product of more than fp32's 24 bits is cut off and its last bit set (to odd), so that the rounding
+// behind it is that of the exact product.  (A function of its own: in line it made the usual case's code longer, 2.4 -> 2.5 us for
+// 77 tokens.)
+__device__ __noinline__ uint32_t products_odd(uint32_t codes, float s) {
+    const float2 x = __half22float2(e4m3x2_to_half2(codes));
+    const float a = __fmul_rz(x.x, s), b = __fmul_rz(x.y, s);
+    const uint32_t more_a = __fmaf_rn(x.x, s, -a) != 0.f ? 1u : 0u, more_b = __fmaf_rn(x.y, s, -b) != 0.f ? 1u : 0u;
+    return pack_bf16(__uint_as_float(__float_as_uint(a) | more_a), __uint_as_float(__float_as_uint(b) | more_b));
+}
+
 __global__ void __launch_bounds__(kRead8Threads, 4) hsp_read_q8_kernel(const __grid_constant__ ReadQ8Args a, const __grid_constant__ Read8Shape g) {
     __shared__ Read8Place places[2][kRead8Tokens];
     griddep_wait();
@@ -90,11 +100,15 @@ __global__ void __launch_bounds__(kRead8Threads, 4) hsp_read_q8_kernel(const __g
                 const int tok = by(e), x = e - tok * per;
                 const uint32_t w[4] = {c[u].x, c[u].y, c[u].z, c[u].w};
                 uint32_t o[8];
+                if (__builtin_expect((__float_as_uint(scale[u]) & 15u) == 0u, true)) {  // (a code has four bits: the product is exact)
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const float2 lo = __half22float2(e4m3x2_to_half2(w[k] & 0xffffu)), hi = __half22float2(e4m3x2_to_half2(w[k] >> 16));
-                    o[2 * k] = pack_bf16(lo.x * scale[u], lo.y * scale[u]);
-                    o[2 * k + 1] = pack_bf16(hi.x * scale[u], hi.y * scale[u]);
+                    for (int k = 0; k < 8; ++k) {
+                        const float2 x = __half22float2(e4m3x2_to_half2(k & 1 ? w[k / 2] >> 16 : w[k / 2] & 0xffffu));
+                        o[k] = pack_bf16(x.x * scale[u], x.y * scale[u]);
+                    }
+                } else {
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) o[k] = products_odd(k & 1 ? w[k / 2] >> 16 : w[k / 2] & 0xffffu, scale[u]);
                 }
                 __nv_bfloat16 *to = out + tok * out_row + x * 16;  // (a token's heads lie one after another)
                 if (g.wide) {
