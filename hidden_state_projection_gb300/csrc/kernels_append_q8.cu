@@ -6,6 +6,7 @@
 //       stand in front of them;  code = round(x / s);
 //   where s grew, the codes in front are rounded to it (a shift of their exponents, exact unless the result
 //   is below the smallest normal code).
+// Under a scale that is another writer's and no power of two the quotients are made in 64 bits, element by element.
 // A turned value is rounded once, from the exact sum of its two products, so a code does not depend on the order of
 // operations: the sum is made in fp32, and again exactly (dot2_odd) where its error could carry it over the border between
 // two codes or two scales.
@@ -57,6 +58,51 @@ struct Append8Run {
 };
 
 __device__ __forceinline__ int append8_pos(const AppendQ8Args &a, int i, int len) { return a.positions ? a.positions[i] : len - 1; }
+
+// (a c + b d) / s rounded to odd (NaN where the sum is beyond 448 * 2^60): in 64 bits the products (of 32 bits) are exact, the sum is
+// made odd, so that it lies on the exact sum's side of s times any number of few bits, and the quotient by its remainder's sign.
+static __device__ __noinline__ float quotient_odd(float a, float c, float b, float d, float s) {
+    const double p = static_cast<double>(a) * c, q = static_cast<double>(b) * d, t = s;
+    auto odd64 = [](double h, double rest) {  // h, moved towards the rest unless its last bit is set
+        long long u = __double_as_longlong(h);
+        if (rest != 0. && (u & 1) == 0 && h != 0.) u += (rest > 0.) == (h > 0.) ? 1 : -1;
+        return __longlong_as_double(u);
+    };
+    const double sum = __dadd_rn(p, q), bb = __dsub_rn(sum, p);
+    const double h = odd64(sum, __dadd_rn(__dsub_rn(p, __dsub_rn(sum, bb)), __dsub_rn(q, bb)));
+    if (!(fabs(h) <= static_cast<double>(kQ8Top * 0x1p60f))) return __uint_as_float(0x7fc00000u);
+    const double r = __ddiv_rn(h, t), y = odd64(r, __fma_rn(-r, t, h));
+    const float f = __double2float_rz(y);
+    return __uint_as_float(__float_as_uint(f) | (static_cast<double>(f) != y ? 1u : 0u));
+}
+
+// The codes of pieces e, e + step, ... below `items` of a run under a scale that is no power of two: what another writer left in a
+// block whose new tokens ask for no more.  Columns from `turned` on are turned.
+static __device__ __noinline__ void append8_divided(const AppendQ8Args &a, const __nv_bfloat16 *rows, int64_t stride, int per, int turned, const int16_t *lines,
+                                             int pos0, uint8_t *codes, int64_t token, float scale, int e, int step, int items) {
+    const int half = a.rot / 2;
+#pragma unroll 1
+    for (; e < items; e += step) {
+        const int j = e / per, line = lines[j];
+        if (line < 0) continue;
+        const __nv_bfloat16 *row = rows + j * stride;
+#pragma unroll 1
+        for (int x = (e - j * per) * 8, end = x + 8; x < end; ++x) {
+            float c = 1.f, s = 0.f, w = 0.f;
+            if (x >= turned) {
+                const int y = x - turned, pair = a.interleaved ? y >> 1 : y < half ? y : y - half;
+                const bool second = a.interleaved ? (y & 1) != 0 : y >= half;
+                const int away = a.interleaved ? 1 : half;
+                const float *cs = a.cos_sin + static_cast<int64_t>(pos0 + line) * a.rot;
+                c = cs[pair];
+                s = cs[half + pair];
+                w = second ? __bfloat162float(row[x - away]) : -__bfloat162float(row[x + away]);
+            }
+            const float y = quotient_odd(__bfloat162float(row[x]), c, w, s, scale);
+            codes[line * token + x] = static_cast<uint8_t>(float2_to_e4m3x2(y, 0.f) & 0xffu);
+        }
+    }
+}
 
 // A group of G lanes (8, 32, 128 or the CTA's 256) makes one unit's scale and codes.
 template <int G>
@@ -201,10 +247,15 @@ struct Append8Unit {
         // The largest number lies between lo and hi (fast sums); they ask for the same scale unless it lies at the border of
         // two, and then it is sought again, exactly.
         enum { kLargest, kLargestExact, kCodes } phase = kLargest;
-        float lo, hi, inv = 0.f;
+        float lo, hi, inv = 0.f;  // inv: 1 / scale (below zero: minus the scale, which is no power of two)
         int line;  // first new line of the block
 #pragma unroll 1
         for (;;) {
+            if (inv < 0.f) {
+                append8_divided(a, rows, stride, per, is_k ? g.plain * 8 : s.dim, lines, pos0, codes, s.token, -inv, t + sub * G,
+                                G * (G == 256 ? g.subs : 1), items);
+                return;
+            }
             lo = hi = 0.f;
             line = block;
 #pragma unroll 1
@@ -266,7 +317,7 @@ struct Append8Unit {
             phase = kCodes;
             float now = two_to(q8_exponent(hi));
             if (line > 0 && old >= now) now = old;  // (also where another CTA of the cluster has written it already)
-            inv = 1.f / now;                        // (exact for the powers of two that this kernel writes)
+            inv = (__float_as_uint(now) & 0x7fffffu) == 0 ? 1.f / now : -now;  // (1 / now is exact)
             if (sub != 0) continue;
             if (line > 0 && now > old) {
                 // the codes in front, under the new scale
@@ -281,7 +332,9 @@ struct Append8Unit {
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
                         const float2 p = __half22float2(e4m3x2_to_half2(w[k] & 0xffffu)), q = __half22float2(e4m3x2_to_half2(w[k] >> 16));
-                        w[k] = float2_to_e4m3x2(p.x * by_new, p.y * by_new) | float2_to_e4m3x2(q.x * by_new, q.y * by_new) << 16;
+                        // (to odd: an old scale of another writer's may have more bits than a product with it holds)
+                        w[k] = float2_to_e4m3x2(product_odd(p.x, by_new), product_odd(p.y, by_new)) |
+                               float2_to_e4m3x2(product_odd(q.x, by_new), product_odd(q.y, by_new)) << 16;
                     }
                     *at = c;
                 }

@@ -33,14 +33,11 @@ __device__ __forceinline__ void store32(void *p, const uint32_t (&o)[8]) {
                  : "memory");
 }
 
-// Two codes times s, in bf16: a product of more than fp32's 24 bits is cut off and its last bit set (to odd), so that the rounding
-// behind it is that of the exact product.  (A function of its own: in line it made the usual case's code longer, 2.4 -> 2.5 us for
-// 77 tokens.)
+// Two codes times s, in bf16, where fp32 does not hold the products.  (A function of its own: in line it made the usual case's code longer,
+// 2.4 -> 2.5 us for 77 tokens.)
 __device__ __noinline__ uint32_t products_odd(uint32_t codes, float s) {
     const float2 x = __half22float2(e4m3x2_to_half2(codes));
-    const float a = __fmul_rz(x.x, s), b = __fmul_rz(x.y, s);
-    const uint32_t more_a = __fmaf_rn(x.x, s, -a) != 0.f ? 1u : 0u, more_b = __fmaf_rn(x.y, s, -b) != 0.f ? 1u : 0u;
-    return pack_bf16(__uint_as_float(__float_as_uint(a) | more_a), __uint_as_float(__float_as_uint(b) | more_b));
+    return pack_bf16(product_odd(x.x, s), product_odd(x.y, s));
 }
 
 __global__ void __launch_bounds__(kRead8Threads, 4) hsp_read_q8_kernel(const __grid_constant__ ReadQ8Args a, const __grid_constant__ Read8Shape g) {

@@ -43,6 +43,13 @@ __device__ __forceinline__ int q8_exponent(float amax) {
     return max(kQ8MinExp, min(kQ8MaxExp, e));
 }
 
+// x * s cut off to fp32 and, where something was cut off, its last bit set (rounded to odd): the rounding to fewer bits behind it is that of
+// the exact product.
+__device__ __forceinline__ float product_odd(float x, float s) {
+    const float p = __fmul_rz(x, s);
+    return __uint_as_float(__float_as_uint(p) | (__fmaf_rn(x, s, -p) != 0.f ? 1u : 0u));
+}
+
 // a c + b d rounded to odd, two at a time: floats whose last bits say whether something was cut off, so that the rounding to
 // a code (which is shorter by far) is that of the exact sum.  The products' errors and the sum's are found with fused
 // multiply-adds and the two-sum of Knuth (a few bits beyond 2^-70 of the larger product aside).
