@@ -166,7 +166,8 @@ struct Append8Unit {
             for (int e = 0; e < 4; ++e) most = fmaxf(most, fmaxf(fabsf(v[e].x), fabsf(v[e].y)));
         };
         largest();
-        if (most > kQ8Top * 0x1p60f) {  // out of range: NaN, and none that counts
+        if (most > kQ8Top * 0x1p60f * (1.f - 0x1p-20f)) {  // out of range: NaN, and none that counts (a fast sum may lie on either side)
+            if (size > 0.f) size = INFINITY;
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 if (fabsf(v[e].x) > kQ8Top * 0x1p60f) v[e].x = __uint_as_float(0x7fc00000u);
@@ -292,7 +293,7 @@ struct Append8Unit {
                         const float slack = exact ? 0.f : size[k] * inv * 0x1p-22f;
                         c.x = codes4(slack, 0);
                         c.y = codes4(slack, 2);
-                        if (slack > 0.f) near |= c.x != codes4(-slack, 0) || c.y != codes4(-slack, 2);
+                        if (slack > 0.f) near |= slack > kQ8Top || c.x != codes4(-slack, 0) || c.y != codes4(-slack, 2);
                         *reinterpret_cast<uint2 *>(codes + static_cast<int64_t>(where[k]) * s.token + column[k]) = c;
                     }
                     if (!near) break;
