@@ -91,9 +91,13 @@ proj_status attn8_shape(int batch, int heads, int kv_heads, int k_dim, int v_dim
     if (s->slots > hsp::kAttnMaxSlots) s->slots = hsp::kAttnMaxSlots;
     if (!latent) s->slots &= ~1;  // (as above)
     s->smem = fixed + s->slots * group_bytes;
-    // (a part's start and end in tiles: 61 sequences up to 4099 tokens, 8 kv heads of 128 columns with 4 heads each, 65.3 us (1), 60.3
-    // (2), 59.7 (3), 60.2 (4); 48 latent sequences with 128 heads 58.5, 58.8, 59.3, 59.3; 13 x 4 kv heads of 64 columns 16.7, 17.0, 17.1)
-    s->weight = v_dim == 64 ? 1 : latent ? 2 : 3;
+    // A part's start and end in tiles.  us with 1, 2 and 3 (sequences x kv heads x heads of each, up to so many tokens), latent: 8 x 16 heads, 2000
+    // 17.0, 16.5, 16.3; 40 x 16, 3000 23.3, 22.2, 23.0; 100 x 64, 2000 45.9, 42.1, 43.3; 48 x 128, 6001 62.9, 59.7, 59.4; 100 x 128, 700 44.9, 44.9,
+    // 42.1; 64 columns: 13 x 4 x 7, 2333 14.9, 15.7, 15.9; 16 x 8 x 4, 2000 19.0, 16.9, 17.3; 61 x 8 x 4, 4099 58.7, 55.4, 55.3; 60 x 2 x 24, 2000
+    // 21.4, 20.2, 21.3; 60 x 2 x 64, 2000 29.6, 27.4, 25.9; 128 columns: 13 x 4 x 7, 2333 15.8, 16.4, 16.6; 18 x 8 x 8, 1000 16.8, 15.7, 16.7; 61 x 8 x 4,
+    // 4099 67.5, 62.4, 61.9; 200 x 8 x 4, 600 72.4, 71.5, 72.3; 30 x 5 x 1, 6000 38.6, 35.0, 34.3.  Of 49 shapes 2 is the best or within 2 % of
+    // it in 42, 3 in 37 and 1 in 19.
+    s->weight = 2;
     return PROJ_OK;
 }
 
