@@ -605,11 +605,13 @@ def cache_copy_pages(pools: Sequence[torch.Tensor], src, dst, stream=None) -> No
 def paged_attention_q8_workspace_bytes(batch: int, heads: int, kv_heads: int, k_dim: int, v_dim: int, latent: bool) -> int:
     """Workspace bytes of proj_paged_attention_q8 (raises if the sizes are not supported)."""
     n = int(lib().proj_paged_attention_q8_workspace_bytes(_i32(batch), _i32(heads), _i32(kv_heads), _i32(k_dim), _i32(v_dim), int(latent)))
-    if n == 0 and batch < 0:
-        raise ProjError(1, lib().proj_last_error_string().decode())
-    if n == 0:  # the same heads and columns are refused of a bf16 cache, with the status that goes with the text
+    if n == 0:
+        text = lib().proj_last_error_string().decode()
+        if batch < 0:
+            raise ProjError(1, text)
+        # the same heads and columns are refused of a bf16 cache, with the status that goes with the text
         paged_attention_workspace_bytes(heads, kv_heads, k_dim, v_dim, latent)
-        raise ProjError(2, "unsupported heads and columns")
+        raise ProjError(2, text)
     return n
 
 

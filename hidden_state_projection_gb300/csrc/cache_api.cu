@@ -115,8 +115,10 @@ size_t attn_workspace(const AttnShape &s, int ctas) {
 }
 
 // Of a cache in 8 bits, in front: the queries' images.
-size_t attn8_images(const AttnShape &s, int batch, int kv_heads, int k_dim) {
-    return up256(static_cast<size_t>(batch) * kv_heads * s.head_tiles * hsp::attn8_image_bytes(k_dim, s.N));
+proj_status attn8_images(const AttnShape &s, int batch, int heads, int kv_heads, int k_dim, size_t *bytes) {
+    *bytes = up256(static_cast<size_t>(batch) * kv_heads * s.head_tiles * hsp::attn8_image_bytes(k_dim, s.N));
+    if (*bytes >= (size_t(1) << 40)) return api_fail(PROJ_ERR_UNSUPPORTED_SHAPE, "batch=%d of %d heads is too large", batch, heads);
+    return PROJ_OK;
 }
 
 proj_status check_kv(const proj_kv_pages *kv) {
@@ -688,7 +690,9 @@ size_t proj_paged_attention_q8_workspace_bytes(int32_t batch, int32_t heads, int
         api_fail(PROJ_ERR_INVALID_ARG, "batch=%d is negative", batch);
         return 0;
     }
-    return attn8_images(s, batch, kv_heads, k_dim) + attn_workspace(s, attn_ctas(s, hsp::api_plan_sms()));
+    size_t images;
+    if (attn8_images(s, batch, heads, kv_heads, k_dim, &images) != PROJ_OK) return 0;
+    return images + attn_workspace(s, attn_ctas(s, hsp::api_plan_sms()));
 }
 
 proj_status proj_paged_attention_q8(const void *q, int64_t q_row_stride, int64_t q_head_stride, const proj_kv_pages_q8 *kv,
@@ -709,8 +713,8 @@ proj_status proj_paged_attention_q8(const void *q, int64_t q_row_stride, int64_t
     if ((st = hsp::api_device(&dev)) != PROJ_OK) return st;
     const int ctas = attn_ctas(s, dev.sms);
     const bool split = static_cast<int64_t>(index->max_pages) * index->page_size > PROJ_UNCUT_TOKENS;
-    const size_t images = attn8_images(s, batch, kv->kv_heads, kv->k_dim);
-    if (images >= (size_t(1) << 40)) return api_fail(PROJ_ERR_UNSUPPORTED_SHAPE, "batch=%d of %d heads is too large", batch, heads);
+    size_t images;
+    if ((st = attn8_images(s, batch, heads, kv->kv_heads, kv->k_dim, &images)) != PROJ_OK) return st;
     if ((st = check_workspace(workspace, workspace_bytes, images + (split ? attn_workspace(s, ctas) : 0))) != PROJ_OK) return st;
     hsp::Attn8LaunchReq r{};
     const int width = kv->v_dim >= 128 ? 128 : 64;
