@@ -14,7 +14,7 @@
 // lie side by side in tensor memory and are added in the softmax.
 //
 // Weights.  The scale of a token's values goes into its weight: w_t = p_t vs_t, in the softmax's own units
-// 2^(s_t + log2 vs_t - m).  w = Wh + Wl, Wh rounded to e4m3, the rest to e5m2: at most 2^-7 of w while w is at least
+// 2^(s_t + log2 vs_t - m).  w = Wh + Wl of w in fp16 (2^-11), Wh rounded to e4m3, the rest to e5m2: at most 2^-7 of w while w is at least
 // 2^-6 (the rest of a smaller one is half of 2^-9 or less, and e5m2 keeps an eighth of that), largest 448.  Two 8-bit
 // pieces have not the range of a bf16 number, so the reference point m (a whole number) follows the tiles in both directions: a tile whose
 // largest weight in some column is beyond 2^8.75, or below 2^-4, moves that column's m (largest weight to 2^3 .. 2^4) and
@@ -30,7 +30,7 @@
 // weights took their probabilities with them: of two tokens with equal scores, one with values of zero, the other came out
 // whole.)  What is lost is what fp32 has no number for: weights below 2^-126 of the reference point, 2^-129 of the row's largest, which
 // takes values' scales more than 2^90 apart.  (With those summed apart, and sums moved from point to point in two steps, the
-// grouped batch below took 66.8 us.)  The mask of the large weights takes 0.5 of the 128 heads' 59.  lse takes u.  Sums
+// grouped batch below took 66.8 us, not 61.6 as then.)  The mask of the large weights takes 0.5 of the 128 heads' 59.  lse takes u.  Sums
 // and statistics are fp32.
 //
 // Warps: four for the softmax of every 16 heads (they also carry O^T out), a copy producer, an issuer of the scores, an
@@ -44,9 +44,9 @@
 // and the copies hide behind it.  Fewer heads: memory.  Beside the tiles stand 4.5 us from the launch to the first copy, 4 to
 // 5 from there to the first weights (DRAM, and code that runs for the first time), 5 us for each further part (its queries,
 // 128 KB of partial O^T at 28 bytes a cycle) and the join.  With the queries' kernel and the join: 48 sequences up to 6001
-// tokens, 128 heads of 576 columns 58.3 us (bf16 cache 61.9); one of 131071 tokens, 64 heads of 512 columns 34.9 (41.0);
-// 61 sequences up to 4099 tokens, 32 heads over 8 of 128 columns 61.0 (91.4; 253 MB, 56 % of the DRAM's rate); 13 sequences up to
-// 2333 tokens, 28 heads over 4 of 64 columns 15.3; 1 sequence of 77 tokens, 16 heads, not cut 8.0.
+// tokens, 128 heads of 576 columns 59.3 us (bf16 cache 61.9); one of 131071 tokens, 64 heads of 512 columns 35.0 (41.0);
+// 61 sequences up to 4099 tokens, 32 heads over 8 of 128 columns 63.4 (91.4; 253 MB, 53 % of the DRAM's rate); 13 sequences up to
+// 2333 tokens, 28 heads over 4 of 64 columns 15.3; 1 sequence of 77 tokens, 16 heads, not cut 8.1.
 #pragma once
 
 #include <cuda_fp16.h>

@@ -20,9 +20,9 @@
 // Bytes: two read and one written per number of the cache, two and two per query's.  What bounds it is latency (row,
 // position, length and page before the first new row, a scale between the two looks at the numbers), so what counts are short
 // code and many lanes: with a warp for 256 pieces, eight each, 2047 tokens of 8 heads of 128 columns took 29 us.  One GB300,
-// us: 8 latent tokens with 16 query heads 4.3; 2047 tokens of 8 kv and 32 query heads of 128 columns 20.0 (14.3 without
-// queries, 7.1 at the copy rate); 1501 latent tokens with 16 query heads 19.0 (11.3; 8.7).  With the queries in a second launch
-// beside this one 5.1, 21.4 and 21.7.
+// us: 8 latent tokens with 16 query heads 4.1; 2047 tokens of 8 kv and 32 query heads of 128 columns 19.9 (14.3 without
+// queries, 7.1 at the copy rate); 1501 latent tokens with 16 query heads 19.0 (11.3; 8.7): most of the queries' CTAs start where the
+// cache's, which fill the GPU, end.  With the queries in a second launch beside this one 5.1, 21.4 and 21.7.
 #include <cuda_bf16.h>
 #include <stdint.h>
 
