@@ -573,7 +573,8 @@ __global__ void __launch_bounds__(attn8_threads(N), PER_SM)
                             const int at = 4 * j + 2 * (r & 1);
                             const float2 x = fma2(make_float2(lo[r >> 1][at], lo[r >> 1][at + 1]), make_float2(0.0625f, 0.0625f),
                                                   make_float2(hi[r >> 1][at], hi[r >> 1][at + 1]));
-                            s[r][j] = fma2(mul2(x, unit[j]), make_float2(ksc[r], ksc[r]), make_float2(vlog[r], vlog[r]));
+                            // (the unit, a power of two, goes to the scale: with the product of large queries it may pass fp32's range)
+                            s[r][j] = fma2(x, mul2(unit[j], make_float2(ksc[r], ksc[r])), make_float2(vlog[r], vlog[r]));
                         }
                 }
                 if (__builtin_expect(valid < T, false)) {

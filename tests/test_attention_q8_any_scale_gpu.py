@@ -32,3 +32,11 @@ def test_scales_at_the_ends_of_the_range(hsp, d, heads, kv, exponent):
     args[3].copy_(m.flip(0) * 2.0 ** -60)
     args[0] = args[0] * 2.0 ** 50
     check(hsp, args, 0.5, d)
+
+
+@pytest.mark.parametrize("latent,dk,dv,heads,kv", KINDS)
+def test_queries_at_the_end_of_their_range(hsp, latent, dk, dv, heads, kv):
+    """Queries of 2^120 over keys of 2^-54 and less: q . codes passes fp32's range, the scores are about one."""
+    args = list(make([700, 40], heads, kv, dk, latent, 16, 9, block=4, spread=0, std=2.0 ** -48))
+    args[0] = (args[0].float().clamp(-3, 3) * 2.0 ** 120).to(args[0].dtype)
+    check(hsp, args, 2.0 ** -74, dv)
