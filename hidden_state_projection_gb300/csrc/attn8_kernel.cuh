@@ -45,7 +45,7 @@
 // 5 from there to the first weights (DRAM, and code that runs for the first time), 5 us for each further part (its queries,
 // 128 KB of partial O^T at 28 bytes a cycle) and the join.  With the queries' kernel and the join: 48 sequences up to 6001
 // tokens, 128 heads of 576 columns 59.3 us (bf16 cache 61.9); one of 131071 tokens, 64 heads of 512 columns 35.0 (41.0);
-// 61 sequences up to 4099 tokens, 32 heads over 8 of 128 columns 63.4 (91.4; 253 MB, 53 % of the DRAM's rate); 13 sequences up to
+// 61 sequences up to 4099 tokens, 32 heads over 8 of 128 columns 61.0 to 63.4 (91.4; 253 MB, 53 % of the DRAM's rate); 13 sequences up to
 // 2333 tokens, 28 heads over 4 of 64 columns 15.3; 1 sequence of 77 tokens, 16 heads, not cut 8.1.
 #pragma once
 
